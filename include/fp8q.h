@@ -80,6 +80,15 @@ typedef enum {
 
 typedef enum { FP8_OUT_BF16 = 0, FP8_OUT_FP32 = 1 } fp8_out_dtype;
 
+/* Element type of the row operators (layer norm, activation, expert dispatch). */
+typedef enum { FP8_DT_BF16 = 0, FP8_DT_FP32 = 1 } fp8_dtype;
+
+typedef enum {
+  FP8_ACT_SILU = 0,      /* x / (1 + exp(-x)) */
+  FP8_ACT_GELU = 1,      /* x (1 + erf(x / sqrt 2)) / 2 */
+  FP8_ACT_GELU_TANH = 2  /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2 */
+} fp8_act;
+
 /*
  * fp8_amax -- per-tensor amax.  Colossal-AI FP8 page, "current scaling" (the
  * scale is computed from the maximum of the current tensor).
@@ -337,6 +346,149 @@ fp8_status fp8_scaled_gemm_amax(const uint8_t* A, fp8_format fa, fp8_recipe ra, 
                                 fp8_format fb, fp8_recipe rb, const void* sB, int64_t M, int64_t N, int64_t K, void* C,
                                 fp8_out_dtype out, float* c_amax, const float* c_scale, fp8_format fc, uint8_t* C_q,
                                 float* c_scale_inv, cudaStream_t stream);
+
+/*
+ * The row operators: what stands between the FP8 linear layers of a transformer block.
+ * Guide, "code changes" (the layers around the three GEMMs stay in BF16 / FP32); the
+ * formulas are the standard ones and given with each call.  For all of them:
+ *   - a matrix argument is [rows, cols] of `dt` with its own row stride ld* >= cols in
+ *     elements (FP8_ERR_SHAPE below it; ignored for a single row) and may start at any
+ *     element (alignment: the element's size).  Rows whose pointer and stride are
+ *     multiples of 16 bytes, with cols a multiple of 16 bytes, are read and written in
+ *     16-byte accesses; anything else element by element, with the same results.
+ *   - outputs must not overlap inputs or each other.
+ *   - arithmetic and every sum are binary32, rounded once to the output's type; results
+ *     are deterministic.
+ *   - the 8-bit copy of a [rows, cols] matrix for the backward pass is the blockwise
+ *     1x128 recipe with a ragged last block: u8 codes [rows, cols] with row stride ldq,
+ *     and float multipliers [rows, ceil(cols / 128)] (dense).  Where cols % 128 == 0 and
+ *     ldq == cols it is FP8_BLOCK_1x128's row-wise copy, which fp8_dequantize reads.
+ */
+
+/*
+ * fp8_layer_norm -- with m the mean and v the (biased) variance of a row of x,
+ *   xh = (x - m) r,  r = 1 / sqrt(v + eps),  y = xh weight + bias
+ *   x           device, [rows, cols] dt
+ *   weight, bias  device, [cols] wdt, each nullable (1 and 0)
+ *   eps         >= 0
+ *   y           device, [rows, cols] dt
+ *   mean, rstd  device, [rows] float, each nullable: m and r, for the backward pass
+ *   fmt, q, ldq, s  q and s both or neither: the 8-bit copy of xh (taken from its
+ *               binary32 values), from which the backward pass needs neither x nor mean
+ * A row with a NaN or an infinity gives a row of NaN.  rows or cols == 0 is a no-op.
+ */
+fp8_status fp8_layer_norm(const void* x, int64_t rows, int64_t cols, int64_t ldx, fp8_dtype dt, const void* weight,
+                          const void* bias, fp8_dtype wdt, float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                          fp8_format fmt, uint8_t* q, int64_t ldq, float* s, cudaStream_t stream);
+
+/*
+ * fp8_layer_norm_backward -- with g = dy weight, c1 = mean(g), c2 = mean(g xh) of a row,
+ *   dx = r (g - c1 - xh c2),  dweight = sum over rows of dy xh,  dbias = sum of dy
+ *   dy          device, [rows, cols] dt
+ *   x, mean     the forward pass's input and means, or both NULL and
+ *   fmt, q, ldq, s  its 8-bit copy (exactly one of the two)
+ *   rstd        device, [rows] float
+ *   weight      device, [cols] wdt, nullable (1)
+ *   dx          device, [rows, cols] dt
+ *   dweight, dbias  device, [cols] wdt, each nullable
+ *   workspace   device, 16-byte aligned, fp8_layer_norm_workspace bytes; may be NULL when
+ *               dweight and dbias are.  Its contents need no initialisation and mean
+ *               nothing after the call.
+ * rows == 0 sets dweight and dbias to 0; cols == 0 is a no-op.
+ */
+fp8_status fp8_layer_norm_backward(const void* dy, int64_t rows, int64_t cols, int64_t lddy, fp8_dtype dt, const void* x,
+                                   int64_t ldx, const float* mean, const float* rstd, fp8_format fmt, const uint8_t* q,
+                                   int64_t ldq, const float* s, const void* weight, fp8_dtype wdt, void* dx, int64_t lddx,
+                                   void* dweight, void* dbias, void* workspace, int64_t workspace_bytes,
+                                   cudaStream_t stream);
+/* *bytes (host): the workspace of fp8_layer_norm_backward for this shape; at most
+ * 304 * 8 * cols.  No device call. */
+fp8_status fp8_layer_norm_workspace(int64_t rows, int64_t cols, int64_t* bytes);
+
+/*
+ * fp8_gated_act -- y = f(a) b, or y = f(a) with b NULL; f is `act`.
+ *   a, b        device, [rows, cols] dt, each with its own stride (the halves of one
+ *               [rows, 2 cols] product, for instance); b nullable
+ *   y           device, [rows, cols] dt
+ *   fmt, qa, sa, qb, sb, ldq  optional 8-bit copies of a and b for the backward pass
+ *               (codes and multipliers both or neither; qb needs b; one stride for both)
+ * rows or cols == 0 is a no-op.
+ */
+fp8_status fp8_gated_act(const void* a, int64_t rows, int64_t cols, int64_t lda, fp8_dtype dt, fp8_act act, const void* b,
+                         int64_t ldb, void* y, int64_t ldy, fp8_format fmt, uint8_t* qa, float* sa, uint8_t* qb, float* sb,
+                         int64_t ldq, cudaStream_t stream);
+
+/*
+ * fp8_gated_act_backward -- da = dy b f'(a) and db = dy f(a), or da = dy f'(a).
+ *   dy          device, [rows, cols] dt
+ *   a, b        the forward pass's inputs (b NULL: not gated), or both NULL and
+ *   fmt, qa, sa, qb, sb, ldq  their 8-bit copies: f and f' are taken at the values these
+ *               stand for (exactly one of a and qa; qb, sb NULL: not gated)
+ *   da, db      device, [rows, cols] dt; db exactly when gated
+ */
+fp8_status fp8_gated_act_backward(const void* dy, int64_t rows, int64_t cols, int64_t lddy, fp8_dtype dt, fp8_act act,
+                                  const void* a, int64_t lda, const void* b, int64_t ldb, fp8_format fmt,
+                                  const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb, int64_t ldq,
+                                  void* da, int64_t ldda, void* db, int64_t lddb, cudaStream_t stream);
+
+/*
+ * fp8_moe_route -- the choices of `tokens` tokens, k each, sorted by expert.  With choice
+ * i = token * k + j:
+ *   experts     device, [tokens, k] int32 (id_bytes 4) or int64 (8); a choice outside
+ *               [0, n_experts) is dropped
+ *   n_experts   1..1024;  align >= 1: every expert's segment is padded to a multiple of it
+ *               (128 makes the segments operands of fp8_scaled_gemm)
+ *   offsets     device, [n_experts + 1] int32: the segments' first rows; the last entry is
+ *               the number of rows in use
+ *   pos         device, [tokens, k] int32: the choice's row (its expert's choices keep
+ *               their order), -1 when dropped
+ *   src         device, [capacity] int32: the row's choice i, -1 for rows that pad
+ *   capacity    rows, at least fp8_moe_sizes' (FP8_ERR_SHAPE below it)
+ *   workspace   device, 4-byte aligned, fp8_moe_sizes' bytes (NULL when that is 0)
+ * tokens * k and capacity must be below 2^31 (FP8_ERR_SHAPE).
+ */
+fp8_status fp8_moe_route(const void* experts, int32_t id_bytes, int64_t tokens, int32_t k, int32_t n_experts, int32_t align,
+                         int32_t* offsets, int32_t* pos, int32_t* src, int64_t capacity, void* workspace,
+                         int64_t workspace_bytes, cudaStream_t stream);
+/* Host arithmetic only: *capacity = the most rows a routing of this size can use,
+ * *workspace_bytes = fp8_moe_route's workspace. */
+fp8_status fp8_moe_sizes(int64_t tokens, int32_t k, int32_t n_experts, int32_t align, int64_t* capacity,
+                         int64_t* workspace_bytes);
+
+/*
+ * fp8_moe_dispatch -- every token's row copied to its choices' rows:
+ *   xs[r] = x[src[r] / k], and 0 where src[r] is -1
+ *   x   device, [tokens, cols] dt;  xs  device, [capacity, cols] dt
+ *   pos, src   as fp8_moe_route wrote them (entries of pos outside [-1, capacity) are
+ *              skipped and reported as FP8_ERR_DEVICE_STATE by fp8_get_device_status)
+ */
+fp8_status fp8_moe_dispatch(const void* x, int64_t tokens, int64_t cols, int64_t ldx, fp8_dtype dt, int32_t k,
+                            const int32_t* pos, const int32_t* src, int64_t capacity, void* xs, int64_t ldxs,
+                            cudaStream_t stream);
+
+/*
+ * fp8_moe_combine -- y[t] = sum over j of weights[t, j] ys[pos[t, j]], in order of j, over
+ * the choices that were not dropped (neither their weights nor any row are read for those
+ * that were; a token with none gives 0).  weights NULL: 1, which is also the gradient of
+ * fp8_moe_dispatch (ys its output's gradient, y its input's).
+ *   ys  device, [capacity, cols] dt;  y  device, [tokens, cols] dt
+ *   weights  device, [tokens, k] float, nullable
+ */
+fp8_status fp8_moe_combine(const void* ys, int64_t capacity, int64_t cols, int64_t ldys, fp8_dtype dt, int64_t tokens,
+                           int32_t k, const int32_t* pos, const float* weights, void* y, int64_t ldy, cudaStream_t stream);
+
+/*
+ * fp8_moe_combine_backward -- the gradients of fp8_moe_combine:
+ *   dys[r] = weights[src[r]] dy[src[r] / k], 0 where src[r] is -1
+ *   dweights[t, j] = <dy[t], ys[pos[t, j]]>, 0 for a dropped choice
+ *   dy  device, [tokens, cols] dt;  ys, dys  device, [capacity, cols] dt
+ *   weights  device, [tokens, k] float, nullable (1)
+ *   dweights  device, [tokens, k] float, nullable (ys is then not read and may be NULL)
+ */
+fp8_status fp8_moe_combine_backward(const void* dy, int64_t tokens, int64_t cols, int64_t lddy, fp8_dtype dt, int32_t k,
+                                    const int32_t* pos, const int32_t* src, const float* weights, const void* ys,
+                                    int64_t ldys, int64_t capacity, void* dys, int64_t lddys, float* dweights,
+                                    cudaStream_t stream);
 
 /*
  * fp8_get_device_status -- synchronize `stream`, then read and clear the

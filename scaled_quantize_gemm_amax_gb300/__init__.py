@@ -12,16 +12,21 @@ Entry points with the C names take tensors (or None for NULL) and raise
 ``fp8_cast_transpose_multi``,
 ``fp8_dequantize``, ``fp8_allreduce_sum``, ``fp8_scaled_gemm``, ``fp8_scaled_gemm_amax``,
 ``fp8_get_device_status``, ``fp8_debug_wait_timeout``, ``fp8_debug_gemm_plan``,
-``fp8_debug_index_check``.  ``cast_transpose`` /
-``dequantize`` / ``scaled_gemm`` / ``scaled_gemm_amax`` are allocation helpers
+``fp8_debug_index_check``; and the row operators between the linear layers,
+``fp8_layer_norm``, ``fp8_layer_norm_backward``, ``fp8_gated_act``,
+``fp8_gated_act_backward``, ``fp8_moe_route``, ``fp8_moe_dispatch``, ``fp8_moe_combine``,
+``fp8_moe_combine_backward`` (with ``fp8_layer_norm_workspace`` and ``fp8_moe_sizes``).
+``cast_transpose`` / ``dequantize`` / ``scaled_gemm`` / ``scaled_gemm_amax`` /
+``layer_norm`` / ``gated_act`` / ``moe_route`` ... are allocation helpers
 over them; ``linear`` holds the FP8 linear layer and the autocast scope built
-on these calls.
+on these calls, ``blocks`` the differentiable row operators and an expert MLP block.
 """
 from __future__ import annotations
 
 import ctypes
 import enum
 import os
+import typing
 
 import torch
 
@@ -34,6 +39,11 @@ __all__ = [
     "fp8_debug_wait_timeout", "fp8_debug_gemm_plan", "fp8_debug_index_check", "fp8_status_string",
     "scale_shape", "cast_transpose", "cast_transpose_multi", "dequantize", "allreduce_sum", "scaled_gemm", "scaled_gemm_amax",
     "DelayedScaling",
+    "Activation", "MoeRoute",
+    "fp8_layer_norm", "fp8_layer_norm_backward", "fp8_layer_norm_workspace", "fp8_gated_act", "fp8_gated_act_backward",
+    "fp8_moe_route", "fp8_moe_sizes", "fp8_moe_dispatch", "fp8_moe_combine", "fp8_moe_combine_backward",
+    "layer_norm", "layer_norm_backward", "gated_act", "gated_act_backward", "moe_route", "moe_dispatch", "moe_combine",
+    "moe_combine_backward", "moe_dispatch_backward",
 ]
 
 
@@ -67,6 +77,12 @@ class Recipe(enum.IntEnum):
 class OutDtype(enum.IntEnum):
     BF16 = 0
     FP32 = 1
+
+
+class Activation(enum.IntEnum):
+    SILU = 0
+    GELU = 1
+    GELU_TANH = 2
 
 
 class FP8Error(RuntimeError):
@@ -110,6 +126,18 @@ _SIGNATURES = {
     "fp8_allreduce_sum_noalloc": [_P, _I32, _I64, _E, _P, _P, _P, _P],
     "fp8_scaled_gemm": [_P, _E, _E, _P, _P, _E, _E, _P, _I64, _I64, _I64, _P, _E, _P],
     "fp8_scaled_gemm_amax": [_P, _E, _E, _P, _P, _E, _E, _P, _I64, _I64, _I64, _P, _E, _P, _P, _E, _P, _P, _P],
+    "fp8_layer_norm": [_P, _I64, _I64, _I64, _E, _P, _P, _E, ctypes.c_float, _P, _I64, _P, _P, _E, _P, _I64, _P, _P],
+    "fp8_layer_norm_backward": [_P, _I64, _I64, _I64, _E, _P, _I64, _P, _P, _E, _P, _I64, _P, _P, _E, _P, _I64, _P, _P, _P,
+                                _I64, _P],
+    "fp8_layer_norm_workspace": [_I64, _I64, _P],
+    "fp8_gated_act": [_P, _I64, _I64, _I64, _E, _E, _P, _I64, _P, _I64, _E, _P, _P, _P, _P, _I64, _P],
+    "fp8_gated_act_backward": [_P, _I64, _I64, _I64, _E, _E, _P, _I64, _P, _I64, _E, _P, _P, _P, _P, _I64, _P, _I64, _P,
+                               _I64, _P],
+    "fp8_moe_route": [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P, _I64, _P, _I64, _P],
+    "fp8_moe_sizes": [_I64, _I32, _I32, _I32, _P, _P],
+    "fp8_moe_dispatch": [_P, _I64, _I64, _I64, _E, _I32, _P, _P, _I64, _P, _I64, _P],
+    "fp8_moe_combine": [_P, _I64, _I64, _I64, _E, _I64, _I32, _P, _P, _P, _I64, _P],
+    "fp8_moe_combine_backward": [_P, _I64, _I64, _I64, _E, _I32, _P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _P],
     "fp8_get_device_status": [_P],
     "fp8_debug_wait_timeout": [_P],
     "fp8_debug_gemm_plan": [_E, _E, _E, _I64, _I64, _I64, _I32, _I32, _I32, _P],
@@ -278,6 +306,196 @@ def fp8_scaled_gemm_amax(a, fa, ra, sa, b, fb, rb, sb, c, out, c_amax, c_scale, 
                                                int(fc), _ptr(c_q), _ptr(c_scale_inv), _stream(stream)))
 
 
+def _rows(t, what: str):
+    """(rows, cols, row stride) of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{what}: a 2-D tensor with contiguous rows is needed, not shape {tuple(t.shape)} "
+                         f"stride {t.stride()}")
+    return t.shape[0], t.shape[1], t.stride(0)
+
+
+_DTYPE_CODE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _dtype(t, what: str) -> int:
+    try:
+        return _DTYPE_CODE[t.dtype]
+    except KeyError:
+        raise TypeError(f"{what}: bfloat16 or float32 is needed, not {t.dtype}") from None
+
+
+def _like(t, ref, what: str):
+    """The row stride of `t`, which must have the shape and type of `ref` (None: 0)."""
+    if t is None:
+        return 0
+    if t.shape != ref.shape or t.dtype != ref.dtype:
+        raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)}, expected {ref.dtype} {tuple(ref.shape)}")
+    return _rows(t, what)[2]
+
+
+def _vector(t, n: int, what: str, dtype=torch.float32):
+    """A dense vector (or matrix) of n elements of `dtype` (None passes)."""
+    if t is not None and (t.numel() != n or t.dtype != dtype or not t.is_contiguous()):
+        raise ValueError(f"{what}: {n} contiguous {dtype} elements are needed, not {t.dtype} {tuple(t.shape)}")
+
+
+def _codes(q, s, rows: int, cols: int, what: str) -> int:
+    """The row stride of an 8-bit copy's codes, having checked codes and multipliers (both None: 0)."""
+    if q is None and s is None:
+        return 0
+    if q is None or s is None or q.element_size() != 1 or q.shape != (rows, cols):
+        raise ValueError(f"{what}: codes [{rows}, {cols}] of one byte and their multipliers are needed")
+    _vector(s, rows * ((cols + 127) // 128), f"{what} multipliers")
+    return _rows(q, what)[2]
+
+
+def _params(weight, bias, cols: int):
+    """The type code of weight and bias (either may be None)."""
+    p = weight if weight is not None else bias
+    if p is None:
+        return 1
+    code = _dtype(p, "weight / bias")
+    _vector(weight, cols, "weight", p.dtype)
+    _vector(bias, cols, "bias", p.dtype)
+    return code
+
+
+def _on_gpu(*tensors):
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"a CUDA tensor is needed, not one on {t.device}")
+
+
+def fp8_layer_norm(x, weight, bias, eps, y, mean, rstd, fmt, q, s, stream=None):
+    rows, cols, ldx = _rows(x, "x")
+    dt, wdt = _dtype(x, "x"), _params(weight, bias, cols)
+    ldy, ldq = _like(y, x, "y"), _codes(q, s, rows, cols, "q")
+    _vector(mean, rows, "mean")
+    _vector(rstd, rows, "rstd")
+    _on_gpu(x, weight, bias, y, mean, rstd, q, s)
+    _check("fp8_layer_norm",
+           load_library().fp8_layer_norm(_ptr(x), rows, cols, ldx, dt, _ptr(weight), _ptr(bias), wdt, eps, _ptr(y), ldy,
+                                         _ptr(mean), _ptr(rstd), int(fmt), _ptr(q), ldq, _ptr(s), _stream(stream)))
+
+
+def fp8_layer_norm_workspace(rows: int, cols: int) -> int:
+    """Bytes of fp8_layer_norm_backward's workspace (host arithmetic)."""
+    n = ctypes.c_int64()
+    _check("fp8_layer_norm_workspace", load_library().fp8_layer_norm_workspace(rows, cols, ctypes.addressof(n)))
+    return n.value
+
+
+def fp8_layer_norm_backward(dy, x, mean, rstd, fmt, q, s, weight, dx, dweight, dbias, workspace, stream=None):
+    rows, cols, lddy = _rows(dy, "dy")
+    dt = _dtype(dy, "dy")
+    wdt = _params(weight, dweight, cols)
+    wdt = wdt if weight is not None or dweight is not None else _params(None, dbias, cols)
+    ldx, lddx, ldq = _like(x, dy, "x"), _like(dx, dy, "dx"), _codes(q, s, rows, cols, "q")
+    for t in (dweight, dbias):
+        if t is not None:
+            _vector(t, cols, "dweight / dbias", (torch.bfloat16, torch.float32)[wdt])
+    _vector(mean, rows, "mean")
+    _vector(rstd, rows, "rstd")
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _on_gpu(dy, x, mean, rstd, q, s, weight, dx, dweight, dbias, workspace)
+    _check("fp8_layer_norm_backward",
+           load_library().fp8_layer_norm_backward(_ptr(dy), rows, cols, lddy, dt, _ptr(x), ldx, _ptr(mean), _ptr(rstd),
+                                                  int(fmt), _ptr(q), ldq, _ptr(s), _ptr(weight), wdt, _ptr(dx), lddx,
+                                                  _ptr(dweight), _ptr(dbias), _ptr(workspace), nbytes, _stream(stream)))
+
+
+def fp8_gated_act(a, b, act, y, fmt, qa, sa, qb, sb, stream=None):
+    rows, cols, lda = _rows(a, "a")
+    ldb, ldy = _like(b, a, "b"), _like(y, a, "y")
+    ldq, ldqb = _codes(qa, sa, rows, cols, "qa"), _codes(qb, sb, rows, cols, "qb")
+    if qa is not None and qb is not None and ldq != ldqb and rows > 1:
+        raise ValueError("qa and qb: one row stride is needed for both")
+    _on_gpu(a, b, y, qa, sa, qb, sb)
+    _check("fp8_gated_act",
+           load_library().fp8_gated_act(_ptr(a), rows, cols, lda, _dtype(a, "a"), int(act), _ptr(b), ldb, _ptr(y), ldy,
+                                        int(fmt), _ptr(qa), _ptr(sa), _ptr(qb), _ptr(sb), ldq or ldqb, _stream(stream)))
+
+
+def fp8_gated_act_backward(dy, act, a, b, fmt, qa, sa, qb, sb, da, db, stream=None):
+    rows, cols, lddy = _rows(dy, "dy")
+    lda, ldb = _like(a, dy, "a"), _like(b, dy, "b")
+    ldda, lddb = _like(da, dy, "da"), _like(db, dy, "db")
+    ldq, ldqb = _codes(qa, sa, rows, cols, "qa"), _codes(qb, sb, rows, cols, "qb")
+    if qa is not None and qb is not None and ldq != ldqb and rows > 1:
+        raise ValueError("qa and qb: one row stride is needed for both")
+    _on_gpu(dy, a, b, qa, sa, qb, sb, da, db)
+    _check("fp8_gated_act_backward",
+           load_library().fp8_gated_act_backward(_ptr(dy), rows, cols, lddy, _dtype(dy, "dy"), int(act), _ptr(a), lda,
+                                                 _ptr(b), ldb, int(fmt), _ptr(qa), _ptr(sa), _ptr(qb), _ptr(sb), ldq,
+                                                 _ptr(da), ldda, _ptr(db), lddb, _stream(stream)))
+
+
+def fp8_moe_sizes(tokens: int, k: int, n_experts: int, align: int):
+    """(rows a routing of this size can use, bytes of fp8_moe_route's workspace); host arithmetic."""
+    out = (ctypes.c_int64 * 2)()
+    at = ctypes.addressof(out)
+    _check("fp8_moe_sizes", load_library().fp8_moe_sizes(tokens, k, n_experts, align, at, at + 8))
+    return out[0], out[1]
+
+
+def fp8_moe_route(experts, n_experts: int, align: int, offsets, pos, src, workspace, stream=None):
+    if experts.dim() != 2 or experts.dtype not in (torch.int32, torch.int64) or not experts.is_contiguous():
+        raise ValueError("experts: a contiguous [tokens, k] int32 or int64 tensor is needed")
+    tokens, k = experts.shape
+    _vector(offsets, n_experts + 1, "offsets", torch.int32)
+    _vector(pos, tokens * k, "pos", torch.int32)
+    _vector(src, src.numel(), "src", torch.int32)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _on_gpu(experts, offsets, pos, src, workspace)
+    _check("fp8_moe_route",
+           load_library().fp8_moe_route(_ptr(experts), experts.element_size(), tokens, k, n_experts, align, _ptr(offsets),
+                                        _ptr(pos), _ptr(src), src.numel(), _ptr(workspace), nbytes, _stream(stream)))
+
+
+def _scattered(x, pos, src, out):
+    """Checks of the operators that copy [tokens, cols] rows to [capacity, cols]; (tokens, cols, ldx, k, capacity, ldout)."""
+    tokens, cols, ldx = _rows(x, "rows of tokens")
+    if pos.dim() != 2 or pos.shape[0] != tokens:
+        raise ValueError(f"pos: shape ({tokens}, k) is needed, not {tuple(pos.shape)}")
+    _vector(pos, pos.numel(), "pos", torch.int32)
+    _vector(src, src.numel(), "src", torch.int32)
+    if out.shape != (src.numel(), cols) or out.dtype != x.dtype:
+        raise ValueError(f"rows of choices: {x.dtype} ({src.numel()}, {cols}) is needed, not {out.dtype} {tuple(out.shape)}")
+    return tokens, cols, ldx, pos.shape[1], src.numel(), _rows(out, "rows of choices")[2]
+
+
+def fp8_moe_dispatch(x, pos, src, xs, stream=None):
+    tokens, cols, ldx, k, capacity, ldxs = _scattered(x, pos, src, xs)
+    _on_gpu(x, pos, src, xs)
+    _check("fp8_moe_dispatch",
+           load_library().fp8_moe_dispatch(_ptr(x), tokens, cols, ldx, _dtype(x, "x"), k, _ptr(pos), _ptr(src), capacity,
+                                           _ptr(xs), ldxs, _stream(stream)))
+
+
+def fp8_moe_combine(ys, pos, weights, y, stream=None):
+    capacity, cols, ldys = _rows(ys, "ys")
+    tokens, k = pos.shape
+    _vector(pos, tokens * k, "pos", torch.int32)
+    _vector(weights, tokens * k, "weights")
+    if y.shape != (tokens, cols) or y.dtype != ys.dtype:
+        raise ValueError(f"y: {ys.dtype} ({tokens}, {cols}) is needed, not {y.dtype} {tuple(y.shape)}")
+    _on_gpu(ys, pos, weights, y)
+    _check("fp8_moe_combine",
+           load_library().fp8_moe_combine(_ptr(ys), capacity, cols, ldys, _dtype(ys, "ys"), tokens, k, _ptr(pos),
+                                          _ptr(weights), _ptr(y), _rows(y, "y")[2], _stream(stream)))
+
+
+def fp8_moe_combine_backward(dy, pos, src, weights, ys, dys, dweights, stream=None):
+    tokens, cols, lddy, k, capacity, lddys = _scattered(dy, pos, src, dys)
+    _vector(weights, tokens * k, "weights")
+    _vector(dweights, tokens * k, "dweights")
+    _on_gpu(dy, pos, src, weights, ys, dys, dweights)
+    _check("fp8_moe_combine_backward",
+           load_library().fp8_moe_combine_backward(_ptr(dy), tokens, cols, lddy, _dtype(dy, "dy"), k, _ptr(pos), _ptr(src),
+                                                   _ptr(weights), _ptr(ys), _like(ys, dys, "ys"), capacity, _ptr(dys),
+                                                   lddys, _ptr(dweights), _stream(stream)))
+
+
 def fp8_get_device_status(stream=None) -> Status:
     return Status(load_library().fp8_get_device_status(_stream(stream)))
 
@@ -390,6 +608,130 @@ def scaled_gemm_amax(a, fa, ra, sa, b, fb, rb, sb, c_scale, fc=Format.E4M3, out=
     c_scale_inv = torch.empty(1, dtype=torch.float32, device=dev)
     fp8_scaled_gemm_amax(a, fa, ra, sa, b, fb, rb, sb, c, out, c_amax, c_scale, fc, c_q, c_scale_inv, stream)
     return c, c_amax, c_q, c_scale_inv
+
+
+# ------------------------------------------------------------------ row operators, outputs allocated
+def _codes_like(x, rows: int, cols: int):
+    """Codes and multipliers of an 8-bit copy.  The codes' row stride is padded to 16 bytes."""
+    ld = (cols + 15) // 16 * 16
+    q = torch.empty((rows, ld), dtype=torch.uint8, device=x.device)
+    return q if ld == cols else q[:, :cols], torch.empty((rows, (cols + 127) // 128), dtype=torch.float32, device=x.device)
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, checkpoint=None, stats: bool = True, stream=None):
+    """Allocate outputs and run fp8_layer_norm on x [rows, cols].
+
+    Returns (y, mean, rstd, q, s).  checkpoint: a Format keeps the normalised rows in 8 bits
+    (q, s; else None).  stats=False skips mean and rstd (inference)."""
+    rows, cols = x.shape
+    y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    mean = rstd = q = s = None
+    if stats:
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    if checkpoint is not None:
+        q, s = _codes_like(x, rows, cols)
+    fp8_layer_norm(x, weight, bias, eps, y, mean, rstd, checkpoint or 0, q, s, stream)
+    return y, mean, rstd, q, s
+
+
+def layer_norm_backward(dy, rstd, weight=None, x=None, mean=None, q=None, s=None, fmt=Format.E4M3, param_grads: bool = True,
+                        param_dtype=None, stream=None):
+    """Allocate outputs and run fp8_layer_norm_backward; x and mean, or the 8-bit copy q and s.
+
+    Returns (dx, dweight, dbias), the last two in the weight's type (param_dtype without a
+    weight; default float32), or None with param_grads=False."""
+    rows, cols = dy.shape
+    dx = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device)
+    dw = db = workspace = None
+    if param_grads:
+        dt = weight.dtype if weight is not None else param_dtype or torch.float32
+        dw = torch.empty(cols, dtype=dt, device=dy.device)
+        db = torch.empty(cols, dtype=dt, device=dy.device)
+        workspace = torch.empty(fp8_layer_norm_workspace(rows, cols), dtype=torch.uint8, device=dy.device)
+    fp8_layer_norm_backward(dy, x, mean, rstd, fmt, q, s, weight, dx, dw, db, workspace, stream)
+    return dx, dw, db
+
+
+def gated_act(a, b=None, act=Activation.SILU, checkpoint=None, stream=None):
+    """Allocate outputs and run fp8_gated_act: f(a) * b, or f(a) without b.
+
+    Returns (y, qa, sa, qb, sb); the 8-bit copies only with checkpoint=Format (else None)."""
+    rows, cols = a.shape
+    y = torch.empty((rows, cols), dtype=a.dtype, device=a.device)
+    qa = sa = qb = sb = None
+    if checkpoint is not None:
+        qa, sa = _codes_like(a, rows, cols)
+        if b is not None:
+            qb, sb = _codes_like(a, rows, cols)
+    fp8_gated_act(a, b, act, y, checkpoint or 0, qa, sa, qb, sb, stream)
+    return y, qa, sa, qb, sb
+
+
+def gated_act_backward(dy, act=Activation.SILU, a=None, b=None, qa=None, sa=None, qb=None, sb=None, fmt=Format.E4M3,
+                       stream=None):
+    """Allocate outputs and run fp8_gated_act_backward; a (and b), or their 8-bit copies.
+
+    Returns (da, db): the halves of one [rows, 2 cols] tensor, or (da, None) when not gated."""
+    rows, cols = dy.shape
+    if b is None and qb is None:
+        da, db = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device), None
+    else:
+        d = torch.empty((rows, 2 * cols), dtype=dy.dtype, device=dy.device)
+        da, db = d[:, :cols], d[:, cols:]
+    fp8_gated_act_backward(dy, act, a, b, fmt, qa, sa, qb, sb, da, db, stream)
+    return da, db
+
+
+class MoeRoute(typing.NamedTuple):
+    """Where a router's choices go: fp8_moe_route's offsets [E + 1], pos [tokens, k], src [capacity]."""
+    offsets: torch.Tensor
+    pos: torch.Tensor
+    src: torch.Tensor
+
+
+def moe_route(experts, n_experts: int, align: int = 1, stream=None) -> MoeRoute:
+    """Allocate outputs and run fp8_moe_route on experts [tokens, k] (a choice outside [0, n_experts) is dropped).
+
+    align=128 makes every expert's segment an operand of scaled_gemm."""
+    tokens, k = experts.shape
+    capacity, nbytes = fp8_moe_sizes(tokens, k, n_experts, align)
+    dev = experts.device
+    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
+    pos = torch.empty((tokens, k), dtype=torch.int32, device=dev)
+    src = torch.empty(capacity, dtype=torch.int32, device=dev)
+    workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    fp8_moe_route(experts, n_experts, align, offsets, pos, src, workspace, stream)
+    return MoeRoute(offsets, pos, src)
+
+
+def moe_dispatch(x, route: MoeRoute, stream=None):
+    """xs [capacity, cols]: every token's row at its choices' rows, 0 in the rows that pad."""
+    xs = torch.empty((route.src.numel(), x.shape[1]), dtype=x.dtype, device=x.device)
+    fp8_moe_dispatch(x, route.pos, route.src, xs, stream)
+    return xs
+
+
+def moe_combine(ys, route: MoeRoute, weights=None, stream=None):
+    """y [tokens, cols]: the choices' rows of ys summed with weights [tokens, k] float32 (None: 1)."""
+    y = torch.empty((route.pos.shape[0], ys.shape[1]), dtype=ys.dtype, device=ys.device)
+    fp8_moe_combine(ys, route.pos, weights, y, stream)
+    return y
+
+
+def moe_combine_backward(dy, ys, route: MoeRoute, weights=None, stream=None):
+    """The gradients of moe_combine: (dys [capacity, cols], dweights [tokens, k] or None without weights)."""
+    dys = torch.empty((route.src.numel(), dy.shape[1]), dtype=dy.dtype, device=dy.device)
+    dw = None
+    if weights is not None:
+        dw = torch.empty(route.pos.shape, dtype=torch.float32, device=dy.device)
+    fp8_moe_combine_backward(dy, route.pos, route.src, weights, ys if dw is not None else None, dys, dw, stream)
+    return dys, dw
+
+
+def moe_dispatch_backward(dxs, route: MoeRoute, stream=None):
+    """The gradient of moe_dispatch: every token's choices' rows of dxs, summed."""
+    return moe_combine(dxs, route, None, stream)
 
 
 class DelayedScaling:

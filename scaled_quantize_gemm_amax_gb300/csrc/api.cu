@@ -635,3 +635,345 @@ fp8_status fp8_debug_wait_timeout(cudaStream_t stream) {
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------ row operators
+namespace {
+
+bool valid_dt(fp8_dtype d) { return d == FP8_DT_BF16 || d == FP8_DT_FP32; }
+uintptr_t elem_size(fp8_dtype d) { return d == FP8_DT_FP32 ? 4 : 2; }
+
+// Whether a row stride can hold `cols` (a single row's stride is not used: set to cols).
+bool row_stride(int64_t rows, int64_t cols, int64_t* ld) {
+  if (rows <= 1) *ld = cols;
+  return *ld >= cols && *ld <= kMaxDim;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8_status fp8_layer_norm(const void* x, int64_t rows, int64_t cols, int64_t ldx, fp8_dtype dt, const void* weight,
+                          const void* bias, fp8_dtype wdt, float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                          fp8_format fmt, uint8_t* q, int64_t ldq, float* s, cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_layer_norm");
+  if (rows < 0 || cols < 0 || !valid_dt(dt) || !valid_dt(wdt) || !valid_fmt(fmt) || !(eps >= 0.0f)) return FP8_ERR_INVALID_ARG;
+  if ((q == nullptr) != (s == nullptr) && rows > 0 && cols > 0) return FP8_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return FP8_OK;
+  if (x == nullptr || y == nullptr) return FP8_ERR_INVALID_ARG;
+  if (rows > kMaxDim || cols > kMaxDim || !row_stride(rows, cols, &ldx) || !row_stride(rows, cols, &ldy) ||
+      (q != nullptr && !row_stride(rows, cols, &ldq)))
+    return FP8_ERR_SHAPE;
+  const uintptr_t es = elem_size(dt), ws = elem_size(wdt);
+  if (!aligned(x, es) || !aligned(y, es) || !aligned(weight, ws) || !aligned(bias, ws) || !aligned(mean, 4) ||
+      !aligned(rstd, 4) || !aligned(s, 4))
+    return FP8_ERR_ALIGNMENT;
+  DeviceInfo* d;
+  if (fp8_status st = device_info(&d)) return st;
+  NormParams p{};
+  p.x = x;
+  p.rows = rows;
+  p.cols = cols;
+  p.ldx = ldx;
+  p.f32 = dt == FP8_DT_FP32;
+  p.w = weight;
+  p.b = bias;
+  p.w_f32 = wdt == FP8_DT_FP32;
+  p.eps = eps;
+  p.y = y;
+  p.ldy = ldy;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.e5m2 = fmt == FP8_E5M2;
+  p.q = q;
+  p.ldq = ldq;
+  p.s = s;
+  return cuda_status(launch_norm(p, d->num_sms, stream));
+}
+
+fp8_status fp8_layer_norm_workspace(int64_t rows, int64_t cols, int64_t* bytes) {
+  ApiRange nvtx_range("fp8_layer_norm_workspace");
+  if (rows < 0 || cols < 0 || bytes == nullptr) return FP8_ERR_INVALID_ARG;
+  if (rows > kMaxDim || cols > kMaxDim) return FP8_ERR_SHAPE;
+  *bytes = static_cast<int64_t>(norm_partials(rows)) * 2 * cols * static_cast<int64_t>(sizeof(float));
+  return FP8_OK;
+}
+
+fp8_status fp8_layer_norm_backward(const void* dy, int64_t rows, int64_t cols, int64_t lddy, fp8_dtype dt, const void* x,
+                                   int64_t ldx, const float* mean, const float* rstd, fp8_format fmt, const uint8_t* q,
+                                   int64_t ldq, const float* s, const void* weight, fp8_dtype wdt, void* dx, int64_t lddx,
+                                   void* dweight, void* dbias, void* workspace, int64_t workspace_bytes,
+                                   cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_layer_norm_backward");
+  if (rows < 0 || cols < 0 || !valid_dt(dt) || !valid_dt(wdt) || !valid_fmt(fmt)) return FP8_ERR_INVALID_ARG;
+  if (cols == 0) return FP8_OK;
+  if (rows > 0) {
+    if (dy == nullptr || dx == nullptr || rstd == nullptr) return FP8_ERR_INVALID_ARG;
+    if ((x == nullptr) == (q == nullptr) || (x == nullptr) != (mean == nullptr) || (q == nullptr) != (s == nullptr))
+      return FP8_ERR_INVALID_ARG;
+  }
+  const bool params = dweight != nullptr || dbias != nullptr;
+  if (params && workspace == nullptr) return FP8_ERR_INVALID_ARG;
+  if (rows > kMaxDim || cols > kMaxDim) return FP8_ERR_SHAPE;
+  if (!row_stride(rows, cols, &lddy) || !row_stride(rows, cols, &lddx) || (x != nullptr && !row_stride(rows, cols, &ldx)) ||
+      (q != nullptr && !row_stride(rows, cols, &ldq)))
+    return FP8_ERR_SHAPE;
+  int64_t need = 0;
+  if (params) {
+    if (fp8_status st = fp8_layer_norm_workspace(rows, cols, &need)) return st;
+    if (workspace_bytes < need) return FP8_ERR_SHAPE;
+    if (!aligned(workspace, 16)) return FP8_ERR_ALIGNMENT;
+  }
+  const uintptr_t es = elem_size(dt), ws = elem_size(wdt);
+  if (!aligned(dy, es) || !aligned(x, es) || !aligned(dx, es) || !aligned(weight, ws) || !aligned(dweight, ws) ||
+      !aligned(dbias, ws) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(s, 4))
+    return FP8_ERR_ALIGNMENT;
+  if (rows == 0 && !params) return FP8_OK;
+  DeviceInfo* d;
+  if (fp8_status st = device_info(&d)) return st;
+  NormBwdParams p{};
+  p.dy = dy;
+  p.rows = rows;
+  p.cols = cols;
+  p.lddy = lddy;
+  p.f32 = dt == FP8_DT_FP32;
+  p.x = x;
+  p.ldx = ldx;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.e5m2 = fmt == FP8_E5M2;
+  p.q = q;
+  p.ldq = ldq;
+  p.s = s;
+  p.w = weight;
+  p.w_f32 = wdt == FP8_DT_FP32;
+  p.dx = dx;
+  p.lddx = lddx;
+  p.dw = dweight;
+  p.db = dbias;
+  p.partial = static_cast<float*>(workspace);
+  return cuda_status(launch_norm_backward(p, d->num_sms, stream));
+}
+
+fp8_status fp8_gated_act(const void* a, int64_t rows, int64_t cols, int64_t lda, fp8_dtype dt, fp8_act act, const void* b,
+                         int64_t ldb, void* y, int64_t ldy, fp8_format fmt, uint8_t* qa, float* sa, uint8_t* qb, float* sb,
+                         int64_t ldq, cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_gated_act");
+  if (rows < 0 || cols < 0 || !valid_dt(dt) || !valid_fmt(fmt) || act < FP8_ACT_SILU || act > FP8_ACT_GELU_TANH)
+    return FP8_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return FP8_OK;
+  if (a == nullptr || y == nullptr || (qa == nullptr) != (sa == nullptr) || (qb == nullptr) != (sb == nullptr) ||
+      (qb != nullptr && b == nullptr))
+    return FP8_ERR_INVALID_ARG;
+  if (rows > kMaxDim || cols > kMaxDim || !row_stride(rows, cols, &lda) || !row_stride(rows, cols, &ldy) ||
+      (b != nullptr && !row_stride(rows, cols, &ldb)) ||
+      ((qa != nullptr || qb != nullptr) && !row_stride(rows, cols, &ldq)))
+    return FP8_ERR_SHAPE;
+  const uintptr_t es = elem_size(dt);
+  if (!aligned(a, es) || !aligned(b, es) || !aligned(y, es) || !aligned(sa, 4) || !aligned(sb, 4)) return FP8_ERR_ALIGNMENT;
+  DeviceInfo* d;
+  if (fp8_status st = device_info(&d)) return st;
+  ActParams p{};
+  p.a = a;
+  p.rows = rows;
+  p.cols = cols;
+  p.lda = lda;
+  p.f32 = dt == FP8_DT_FP32;
+  p.act = act;
+  p.b = b;
+  p.ldb = ldb;
+  p.y = y;
+  p.ldy = ldy;
+  p.e5m2 = fmt == FP8_E5M2;
+  p.qa = qa;
+  p.qb = qb;
+  p.ldq = ldq;
+  p.sa = sa;
+  p.sb = sb;
+  return cuda_status(launch_act(p, d->num_sms, stream));
+}
+
+fp8_status fp8_gated_act_backward(const void* dy, int64_t rows, int64_t cols, int64_t lddy, fp8_dtype dt, fp8_act act,
+                                  const void* a, int64_t lda, const void* b, int64_t ldb, fp8_format fmt,
+                                  const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb, int64_t ldq,
+                                  void* da, int64_t ldda, void* db, int64_t lddb, cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_gated_act_backward");
+  if (rows < 0 || cols < 0 || !valid_dt(dt) || !valid_fmt(fmt) || act < FP8_ACT_SILU || act > FP8_ACT_GELU_TANH)
+    return FP8_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return FP8_OK;
+  if (dy == nullptr || da == nullptr || (a == nullptr) == (qa == nullptr) || (qa == nullptr) != (sa == nullptr) ||
+      (qb == nullptr) != (sb == nullptr))
+    return FP8_ERR_INVALID_ARG;
+  const bool gated = b != nullptr || qb != nullptr;
+  // both inputs from memory or both from codes
+  if ((b != nullptr && a == nullptr) || (qb != nullptr && qa == nullptr) || gated != (db != nullptr)) return FP8_ERR_INVALID_ARG;
+  if (rows > kMaxDim || cols > kMaxDim || !row_stride(rows, cols, &lddy) || !row_stride(rows, cols, &ldda) ||
+      (a != nullptr && !row_stride(rows, cols, &lda)) || (b != nullptr && !row_stride(rows, cols, &ldb)) ||
+      (qa != nullptr && !row_stride(rows, cols, &ldq)) || (gated && !row_stride(rows, cols, &lddb)))
+    return FP8_ERR_SHAPE;
+  const uintptr_t es = elem_size(dt);
+  if (!aligned(dy, es) || !aligned(a, es) || !aligned(b, es) || !aligned(da, es) || !aligned(db, es) || !aligned(sa, 4) ||
+      !aligned(sb, 4))
+    return FP8_ERR_ALIGNMENT;
+  DeviceInfo* d;
+  if (fp8_status st = device_info(&d)) return st;
+  ActBwdParams p{};
+  p.dy = dy;
+  p.rows = rows;
+  p.cols = cols;
+  p.lddy = lddy;
+  p.f32 = dt == FP8_DT_FP32;
+  p.act = act;
+  p.a = a;
+  p.b = b;
+  p.lda = lda;
+  p.ldb = ldb;
+  p.e5m2 = fmt == FP8_E5M2;
+  p.qa = qa;
+  p.qb = qb;
+  p.ldq = ldq;
+  p.sa = sa;
+  p.sb = sb;
+  p.da = da;
+  p.db = db;
+  p.ldda = ldda;
+  p.lddb = lddb;
+  return cuda_status(launch_act_backward(p, d->num_sms, stream));
+}
+
+fp8_status fp8_moe_sizes(int64_t tokens, int32_t k, int32_t n_experts, int32_t align, int64_t* capacity,
+                         int64_t* workspace_bytes) {
+  ApiRange nvtx_range("fp8_moe_sizes");
+  if (tokens < 0 || k < 1 || n_experts < 1 || align < 1 || capacity == nullptr || workspace_bytes == nullptr)
+    return FP8_ERR_INVALID_ARG;
+  if (n_experts > kMaxExperts || tokens > kMaxDim || tokens * k > kMaxDim) return FP8_ERR_SHAPE;
+  // every expert with choices pads at most align - 1 rows, and the sum is a multiple of align
+  const int64_t n = tokens * k, used = n < n_experts ? n : n_experts;
+  const int64_t rows = (n + used * (align - 1)) / align * align;
+  if (rows > kMaxDim) return FP8_ERR_SHAPE;
+  *capacity = rows;
+  const int blocks = route_blocks(n);
+  *workspace_bytes = blocks > 1 ? static_cast<int64_t>(blocks) * n_experts * static_cast<int64_t>(sizeof(int)) : 0;
+  return FP8_OK;
+}
+
+fp8_status fp8_moe_route(const void* experts, int32_t id_bytes, int64_t tokens, int32_t k, int32_t n_experts, int32_t align,
+                         int32_t* offsets, int32_t* pos, int32_t* src, int64_t capacity, void* workspace,
+                         int64_t workspace_bytes, cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_moe_route");
+  int64_t rows = 0, need = 0;
+  if (id_bytes != 4 && id_bytes != 8) return FP8_ERR_INVALID_ARG;
+  if (fp8_status st = fp8_moe_sizes(tokens, k, n_experts, align, &rows, &need)) return st;
+  if (offsets == nullptr || (tokens > 0 && (experts == nullptr || pos == nullptr)) || (capacity > 0 && src == nullptr) ||
+      (need > 0 && workspace == nullptr))
+    return FP8_ERR_INVALID_ARG;
+  if (capacity < rows || capacity > kMaxDim || workspace_bytes < need) return FP8_ERR_SHAPE;
+  if (!aligned(experts, static_cast<uintptr_t>(id_bytes)) || !aligned(offsets, 4) || !aligned(pos, 4) || !aligned(src, 4) ||
+      (need > 0 && !aligned(workspace, 4)))
+    return FP8_ERR_ALIGNMENT;
+  RouteParams p{};
+  p.experts = experts;
+  p.ids64 = id_bytes == 8;
+  p.n = tokens * k;
+  p.n_experts = n_experts;
+  p.align = align;
+  p.capacity = capacity;
+  p.offsets = offsets;
+  p.pos = pos;
+  p.src = src;
+  p.counts = static_cast<int*>(workspace);
+  return cuda_status(launch_route(p, stream));
+}
+
+fp8_status fp8_moe_combine(const void* ys, int64_t capacity, int64_t cols, int64_t ldys, fp8_dtype dt, int64_t tokens,
+                           int32_t k, const int32_t* pos, const float* weights, void* y, int64_t ldy, cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_moe_combine");
+  if (capacity < 0 || cols < 0 || tokens < 0 || k < 1 || !valid_dt(dt)) return FP8_ERR_INVALID_ARG;
+  if (tokens == 0 || cols == 0) return FP8_OK;
+  if (pos == nullptr || y == nullptr || (capacity > 0 && ys == nullptr)) return FP8_ERR_INVALID_ARG;
+  if (cols > kMaxDim || capacity > kMaxDim || tokens > kMaxDim || tokens * k > kMaxDim || !row_stride(capacity, cols, &ldys) ||
+      !row_stride(tokens, cols, &ldy))
+    return FP8_ERR_SHAPE;
+  const uintptr_t es = elem_size(dt);
+  if (!aligned(ys, es) || !aligned(y, es) || !aligned(pos, 4) || !aligned(weights, 4)) return FP8_ERR_ALIGNMENT;
+  DeviceInfo* d;
+  if (fp8_status st = device_info(&d)) return st;
+  CombineParams p{};
+  p.ys = ys;
+  p.capacity = capacity;
+  p.ldys = ldys;
+  p.tokens = tokens;
+  p.cols = cols;
+  p.k = k;
+  p.f32 = dt == FP8_DT_FP32;
+  p.pos = pos;
+  p.weights = weights;
+  p.y = y;
+  p.ldy = ldy;
+  p.err = d->err;
+  return cuda_status(launch_combine(p, d->num_sms, stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// fp8_moe_dispatch and fp8_moe_combine_backward: rows to segments, with weights and dots
+fp8_status scatter_rows(const void* in, int64_t tokens, int64_t cols, int64_t ldin, fp8_dtype dt, int32_t k,
+                        const int32_t* pos, const int32_t* src, const float* weights, const void* other, int64_t ldother,
+                        int64_t capacity, void* out, int64_t ldout, float* dots, cudaStream_t stream) {
+  if (capacity < 0 || cols < 0 || tokens < 0 || k < 1 || !valid_dt(dt)) return FP8_ERR_INVALID_ARG;
+  const bool rows = capacity > 0 && cols > 0, any = tokens > 0;
+  if ((any && (pos == nullptr || (in == nullptr && cols > 0))) || (rows && (src == nullptr || out == nullptr)) ||
+      (rows && any && dots != nullptr && other == nullptr))
+    return FP8_ERR_INVALID_ARG;
+  if (cols > kMaxDim || capacity > kMaxDim || tokens > kMaxDim || tokens * k > kMaxDim || !row_stride(tokens, cols, &ldin) ||
+      !row_stride(capacity, cols, &ldout) || (dots != nullptr && !row_stride(capacity, cols, &ldother)))
+    return FP8_ERR_SHAPE;
+  const uintptr_t es = elem_size(dt);
+  if (!aligned(in, es) || !aligned(out, es) || !aligned(other, es) || !aligned(pos, 4) || !aligned(src, 4) ||
+      !aligned(weights, 4) || !aligned(dots, 4))
+    return FP8_ERR_ALIGNMENT;
+  // nothing to copy and nothing to sum: rows of no columns, or no rows and no dots
+  if (!rows && !(any && dots != nullptr)) return FP8_OK;
+  DeviceInfo* d;
+  if (fp8_status st = device_info(&d)) return st;
+  ScatterParams p{};
+  p.in = in;
+  p.tokens = tokens;
+  p.cols = cols;
+  p.ldin = ldin;
+  p.k = k;
+  p.f32 = dt == FP8_DT_FP32;
+  p.pos = pos;
+  p.src = src;
+  p.capacity = capacity;
+  p.weights = weights;
+  p.out = out;
+  p.ldout = ldout;
+  p.other = other;
+  p.ldother = ldother;
+  p.dots = dots;
+  p.err = d->err;
+  return cuda_status(launch_scatter(p, d->num_sms, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8_status fp8_moe_dispatch(const void* x, int64_t tokens, int64_t cols, int64_t ldx, fp8_dtype dt, int32_t k,
+                            const int32_t* pos, const int32_t* src, int64_t capacity, void* xs, int64_t ldxs,
+                            cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_moe_dispatch");
+  return scatter_rows(x, tokens, cols, ldx, dt, k, pos, src, nullptr, nullptr, 0, capacity, xs, ldxs, nullptr, stream);
+}
+
+fp8_status fp8_moe_combine_backward(const void* dy, int64_t tokens, int64_t cols, int64_t lddy, fp8_dtype dt, int32_t k,
+                                    const int32_t* pos, const int32_t* src, const float* weights, const void* ys,
+                                    int64_t ldys, int64_t capacity, void* dys, int64_t lddys, float* dweights,
+                                    cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_moe_combine_backward");
+  return scatter_rows(dy, tokens, cols, lddy, dt, k, pos, src, weights, ys, ldys, capacity, dys, lddys, dweights, stream);
+}
+
+}  // extern "C"

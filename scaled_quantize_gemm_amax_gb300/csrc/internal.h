@@ -128,6 +128,132 @@ int noalloc_max_ranks();
 cudaError_t launch_allreduce_noalloc(const void* g, int k, int64_t n, bool e5m2, uint8_t* q, float* scale_inv,
                                      float* out, cudaStream_t s);
 
+// ---- layer norm (norm.cu); strides (ld*) in elements, f32: binary32 data, else bf16
+struct NormParams {
+  const void* x;
+  int64_t rows, cols, ldx;
+  int f32;
+  const void* w;         // weight and bias [cols], null: 1 and 0
+  const void* b;
+  int w_f32;
+  float eps;
+  void* y;
+  int64_t ldy;
+  float* mean;           // [rows], null: not stored
+  float* rstd;
+  int e5m2;
+  uint8_t* q;            // [rows, cols] codes of the normalised rows, null: none
+  int64_t ldq;
+  float* s;              // [rows, ceil(cols / 128)] their multipliers
+};
+struct NormBwdParams {
+  const void* dy;
+  int64_t rows, cols, lddy;
+  int f32;
+  const void* x;         // the input and its rows' means; null: q and s
+  int64_t ldx;
+  const float* mean;
+  const float* rstd;
+  int e5m2;
+  const uint8_t* q;
+  int64_t ldq;
+  const float* s;
+  const void* w;
+  int w_f32;
+  void* dx;
+  int64_t lddx;
+  void* dw;              // [cols], each nullable
+  void* db;
+  float* partial;        // [norm_partials(rows)][2][cols]
+};
+constexpr int kMaxNormPartials = 304;
+int norm_partials(int64_t rows);
+cudaError_t launch_norm(const NormParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s);
+
+// ---- gated and plain activations (act.cu)
+enum Act : int { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2 };
+struct ActParams {
+  const void* a;
+  int64_t rows, cols, lda;
+  int f32, act;
+  const void* b;         // null: not gated
+  int64_t ldb;
+  void* y;
+  int64_t ldy;
+  int e5m2;
+  uint8_t* qa;           // [rows, cols] codes and multipliers of a and b, null: none
+  uint8_t* qb;
+  int64_t ldq;
+  float* sa;
+  float* sb;
+};
+struct ActBwdParams {
+  const void* dy;
+  int64_t rows, cols, lddy;
+  int f32, act;
+  const void* a;         // a and b, or their codes
+  const void* b;
+  int64_t lda, ldb;
+  int e5m2;
+  const uint8_t* qa;
+  const uint8_t* qb;
+  int64_t ldq;
+  const float* sa;
+  const float* sb;
+  void* da;
+  void* db;              // null: not gated
+  int64_t ldda, lddb;
+};
+cudaError_t launch_act(const ActParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_act_backward(const ActBwdParams& p, int num_sms, cudaStream_t s);
+
+// ---- expert routing (moe.cu)
+constexpr int kMaxExperts = 1024;
+struct RouteParams {
+  const void* experts;   // [n] int32 or int64
+  int ids64;
+  int64_t n;
+  int n_experts;
+  int align;
+  int64_t capacity;
+  int* offsets;          // [n_experts + 1]
+  int* pos;              // [n]
+  int* src;              // [capacity]
+  int* counts;           // [route_blocks(n)][n_experts]
+  int64_t per_block;     // set by the launcher
+};
+int route_blocks(int64_t n);
+cudaError_t launch_route(RouteParams p, cudaStream_t s);
+struct ScatterParams {
+  const void* in;        // [tokens, cols]
+  int64_t tokens, cols, ldin;
+  int k, f32;
+  const int* pos;        // [tokens, k]
+  const int* src;        // [capacity]
+  int64_t capacity;
+  const float* weights;  // [tokens, k], null: 1
+  void* out;             // [capacity, cols]
+  int64_t ldout;
+  const void* other;     // [capacity, cols], read for the dots only
+  int64_t ldother;
+  float* dots;           // [tokens, k], null: none
+  uint32_t* err;
+};
+cudaError_t launch_scatter(const ScatterParams& p, int num_sms, cudaStream_t s);
+struct CombineParams {
+  const void* ys;        // [capacity, cols]
+  int64_t capacity, ldys;
+  int64_t tokens, cols;
+  int k, f32;
+  const int* pos;
+  const float* weights;  // null: 1
+  void* y;               // [tokens, cols]
+  int64_t ldy;
+  uint32_t* err;
+};
+cudaError_t launch_combine(const CombineParams& p, int num_sms, cudaStream_t s);
+
 // ---- scaled GEMM (gemm.cu)
 struct GemmParams {
   int64_t M, N, K;
