@@ -40,84 +40,130 @@ __device__ __forceinline__ float2 act_grad(float x) {
   return {x * s, fmaf(xc * s * (1.0f - s), du, s)};
 }
 
-// A warp per 128-column group.
-template <typename T, int ACT>
+// Pieces (rows x pieces of a row) shared out over all warps: piece `at`, `at` + stride, ...
+// advanced without a division a step.
+struct Walk {
+  int64_t row, piece, row_step, piece_step, per_row;
+  __device__ Walk(int64_t at, int64_t stride, int64_t pieces) : per_row(pieces) {
+    row = at / pieces;
+    piece = at - row * pieces;
+    row_step = stride / pieces;
+    piece_step = stride - row_step * pieces;
+  }
+  __device__ void next() {
+    row += row_step;
+    piece += piece_step;
+    if (piece >= per_row) {
+      piece -= per_row;
+      ++row;
+    }
+  }
+};
+
+template <typename T, bool VECTOR, int ACT, bool GATED>
 __global__ void __launch_bounds__(kThreads) k_act(const ActParams p) {
+  using P = Piece<T, VECTOR>;
   const int lane = threadIdx.x & 31;
-  const int64_t groups = (p.cols + 127) / 128, total = p.rows * groups;
+  const int64_t groups = (p.cols + 127) / 128;
+  Walk at(static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), static_cast<int64_t>(gridDim.x) * kWarps,
+          (p.cols + P::WC - 1) / P::WC);
   pdl_wait();
   pdl_launch_dependents();
-  for (int64_t at = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); at < total;
-       at += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t row = at / groups, g = at - row * groups;
-    float a[4], b[4];
+  for (; at.row < p.rows; at.next()) {
+    const int64_t row = at.row, c0 = at.piece * P::WC;
+    float a[P::E], b[P::E], y[P::E];
+    P::load(static_cast<const T*>(p.a) + row * p.lda, c0, lane, p.cols, a);
+    if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb, c0, lane, p.cols, b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t c = group_col(g, lane, i);
-      a[i] = b[i] = 0.0f;
-      if (c < p.cols) {
-        a[i] = ld_elem(static_cast<const T*>(p.a) + row * p.lda + c);
-        if (p.b != nullptr) b[i] = ld_elem(static_cast<const T*>(p.b) + row * p.ldb + c);
-        const float f = act_value<ACT>(a[i]);
-        st_elem(static_cast<T*>(p.y) + row * p.ldy + c, p.b != nullptr ? f * b[i] : f);
-      }
-    }
-    if (p.qa != nullptr) store_group8(a, g, lane, p.cols, p.e5m2, p.qa + row * p.ldq, p.sa + row * groups);
-    if (p.qb != nullptr) store_group8(b, g, lane, p.cols, p.e5m2, p.qb + row * p.ldq, p.sb + row * groups);
+    for (int i = 0; i < P::E; ++i) y[i] = GATED ? act_value<ACT>(a[i]) * b[i] : act_value<ACT>(a[i]);
+    P::store(static_cast<T*>(p.y) + row * p.ldy, c0, lane, p.cols, y);
+    if (p.qa != nullptr) P::store_codes(p.qa + row * p.ldq, p.sa + row * groups, c0, lane, p.cols, p.e5m2, a);
+    if (GATED && p.qb != nullptr) P::store_codes(p.qb + row * p.ldq, p.sb + row * groups, c0, lane, p.cols, p.e5m2, b);
   }
 }
 
-template <typename T, int ACT>
+template <typename T, bool VECTOR, int ACT, bool GATED, bool CODES>
 __global__ void __launch_bounds__(kThreads) k_act_backward(const ActBwdParams p) {
+  using P = Piece<T, VECTOR>;
   const int lane = threadIdx.x & 31;
-  const int64_t groups = (p.cols + 127) / 128, total = p.rows * groups;
-  auto value = [&](const void* v, int64_t ld, const uint8_t* q, const float* s, int64_t row, int64_t c) {
-    if (q == nullptr) return ld_elem(static_cast<const T*>(v) + row * ld + c);
-    float x, unused;
-    decode_pair(q[row * p.ldq + c], p.e5m2, x, unused);
-    return x * s[row * groups + c / 128];
-  };
+  const int64_t groups = (p.cols + 127) / 128;
+  Walk at(static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), static_cast<int64_t>(gridDim.x) * kWarps,
+          (p.cols + P::WC - 1) / P::WC);
   pdl_wait();
   pdl_launch_dependents();
-  for (int64_t at = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); at < total;
-       at += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t row = at / groups, g = at - row * groups;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t c = group_col(g, lane, i);
-      if (c >= p.cols) continue;
-      const float dy = ld_elem(static_cast<const T*>(p.dy) + row * p.lddy + c);
-      const float2 f = act_grad<ACT>(value(p.a, p.lda, p.qa, p.sa, row, c));
-      if (p.db == nullptr) {
-        st_elem(static_cast<T*>(p.da) + row * p.ldda + c, dy * f.y);
-      } else {
-        st_elem(static_cast<T*>(p.da) + row * p.ldda + c, dy * value(p.b, p.ldb, p.qb, p.sb, row, c) * f.y);
-        st_elem(static_cast<T*>(p.db) + row * p.lddb + c, dy * f.x);
-      }
+  for (; at.row < p.rows; at.next()) {
+    const int64_t row = at.row, c0 = at.piece * P::WC;
+    float dy[P::E], a[P::E], b[P::E];
+    P::load(static_cast<const T*>(p.dy) + row * p.lddy, c0, lane, p.cols, dy);
+    if (CODES) {
+      P::load_codes(p.qa + row * p.ldq, p.sa + row * groups, c0, lane, p.cols, p.e5m2, a);
+      if (GATED) P::load_codes(p.qb + row * p.ldq, p.sb + row * groups, c0, lane, p.cols, p.e5m2, b);
+    } else {
+      P::load(static_cast<const T*>(p.a) + row * p.lda, c0, lane, p.cols, a);
+      if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb, c0, lane, p.cols, b);
     }
+#pragma unroll
+    for (int i = 0; i < P::E; ++i) {
+      const float2 f = act_grad<ACT>(a[i]);
+      a[i] = (GATED ? dy[i] * b[i] : dy[i]) * f.y;
+      if (GATED) b[i] = dy[i] * f.x;
+    }
+    P::store(static_cast<T*>(p.da) + row * p.ldda, c0, lane, p.cols, a);
+    if (GATED) P::store(static_cast<T*>(p.db) + row * p.lddb, c0, lane, p.cols, b);
   }
 }
 
-int grid_of(int64_t rows, int64_t cols, int num_sms) {
-  const int64_t want = (rows * ((cols + 127) / 128) + kWarps - 1) / kWarps, cap = static_cast<int64_t>(num_sms) * 8;
-  return static_cast<int>(want < 1 ? 1 : (want > cap ? cap : want));
+dim3 grid_of(int64_t rows, int64_t cols, int64_t wc, int num_sms) {
+  const int64_t want = (rows * ((cols + wc - 1) / wc) + kWarps - 1) / kWarps, cap = static_cast<int64_t>(num_sms) * 8;
+  return dim3(static_cast<unsigned>(want < cap ? want : cap));
+}
+
+template <typename T, bool VECTOR, int ACT>
+cudaError_t run_act(const ActParams& p, int num_sms, cudaStream_t s) {
+  const dim3 grid = grid_of(p.rows, p.cols, Piece<T, VECTOR>::WC, num_sms), block(kThreads);
+  return p.b != nullptr ? launch_pdl(k_act<T, VECTOR, ACT, true>, grid, block, 0, s, 1, p)
+                        : launch_pdl(k_act<T, VECTOR, ACT, false>, grid, block, 0, s, 1, p);
+}
+
+template <typename T, bool VECTOR, int ACT>
+cudaError_t run_act_backward(const ActBwdParams& p, int num_sms, cudaStream_t s) {
+  const dim3 grid = grid_of(p.rows, p.cols, Piece<T, VECTOR>::WC, num_sms), block(kThreads);
+  if (p.qa != nullptr)
+    return p.db != nullptr ? launch_pdl(k_act_backward<T, VECTOR, ACT, true, true>, grid, block, 0, s, 1, p)
+                           : launch_pdl(k_act_backward<T, VECTOR, ACT, false, true>, grid, block, 0, s, 1, p);
+  return p.db != nullptr ? launch_pdl(k_act_backward<T, VECTOR, ACT, true, false>, grid, block, 0, s, 1, p)
+                         : launch_pdl(k_act_backward<T, VECTOR, ACT, false, false>, grid, block, 0, s, 1, p);
+}
+
+template <typename T, bool VECTOR>
+cudaError_t of_kind(const ActParams& p, int n, cudaStream_t s) {
+  return p.act == kActSilu ? run_act<T, VECTOR, kActSilu>(p, n, s)
+         : p.act == kActGelu ? run_act<T, VECTOR, kActGelu>(p, n, s) : run_act<T, VECTOR, kActGeluTanh>(p, n, s);
+}
+template <typename T, bool VECTOR>
+cudaError_t of_kind(const ActBwdParams& p, int n, cudaStream_t s) {
+  return p.act == kActSilu ? run_act_backward<T, VECTOR, kActSilu>(p, n, s)
+         : p.act == kActGelu ? run_act_backward<T, VECTOR, kActGelu>(p, n, s) : run_act_backward<T, VECTOR, kActGeluTanh>(p, n, s);
 }
 
 }  // namespace
 
 cudaError_t launch_act(const ActParams& p, int num_sms, cudaStream_t s) {
-  const dim3 grid(grid_of(p.rows, p.cols, num_sms)), block(kThreads);
-#define FP8Q_ACT(A) (p.f32 ? launch_pdl(k_act<float, A>, grid, block, 0, s, 1, p) : launch_pdl(k_act<uint16_t, A>, grid, block, 0, s, 1, p))
-  return p.act == kActSilu ? FP8Q_ACT(kActSilu) : p.act == kActGelu ? FP8Q_ACT(kActGelu) : FP8Q_ACT(kActGeluTanh);
-#undef FP8Q_ACT
+  const int64_t size = p.f32 ? 4 : 2, e = 16 / size;
+  const bool vec = takes(p.a, p.lda, p.cols, size, 16) && takes(p.b, p.ldb, p.cols, size, 16) &&
+                   takes(p.y, p.ldy, p.cols, size, 16) && takes(p.qa, p.ldq, p.cols, 1, e) && takes(p.qb, p.ldq, p.cols, 1, e);
+  if (p.f32) return vec ? of_kind<float, true>(p, num_sms, s) : of_kind<float, false>(p, num_sms, s);
+  return vec ? of_kind<uint16_t, true>(p, num_sms, s) : of_kind<uint16_t, false>(p, num_sms, s);
 }
 
 cudaError_t launch_act_backward(const ActBwdParams& p, int num_sms, cudaStream_t s) {
-  const dim3 grid(grid_of(p.rows, p.cols, num_sms)), block(kThreads);
-#define FP8Q_ACT(A) \
-  (p.f32 ? launch_pdl(k_act_backward<float, A>, grid, block, 0, s, 1, p) : launch_pdl(k_act_backward<uint16_t, A>, grid, block, 0, s, 1, p))
-  return p.act == kActSilu ? FP8Q_ACT(kActSilu) : p.act == kActGelu ? FP8Q_ACT(kActGelu) : FP8Q_ACT(kActGeluTanh);
-#undef FP8Q_ACT
+  const int64_t size = p.f32 ? 4 : 2, e = 16 / size;
+  const bool vec = takes(p.dy, p.lddy, p.cols, size, 16) && takes(p.a, p.lda, p.cols, size, 16) &&
+                   takes(p.b, p.ldb, p.cols, size, 16) && takes(p.da, p.ldda, p.cols, size, 16) &&
+                   takes(p.db, p.lddb, p.cols, size, 16) && takes(p.qa, p.ldq, p.cols, 1, e) &&
+                   takes(p.qb, p.ldq, p.cols, 1, e);
+  if (p.f32) return vec ? of_kind<float, true>(p, num_sms, s) : of_kind<float, false>(p, num_sms, s);
+  return vec ? of_kind<uint16_t, true>(p, num_sms, s) : of_kind<uint16_t, false>(p, num_sms, s);
 }
 
 }  // namespace fp8q

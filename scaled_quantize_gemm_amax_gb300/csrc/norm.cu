@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_any(const NormParams p) {
       float xh[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t c = group_col(g, lane, i);
+        const int64_t c = Piece<T, false>::col(g * 128, lane, i);
         xh[i] = 0.0f;
         if (c < p.cols) {
           xh[i] = (ld_elem(x + c) - mean) * rstd;
@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kThreads) k_norm_any(const NormParams p) {
           st_elem(y + c, fmaf(xh[i], w, b));
         }
       }
-      if (p.q != nullptr) store_group8(xh, g, lane, p.cols, p.e5m2, p.q + row * p.ldq, p.s + row * groups);
+      if (p.q != nullptr)
+        Piece<T, false>::store_codes(p.q + row * p.ldq, p.s + row * groups, g * 128, lane, p.cols, p.e5m2, xh);
     }
   }
 }

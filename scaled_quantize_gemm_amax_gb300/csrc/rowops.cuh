@@ -44,24 +44,130 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// The columns of 128-column group `g` that lane `lane` of a warp holds, element i of 4:
-// consecutive lanes on consecutive columns, so any element alignment coalesces.
-__device__ __forceinline__ int64_t group_col(int64_t g, int lane, int i) { return g * 128 + lane + 32 * i; }
+// ------------------------------------------------------------------ a warp's piece of a row
+// How a warp holds WC consecutive columns of a row, E values a lane.
+//   VECTOR      lane l holds E = 16 bytes' worth of consecutive columns: one 16-byte access a
+//               lane.  Needs a 16-byte aligned row and cols % E == 0 (a lane is all in or all out).
+//   otherwise   lane l holds columns l, l + 32, l + 64, l + 96: consecutive lanes on consecutive
+//               columns, so any element alignment coalesces.
+// 128-column groups (the 8-bit copy's) never cross lanes' bounds: kGroupLanes lanes hold one.
+template <typename T, bool VECTOR>
+struct Piece {
+  static constexpr int E = VECTOR ? 16 / static_cast<int>(sizeof(T)) : 4;
+  static constexpr int WC = 32 * E;
+  static constexpr int kGroupLanes = 128 / E;
 
-// The 8-bit copy of one group held by a warp as above: the blockwise recipe's rule,
-// codes = satRNE(v * FMAX / amax), multiplier 1 / (FMAX / amax).  v = 0 past `cols`.
-__device__ __forceinline__ void store_group8(const float (&v)[4], int64_t g, int lane, int64_t cols, bool e5m2, uint8_t* q_row,
-                                             float* s_row) {
-  float a = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) a = fmaxf(a, fabsf(v[i]));   // a NaN operand is ignored
-  const float sc = scale_from_amax(warp_max(a), fmax_of(e5m2));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t c = group_col(g, lane, i);
-    if (c < cols) q_row[c] = static_cast<uint8_t>(cvt_pair(__fmul_rn(v[i], sc), 0.0f, e5m2));
+  __device__ static __forceinline__ int64_t col(int64_t c0, int lane, int i) {
+    return VECTOR ? c0 + lane * E + i : c0 + lane + 32 * i;
   }
-  if (lane == 0) s_row[g] = recip_rn(sc);
+  // v = the row's values, 0 past its end
+  __device__ static __forceinline__ void load(const T* row, int64_t c0, int lane, int64_t cols, float (&v)[E]) {
+    if constexpr (VECTOR) {
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (col(c0, lane, 0) < cols) w = __ldg(reinterpret_cast<const uint4*>(row + col(c0, lane, 0)));
+      unpack(w, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = col(c0, lane, i) < cols ? ld_elem(row + col(c0, lane, i)) : 0.0f;
+    }
+  }
+  __device__ static __forceinline__ void unpack(const uint4& w, float (&v)[E]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        v[2 * i] = bf16lo(u[i]);
+        v[2 * i + 1] = bf16hi(u[i]);
+      } else {
+        v[i] = __uint_as_float(u[i]);
+      }
+    }
+  }
+  __device__ static __forceinline__ void store(T* row, int64_t c0, int lane, int64_t cols, const float (&v)[E]) {
+    if constexpr (VECTOR) {
+      if (col(c0, lane, 0) >= cols) return;
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 2)
+          u[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+        else
+          u[i] = __float_as_uint(v[i]);
+      }
+      *reinterpret_cast<uint4*>(row + col(c0, lane, 0)) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (col(c0, lane, i) < cols) st_elem(row + col(c0, lane, i), v[i]);
+    }
+  }
+  // The 8-bit copy of the piece by the blockwise recipe's rule: codes = satRNE(v FMAX / amax),
+  // multiplier 1 / (FMAX / amax), per 128 columns.  v = 0 past the row's end.
+  __device__ static __forceinline__ void store_codes(uint8_t* q_row, float* s_row, int64_t c0, int lane, int64_t cols, bool e5m2,
+                                                     const float (&v)[E]) {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) a = fmaxf(a, fabsf(v[i]));   // a NaN operand is ignored
+#pragma unroll
+    for (int o = kGroupLanes / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+    const float sc = scale_from_amax(a, fmax_of(e5m2));
+    if constexpr (VECTOR) {
+      if (col(c0, lane, 0) >= cols) return;
+      uint32_t u[E / 4];
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i)
+        u[i] = cvt_pair(__fmul_rn(v[4 * i], sc), __fmul_rn(v[4 * i + 1], sc), e5m2) |
+               cvt_pair(__fmul_rn(v[4 * i + 2], sc), __fmul_rn(v[4 * i + 3], sc), e5m2) << 16;
+      if constexpr (E == 8)
+        *reinterpret_cast<uint2*>(q_row + col(c0, lane, 0)) = make_uint2(u[0], u[1]);
+      else
+        *reinterpret_cast<uint32_t*>(q_row + col(c0, lane, 0)) = u[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (col(c0, lane, i) < cols)
+          q_row[col(c0, lane, i)] = static_cast<uint8_t>(cvt_pair(__fmul_rn(v[i], sc), 0.0f, e5m2));
+    }
+    if (lane % kGroupLanes == 0) s_row[col(c0, lane, 0) / 128] = recip_rn(sc);
+  }
+  // The values the codes stand for (each product rounded to binary32), 0 past the row's end.
+  __device__ static __forceinline__ void load_codes(const uint8_t* q_row, const float* s_row, int64_t c0, int lane, int64_t cols,
+                                                    bool e5m2, float (&v)[E]) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = 0.0f;
+    if (col(c0, lane, 0) >= cols) return;
+    const float s = __ldg(s_row + col(c0, lane, 0) / 128);
+    if constexpr (VECTOR) {
+      uint32_t u[E / 4];
+      if constexpr (E == 8) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(q_row + col(c0, lane, 0)));
+        u[0] = w.x;
+        u[1] = w.y;
+      } else {
+        u[0] = __ldg(reinterpret_cast<const uint32_t*>(q_row + col(c0, lane, 0)));
+      }
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        decode_pair(u[i] & 0xFFFFu, e5m2, v[4 * i], v[4 * i + 1]);
+        decode_pair(u[i] >> 16, e5m2, v[4 * i + 2], v[4 * i + 3]);
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] *= s;
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        float x = 0.0f, unused;
+        if (col(c0, lane, i) < cols) decode_pair(q_row[col(c0, lane, i)], e5m2, x, unused);
+        v[i] = x * s;
+      }
+    }
+  }
+};
+
+// Whether a [rows, cols] matrix of `size`-byte elements, row stride ld, takes accesses of
+// `bytes` bytes throughout (null matrices do).
+inline bool takes(const void* p, int64_t ld, int64_t cols, int64_t size, int64_t bytes) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * size % bytes == 0 && cols * size % bytes == 0);
 }
 
 }  // namespace fp8q
