@@ -40,26 +40,6 @@ __device__ __forceinline__ float2 act_grad(float x) {
   return {x * s, fmaf(xc * s * (1.0f - s), du, s)};
 }
 
-// Pieces (rows x pieces of a row) shared out over all warps: piece `at`, `at` + stride, ...
-// advanced without a division a step.
-struct Walk {
-  int64_t row, piece, row_step, piece_step, per_row;
-  __device__ Walk(int64_t at, int64_t stride, int64_t pieces) : per_row(pieces) {
-    row = at / pieces;
-    piece = at - row * pieces;
-    row_step = stride / pieces;
-    piece_step = stride - row_step * pieces;
-  }
-  __device__ void next() {
-    row += row_step;
-    piece += piece_step;
-    if (piece >= per_row) {
-      piece -= per_row;
-      ++row;
-    }
-  }
-};
-
 template <typename T, bool VECTOR, int ACT, bool GATED>
 __global__ void __launch_bounds__(kThreads) k_act(const ActParams p) {
   using P = Piece<T, VECTOR>;
@@ -70,15 +50,16 @@ __global__ void __launch_bounds__(kThreads) k_act(const ActParams p) {
   pdl_wait();
   pdl_launch_dependents();
   for (; at.row < p.rows; at.next()) {
-    const int64_t row = at.row, c0 = at.piece * P::WC;
+    const int64_t row = at.row;
+    const int c0 = static_cast<int>(at.piece * P::WC), cols = static_cast<int>(p.cols);
     float a[P::E], b[P::E], y[P::E];
-    P::load(static_cast<const T*>(p.a) + row * p.lda, c0, lane, p.cols, a);
-    if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb, c0, lane, p.cols, b);
+    P::load(static_cast<const T*>(p.a) + row * p.lda, c0, lane, cols, a);
+    if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb, c0, lane, cols, b);
 #pragma unroll
     for (int i = 0; i < P::E; ++i) y[i] = GATED ? act_value<ACT>(a[i]) * b[i] : act_value<ACT>(a[i]);
-    P::store(static_cast<T*>(p.y) + row * p.ldy, c0, lane, p.cols, y);
-    if (p.qa != nullptr) P::store_codes(p.qa + row * p.ldq, p.sa + row * groups, c0, lane, p.cols, p.e5m2, a);
-    if (GATED && p.qb != nullptr) P::store_codes(p.qb + row * p.ldq, p.sb + row * groups, c0, lane, p.cols, p.e5m2, b);
+    P::store(static_cast<T*>(p.y) + row * p.ldy, c0, lane, cols, y);
+    if (p.qa != nullptr) P::store_codes(p.qa + row * p.ldq, p.sa + row * groups, c0, lane, cols, p.e5m2, a);
+    if (GATED && p.qb != nullptr) P::store_codes(p.qb + row * p.ldq, p.sb + row * groups, c0, lane, cols, p.e5m2, b);
   }
 }
 
@@ -92,15 +73,16 @@ __global__ void __launch_bounds__(kThreads) k_act_backward(const ActBwdParams p)
   pdl_wait();
   pdl_launch_dependents();
   for (; at.row < p.rows; at.next()) {
-    const int64_t row = at.row, c0 = at.piece * P::WC;
+    const int64_t row = at.row;
+    const int c0 = static_cast<int>(at.piece * P::WC), cols = static_cast<int>(p.cols);
     float dy[P::E], a[P::E], b[P::E];
-    P::load(static_cast<const T*>(p.dy) + row * p.lddy, c0, lane, p.cols, dy);
+    P::load(static_cast<const T*>(p.dy) + row * p.lddy, c0, lane, cols, dy);
     if (CODES) {
-      P::load_codes(p.qa + row * p.ldq, p.sa + row * groups, c0, lane, p.cols, p.e5m2, a);
-      if (GATED) P::load_codes(p.qb + row * p.ldq, p.sb + row * groups, c0, lane, p.cols, p.e5m2, b);
+      P::load_codes(p.qa + row * p.ldq, p.sa + row * groups, c0, lane, cols, p.e5m2, a);
+      if (GATED) P::load_codes(p.qb + row * p.ldq, p.sb + row * groups, c0, lane, cols, p.e5m2, b);
     } else {
-      P::load(static_cast<const T*>(p.a) + row * p.lda, c0, lane, p.cols, a);
-      if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb, c0, lane, p.cols, b);
+      P::load(static_cast<const T*>(p.a) + row * p.lda, c0, lane, cols, a);
+      if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb, c0, lane, cols, b);
     }
 #pragma unroll
     for (int i = 0; i < P::E; ++i) {
@@ -108,8 +90,8 @@ __global__ void __launch_bounds__(kThreads) k_act_backward(const ActBwdParams p)
       a[i] = (GATED ? dy[i] * b[i] : dy[i]) * f.y;
       if (GATED) b[i] = dy[i] * f.x;
     }
-    P::store(static_cast<T*>(p.da) + row * p.ldda, c0, lane, p.cols, a);
-    if (GATED) P::store(static_cast<T*>(p.db) + row * p.lddb, c0, lane, p.cols, b);
+    P::store(static_cast<T*>(p.da) + row * p.ldda, c0, lane, cols, a);
+    if (GATED) P::store(static_cast<T*>(p.db) + row * p.lddb, c0, lane, cols, b);
   }
 }
 

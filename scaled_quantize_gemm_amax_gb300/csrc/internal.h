@@ -128,7 +128,7 @@ int noalloc_max_ranks();
 cudaError_t launch_allreduce_noalloc(const void* g, int k, int64_t n, bool e5m2, uint8_t* q, float* scale_inv,
                                      float* out, cudaStream_t s);
 
-// ---- layer norm (norm.cu); strides (ld*) in elements, f32: binary32 data, else bf16
+// ---- layer norm (norm.cu, norm_backward.cu); strides (ld*) in elements, f32: binary32 data, else bf16
 struct NormParams {
   const void* x;
   int64_t rows, cols, ldx;
@@ -166,7 +166,7 @@ struct NormBwdParams {
   void* db;
   float* partial;        // [norm_partials(rows)][2][cols]
 };
-constexpr int kMaxNormPartials = 304;
+constexpr int kMaxNormPartials = 304;   // most blocks of the backward pass
 int norm_partials(int64_t rows);
 cudaError_t launch_norm(const NormParams& p, int num_sms, cudaStream_t s);
 cudaError_t launch_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s);

@@ -44,6 +44,34 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// Two binary32 operations in one instruction (sm_100 and later), each rounded to nearest.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // ------------------------------------------------------------------ a warp's piece of a row
 // How a warp holds WC consecutive columns of a row, E values a lane.
 //   VECTOR      lane l holds E = 16 bytes' worth of consecutive columns: one 16-byte access a
@@ -57,11 +85,11 @@ struct Piece {
   static constexpr int WC = 32 * E;
   static constexpr int kGroupLanes = 128 / E;
 
-  __device__ static __forceinline__ int64_t col(int64_t c0, int lane, int i) {
+  __device__ static __forceinline__ int col(int c0, int lane, int i) {
     return VECTOR ? c0 + lane * E + i : c0 + lane + 32 * i;
   }
   // v = the row's values, 0 past its end
-  __device__ static __forceinline__ void load(const T* row, int64_t c0, int lane, int64_t cols, float (&v)[E]) {
+  __device__ static __forceinline__ void load(const T* row, int c0, int lane, int cols, float (&v)[E]) {
     if constexpr (VECTOR) {
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
       if (col(c0, lane, 0) < cols) w = __ldg(reinterpret_cast<const uint4*>(row + col(c0, lane, 0)));
@@ -83,7 +111,7 @@ struct Piece {
       }
     }
   }
-  __device__ static __forceinline__ void store(T* row, int64_t c0, int lane, int64_t cols, const float (&v)[E]) {
+  __device__ static __forceinline__ void store(T* row, int c0, int lane, int cols, const float (&v)[E]) {
     if constexpr (VECTOR) {
       if (col(c0, lane, 0) >= cols) return;
       uint32_t u[4];
@@ -103,7 +131,7 @@ struct Piece {
   }
   // The 8-bit copy of the piece by the blockwise recipe's rule: codes = satRNE(v FMAX / amax),
   // multiplier 1 / (FMAX / amax), per 128 columns.  v = 0 past the row's end.
-  __device__ static __forceinline__ void store_codes(uint8_t* q_row, float* s_row, int64_t c0, int lane, int64_t cols, bool e5m2,
+  __device__ static __forceinline__ void store_codes(uint8_t* q_row, float* s_row, int c0, int lane, int cols, bool e5m2,
                                                      const float (&v)[E]) {
     float a = 0.0f;
 #pragma unroll
@@ -128,31 +156,35 @@ struct Piece {
         if (col(c0, lane, i) < cols)
           q_row[col(c0, lane, i)] = static_cast<uint8_t>(cvt_pair(__fmul_rn(v[i], sc), 0.0f, e5m2));
     }
-    if (lane % kGroupLanes == 0) s_row[col(c0, lane, 0) / 128] = recip_rn(sc);
+    if (lane % kGroupLanes == 0 && col(c0, lane, 0) < cols) s_row[col(c0, lane, 0) / 128] = recip_rn(sc);
+  }
+  // E consecutive codes (aligned to E bytes, in global or shared memory) times s, 0 if not `valid`
+  __device__ static __forceinline__ void decode(const uint8_t* q, float s, bool valid, bool e5m2, float (&v)[E]) {
+    uint32_t u[E / 4];
+    if constexpr (E == 8) {
+      const uint2 w = *reinterpret_cast<const uint2*>(q);
+      u[0] = w.x;
+      u[1] = w.y;
+    } else {
+      u[0] = *reinterpret_cast<const uint32_t*>(q);
+    }
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+      decode_pair(u[i] & 0xFFFFu, e5m2, v[4 * i], v[4 * i + 1]);
+      decode_pair(u[i] >> 16, e5m2, v[4 * i + 2], v[4 * i + 3]);
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = valid ? v[i] * s : 0.0f;
   }
   // The values the codes stand for (each product rounded to binary32), 0 past the row's end.
-  __device__ static __forceinline__ void load_codes(const uint8_t* q_row, const float* s_row, int64_t c0, int lane, int64_t cols,
+  __device__ static __forceinline__ void load_codes(const uint8_t* q_row, const float* s_row, int c0, int lane, int cols,
                                                     bool e5m2, float (&v)[E]) {
 #pragma unroll
     for (int i = 0; i < E; ++i) v[i] = 0.0f;
     if (col(c0, lane, 0) >= cols) return;
     const float s = __ldg(s_row + col(c0, lane, 0) / 128);
     if constexpr (VECTOR) {
-      uint32_t u[E / 4];
-      if constexpr (E == 8) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(q_row + col(c0, lane, 0)));
-        u[0] = w.x;
-        u[1] = w.y;
-      } else {
-        u[0] = __ldg(reinterpret_cast<const uint32_t*>(q_row + col(c0, lane, 0)));
-      }
-#pragma unroll
-      for (int i = 0; i < E / 4; ++i) {
-        decode_pair(u[i] & 0xFFFFu, e5m2, v[4 * i], v[4 * i + 1]);
-        decode_pair(u[i] >> 16, e5m2, v[4 * i + 2], v[4 * i + 3]);
-      }
-#pragma unroll
-      for (int i = 0; i < E; ++i) v[i] *= s;
+      decode(q_row + col(c0, lane, 0), s, true, e5m2, v);
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i) {
@@ -163,6 +195,61 @@ struct Piece {
     }
   }
 };
+
+// Pieces (rows x pieces of a row) shared out over all warps: piece `at`, `at` + stride, ...
+// advanced without a division a step.
+struct Walk {
+  int64_t row, piece, row_step, piece_step, per_row;
+  __device__ Walk(int64_t at, int64_t stride, int64_t pieces) : per_row(pieces) {
+    row = at / pieces;
+    piece = at - row * pieces;
+    row_step = stride / pieces;
+    piece_step = stride - row_step * pieces;
+  }
+  __device__ void next() {
+    row += row_step;
+    piece += piece_step;
+    if (piece >= per_row) {
+      piece -= per_row;
+      ++row;
+    }
+  }
+};
+
+// A piece of a parameter vector (`none` without one and past its end); VECTOR: 16-byte aligned.
+template <typename P, bool VECTOR>
+__device__ __forceinline__ void load_param(const void* v, bool f32, int c0, int lane, int cols, float none, float (&out)[P::E]) {
+#pragma unroll
+  for (int i = 0; i < P::E; ++i) out[i] = none;
+  if (v == nullptr) return;
+  if constexpr (VECTOR) {
+    const int c = P::col(c0, lane, 0);
+    if (c >= cols) return;
+    if (f32) {
+#pragma unroll
+      for (int i = 0; i < P::E / 4; ++i) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(v) + c) + i);
+        out[4 * i] = w.x;
+        out[4 * i + 1] = w.y;
+        out[4 * i + 2] = w.z;
+        out[4 * i + 3] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < P::E / 4; ++i) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(v) + c) + i);
+        out[4 * i] = bf16lo(w.x);
+        out[4 * i + 1] = bf16hi(w.x);
+        out[4 * i + 2] = bf16lo(w.y);
+        out[4 * i + 3] = bf16hi(w.y);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P::E; ++i)
+      if (P::col(c0, lane, i) < cols) out[i] = ld_param(v, f32, P::col(c0, lane, i));
+  }
+}
 
 // Whether a [rows, cols] matrix of `size`-byte elements, row stride ld, takes accesses of
 // `bytes` bytes throughout (null matrices do).
