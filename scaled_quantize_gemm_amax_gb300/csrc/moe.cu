@@ -143,70 +143,159 @@ __device__ __forceinline__ bool valid_row(int pos, int64_t capacity, uint32_t* e
   return false;
 }
 
-// Block per token: rows out[pos_j] = w_j in[t] and the dots <in[t], other[pos_j]>; after the
-// tokens, a warp per row of `out` that no choice fills, set to zero.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_scatter(const ScatterParams p) {
-  __shared__ float red[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// What a lane has in flight: two pieces of a row, and four choices.
+constexpr int kPieces = 2;
+constexpr int kFlight = 4;
+
+// The choices j0 .. j0 + 31 of token t, one a lane: their rows and weights (-1 and 0 for those
+// dropped, whose weights are not read).
+struct Choices {
+  int pos;
+  float w;
+  __device__ Choices(const int* p_pos, const float* weights, int64_t t, int k, int j0, int lane, int64_t capacity, uint32_t* err) {
+    pos = -1;
+    w = 0.0f;
+    if (j0 + lane < k) {
+      const int64_t at = t * k + j0 + lane;
+      pos = __ldg(p_pos + at);
+      if (!valid_row(pos, capacity, err)) pos = -1;
+      if (pos >= 0) w = weights != nullptr ? __ldg(weights + at) : 1.0f;
+    }
+  }
+};
+
+// `warps` warps per token (a block has 8 / warps tokens at a time), each holding its pieces of
+// the token's row: rows out[pos_j] = w_j in[t], and the dots <in[t], other[pos_j]>.  The token's
+// row is read once for all its choices.  After the tokens, a warp per kZeroRows rows of `out`
+// sets those that no choice fills to zero.
+constexpr int kZeroRows = 4;
+template <typename T, bool VECTOR, bool DOTS>
+__global__ void __launch_bounds__(kThreads) k_scatter(const ScatterParams p, const int warps) {
+  using P = Piece<T, VECTOR>;
+  __shared__ float part[2][kWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / warps, w_in = warp - group * warps;
+  const int cols = static_cast<int>(p.cols), block_cols = warps * kPieces * P::WC;
+  const int64_t per_item = static_cast<int64_t>(warps) * kZeroRows, items = p.tokens + (p.capacity + per_item - 1) / per_item;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kWarps / warps);
+  int buf = 0;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t items = p.tokens + (p.capacity + kWarps - 1) / kWarps;
-  for (int64_t t = blockIdx.x; t < items; t += gridDim.x) {
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kWarps / warps) + group; t < items; t += step) {
     if (t >= p.tokens) {
-      const int64_t r = (t - p.tokens) * kWarps + warp;
-      if (r < p.capacity && p.src[r] < 0) {
-        T* out = static_cast<T*>(p.out) + r * p.ldout;
-        for (int64_t c = lane; c < p.cols; c += 32) st_elem(out + c, 0.0f);
+      const int64_t r0 = ((t - p.tokens) * warps + w_in) * kZeroRows, r = r0 + lane;
+      uint32_t empty = __ballot_sync(0xFFFFFFFFu, lane < kZeroRows && r < p.capacity && __ldg(p.src + r) < 0);
+      float zero[P::E];
+#pragma unroll
+      for (int i = 0; i < P::E; ++i) zero[i] = 0.0f;
+      for (; empty != 0; empty &= empty - 1) {
+        T* out = static_cast<T*>(p.out) + (r0 + __ffs(empty) - 1) * p.ldout;
+        for (int c0 = 0; c0 < cols; c0 += P::WC) P::store(out, c0, lane, cols, zero);
       }
       continue;
     }
     const T* in = static_cast<const T*>(p.in) + t * p.ldin;
-    for (int j = 0; j < p.k; ++j) {
-      const int pos = p.pos[t * p.k + j];
-      const bool kept = valid_row(pos, p.capacity, p.err);
-      float dot = 0.0f;
-      if (kept) {
-        T* out = static_cast<T*>(p.out) + pos * p.ldout;
-        const float w = p.weights != nullptr ? p.weights[t * p.k + j] : 1.0f;
-        const T* other = p.dots != nullptr ? static_cast<const T*>(p.other) + pos * p.ldother : nullptr;
-        for (int64_t c = threadIdx.x; c < p.cols; c += kThreads) {
-          const float v = ld_elem(in + c);
-          st_elem(out + c, w * v);
-          if (other != nullptr) dot = fmaf(v, ld_elem(other + c), dot);
+    for (int j0 = 0; j0 < p.k; j0 += 32) {
+      const Choices c(p.pos, p.weights, t, p.k, j0, lane, p.capacity, p.err);
+      const int n = min(32, p.k - j0);
+      float my_dot = 0.0f;   // of choice j0 + lane
+      for (int cb = w_in * kPieces * P::WC; cb < cols; cb += block_cols) {
+        float v[kPieces][P::E];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) P::load(in, cb + i * P::WC, lane, cols, v[i]);
+        for (int j = 0; j < n; j += kFlight) {
+          float o[DOTS ? kFlight : 1][kPieces][P::E];
+          if constexpr (DOTS) {
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+              const int pos = __shfl_sync(0xFFFFFFFFu, c.pos, (j + u) & 31);
+              const bool on = j + u < n && pos >= 0;
+              const T* other = static_cast<const T*>(p.other) + (on ? pos : 0) * p.ldother;
+#pragma unroll
+              for (int i = 0; i < kPieces; ++i) P::load(other, cb + i * P::WC, lane, on ? cols : 0, o[u][i]);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < kFlight; ++u) {
+            if (j + u >= n) break;
+            const int pos = __shfl_sync(0xFFFFFFFFu, c.pos, j + u);
+            const float w = __shfl_sync(0xFFFFFFFFu, c.w, j + u);
+            if (pos < 0) continue;
+            T* out = static_cast<T*>(p.out) + pos * p.ldout;
+            float dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+              float y[P::E];
+#pragma unroll
+              for (int e = 0; e < P::E; ++e) {
+                y[e] = w * v[i][e];
+                if constexpr (DOTS) dot = fmaf(v[i][e], o[u][i][e], dot);
+              }
+              P::store(out, cb + i * P::WC, lane, cols, y);
+            }
+            if constexpr (DOTS) {
+              dot = warp_sum(dot);
+              if (lane == j + u) my_dot += dot;
+            }
+          }
         }
       }
-      if (p.dots != nullptr) {
-        dot = warp_sum(dot);
-        __syncthreads();
-        if (lane == 0) red[warp] = dot;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-          float d = 0.0f;
-          for (int w = 0; w < kWarps; ++w) d += red[w];
-          p.dots[t * p.k + j] = d;
+      if constexpr (DOTS) {
+        // the warps' parts in order (the buffer after next is written past another barrier)
+        if (warps > 1) {
+          part[buf][warp][lane] = my_dot;
+          asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
+          my_dot = 0.0f;
+          for (int i = 0; i < warps; ++i) my_dot += part[buf][group * warps + i][lane];
+          buf ^= 1;
         }
+        if (w_in == 0 && lane < n) p.dots[t * p.k + j0 + lane] = my_dot;
       }
     }
   }
 }
 
-// Block per token: y[t] = sum_j w_j ys[pos_j], the choices in order.
-template <typename T>
+// A warp per kPieces pieces of a token's row: y[t] = sum_j w_j ys[pos_j], the choices in order.
+template <typename T, bool VECTOR>
 __global__ void __launch_bounds__(kThreads) k_combine(const CombineParams p) {
+  using P = Piece<T, VECTOR>;
+  const int lane = threadIdx.x & 31, cols = static_cast<int>(p.cols);
+  Walk at(static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), static_cast<int64_t>(gridDim.x) * kWarps,
+          (p.cols + kPieces * P::WC - 1) / (kPieces * P::WC));
   pdl_wait();
   pdl_launch_dependents();
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-    for (int64_t c = threadIdx.x; c < p.cols; c += kThreads) {
-      float acc = 0.0f;
-      for (int j = 0; j < p.k; ++j) {
-        const int pos = p.pos[t * p.k + j];
-        if (!valid_row(pos, p.capacity, p.err)) continue;
-        const float v = ld_elem(static_cast<const T*>(p.ys) + pos * p.ldys + c);
-        acc = p.weights != nullptr ? fmaf(p.weights[t * p.k + j], v, acc) : acc + v;
+  for (; at.row < p.tokens; at.next()) {
+    const int c0 = static_cast<int>(at.piece) * kPieces * P::WC;
+    float acc[kPieces][P::E];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+      for (int e = 0; e < P::E; ++e) acc[i][e] = 0.0f;
+    for (int j0 = 0; j0 < p.k; j0 += 32) {
+      const Choices c(p.pos, p.weights, at.row, p.k, j0, lane, p.capacity, p.err);
+      const int n = min(32, p.k - j0);
+      for (int j = 0; j < n; j += kFlight) {
+        float v[kFlight][kPieces][P::E], w[kFlight];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+          const int pos = __shfl_sync(0xFFFFFFFFu, c.pos, (j + u) & 31);
+          w[u] = __shfl_sync(0xFFFFFFFFu, c.w, (j + u) & 31);
+          const bool on = j + u < n && pos >= 0;
+          const T* ys = static_cast<const T*>(p.ys) + (on ? pos : 0) * p.ldys;
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) P::load(ys, c0 + i * P::WC, lane, on ? cols : 0, v[u][i]);
+        }
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u)
+          if (j + u < n)
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+              for (int e = 0; e < P::E; ++e) acc[i][e] = fmaf(w[u], v[u][i][e], acc[i][e]);
       }
-      st_elem(static_cast<T*>(p.y) + t * p.ldy + c, acc);
     }
+    T* y = static_cast<T*>(p.y) + at.row * p.ldy;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) P::store(y, c0 + i * P::WC, lane, cols, acc[i]);
   }
 }
 
@@ -243,16 +332,41 @@ cudaError_t launch_route(RouteParams p, cudaStream_t s) {
   return launch_pdl(k_route_place, dim3(blocks), dim3(kRouteThreads), place_smem(p.n_experts), s, 1, p);
 }
 
+namespace {
+
+template <typename T, bool VECTOR>
+cudaError_t run_scatter(const ScatterParams& p, int num_sms, cudaStream_t s) {
+  // a warp for every kPieces pieces of a row, up to a block's 8
+  const int64_t wc = Piece<T, VECTOR>::WC * kPieces;
+  int warps = 1;
+  while (warps < kWarps && warps * wc < p.cols) warps *= 2;
+  const int64_t per_item = static_cast<int64_t>(warps) * kZeroRows, items = p.tokens + (p.capacity + per_item - 1) / per_item;
+  const dim3 grid(grid_of((items + kWarps / warps - 1) / (kWarps / warps), num_sms, 8));
+  return p.dots != nullptr ? launch_pdl(k_scatter<T, VECTOR, true>, grid, dim3(kThreads), 0, s, 1, p, warps)
+                           : launch_pdl(k_scatter<T, VECTOR, false>, grid, dim3(kThreads), 0, s, 1, p, warps);
+}
+
+template <typename T, bool VECTOR>
+cudaError_t run_combine(const CombineParams& p, int num_sms, cudaStream_t s) {
+  const int64_t wc = Piece<T, VECTOR>::WC * kPieces, items = p.tokens * ((p.cols + wc - 1) / wc);
+  return launch_pdl(k_combine<T, VECTOR>, dim3(grid_of((items + kWarps - 1) / kWarps, num_sms, 8)), dim3(kThreads), 0, s, 1, p);
+}
+
+}  // namespace
+
 cudaError_t launch_scatter(const ScatterParams& p, int num_sms, cudaStream_t s) {
-  const dim3 grid(grid_of(p.tokens + (p.capacity + kWarps - 1) / kWarps, num_sms, 8));
-  return p.f32 ? launch_pdl(k_scatter<float>, grid, dim3(kThreads), 0, s, 1, p)
-               : launch_pdl(k_scatter<uint16_t>, grid, dim3(kThreads), 0, s, 1, p);
+  const int64_t size = p.f32 ? 4 : 2;
+  const bool vec = takes(p.in, p.ldin, p.cols, size, 16) && takes(p.out, p.ldout, p.cols, size, 16) &&
+                   (p.dots == nullptr || takes(p.other, p.ldother, p.cols, size, 16));
+  if (p.f32) return vec ? run_scatter<float, true>(p, num_sms, s) : run_scatter<float, false>(p, num_sms, s);
+  return vec ? run_scatter<uint16_t, true>(p, num_sms, s) : run_scatter<uint16_t, false>(p, num_sms, s);
 }
 
 cudaError_t launch_combine(const CombineParams& p, int num_sms, cudaStream_t s) {
-  const dim3 grid(grid_of(p.tokens, num_sms, 8));
-  return p.f32 ? launch_pdl(k_combine<float>, grid, dim3(kThreads), 0, s, 1, p)
-               : launch_pdl(k_combine<uint16_t>, grid, dim3(kThreads), 0, s, 1, p);
+  const int64_t size = p.f32 ? 4 : 2;
+  const bool vec = takes(p.ys, p.ldys, p.cols, size, 16) && takes(p.y, p.ldy, p.cols, size, 16);
+  if (p.f32) return vec ? run_combine<float, true>(p, num_sms, s) : run_combine<float, false>(p, num_sms, s);
+  return vec ? run_combine<uint16_t, true>(p, num_sms, s) : run_combine<uint16_t, false>(p, num_sms, s);
 }
 
 }  // namespace fp8q
