@@ -17,99 +17,201 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-template <int ACT>
-__device__ __forceinline__ float act_value(float x) {
-  if (ACT == kActSilu) return x / (1.0f + expf(-x));
-  if (ACT == kActGelu) return x * (0.5f + 0.5f * erff(x * 0.70710678f));
-  const float u = 1.59576912f * fmaf(0.044715f * x * x, x, x);
-  return x / (1.0f + expf(-u));
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// f(x) in .x and f'(x) in .y
+constexpr float kLog2e = 1.44269504f;
+
+// s = 1 / (1 + exp(-u)) with u = x (SiLU) or GELU tanh's argument.  The base-2 exponent of
+// SiLU is the product with log2 e in two parts, so that its error is one rounding; infinite
+// exponentials give 0.
 template <int ACT>
-__device__ __forceinline__ float2 act_grad(float x) {
-  if (ACT == kActGelu) {
-    const float cdf = 0.5f + 0.5f * erff(x * 0.70710678f);
-    return {x * cdf, fmaf(x, 0.39894228f * expf(-0.5f * x * x), cdf)};
+__device__ __forceinline__ float2 sigmoid2(float2 x, float2 x2) {
+  float2 t;
+  if (ACT == kActSilu) {
+    constexpr float kLo = static_cast<float>(1.44269504088896341 - static_cast<double>(kLog2e));
+    t = fma2(x, both(-kLog2e), mul2(x, both(-kLo)));
+  } else {
+    constexpr float kA = static_cast<float>(2 * 0.79788456080286536 * 1.44269504088896341);
+    t = mul2(x, fma2(x2, both(-0.044715f * kA), both(-kA)));
   }
-  // beyond +-128 s is 0 or 1 and the product with (1 - s) is 0: the clamp keeps it from being 0 * inf
-  const float xc = fminf(fmaxf(x, -128.0f), 128.0f), x2 = xc * xc;
-  const float u = ACT == kActSilu ? x : 1.59576912f * fmaf(0.044715f * x * x, x, x);
-  const float du = ACT == kActSilu ? 1.0f : 1.59576912f * fmaf(0.134145f, x2, 1.0f);
-  const float s = 1.0f / (1.0f + expf(-u));
-  return {x * s, fmaf(xc * s * (1.0f - s), du, s)};
+  const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.0f));
+  return make_float2(rcp(d.x), rcp(d.y));
 }
+
+// The normal distribution function P(x) = 1/2 + x R(x^2): R, smooth and even, by a polynomial of
+// degree 14 in v = 2 x^2 / 5.25^2 - 1, fitted on |x| <= 5.25 (least squares on Chebyshev nodes,
+// reweighted to an even error); beyond, R is held and P saturates to 0 and 1, off by at most
+// 7.6e-8.  Error of P below 2^-23 in binary32.  No exponential and no branch: two values in
+// 10 instructions each, where the library's erf took 25 and made GELU bound by issue slots.
+__device__ __forceinline__ float2 normal_cdf2(float2 x, float2 x2) {
+  constexpr float kR[15] = {0.13465935f,       -0.067126818f,    0.0496457852f,    -0.0397634134f,  0.0320314392f,
+                            -0.0250419322f,    0.0185386483f,    -0.0127752507f,   0.00841787085f,  -0.00544851972f,
+                            0.00289236126f,    -0.00103953469f,  0.000664732244f,  -0.000656583812f, 0.00023995011f};
+  const float2 u = make_float2(fminf(x2.x, 27.5625f), fminf(x2.y, 27.5625f));
+  const float2 v = fma2(u, both(2.0f / 27.5625f), both(-1.0f));
+  float2 r = both(kR[14]);
+#pragma unroll
+  for (int i = 13; i >= 0; --i) r = fma2(r, v, both(kR[i]));
+  return make_float2(__saturatef(fmaf(x.x, r.x, 0.5f)), __saturatef(fmaf(x.y, r.y, 0.5f)));
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 act_value2(float2 x) {
+  const float2 x2 = mul2(x, x);
+  return mul2(x, ACT == kActGelu ? normal_cdf2(x, x2) : sigmoid2<ACT>(x, x2));
+}
+
+// f and f' at x
+template <int ACT>
+__device__ __forceinline__ void act_grad2(float2 x, float2& f, float2& df) {
+  const float2 x2 = mul2(x, x);
+  if (ACT == kActGelu) {
+    const float2 cdf = normal_cdf2(x, x2), t = mul2(x2, both(-0.5f * kLog2e));
+    f = mul2(x, cdf);
+    df = fma2(mul2(x, both(0.39894228f)), make_float2(ex2(t.x), ex2(t.y)), cdf);
+    return;
+  }
+  const float2 s = sigmoid2<ACT>(x, x2);
+  f = mul2(x, s);
+  float2 g = mul2(f, fma2(s, both(-1.0f), both(1.0f)));   // x s (1 - s)
+  if (ACT == kActGeluTanh) {
+    // u': x^2 is held below the overflow of its multiple, where g is 0 already
+    const float2 c = make_float2(fminf(x2.x, 1e30f), fminf(x2.y, 1e30f));
+    g = mul2(g, fma2(c, both(1.59576912f * 0.134145f), both(1.59576912f)));
+  }
+  df = add2(g, s);
+}
+
+// A warp takes kPieces pieces of a row at a time: enough loads in flight, and the 8-bit copies
+// of all of them share the divisions.
+constexpr int kPieces = 2;
 
 template <typename T, bool VECTOR, int ACT, bool GATED>
-__global__ void __launch_bounds__(kThreads) k_act(const ActParams p) {
+__global__ void __launch_bounds__(kThreads, 4) k_act(const ActParams p) {
   using P = Piece<T, VECTOR>;
-  const int lane = threadIdx.x & 31;
-  const int64_t groups = (p.cols + 127) / 128;
+  constexpr int E = P::E;
+  const int lane = threadIdx.x & 31, cols = static_cast<int>(p.cols), groups = (cols + 127) / 128;
   Walk at(static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), static_cast<int64_t>(gridDim.x) * kWarps,
-          (p.cols + P::WC - 1) / P::WC);
+          (cols + kPieces * P::WC - 1) / (kPieces * P::WC));
   pdl_wait();
   pdl_launch_dependents();
   for (; at.row < p.rows; at.next()) {
     const int64_t row = at.row;
-    const int c0 = static_cast<int>(at.piece * P::WC), cols = static_cast<int>(p.cols);
-    float a[P::E], b[P::E], y[P::E];
-    P::load(static_cast<const T*>(p.a) + row * p.lda, c0, lane, cols, a);
-    if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb, c0, lane, cols, b);
+    const int c0 = static_cast<int>(at.piece) * kPieces * P::WC;
+    float a[kPieces][E], b[kPieces][E];
 #pragma unroll
-    for (int i = 0; i < P::E; ++i) y[i] = GATED ? act_value<ACT>(a[i]) * b[i] : act_value<ACT>(a[i]);
-    P::store(static_cast<T*>(p.y) + row * p.ldy, c0, lane, cols, y);
-    if (p.qa != nullptr) P::store_codes(p.qa + row * p.ldq, p.sa + row * groups, c0, lane, cols, p.e5m2, a);
-    if (GATED && p.qb != nullptr) P::store_codes(p.qb + row * p.ldq, p.sb + row * groups, c0, lane, cols, p.e5m2, b);
+    for (int k = 0; k < kPieces; ++k) {
+      P::load(static_cast<const T*>(p.a) + row * p.lda, c0 + k * P::WC, lane, cols, a[k]);
+      if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb, c0 + k * P::WC, lane, cols, b[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      float y[E];
+#pragma unroll
+      for (int i = 0; i < E; i += 2) {
+        float2 f = act_value2<ACT>(make_float2(a[k][i], a[k][i + 1]));
+        if (GATED) f = mul2(f, make_float2(b[k][i], b[k][i + 1]));
+        y[i] = f.x;
+        y[i + 1] = f.y;
+      }
+      P::store(static_cast<T*>(p.y) + row * p.ldy, c0 + k * P::WC, lane, cols, y);
+    }
+    const int at_c[kPieces] = {c0, c0 + P::WC};
+    if (p.qa != nullptr) {
+      uint8_t* const q = p.qa + row * p.ldq;
+      float* const s = p.sa + row * groups;
+      store_copies<P, kPieces>({q, q}, {s, s}, at_c, lane, cols, p.e5m2, a);
+    }
+    if (GATED && p.qb != nullptr) {
+      uint8_t* const q = p.qb + row * p.ldq;
+      float* const s = p.sb + row * groups;
+      store_copies<P, kPieces>({q, q}, {s, s}, at_c, lane, cols, p.e5m2, b);
+    }
   }
 }
 
 template <typename T, bool VECTOR, int ACT, bool GATED, bool CODES>
-__global__ void __launch_bounds__(kThreads) k_act_backward(const ActBwdParams p) {
+__global__ void __launch_bounds__(kThreads, 4) k_act_backward(const ActBwdParams p) {
   using P = Piece<T, VECTOR>;
-  const int lane = threadIdx.x & 31;
-  const int64_t groups = (p.cols + 127) / 128;
+  constexpr int E = P::E;
+  const int lane = threadIdx.x & 31, cols = static_cast<int>(p.cols), groups = (cols + 127) / 128;
   Walk at(static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), static_cast<int64_t>(gridDim.x) * kWarps,
-          (p.cols + P::WC - 1) / P::WC);
+          (cols + kPieces * P::WC - 1) / (kPieces * P::WC));
   pdl_wait();
   pdl_launch_dependents();
   for (; at.row < p.rows; at.next()) {
     const int64_t row = at.row;
-    const int c0 = static_cast<int>(at.piece * P::WC), cols = static_cast<int>(p.cols);
-    float dy[P::E], a[P::E], b[P::E];
-    P::load(static_cast<const T*>(p.dy) + row * p.lddy, c0, lane, cols, dy);
-    if (CODES) {
-      P::load_codes(p.qa + row * p.ldq, p.sa + row * groups, c0, lane, cols, p.e5m2, a);
-      if (GATED) P::load_codes(p.qb + row * p.ldq, p.sb + row * groups, c0, lane, cols, p.e5m2, b);
-    } else {
-      P::load(static_cast<const T*>(p.a) + row * p.lda, c0, lane, cols, a);
-      if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb, c0, lane, cols, b);
+    const int c0 = static_cast<int>(at.piece) * kPieces * P::WC;
+    float dy[kPieces][E], a[kPieces][E], b[kPieces][E];
+    typename P::Codes ca[kPieces], cb[kPieces];
+    float sa[kPieces], sb[kPieces];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int c = c0 + k * P::WC;
+      P::load(static_cast<const T*>(p.dy) + row * p.lddy, c, lane, cols, dy[k]);
+      if (CODES) {
+        ca[k] = P::load_codes(p.qa + row * p.ldq, c, lane, cols);
+        sa[k] = P::load_multiplier(p.sa + row * groups, c, lane, cols);
+        if (GATED) {
+          cb[k] = P::load_codes(p.qb + row * p.ldq, c, lane, cols);
+          sb[k] = P::load_multiplier(p.sb + row * groups, c, lane, cols);
+        }
+      } else {
+        P::load(static_cast<const T*>(p.a) + row * p.lda, c, lane, cols, a[k]);
+        if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb, c, lane, cols, b[k]);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < P::E; ++i) {
-      const float2 f = act_grad<ACT>(a[i]);
-      a[i] = (GATED ? dy[i] * b[i] : dy[i]) * f.y;
-      if (GATED) b[i] = dy[i] * f.x;
+    for (int k = 0; k < kPieces; ++k) {
+      const int c = c0 + k * P::WC;
+      if (CODES) {
+        P::decode(ca[k], sa[k], p.e5m2, a[k]);
+        if (GATED) P::decode(cb[k], sb[k], p.e5m2, b[k]);
+      }
+#pragma unroll
+      for (int i = 0; i < E; i += 2) {
+        const float2 d = make_float2(dy[k][i], dy[k][i + 1]);
+        float2 f, df, da;
+        act_grad2<ACT>(make_float2(a[k][i], a[k][i + 1]), f, df);
+        da = mul2(GATED ? mul2(d, make_float2(b[k][i], b[k][i + 1])) : d, df);
+        a[k][i] = da.x;
+        a[k][i + 1] = da.y;
+        if (GATED) {
+          f = mul2(d, f);
+          b[k][i] = f.x;
+          b[k][i + 1] = f.y;
+        }
+      }
+      P::store(static_cast<T*>(p.da) + row * p.ldda, c, lane, cols, a[k]);
+      if (GATED) P::store(static_cast<T*>(p.db) + row * p.lddb, c, lane, cols, b[k]);
     }
-    P::store(static_cast<T*>(p.da) + row * p.ldda, c0, lane, cols, a);
-    if (GATED) P::store(static_cast<T*>(p.db) + row * p.lddb, c0, lane, cols, b);
   }
 }
 
 dim3 grid_of(int64_t rows, int64_t cols, int64_t wc, int num_sms) {
-  const int64_t want = (rows * ((cols + wc - 1) / wc) + kWarps - 1) / kWarps, cap = static_cast<int64_t>(num_sms) * 8;
+  const int64_t want = (rows * ((cols + wc - 1) / wc) + kWarps - 1) / kWarps, cap = static_cast<int64_t>(num_sms) * 4;
   return dim3(static_cast<unsigned>(want < cap ? want : cap));
 }
 
 template <typename T, bool VECTOR, int ACT>
 cudaError_t run_act(const ActParams& p, int num_sms, cudaStream_t s) {
-  const dim3 grid = grid_of(p.rows, p.cols, Piece<T, VECTOR>::WC, num_sms), block(kThreads);
+  const dim3 grid = grid_of(p.rows, p.cols, kPieces * Piece<T, VECTOR>::WC, num_sms), block(kThreads);
   return p.b != nullptr ? launch_pdl(k_act<T, VECTOR, ACT, true>, grid, block, 0, s, 1, p)
                         : launch_pdl(k_act<T, VECTOR, ACT, false>, grid, block, 0, s, 1, p);
 }
 
 template <typename T, bool VECTOR, int ACT>
 cudaError_t run_act_backward(const ActBwdParams& p, int num_sms, cudaStream_t s) {
-  const dim3 grid = grid_of(p.rows, p.cols, Piece<T, VECTOR>::WC, num_sms), block(kThreads);
+  const dim3 grid = grid_of(p.rows, p.cols, kPieces * Piece<T, VECTOR>::WC, num_sms), block(kThreads);
   if (p.qa != nullptr)
     return p.db != nullptr ? launch_pdl(k_act_backward<T, VECTOR, ACT, true, true>, grid, block, 0, s, 1, p)
                            : launch_pdl(k_act_backward<T, VECTOR, ACT, false, true>, grid, block, 0, s, 1, p);

@@ -76,8 +76,11 @@ __global__ void __launch_bounds__(kThreads) k_norm_any(const NormParams p) {
           st_elem(y + c, fmaf(xh[i], w, b));
         }
       }
-      if (p.q != nullptr)
-        Piece<T, false>::store_codes(p.q + row * p.ldq, p.s + row * groups, g * 128, lane, static_cast<int>(p.cols), p.e5m2, xh);
+      if (p.q != nullptr) {
+        const float v[1][4] = {{xh[0], xh[1], xh[2], xh[3]}};
+        store_copies<Piece<T, false>, 1>({p.q + row * p.ldq}, {p.s + row * groups}, {g * 128}, lane, static_cast<int>(p.cols),
+                                         p.e5m2, v);
+      }
     }
   }
 }
@@ -90,7 +93,7 @@ template <typename T, bool VECTOR, bool WIDE>
 __global__ void __launch_bounds__((WIDE ? kNormWarpsMost : kBlockWarps) * 32)
     k_norm(const NormParams p, const int warps, const int stages) {
   using P = Piece<T, VECTOR>;
-  constexpr int J = 16 / P::E;
+  constexpr int E = P::E, J = 16 / E;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2][kNormWarpsMost];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / warps, w_in = warp - group * warps;
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__((WIDE ? kNormWarpsMost : kBlockWarps) * 32)
   for (int s = 0; s < stages; ++s) issue(row + s * step, s);
   // weight and bias of this thread's columns, kept for all its rows (rows of more than kBlockWarps warps
   // have 64 registers a thread and read them again each time)
-  float w[WIDE ? 1 : J][P::E], b[WIDE ? 1 : J][P::E];
+  float w[WIDE ? 1 : J][E], b[WIDE ? 1 : J][E];
   if constexpr (!WIDE) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__((WIDE ? kNormWarpsMost : kBlockWarps) * 32)
     }
   }
   for (int s = 0, buf = 0; row < p.rows; row += step, s = s + 1 == stages ? 0 : s + 1, buf ^= 1) {
-    float x[J][P::E];
+    float x[J][E];
     if constexpr (VECTOR) {
       cp_async_wait_oldest(stages);
 #pragma unroll
@@ -142,20 +145,28 @@ __global__ void __launch_bounds__((WIDE ? kNormWarpsMost : kBlockWarps) * 32)
 #pragma unroll
       for (int j = 0; j < J; ++j) P::load(in, base + j * P::WC, lane, cols, x[j]);
     }
-    float sum = 0.0f;
+    float2 acc = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int i = 0; i < P::E; ++i) sum += x[j][i];
-    float mean = warp_sum(sum) * inv_nw, m2 = 0.0f;
+      for (int i = 0; i < E; i += 2) acc = add2(acc, make_float2(x[j][i], x[j][i + 1]));
+    float mean = warp_sum(acc.x + acc.y) * inv_nw;
+    acc = both(0.0f);
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+    for (int j = 0; j < J; ++j) {
+      float2 sq = both(0.0f);
 #pragma unroll
-      for (int i = 0; i < P::E; ++i) {
-        const float d = P::col(base + j * P::WC, lane, i) < cols ? x[j][i] - mean : 0.0f;
-        m2 = fmaf(d, d, m2);
+      for (int i = 0; i < E; i += 2) {
+        float2 d = add2(make_float2(x[j][i], x[j][i + 1]), both(-mean));
+        if (!VECTOR) {
+          if (!P::valid(base + j * P::WC, lane, cols, i)) d.x = 0.0f;
+          if (!P::valid(base + j * P::WC, lane, cols, i + 1)) d.y = 0.0f;
+        }
+        sq = fma2(d, d, sq);
       }
-    m2 = warp_sum(m2);
+      if (!VECTOR || P::valid(base + j * P::WC, lane, cols, 0)) acc = add2(acc, sq);
+    }
+    float m2 = warp_sum(acc.x + acc.y);
     if (warps > 1) {
       if (lane == 0) red[buf][warp] = make_float2(mean, m2);
       group_sync(group, warps);
@@ -175,18 +186,31 @@ __global__ void __launch_bounds__((WIDE ? kNormWarpsMost : kBlockWarps) * 32)
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int c0 = base + j * P::WC;
-      float y[P::E];
+      float y[E];
       if constexpr (WIDE) {
         load_param<P, VECTOR>(p.w, p.w_f32, c0, lane, cols, 1.0f, w[0]);
         load_param<P, VECTOR>(p.b, p.w_f32, c0, lane, cols, 0.0f, b[0]);
       }
+      const int k = WIDE ? 0 : j;
 #pragma unroll
-      for (int i = 0; i < P::E; ++i) {
-        x[j][i] = P::col(c0, lane, i) < cols ? (x[j][i] - mean) * rstd : 0.0f;
-        y[i] = fmaf(x[j][i], w[WIDE ? 0 : j][i], b[WIDE ? 0 : j][i]);
+      for (int i = 0; i < E; i += 2) {
+        const float2 h = mul2(add2(make_float2(x[j][i], x[j][i + 1]), both(-mean)), both(rstd));
+        const float2 v = fma2(h, make_float2(w[k][i], w[k][i + 1]), make_float2(b[k][i], b[k][i + 1]));
+        x[j][i] = h.x;
+        x[j][i + 1] = h.y;
+        y[i] = v.x;
+        y[i + 1] = v.y;
       }
       P::store(static_cast<T*>(p.y) + row * p.ldy, c0, lane, cols, y);
-      if (p.q != nullptr) P::store_codes(p.q + row * p.ldq, p.s + row * copies, c0, lane, cols, p.e5m2, x[j]);
+    }
+    if (p.q != nullptr) {
+      uint8_t* const q = p.q + row * p.ldq;
+      float* const s_row = p.s + row * copies;
+      if constexpr (J == 2)
+        store_copies<P, 2>({q, q}, {s_row, s_row}, {base, base + P::WC}, lane, cols, p.e5m2, x);
+      else
+        store_copies<P, 4>({q, q, q, q}, {s_row, s_row, s_row, s_row}, {base, base + P::WC, base + 2 * P::WC, base + 3 * P::WC},
+                           lane, cols, p.e5m2, x);
     }
   }
 }

@@ -154,14 +154,16 @@ __global__ void __launch_bounds__((WIDE ? kNormWarpsMost : kBlockWarps) * 32)
       P::unpack(*reinterpret_cast<const uint4*>(at + lane * 16), dy);
       if constexpr (CODES) {
         const float* mult = reinterpret_cast<const float*>(mine + s * kStage + J * kPiece);
-        P::decode(at + 512 + lane * kIn, mult[(j * P::WC + lane * E) / 128], P::col(c0, lane, 0) < cols, p.e5m2, xh);
+        // the codes past the row's end are 0, and their multiplier may be anything
+        const float m = P::valid(c0, lane, cols, 0) ? mult[(j * P::WC + lane * E) / 128] : 0.0f;
+        P::decode(P::read_codes(at + 512 + lane * kIn), m, p.e5m2, xh);
       } else {
         P::unpack(*reinterpret_cast<const uint4*>(at + 512 + lane * 16), xh);
       }
     } else {
       P::load(static_cast<const T*>(p.dy) + row * p.lddy, c0, lane, cols, dy);
       if constexpr (CODES)
-        P::load_codes(p.q + row * p.ldq, p.s + row * copies, c0, lane, cols, p.e5m2, xh);
+        P::decode(P::load_codes(p.q + row * p.ldq, c0, lane, cols), P::load_multiplier(p.s + row * copies, c0, lane, cols), p.e5m2, xh);
       else
         P::load(static_cast<const T*>(p.x) + row * p.ldx, c0, lane, cols, xh);
     }

@@ -129,72 +129,139 @@ struct Piece {
         if (col(c0, lane, i) < cols) st_elem(row + col(c0, lane, i), v[i]);
     }
   }
-  // The 8-bit copy of the piece by the blockwise recipe's rule: codes = satRNE(v FMAX / amax),
-  // multiplier 1 / (FMAX / amax), per 128 columns.  v = 0 past the row's end.
-  __device__ static __forceinline__ void store_codes(uint8_t* q_row, float* s_row, int c0, int lane, int cols, bool e5m2,
-                                                     const float (&v)[E]) {
+  __device__ static __forceinline__ bool valid(int c0, int lane, int cols, int i) {
+    return VECTOR ? c0 + lane * E < cols : col(c0, lane, i) < cols;
+  }
+  // max |v| of the lane's columns (NaN ignored)
+  __device__ static __forceinline__ float amax(const float (&v)[E], int c0, int lane, int cols) {
     float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) a = fmaxf(a, fabsf(v[i]));   // a NaN operand is ignored
+    for (int i = 0; i < E; ++i)
+      a = VECTOR ? fmaxf(a, fabsf(v[i])) : fmaxf(a, valid(c0, lane, cols, i) ? fabsf(v[i]) : 0.0f);
+    return !VECTOR || valid(c0, lane, cols, 0) ? a : 0.0f;
+  }
+  // codes = satRNE(v sc)
+  template <bool E5>
+  __device__ static __forceinline__ void encode(uint8_t* q_row, int c0, int lane, int cols, const float (&v)[E], float sc) {
+    uint32_t u[E / 2];
 #pragma unroll
-    for (int o = kGroupLanes / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-    const float sc = scale_from_amax(a, fmax_of(e5m2));
+    for (int i = 0; i < E / 2; ++i) {
+      const float2 m = mul2(make_float2(v[2 * i], v[2 * i + 1]), both(sc));
+      u[i] = E5 ? cvt_pair_e5m2(m.x, m.y) : cvt_pair_e4m3(m.x, m.y);
+    }
     if constexpr (VECTOR) {
-      if (col(c0, lane, 0) >= cols) return;
-      uint32_t u[E / 4];
-#pragma unroll
-      for (int i = 0; i < E / 4; ++i)
-        u[i] = cvt_pair(__fmul_rn(v[4 * i], sc), __fmul_rn(v[4 * i + 1], sc), e5m2) |
-               cvt_pair(__fmul_rn(v[4 * i + 2], sc), __fmul_rn(v[4 * i + 3], sc), e5m2) << 16;
+      if (!valid(c0, lane, cols, 0)) return;
       if constexpr (E == 8)
-        *reinterpret_cast<uint2*>(q_row + col(c0, lane, 0)) = make_uint2(u[0], u[1]);
+        *reinterpret_cast<uint2*>(q_row + c0 + lane * E) = make_uint2(u[0] | u[1] << 16, u[2] | u[3] << 16);
       else
-        *reinterpret_cast<uint32_t*>(q_row + col(c0, lane, 0)) = u[0];
+        *reinterpret_cast<uint32_t*>(q_row + c0 + lane * E) = u[0] | u[1] << 16;
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i)
-        if (col(c0, lane, i) < cols)
-          q_row[col(c0, lane, i)] = static_cast<uint8_t>(cvt_pair(__fmul_rn(v[i], sc), 0.0f, e5m2));
+        if (valid(c0, lane, cols, i)) q_row[col(c0, lane, i)] = static_cast<uint8_t>(u[i / 2] >> (8 * (i % 2)));
     }
-    if (lane % kGroupLanes == 0 && col(c0, lane, 0) < cols) s_row[col(c0, lane, 0) / 128] = recip_rn(sc);
   }
-  // E consecutive codes (aligned to E bytes, in global or shared memory) times s, 0 if not `valid`
-  __device__ static __forceinline__ void decode(const uint8_t* q, float s, bool valid, bool e5m2, float (&v)[E]) {
+  // The codes of a lane's columns, as they lie in memory (VECTOR) or one a byte of the word.
+  struct Codes {
     uint32_t u[E / 4];
+  };
+  __device__ static __forceinline__ Codes read_codes(const uint8_t* q) {   // E consecutive codes at q
+    Codes c;
     if constexpr (E == 8) {
       const uint2 w = *reinterpret_cast<const uint2*>(q);
-      u[0] = w.x;
-      u[1] = w.y;
+      c.u[0] = w.x;
+      c.u[1] = w.y;
     } else {
-      u[0] = *reinterpret_cast<const uint32_t*>(q);
+      c.u[0] = *reinterpret_cast<const uint32_t*>(q);
     }
+    return c;
+  }
+  __device__ static __forceinline__ Codes load_codes(const uint8_t* q_row, int c0, int lane, int cols) {
+    Codes c = {};
+    if constexpr (VECTOR) {
+      if (valid(c0, lane, cols, 0)) c = read_codes(q_row + c0 + lane * E);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (valid(c0, lane, cols, i)) c.u[0] |= static_cast<uint32_t>(q_row[col(c0, lane, i)]) << (8 * i);
+    }
+    return c;
+  }
+  __device__ static __forceinline__ float load_multiplier(const float* s_row, int c0, int lane, int cols) {
+    return valid(c0, lane, cols, 0) ? __ldg(s_row + col(c0, lane, 0) / 128) : 0.0f;
+  }
+  // the values the codes stand for, each product rounded to binary32
+  template <bool E5>
+  __device__ static __forceinline__ void decode(const Codes& c, float s, float (&v)[E]) {
 #pragma unroll
     for (int i = 0; i < E / 4; ++i) {
-      decode_pair(u[i] & 0xFFFFu, e5m2, v[4 * i], v[4 * i + 1]);
-      decode_pair(u[i] >> 16, e5m2, v[4 * i + 2], v[4 * i + 3]);
+      decode_pair(c.u[i] & 0xFFFFu, E5, v[4 * i], v[4 * i + 1]);
+      decode_pair(c.u[i] >> 16, E5, v[4 * i + 2], v[4 * i + 3]);
     }
 #pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = valid ? v[i] * s : 0.0f;
+    for (int i = 0; i < E / 2; ++i) {
+      const float2 m = mul2(make_float2(v[2 * i], v[2 * i + 1]), both(s));
+      v[2 * i] = m.x;
+      v[2 * i + 1] = m.y;
+    }
   }
-  // The values the codes stand for (each product rounded to binary32), 0 past the row's end.
-  __device__ static __forceinline__ void load_codes(const uint8_t* q_row, const float* s_row, int c0, int lane, int cols,
-                                                    bool e5m2, float (&v)[E]) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = 0.0f;
-    if (col(c0, lane, 0) >= cols) return;
-    const float s = __ldg(s_row + col(c0, lane, 0) / 128);
-    if constexpr (VECTOR) {
-      decode(q_row + col(c0, lane, 0), s, true, e5m2, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        float x = 0.0f, unused;
-        if (col(c0, lane, i) < cols) decode_pair(q_row[col(c0, lane, i)], e5m2, x, unused);
-        v[i] = x * s;
-      }
-    }
+  __device__ static __forceinline__ void decode(const Codes& c, float s, bool e5m2, float (&v)[E]) {
+    if (e5m2)
+      decode<true>(c, s, v);
+    else
+      decode<false>(c, s, v);
   }
 };
+
+// The maximum over each `W`-lane group of N values a lane (N = 1, 2 or 4): lane l gets value
+// l % N's.  Each exchange halves the values a lane carries, so N maxima cost log2(W) + N - 1 -
+// log2(N) exchanges instead of N log2(W).
+template <int N, int W>
+__device__ __forceinline__ float group_max(const float (&a)[N], int lane) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  float m;
+  if constexpr (N == 1) {
+    m = a[0];
+  } else {
+    float k[N / 2];
+#pragma unroll
+    for (int h = 0; h < N / 2; ++h) {
+      const float keep = lane & 1 ? a[2 * h + 1] : a[2 * h], give = lane & 1 ? a[2 * h] : a[2 * h + 1];
+      k[h] = fmaxf(keep, __shfl_xor_sync(kAll, give, 1));
+    }
+    m = k[0];
+    if constexpr (N == 4) m = fmaxf(lane & 2 ? k[1] : k[0], __shfl_xor_sync(kAll, lane & 2 ? k[0] : k[1], 2));
+  }
+#pragma unroll
+  for (int o = N; o < W; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+  return m;
+}
+
+// The 8-bit copies of N pieces by the blockwise recipe's rule, codes satRNE(v FMAX / amax) and
+// multiplier 1 / (FMAX / amax) per 128 columns: piece i is v[i] at column c0[i] of the row whose
+// codes and multipliers start at q[i] and s[i].  Each lane makes the two divisions of one piece
+// only (lane % N) and the others' scales come from its neighbours: the divisions would
+// otherwise be a third of the copy's instructions.
+template <typename P, int N>
+__device__ __forceinline__ void store_copies(uint8_t* const (&q)[N], float* const (&s)[N], const int (&c0)[N], int lane,
+                                             int cols, bool e5m2, const float (&v)[N][P::E]) {
+  float a[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = P::amax(v[i], c0[i], lane, cols);
+  const float mine = scale_from_amax(group_max<N, P::kGroupLanes>(a, lane), fmax_of(e5m2));
+  const float inv = recip_rn(mine);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    // lane i of the group: its first lane's column says whether the group exists
+    const int first = P::col(c0[i], lane - i, 0);
+    if (lane % P::kGroupLanes == i && first < cols) s[i][first / 128] = inv;
+    const float sc = N == 1 ? mine : __shfl_sync(0xFFFFFFFFu, mine, (lane & ~(N - 1)) | i);
+    if (e5m2)
+      P::template encode<true>(q[i], c0[i], lane, cols, v[i], sc);
+    else
+      P::template encode<false>(q[i], c0[i], lane, cols, v[i], sc);
+  }
+}
 
 // Pieces (rows x pieces of a row) shared out over all warps: piece `at`, `at` + stride, ...
 // advanced without a division a step.
