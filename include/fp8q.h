@@ -356,7 +356,7 @@ fp8_status fp8_scaled_gemm_amax(const uint8_t* A, fp8_format fa, fp8_recipe ra, 
  *     element (alignment: the element's size).  Rows whose pointer and stride are
  *     multiples of 16 bytes, with cols a multiple of 16 bytes, are read and written in
  *     16-byte accesses; anything else element by element, with the same results.
- *   - rows, strides and capacity are below 2^31, cols below 2^31 - 65536 (FP8_ERR_SHAPE).
+ *   - rows and cols are below 2^31 - 65536, strides and capacity below 2^31 (FP8_ERR_SHAPE).
  *   - outputs must not overlap inputs or each other.
  *   - arithmetic and every sum are binary32, rounded once to the output's type; results
  *     are deterministic.

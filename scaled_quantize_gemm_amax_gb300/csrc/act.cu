@@ -106,12 +106,15 @@ __global__ void __launch_bounds__(kThreads, 4) k_act(const ActParams p) {
   pdl_launch_dependents();
   for (; at.row < p.rows; at.next()) {
     const int64_t row = at.row;
-    const int c0 = static_cast<int>(at.piece) * kPieces * P::WC;
+    const int c = static_cast<int>(at.piece) * kPieces * P::WC + P::first(lane), left = cols - c;
+    const T* pa = static_cast<const T*>(p.a) + row * p.lda + c;
+    const T* pb = static_cast<const T*>(p.b) + row * p.ldb + c;
+    T* py = static_cast<T*>(p.y) + row * p.ldy + c;
     float a[kPieces][E], b[kPieces][E];
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
-      P::load(static_cast<const T*>(p.a) + row * p.lda, c0 + k * P::WC, lane, cols, a[k]);
-      if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb, c0 + k * P::WC, lane, cols, b[k]);
+      P::load(pa + k * P::WC, left - k * P::WC, a[k]);
+      if (GATED) P::load(pb + k * P::WC, left - k * P::WC, b[k]);
     }
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
@@ -123,19 +126,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_act(const ActParams p) {
         y[i] = f.x;
         y[i + 1] = f.y;
       }
-      P::store(static_cast<T*>(p.y) + row * p.ldy, c0 + k * P::WC, lane, cols, y);
+      P::store(py + k * P::WC, left - k * P::WC, y);
     }
-    const int at_c[kPieces] = {c0, c0 + P::WC};
-    if (p.qa != nullptr) {
-      uint8_t* const q = p.qa + row * p.ldq;
-      float* const s = p.sa + row * groups;
-      store_copies<P, kPieces>({q, q}, {s, s}, at_c, lane, cols, p.e5m2, a);
-    }
-    if (GATED && p.qb != nullptr) {
-      uint8_t* const q = p.qb + row * p.ldq;
-      float* const s = p.sb + row * groups;
-      store_copies<P, kPieces>({q, q}, {s, s}, at_c, lane, cols, p.e5m2, b);
-    }
+    const int64_t q = row * p.ldq + c, s = row * groups + c / 128;
+    if (p.qa != nullptr) store_copies<P, kPieces>(p.qa + q, p.sa + s, lane, left, p.e5m2, a);
+    if (GATED && p.qb != nullptr) store_copies<P, kPieces>(p.qb + q, p.sb + s, lane, left, p.e5m2, b);
   }
 }
 
@@ -150,29 +145,30 @@ __global__ void __launch_bounds__(kThreads, 4) k_act_backward(const ActBwdParams
   pdl_launch_dependents();
   for (; at.row < p.rows; at.next()) {
     const int64_t row = at.row;
-    const int c0 = static_cast<int>(at.piece) * kPieces * P::WC;
+    const int c = static_cast<int>(at.piece) * kPieces * P::WC + P::first(lane), left = cols - c;
+    const int64_t q = row * p.ldq + c, s = row * groups + c / 128;
     float dy[kPieces][E], a[kPieces][E], b[kPieces][E];
     typename P::Codes ca[kPieces], cb[kPieces];
     float sa[kPieces], sb[kPieces];
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
-      const int c = c0 + k * P::WC;
-      P::load(static_cast<const T*>(p.dy) + row * p.lddy, c, lane, cols, dy[k]);
+      const int off = k * P::WC, rest = left - off;
+      P::load(static_cast<const T*>(p.dy) + row * p.lddy + c + off, rest, dy[k]);
       if (CODES) {
-        ca[k] = P::load_codes(p.qa + row * p.ldq, c, lane, cols);
-        sa[k] = P::load_multiplier(p.sa + row * groups, c, lane, cols);
+        ca[k] = P::load_codes(p.qa + q + off, rest);
+        sa[k] = rest > 0 ? __ldg(p.sa + s + off / 128) : 0.0f;
         if (GATED) {
-          cb[k] = P::load_codes(p.qb + row * p.ldq, c, lane, cols);
-          sb[k] = P::load_multiplier(p.sb + row * groups, c, lane, cols);
+          cb[k] = P::load_codes(p.qb + q + off, rest);
+          sb[k] = rest > 0 ? __ldg(p.sb + s + off / 128) : 0.0f;
         }
       } else {
-        P::load(static_cast<const T*>(p.a) + row * p.lda, c, lane, cols, a[k]);
-        if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb, c, lane, cols, b[k]);
+        P::load(static_cast<const T*>(p.a) + row * p.lda + c + off, rest, a[k]);
+        if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb + c + off, rest, b[k]);
       }
     }
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
-      const int c = c0 + k * P::WC;
+      const int off = k * P::WC, rest = left - off;
       if (CODES) {
         P::decode(ca[k], sa[k], p.e5m2, a[k]);
         if (GATED) P::decode(cb[k], sb[k], p.e5m2, b[k]);
@@ -191,8 +187,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_act_backward(const ActBwdParams
           b[k][i + 1] = f.y;
         }
       }
-      P::store(static_cast<T*>(p.da) + row * p.ldda, c, lane, cols, a[k]);
-      if (GATED) P::store(static_cast<T*>(p.db) + row * p.lddb, c, lane, cols, b[k]);
+      P::store(static_cast<T*>(p.da) + row * p.ldda + c + off, rest, a[k]);
+      if (GATED) P::store(static_cast<T*>(p.db) + row * p.lddb + c + off, rest, b[k]);
     }
   }
 }

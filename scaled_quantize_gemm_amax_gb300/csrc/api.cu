@@ -640,7 +640,7 @@ fp8_status fp8_debug_wait_timeout(cudaStream_t stream) {
 namespace {
 
 bool valid_dt(fp8_dtype d) { return d == FP8_DT_BF16 || d == FP8_DT_FP32; }
-constexpr int64_t kMaxCols = kMaxDim - 65536;   // column arithmetic is 32-bit and runs a little past the row's end
+constexpr int64_t kMaxExtent = kMaxDim - 65536;   // row and column arithmetic is 32-bit and runs a little past the end
 uintptr_t elem_size(fp8_dtype d) { return d == FP8_DT_FP32 ? 4 : 2; }
 
 // Whether a row stride can hold `cols` (a single row's stride is not used: set to cols).
@@ -661,7 +661,7 @@ fp8_status fp8_layer_norm(const void* x, int64_t rows, int64_t cols, int64_t ldx
   if ((q == nullptr) != (s == nullptr) && rows > 0 && cols > 0) return FP8_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return FP8_OK;
   if (x == nullptr || y == nullptr) return FP8_ERR_INVALID_ARG;
-  if (rows > kMaxDim || cols > kMaxCols || !row_stride(rows, cols, &ldx) || !row_stride(rows, cols, &ldy) ||
+  if (rows > kMaxExtent || cols > kMaxExtent || !row_stride(rows, cols, &ldx) || !row_stride(rows, cols, &ldy) ||
       (q != nullptr && !row_stride(rows, cols, &ldq)))
     return FP8_ERR_SHAPE;
   const uintptr_t es = elem_size(dt), ws = elem_size(wdt);
@@ -694,7 +694,7 @@ fp8_status fp8_layer_norm(const void* x, int64_t rows, int64_t cols, int64_t ldx
 fp8_status fp8_layer_norm_workspace(int64_t rows, int64_t cols, int64_t* bytes) {
   ApiRange nvtx_range("fp8_layer_norm_workspace");
   if (rows < 0 || cols < 0 || bytes == nullptr) return FP8_ERR_INVALID_ARG;
-  if (rows > kMaxDim || cols > kMaxCols) return FP8_ERR_SHAPE;
+  if (rows > kMaxExtent || cols > kMaxExtent) return FP8_ERR_SHAPE;
   *bytes = static_cast<int64_t>(norm_partials(rows)) * 2 * cols * static_cast<int64_t>(sizeof(float));
   return FP8_OK;
 }
@@ -714,7 +714,7 @@ fp8_status fp8_layer_norm_backward(const void* dy, int64_t rows, int64_t cols, i
   }
   const bool params = dweight != nullptr || dbias != nullptr;
   if (params && workspace == nullptr) return FP8_ERR_INVALID_ARG;
-  if (rows > kMaxDim || cols > kMaxCols) return FP8_ERR_SHAPE;
+  if (rows > kMaxExtent || cols > kMaxExtent) return FP8_ERR_SHAPE;
   if (!row_stride(rows, cols, &lddy) || !row_stride(rows, cols, &lddx) || (x != nullptr && !row_stride(rows, cols, &ldx)) ||
       (q != nullptr && !row_stride(rows, cols, &ldq)))
     return FP8_ERR_SHAPE;
@@ -765,7 +765,7 @@ fp8_status fp8_gated_act(const void* a, int64_t rows, int64_t cols, int64_t lda,
   if (a == nullptr || y == nullptr || (qa == nullptr) != (sa == nullptr) || (qb == nullptr) != (sb == nullptr) ||
       (qb != nullptr && b == nullptr))
     return FP8_ERR_INVALID_ARG;
-  if (rows > kMaxDim || cols > kMaxCols || !row_stride(rows, cols, &lda) || !row_stride(rows, cols, &ldy) ||
+  if (rows > kMaxExtent || cols > kMaxExtent || !row_stride(rows, cols, &lda) || !row_stride(rows, cols, &ldy) ||
       (b != nullptr && !row_stride(rows, cols, &ldb)) ||
       ((qa != nullptr || qb != nullptr) && !row_stride(rows, cols, &ldq)))
     return FP8_ERR_SHAPE;
@@ -807,7 +807,7 @@ fp8_status fp8_gated_act_backward(const void* dy, int64_t rows, int64_t cols, in
   const bool gated = b != nullptr || qb != nullptr;
   // both inputs from memory or both from codes
   if ((b != nullptr && a == nullptr) || (qb != nullptr && qa == nullptr) || gated != (db != nullptr)) return FP8_ERR_INVALID_ARG;
-  if (rows > kMaxDim || cols > kMaxCols || !row_stride(rows, cols, &lddy) || !row_stride(rows, cols, &ldda) ||
+  if (rows > kMaxExtent || cols > kMaxExtent || !row_stride(rows, cols, &lddy) || !row_stride(rows, cols, &ldda) ||
       (a != nullptr && !row_stride(rows, cols, &lda)) || (b != nullptr && !row_stride(rows, cols, &ldb)) ||
       (qa != nullptr && !row_stride(rows, cols, &ldq)) || (gated && !row_stride(rows, cols, &lddb)))
     return FP8_ERR_SHAPE;
@@ -891,7 +891,7 @@ fp8_status fp8_moe_combine(const void* ys, int64_t capacity, int64_t cols, int64
   if (capacity < 0 || cols < 0 || tokens < 0 || k < 1 || !valid_dt(dt)) return FP8_ERR_INVALID_ARG;
   if (tokens == 0 || cols == 0) return FP8_OK;
   if (pos == nullptr || y == nullptr || (capacity > 0 && ys == nullptr)) return FP8_ERR_INVALID_ARG;
-  if (cols > kMaxCols || capacity > kMaxDim || tokens > kMaxDim || tokens * k > kMaxDim || !row_stride(capacity, cols, &ldys) ||
+  if (cols > kMaxExtent || capacity > kMaxDim || tokens > kMaxDim || tokens * k > kMaxDim || !row_stride(capacity, cols, &ldys) ||
       !row_stride(tokens, cols, &ldy))
     return FP8_ERR_SHAPE;
   const uintptr_t es = elem_size(dt);
@@ -927,7 +927,7 @@ fp8_status scatter_rows(const void* in, int64_t tokens, int64_t cols, int64_t ld
   if ((any && (pos == nullptr || (in == nullptr && cols > 0))) || (rows && (src == nullptr || out == nullptr)) ||
       (rows && any && dots != nullptr && other == nullptr))
     return FP8_ERR_INVALID_ARG;
-  if (cols > kMaxCols || capacity > kMaxDim || tokens > kMaxDim || tokens * k > kMaxDim || !row_stride(tokens, cols, &ldin) ||
+  if (cols > kMaxExtent || capacity > kMaxDim || tokens > kMaxDim || tokens * k > kMaxDim || !row_stride(tokens, cols, &ldin) ||
       !row_stride(capacity, cols, &ldout) || (dots != nullptr && !row_stride(capacity, cols, &ldother)))
     return FP8_ERR_SHAPE;
   const uintptr_t es = elem_size(dt);

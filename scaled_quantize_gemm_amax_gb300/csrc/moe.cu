@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) k_scatter(const ScatterParams p, con
       for (int i = 0; i < P::E; ++i) zero[i] = 0.0f;
       for (; empty != 0; empty &= empty - 1) {
         T* out = static_cast<T*>(p.out) + (r0 + __ffs(empty) - 1) * p.ldout;
-        for (int c0 = 0; c0 < cols; c0 += P::WC) P::store(out, c0, lane, cols, zero);
+        for (int c = P::first(lane); c < cols; c += P::WC) P::store(out + c, cols - c, zero);
       }
       continue;
     }
@@ -199,9 +199,10 @@ __global__ void __launch_bounds__(kThreads) k_scatter(const ScatterParams p, con
       const int n = min(32, p.k - j0);
       float my_dot = 0.0f;   // of choice j0 + lane
       for (int cb = w_in * kPieces * P::WC; cb < cols; cb += block_cols) {
+        const int first = cb + P::first(lane), left = cols - first;
         float v[kPieces][P::E];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) P::load(in, cb + i * P::WC, lane, cols, v[i]);
+        for (int i = 0; i < kPieces; ++i) P::load(in + first + i * P::WC, left - i * P::WC, v[i]);
         for (int j = 0; j < n; j += kFlight) {
           float o[DOTS ? kFlight : 1][kPieces][P::E];
           if constexpr (DOTS) {
@@ -209,9 +210,9 @@ __global__ void __launch_bounds__(kThreads) k_scatter(const ScatterParams p, con
             for (int u = 0; u < kFlight; ++u) {
               const int pos = __shfl_sync(0xFFFFFFFFu, c.pos, (j + u) & 31);
               const bool on = j + u < n && pos >= 0;
-              const T* other = static_cast<const T*>(p.other) + (on ? pos : 0) * p.ldother;
+              const T* other = static_cast<const T*>(p.other) + (on ? pos : 0) * p.ldother + first;
 #pragma unroll
-              for (int i = 0; i < kPieces; ++i) P::load(other, cb + i * P::WC, lane, on ? cols : 0, o[u][i]);
+              for (int i = 0; i < kPieces; ++i) P::load(other + i * P::WC, on ? left - i * P::WC : 0, o[u][i]);
             }
           }
 #pragma unroll
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) k_scatter(const ScatterParams p, con
             const int pos = __shfl_sync(0xFFFFFFFFu, c.pos, j + u);
             const float w = __shfl_sync(0xFFFFFFFFu, c.w, j + u);
             if (pos < 0) continue;
-            T* out = static_cast<T*>(p.out) + pos * p.ldout;
+            T* out = static_cast<T*>(p.out) + pos * p.ldout + first;
             float dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) k_scatter(const ScatterParams p, con
                 y[e] = w * v[i][e];
                 if constexpr (DOTS) dot = fmaf(v[i][e], o[u][i][e], dot);
               }
-              P::store(out, cb + i * P::WC, lane, cols, y);
+              P::store(out + i * P::WC, left - i * P::WC, y);
             }
             if constexpr (DOTS) {
               dot = warp_sum(dot);
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kThreads) k_combine(const CombineParams p) {
   pdl_wait();
   pdl_launch_dependents();
   for (; at.row < p.tokens; at.next()) {
-    const int c0 = static_cast<int>(at.piece) * kPieces * P::WC;
+    const int first = static_cast<int>(at.piece) * kPieces * P::WC + P::first(lane), left = cols - first;
     float acc[kPieces][P::E];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
@@ -280,9 +281,9 @@ __global__ void __launch_bounds__(kThreads) k_combine(const CombineParams p) {
           const int pos = __shfl_sync(0xFFFFFFFFu, c.pos, (j + u) & 31);
           w[u] = __shfl_sync(0xFFFFFFFFu, c.w, (j + u) & 31);
           const bool on = j + u < n && pos >= 0;
-          const T* ys = static_cast<const T*>(p.ys) + (on ? pos : 0) * p.ldys;
+          const T* ys = static_cast<const T*>(p.ys) + (on ? pos : 0) * p.ldys + first;
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) P::load(ys, c0 + i * P::WC, lane, on ? cols : 0, v[u][i]);
+          for (int i = 0; i < kPieces; ++i) P::load(ys + i * P::WC, on ? left - i * P::WC : 0, v[u][i]);
         }
 #pragma unroll
         for (int u = 0; u < kFlight; ++u)
@@ -293,9 +294,9 @@ __global__ void __launch_bounds__(kThreads) k_combine(const CombineParams p) {
               for (int e = 0; e < P::E; ++e) acc[i][e] = fmaf(w[u], v[u][i][e], acc[i][e]);
       }
     }
-    T* y = static_cast<T*>(p.y) + at.row * p.ldy;
+    T* y = static_cast<T*>(p.y) + at.row * p.ldy + first;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) P::store(y, c0 + i * P::WC, lane, cols, acc[i]);
+    for (int i = 0; i < kPieces; ++i) P::store(y + i * P::WC, left - i * P::WC, acc[i]);
   }
 }
 

@@ -14,6 +14,7 @@ namespace fp8q {
 namespace {
 
 constexpr int kBlockWarps = 24;   // 80 registers a thread
+constexpr int kMostCols = 16384;  // of a row held in registers, its weight and bias in shared memory
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
@@ -42,18 +43,18 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) k_norm_any(const NormParams p) {
   __shared__ float red[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t groups = (p.cols + 127) / 128;
-  const float inv_n = 1.0f / static_cast<float>(p.cols);
+  const int cols = static_cast<int>(p.cols), groups = (cols + 127) / 128;
+  const float inv_n = 1.0f / static_cast<float>(cols);
   pdl_wait();
   pdl_launch_dependents();
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
     T* y = static_cast<T*>(p.y) + row * p.ldy;
     float sum = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.cols; c += kThreads) sum += ld_elem(x + c);
+    for (int c = threadIdx.x; c < cols; c += kThreads) sum += ld_elem(x + c);
     const float mean = block_sum(sum, red) * inv_n;
     float sq = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.cols; c += kThreads) {
+    for (int c = threadIdx.x; c < cols; c += kThreads) {
       const float d = ld_elem(x + c) - mean;
       sq = fmaf(d, d, sq);
     }
@@ -63,87 +64,82 @@ __global__ void __launch_bounds__(kThreads) k_norm_any(const NormParams p) {
       if (p.mean != nullptr) p.mean[row] = mean;
       if (p.rstd != nullptr) p.rstd[row] = rstd;
     }
+    using P = Piece<T, false>;
     for (int g = warp; g < groups; g += kWarps) {
-      float xh[4];
+      const int c = g * 128 + lane, left = cols - c;
+      float v[4], w[4], b[4], xh[1][4];
+      P::load(x + c, left, v);
+      P::load_param(p.w, p.w_f32, c, left, 1.0f, w);
+      P::load_param(p.b, p.w_f32, c, left, 0.0f, b);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int c = Piece<T, false>::col(g * 128, lane, i);
-        xh[i] = 0.0f;
-        if (c < p.cols) {
-          xh[i] = (ld_elem(x + c) - mean) * rstd;
-          const float w = p.w != nullptr ? ld_param(p.w, p.w_f32, c) : 1.0f;
-          const float b = p.b != nullptr ? ld_param(p.b, p.w_f32, c) : 0.0f;
-          st_elem(y + c, fmaf(xh[i], w, b));
-        }
+        xh[0][i] = (v[i] - mean) * rstd;
+        v[i] = fmaf(xh[0][i], w[i], b[i]);
       }
-      if (p.q != nullptr) {
-        const float v[1][4] = {{xh[0], xh[1], xh[2], xh[3]}};
-        store_copies<Piece<T, false>, 1>({p.q + row * p.ldq}, {p.s + row * groups}, {g * 128}, lane, static_cast<int>(p.cols),
-                                         p.e5m2, v);
-      }
+      P::store(y + c, left, v);
+      if (p.q != nullptr) store_copies<P, 1>(p.q + row * p.ldq + c, p.s + row * groups + g, lane, left, p.e5m2, xh);
     }
   }
 }
 
-// Rows of up to 16384 columns.  Each warp takes the mean and the sum of squared differences of
-// its own 512 columns in two passes over registers; the warps' (n, mean, M2) are then joined by
+// Rows of up to kMostCols columns, V values a lane.  Each warp takes the mean and the
+// sum of squared differences of its own columns in two passes over registers; the warps'
+// (n, mean, M2) are then joined by
 //   M2 = sum M2_w + n_w (mean_w - mean)^2
 // so a row costs one barrier and loses no digits to a large mean.
-template <typename T, bool VECTOR, bool WIDE>
-__global__ void __launch_bounds__((WIDE ? kNormWarpsMost : kBlockWarps) * 32)
-    k_norm(const NormParams p, const int warps, const int stages) {
+template <typename T, bool VECTOR, int V>
+__global__ void __launch_bounds__(kBlockWarps * 32) k_norm(const NormParams p, const int warps, const int stages, const int ring) {
   using P = Piece<T, VECTOR>;
-  constexpr int E = P::E, J = 16 / E;
-  extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 red[2][kNormWarpsMost];
+  constexpr int E = P::E, J = V / E, kCols = 32 * V;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 red[2][kBlockWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / warps, w_in = warp - group * warps;
-  const int n_groups = (blockDim.x >> 5) / warps;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * n_groups;
-  const int cols = static_cast<int>(p.cols), base = w_in * kNormWarpCols;
-  const int copies = (cols + 127) / 128;
-  const float n_w = static_cast<float>(min(cols - base, kNormWarpCols));
-  const float inv_nw = 1.0f / n_w, inv_n = 1.0f / static_cast<float>(cols);
-  // this thread's 16 bytes of piece j in stage s: ring + slot + (s * J + j) * 512
-  const uint32_t slot = smem_u32(ring) + warp * stages * J * 512 + lane * 16;
+  const int n_groups = (blockDim.x >> 5) / warps, step = gridDim.x * n_groups;
+  const int rows = static_cast<int>(p.rows), cols = static_cast<int>(p.cols), groups8 = (cols + 127) / 128;
+  const int ldx = static_cast<int>(p.ldx), ldy = static_cast<int>(p.ldy), ldq = static_cast<int>(p.ldq);
+  // this lane's first column and the columns from there to the row's end
+  const int c = w_in * kCols + P::first(lane), left = cols - c;
+  const float inv_nw = 1.0f / static_cast<float>(min(cols - w_in * kCols, kCols)), inv_n = 1.0f / static_cast<float>(cols);
+  // columns of the warp that this lane joins below
+  const float n_l = lane < warps ? static_cast<float>(min(cols - lane * kCols, kCols)) : 0.0f;
+  const T* const x0 = static_cast<const T*>(p.x) + (left > 0 ? c : 0);
+  // this thread's 16 bytes of piece j in stage s: slot + (s * J + j) * 512
+  uint8_t* const slot = smem + ring + (warp * stages * J * 32 + lane) * 16;
+  float* const ws = reinterpret_cast<float*>(smem);
+  float* const bs = ws + warps * kCols;
 
-  auto issue = [&](int64_t row, int s) {
+  auto issue = [&](int row, int s) {
     if constexpr (VECTOR) {
-      if (row < p.rows) {
-        const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+      if (row < rows) {
+        const T* x = x0 + static_cast<int64_t>(row) * ldx;
+        const uint32_t to = smem_u32(slot) + s * J * 512;
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const int c = P::col(base + j * P::WC, lane, 0);
-          cp_async<16>(slot + (s * J + j) * 512, x + (c < cols ? c : 0), c < cols);
-        }
+        for (int j = 0; j < J; ++j) cp_async<16>(to + j * 512, left > j * P::WC ? x + j * P::WC : x, left > j * P::WC);
       }
       cp_async_commit();
     }
   };
   pdl_wait();
   pdl_launch_dependents();
-  int64_t row = static_cast<int64_t>(blockIdx.x) * n_groups + group;
+  int row = blockIdx.x * n_groups + group;
+  start_param<P, V>(p.w, p.w_f32, cols, warps, 1.0f, ws);
+  start_param<P, V>(p.b, p.w_f32, cols, warps, 0.0f, bs);
+  cp_async_commit();
   for (int s = 0; s < stages; ++s) issue(row + s * step, s);
-  // weight and bias of this thread's columns, kept for all its rows (rows of more than kBlockWarps warps
-  // have 64 registers a thread and read them again each time)
-  float w[WIDE ? 1 : J][E], b[WIDE ? 1 : J][E];
-  if constexpr (!WIDE) {
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      load_param<P, VECTOR>(p.w, p.w_f32, base + j * P::WC, lane, cols, 1.0f, w[j]);
-      load_param<P, VECTOR>(p.b, p.w_f32, base + j * P::WC, lane, cols, 0.0f, b[j]);
-    }
-  }
-  for (int s = 0, buf = 0; row < p.rows; row += step, s = s + 1 == stages ? 0 : s + 1, buf ^= 1) {
+  cp_async_wait_oldest(VECTOR ? stages + 1 : 1);
+  settle_param<P, V>(p.w, p.w_f32, warps, ws);
+  settle_param<P, V>(p.b, p.w_f32, warps, bs);
+  __syncthreads();
+  for (int s = 0, buf = 0; row < rows; row += step, buf ^= 1) {
     float x[J][E];
     if constexpr (VECTOR) {
       cp_async_wait_oldest(stages);
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-        P::unpack(*reinterpret_cast<const uint4*>(ring + (slot - smem_u32(ring)) + (s * J + j) * 512), x[j]);
+      for (int j = 0; j < J; ++j) P::unpack(*reinterpret_cast<const uint4*>(slot + (s * J + j) * 512), x[j]);
     } else {
-      const T* in = static_cast<const T*>(p.x) + row * p.ldx;
+      const T* in = x0 + static_cast<int64_t>(row) * ldx;
 #pragma unroll
-      for (int j = 0; j < J; ++j) P::load(in, base + j * P::WC, lane, cols, x[j]);
+      for (int j = 0; j < J; ++j) P::load(in + j * P::WC, left - j * P::WC, x[j]);
     }
     float2 acc = {0.0f, 0.0f};
 #pragma unroll
@@ -159,12 +155,12 @@ __global__ void __launch_bounds__((WIDE ? kNormWarpsMost : kBlockWarps) * 32)
       for (int i = 0; i < E; i += 2) {
         float2 d = add2(make_float2(x[j][i], x[j][i + 1]), both(-mean));
         if (!VECTOR) {
-          if (!P::valid(base + j * P::WC, lane, cols, i)) d.x = 0.0f;
-          if (!P::valid(base + j * P::WC, lane, cols, i + 1)) d.y = 0.0f;
+          if (!P::has(left - j * P::WC, i)) d.x = 0.0f;
+          if (!P::has(left - j * P::WC, i + 1)) d.y = 0.0f;
         }
         sq = fma2(d, d, sq);
       }
-      if (!VECTOR || P::valid(base + j * P::WC, lane, cols, 0)) acc = add2(acc, sq);
+      if (!VECTOR || left > j * P::WC) acc = add2(acc, sq);
     }
     float m2 = warp_sum(acc.x + acc.y);
     if (warps > 1) {
@@ -172,10 +168,9 @@ __global__ void __launch_bounds__((WIDE ? kNormWarpsMost : kBlockWarps) * 32)
       group_sync(group, warps);
       // lane l joins warp l's part of the row (the other buffer is written before this one is reused)
       const float2 v = lane < warps ? red[buf][group * warps + lane] : make_float2(0.0f, 0.0f);
-      const float n_l = lane < warps ? static_cast<float>(min(cols - lane * kNormWarpCols, kNormWarpCols)) : 0.0f;
       mean = warp_sum(n_l * v.x) * inv_n;
       const float d = v.x - mean;
-      m2 = warp_sum(lane < warps ? fmaf(n_l * d, d, v.y) : 0.0f);
+      m2 = warp_sum(fmaf(n_l * d, d, v.y));
     }
     const float rstd = inv_sqrt(fmaf(m2, inv_n, p.eps));
     if (w_in == 0 && lane == 0) {
@@ -183,55 +178,66 @@ __global__ void __launch_bounds__((WIDE ? kNormWarpsMost : kBlockWarps) * 32)
       if (p.rstd != nullptr) p.rstd[row] = rstd;
     }
     issue(row + stages * step, s);
+    s = s + 1 == stages ? 0 : s + 1;
+    T* const y0 = static_cast<T*>(p.y) + static_cast<int64_t>(row) * ldy + c;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int c0 = base + j * P::WC;
-      float y[E];
-      if constexpr (WIDE) {
-        load_param<P, VECTOR>(p.w, p.w_f32, c0, lane, cols, 1.0f, w[0]);
-        load_param<P, VECTOR>(p.b, p.w_f32, c0, lane, cols, 0.0f, b[0]);
-      }
-      const int k = WIDE ? 0 : j;
+      const int off = j * P::WC, rest = left - off;
+      float y[E], w[E], b[E];
+      read_param<P, V>(ws, w_in, j, lane, w);
+      read_param<P, V>(bs, w_in, j, lane, b);
 #pragma unroll
       for (int i = 0; i < E; i += 2) {
         const float2 h = mul2(add2(make_float2(x[j][i], x[j][i + 1]), both(-mean)), both(rstd));
-        const float2 v = fma2(h, make_float2(w[k][i], w[k][i + 1]), make_float2(b[k][i], b[k][i + 1]));
+        const float2 v = fma2(h, make_float2(w[i], w[i + 1]), make_float2(b[i], b[i + 1]));
         x[j][i] = h.x;
         x[j][i + 1] = h.y;
         y[i] = v.x;
         y[i + 1] = v.y;
       }
-      P::store(static_cast<T*>(p.y) + row * p.ldy, c0, lane, cols, y);
+      P::store(y0 + off, rest, y);
     }
     if (p.q != nullptr) {
-      uint8_t* const q = p.q + row * p.ldq;
-      float* const s_row = p.s + row * copies;
-      if constexpr (J == 2)
-        store_copies<P, 2>({q, q}, {s_row, s_row}, {base, base + P::WC}, lane, cols, p.e5m2, x);
-      else
-        store_copies<P, 4>({q, q, q, q}, {s_row, s_row, s_row, s_row}, {base, base + P::WC, base + 2 * P::WC, base + 3 * P::WC},
-                           lane, cols, p.e5m2, x);
+      constexpr int N = J < 4 ? J : 4;
+      uint8_t* const q = p.q + static_cast<int64_t>(row) * ldq + c;
+      float* const s8 = p.s + static_cast<int64_t>(row) * groups8 + c / 128;
+#pragma unroll
+      for (int j = 0; j < J; j += N) {
+        float v[N][E];
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[k][i] = x[j + k][i];
+        store_copies<P, N>(q + j * P::WC, s8 + j * P::WC / 128, lane, left - j * P::WC, p.e5m2, v);
+      }
     }
   }
 }
 
+template <typename T, bool VECTOR, int V>
+cudaError_t run_norm(const NormParams& p, int num_sms, cudaStream_t s) {
+  const NormPlan n = norm_plan(p.rows, p.cols, 32 * V, kBlockWarps, 2, VECTOR ? 32 * V * static_cast<int>(sizeof(T)) : 0, num_sms);
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = ensure_smem_limit(k_norm<T, VECTOR, V>, kNormSmem, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_norm<T, VECTOR, V>, dim3(n.blocks), dim3(static_cast<unsigned>(n.warps * n.groups * 32)), n.smem, s, 1, p,
+                    n.warps, n.stages, n.ring);
+}
+
+// 32 values a lane halve what a row costs besides its values (sums over lanes and warps,
+// addresses); 16 where that would leave lanes empty (rows of up to 512 columns) or where a row's
+// latency counts and there are warps to spare (no more rows than SMs).
 template <typename T, bool VECTOR>
 cudaError_t run_norm(const NormParams& p, int num_sms, cudaStream_t s) {
-  // copies of the rows in flight: 16 columns a lane
-  const NormPlan n = norm_plan(p.rows, p.cols, kBlockWarps, VECTOR ? kNormWarpCols * static_cast<int>(sizeof(T)) : 0, num_sms);
-  static std::atomic<bool> done[2][kMaxDevices];
-  const dim3 block(static_cast<unsigned>(n.warps * n.groups * 32));
-  auto kernel = n.wide ? k_norm<T, VECTOR, true> : k_norm<T, VECTOR, false>;
-  const cudaError_t e = ensure_smem_limit(kernel, kNormSmem, done[n.wide]);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(n.blocks), block, n.smem, s, 1, p, n.warps, n.stages);
+  if (p.cols <= 512 || (p.rows <= num_sms && p.cols <= kBlockWarps * 512)) return run_norm<T, VECTOR, 16>(p, num_sms, s);
+  return run_norm<T, VECTOR, 32>(p, num_sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_norm(const NormParams& p, int num_sms, cudaStream_t s) {
   const int64_t size = p.f32 ? 4 : 2;
-  if (p.cols > kNormWarpsMost * kNormWarpCols) {
+  if (p.cols > kMostCols) {
     const int64_t cap = static_cast<int64_t>(num_sms) * 8;
     const dim3 grid(static_cast<unsigned>(p.rows < cap ? p.rows : cap));
     return p.f32 ? launch_pdl(k_norm_any<float>, grid, dim3(kThreads), 0, s, 1, p)

@@ -1,6 +1,6 @@
 // norm.cuh -- how the layer norm kernels divide rows: a group of `warps` warps holds one row at
-// a time, 512 columns a warp and 16 values a lane, and walks the rows grid-wide.  A block holds as
-// many groups as its warps allow (24 forward, 16 backward: what fits an SM's registers).
+// a time, each warp a fixed number of its columns, and walks the rows grid-wide.  A block holds
+// as many groups as its warps allow (what fits an SM's registers), and there is a block an SM.
 // The next rows of each group are on their way into shared memory by asynchronous copies
 // (every thread copies the bytes it will read itself, so no barrier guards them).
 #pragma once
@@ -9,10 +9,8 @@
 
 namespace fp8q {
 
-constexpr int kNormWarpCols = 512;
-constexpr int kNormWarpsMost = 32;    // of a row: 16384 columns
 constexpr int kNormStages = 4;        // most rows in flight a group
-constexpr int kNormSmem = 200 * 1024; // shared memory for them
+constexpr int kNormSmem = 220 * 1024; // dynamic shared memory of a block: those rows and the parameters
 
 // How a launch divides its rows (host side).
 struct NormPlan {
@@ -20,35 +18,27 @@ struct NormPlan {
   int groups;       // rows a block has at a time
   int stages;       // rows in flight a group
   int blocks;
-  bool wide;        // rows of more warps than a block of the usual kernel has
+  int ring;         // where the rows in flight start in shared memory
   size_t smem;
 };
-// block_warps: warps of a block of the usual kernel; stage_bytes: shared memory of one warp's
-// piece of one row
-inline NormPlan norm_plan(int64_t rows, int64_t cols, int block_warps, int stage_bytes, int num_sms) {
+// warp_cols: columns of a warp; block_warps: most warps of a block; params: parameter vectors kept
+// in shared memory in binary32; stage_bytes: shared memory of one warp's part of one row
+inline NormPlan norm_plan(int64_t rows, int64_t cols, int warp_cols, int block_warps, int params, int stage_bytes, int num_sms) {
   NormPlan n{};
-  n.warps = static_cast<int>((cols + kNormWarpCols - 1) / kNormWarpCols);
-  n.wide = n.warps > block_warps;
-  n.groups = n.wide ? 1 : block_warps / n.warps;
+  n.warps = static_cast<int>((cols + warp_cols - 1) / warp_cols);
+  n.groups = n.warps < block_warps ? block_warps / n.warps : 1;
   if (n.warps > 1 && n.groups > 15) n.groups = 15;   // a named barrier a group, 1..15
   // few rows: spread over the SMs first
   const int64_t per_sm = (rows + num_sms - 1) / num_sms;
   if (n.groups > per_sm) n.groups = static_cast<int>(per_sm);
   const int64_t stage = static_cast<int64_t>(stage_bytes) * n.warps * n.groups;
-  int64_t s = stage > 0 ? kNormSmem / stage : 1;
+  n.ring = params * n.warps * warp_cols * 4;
+  int64_t s = stage > 0 ? (kNormSmem - n.ring) / stage : 1;
   n.stages = static_cast<int>(s < 1 ? 1 : (s > kNormStages ? kNormStages : s));
   const int64_t want = (rows + n.groups - 1) / n.groups;
   n.blocks = static_cast<int>(want < num_sms ? want : num_sms);
-  n.smem = static_cast<size_t>(stage * n.stages);
+  n.smem = static_cast<size_t>(n.ring + stage * n.stages);
   return n;
-}
-
-// Barrier of one group's warps (nothing for a group of one warp).
-__device__ __forceinline__ void group_sync(int group, int warps) {
-  if (warps == 1)
-    __syncwarp();
-  else
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
 }
 
 template <int BYTES>
@@ -60,9 +50,70 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool val
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// A parameter vector (`none` without one; past its end anything finite) in shared memory as
+// binary32, in the order in which a warp's lanes read their pieces, four values a lane: a quad.
+// The block starts the copies here, ahead of its first rows', and finishes them (of bf16: widens
+// them) in settle_param once its own copies have arrived; a barrier follows.
+template <typename P, int V>
+__device__ __forceinline__ int quad_col(int i) {   // first column of quad i
+  constexpr int Q = P::E / 4, J = V / P::E;
+  const int l = i & 31, q = (i >> 5) % Q, j = (i >> 5) / Q % J, w = (i >> 5) / (Q * J);
+  return w * 32 * V + j * P::WC + P::first(l) + P::at(q * 4);
+}
+template <typename P, int V>
+__device__ __forceinline__ void start_param(const void* vec, bool f32, int cols, int warps, float none, float* to) {
+  // every block reads the whole vector: each starts at another place of it
+  const int n = warps * 8 * V, turn = static_cast<int>(blockIdx.x) * 97 % (n / 32) * 32;
+  for (int k = threadIdx.x; k < n; k += blockDim.x) {
+    const int i = k + turn < n ? k + turn : k + turn - n, c = quad_col<P, V>(i);
+    if (vec == nullptr) {
+      reinterpret_cast<float4*>(to)[i] = make_float4(none, none, none, none);
+    } else if (P::kVector) {   // cols is a multiple of 4 and the vector 16-byte aligned
+      const int from = c < cols ? c : 0;
+      if (f32)
+        cp_async<16>(smem_u32(to + 4 * i), static_cast<const float*>(vec) + from, c < cols);
+      else
+        cp_async<8>(smem_u32(to + 4 * i), static_cast<const uint16_t*>(vec) + from, c < cols);
+    } else {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) to[4 * i + m] = c + P::at(m) < cols ? ld_param(vec, f32, c + P::at(m)) : 0.0f;
+    }
+  }
+}
+template <typename P, int V>
+__device__ __forceinline__ void settle_param(const void* vec, bool f32, int warps, float* at) {
+  if (vec == nullptr || f32 || !P::kVector) return;
+  const int n = warps * 8 * V, turn = static_cast<int>(blockIdx.x) * 97 % (n / 32) * 32;
+  for (int k = threadIdx.x; k < n; k += blockDim.x) {
+    const int i = k + turn < n ? k + turn : k + turn - n;
+    const uint2 u = *reinterpret_cast<const uint2*>(at + 4 * i);
+    reinterpret_cast<float4*>(at)[i] = make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
+  }
+}
+// the lane's values of piece j of warp w
+template <typename P, int V>
+__device__ __forceinline__ void read_param(const float* from, int w, int j, int lane, float (&v)[P::E]) {
+#pragma unroll
+  for (int q = 0; q < P::E / 4; ++q) {
+    const float4 u = *reinterpret_cast<const float4*>(from + (w * 32 * V + j * 32 * P::E + q * 128 + lane * 4));
+    v[4 * q] = u.x;
+    v[4 * q + 1] = u.y;
+    v[4 * q + 2] = u.z;
+    v[4 * q + 3] = u.w;
+  }
+}
+
+// Barrier of one group's warps (warps > 1).
+__device__ __forceinline__ void group_sync(int group, int warps) {
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
+}
+
 // until at most `stages` - 1 of the committed copies are outstanding
 __device__ __forceinline__ void cp_async_wait_oldest(int stages) {
-  if (stages == 4)
+  if (stages == 5)
+    asm volatile("cp.async.wait_group 4;" ::: "memory");
+  else if (stages == 4)
     asm volatile("cp.async.wait_group 3;" ::: "memory");
   else if (stages == 3)
     asm volatile("cp.async.wait_group 2;" ::: "memory");

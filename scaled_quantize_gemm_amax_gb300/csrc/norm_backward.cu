@@ -14,7 +14,7 @@ namespace fp8q {
 
 namespace {
 
-constexpr int kBlockWarps = 16;   // 128 registers a thread
+constexpr int kMostCols = 16384;   // of a row held in registers
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
@@ -98,78 +98,94 @@ __global__ void __launch_bounds__(kThreads) k_norm_partial_any(const NormBwdPara
   out[p.cols + c] = db;
 }
 
-// Rows of up to 16384 columns.  WIDE, rows of more than kBlockWarps warps: 64 registers a thread
-// hold the column sums and little else, so dy, xh and w are fetched a second time for dx.
-template <typename T, bool VECTOR, bool CODES, bool WIDE>
-__global__ void __launch_bounds__((WIDE ? kNormWarpsMost : kBlockWarps) * 32)
-    k_norm_backward(const NormBwdParams p, const int warps, const int stages) {
+// Rows of up to kMostCols columns, V values a lane.  The column sums take 2 V of a thread's
+// registers and g V; xh is read from shared memory twice, before and after the row's sums are
+// known.
+template <typename T, bool VECTOR, bool CODES, int V, int BLOCK_WARPS>
+__global__ void __launch_bounds__(BLOCK_WARPS * 32)
+    k_norm_backward(const NormBwdParams p, const int warps, const int stages, const int ring) {
   using P = Piece<T, VECTOR>;
-  constexpr int E = P::E, J = 16 / E, H = E / 2;
+  constexpr int E = P::E, J = V / E, H = E / 2, kGroups = V / 4;   // kGroups: of 128 columns in a warp's part
   constexpr int kIn = CODES ? E : 16;                    // a lane's bytes of x or the codes in one piece
   constexpr int kPiece = 32 * (16 + kIn);                // a warp's bytes of dy and x / codes in one piece
-  constexpr int kStage = J * kPiece + 32;                // and in one row, with 4 multipliers, rstd and mean
-  extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 red[2][kNormWarpsMost];
+  constexpr int kStage = J * kPiece + 48;                // and in one row, with its multipliers, rstd and mean
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float red[2][2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / warps, w_in = warp - group * warps;
-  const int n_groups = (blockDim.x >> 5) / warps;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * n_groups;
-  const int cols = static_cast<int>(p.cols), base = w_in * kNormWarpCols, copies = (cols + 127) / 128;
+  const int n_groups = (blockDim.x >> 5) / warps, step = gridDim.x * n_groups;
+  const int rows = static_cast<int>(p.rows), cols = static_cast<int>(p.cols), groups8 = (cols + 127) / 128;
+  const int lddy = static_cast<int>(p.lddy), ldx = static_cast<int>(p.ldx), ldq = static_cast<int>(p.ldq),
+            lddx = static_cast<int>(p.lddx);
+  // this lane's first column and the columns from there to the row's end
+  const int c = w_in * 32 * V + P::first(lane), left = cols - c, c_in = left > 0 ? c : 0;
   const float inv_n = 1.0f / static_cast<float>(cols);
-  uint8_t* const mine = ring + warp * stages * kStage;
+  uint8_t* const mine = smem + ring + warp * stages * kStage;
+  float* const ws = reinterpret_cast<float*>(smem);
+  const T* const dy0 = static_cast<const T*>(p.dy) + c_in;
+  const T* const x0 = static_cast<const T*>(p.x) + c_in;
+  const uint8_t* const q0 = p.q + c_in;
 
-  // row `row` into stage s: every lane its own bytes of dy and x / codes; lanes 0..5 the warp's
-  // multipliers, rstd and mean
-  auto issue = [&](int64_t row, int s) {
+  // row `row` into stage s: every lane its own bytes of dy and x / codes; the first lanes
+  // the warp's multipliers, rstd and mean
+  auto issue = [&](int row, int s) {
     if constexpr (VECTOR) {
-      if (row < p.rows) {
-        const uint32_t at = smem_u32(mine + s * kStage);
-        const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
+      if (row < rows) {
+        const uint32_t to = smem_u32(mine) + s * kStage;
+        const T* dy = dy0 + static_cast<int64_t>(row) * lddy;
+        const T* x = x0 + static_cast<int64_t>(row) * ldx;
+        const uint8_t* q = q0 + static_cast<int64_t>(row) * ldq;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-          const int c = P::col(base + j * P::WC, lane, 0), c_in = c < cols ? c : 0;
-          cp_async<16>(at + j * kPiece + lane * 16, dy + c_in, c < cols);
+          const bool in = left > j * P::WC;
+          const int off = in ? j * P::WC : 0;
+          cp_async<16>(to + j * kPiece + lane * 16, dy + off, in);
           if constexpr (CODES)
-            cp_async<kIn>(at + j * kPiece + 512 + lane * kIn, p.q + row * p.ldq + c_in, c < cols);
+            cp_async<kIn>(to + j * kPiece + 512 + lane * kIn, q + off, in);
           else
-            cp_async<16>(at + j * kPiece + 512 + lane * 16, static_cast<const T*>(p.x) + row * p.ldx + c_in, c < cols);
+            cp_async<16>(to + j * kPiece + 512 + lane * 16, x + off, in);
         }
-        const int g = base / 128 + lane;
-        const float* scalar = lane == 4 ? p.rstd + row : p.mean + row;
-        bool want = lane == 4 || (lane == 5 && !CODES);
-        if (CODES && lane < 4) {
-          scalar = p.s + row * copies + (g < copies ? g : 0);
-          want = g < copies;
+        const float* scalar = (lane == kGroups ? p.rstd : p.mean) + row;
+        bool want = lane == kGroups || (lane == kGroups + 1 && !CODES);
+        if (CODES && lane < kGroups) {
+          const int g = w_in * kGroups + lane;
+          want = g < groups8;
+          scalar = p.s + static_cast<int64_t>(row) * groups8 + (want ? g : 0);
         }
-        if (want) cp_async<4>(at + J * kPiece + lane * 4, scalar, true);
+        if (want) cp_async<4>(to + J * kPiece + lane * 4, scalar, true);
       }
       cp_async_commit();
     }
   };
-  // dy and xh of piece j of the row in stage s (or, unaligned, of row `row` itself).  Past the
-  // row's end dy is 0; xh is finite there unless the row's scalars are not.
-  auto fetch = [&](int64_t row, int s, int j, float rstd, float mean, float (&dy)[E], float (&xh)[E]) {
-    const int c0 = base + j * P::WC;
-    if constexpr (VECTOR) {
-      const uint8_t* at = mine + s * kStage + j * kPiece;
-      P::unpack(*reinterpret_cast<const uint4*>(at + lane * 16), dy);
-      if constexpr (CODES) {
-        const float* mult = reinterpret_cast<const float*>(mine + s * kStage + J * kPiece);
-        // the codes past the row's end are 0, and their multiplier may be anything
-        const float m = P::valid(c0, lane, cols, 0) ? mult[(j * P::WC + lane * E) / 128] : 0.0f;
-        P::decode(P::read_codes(at + 512 + lane * kIn), m, p.e5m2, xh);
+  // what piece j of a row holds beside dy: the codes' values and their multiplier, or x - mean
+  // and rstd; xh is their product.  Past the row's end dy is 0, and these are finite unless the
+  // row's own scalars are not.
+  auto fetch = [&](int row, int s, int j, float rstd, float mean, float (&h)[E]) -> float {
+    const int rest = left - j * P::WC;
+    if constexpr (CODES) {
+      float m;
+      typename P::Codes k;
+      if constexpr (VECTOR) {
+        k = P::read_codes(mine + s * kStage + j * kPiece + 512 + lane * kIn);
+        // past the row's end the codes are 0, and the multiplier was not copied
+        m = rest > 0 ? reinterpret_cast<const float*>(mine + s * kStage + J * kPiece)[(j * P::WC + P::first(lane)) / 128] : 0.0f;
       } else {
-        P::unpack(*reinterpret_cast<const uint4*>(at + 512 + lane * 16), xh);
+        k = P::load_codes(q0 + static_cast<int64_t>(row) * ldq + j * P::WC, rest);
+        m = rest > 0 ? __ldg(p.s + static_cast<int64_t>(row) * groups8 + (c + j * P::WC) / 128) : 0.0f;
       }
+      P::decode(k, p.e5m2, h);
+      return m;
     } else {
-      P::load(static_cast<const T*>(p.dy) + row * p.lddy, c0, lane, cols, dy);
-      if constexpr (CODES)
-        P::decode(P::load_codes(p.q + row * p.ldq, c0, lane, cols), P::load_multiplier(p.s + row * copies, c0, lane, cols), p.e5m2, xh);
+      if constexpr (VECTOR)
+        P::unpack(*reinterpret_cast<const uint4*>(mine + s * kStage + j * kPiece + 512 + lane * 16), h);
       else
-        P::load(static_cast<const T*>(p.x) + row * p.ldx, c0, lane, cols, xh);
-    }
-    if constexpr (!CODES) {
+        P::load(x0 + static_cast<int64_t>(row) * ldx + j * P::WC, rest, h);
 #pragma unroll
-      for (int i = 0; i < E; ++i) xh[i] = (xh[i] - mean) * rstd;
+      for (int i = 0; i < E; i += 2) {
+        const float2 d = add2(make_float2(h[i], h[i + 1]), both(-mean));
+        h[i] = d.x;
+        h[i + 1] = d.y;
+      }
+      return rstd;
     }
   };
 
@@ -180,159 +196,213 @@ __global__ void __launch_bounds__((WIDE ? kNormWarpsMost : kBlockWarps) * 32)
   for (int j = 0; j < J; ++j)
 #pragma unroll
     for (int i = 0; i < H; ++i) dw[j][i] = db[j][i] = make_float2(0.0f, 0.0f);
-  int64_t row = static_cast<int64_t>(blockIdx.x) * n_groups + group;
+  int row = blockIdx.x * n_groups + group;
+  start_param<P, V>(p.w, p.w_f32, cols, warps, 1.0f, ws);
+  cp_async_commit();
   for (int s = 0; s < stages; ++s) issue(row + s * step, s);
-  float w[WIDE ? 1 : J][E];
-  if constexpr (!WIDE) {
-#pragma unroll
-    for (int j = 0; j < J; ++j) load_param<P, VECTOR>(p.w, p.w_f32, base + j * P::WC, lane, cols, 1.0f, w[j]);
-  }
-  for (int s = 0, buf = 0; row < p.rows; row += step, s = s + 1 == stages ? 0 : s + 1, buf ^= 1) {
+  cp_async_wait_oldest(VECTOR ? stages + 1 : 1);
+  settle_param<P, V>(p.w, p.w_f32, warps, ws);
+  __syncthreads();
+  for (int s = 0, buf = 0; row < rows; row += step, buf ^= 1) {
     float rstd, mean = 0.0f;
     if constexpr (VECTOR) {
       cp_async_wait_oldest(stages);
       __syncwarp();   // the row's scalars were copied by other lanes
       const float* scalars = reinterpret_cast<const float*>(mine + s * kStage + J * kPiece);
-      rstd = scalars[4];
-      if (!CODES) mean = scalars[5];
+      rstd = scalars[kGroups];
+      if (!CODES) mean = scalars[kGroups + 1];
     } else {
       rstd = __ldg(p.rstd + row);
       if (!CODES) mean = __ldg(p.mean + row);
     }
-    float dy[WIDE ? 1 : J][E], xh[WIDE ? 1 : J][E];
-    float2 s1 = {0.0f, 0.0f}, s2 = {0.0f, 0.0f};
+    float2 g[J][H], s1 = {0.0f, 0.0f}, s2 = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      constexpr bool kOne = WIDE;
-      const int k = kOne ? 0 : j;
-      if constexpr (WIDE) load_param<P, VECTOR>(p.w, p.w_f32, base + j * P::WC, lane, cols, 1.0f, w[0]);
-      fetch(row, s, j, rstd, mean, dy[k], xh[k]);
+      float d[E], h[E], w[E];
+      if constexpr (VECTOR)
+        P::unpack(*reinterpret_cast<const uint4*>(mine + s * kStage + j * kPiece + lane * 16), d);
+      else
+        P::load(dy0 + static_cast<int64_t>(row) * lddy + j * P::WC, left - j * P::WC, d);
+      const float2 m = both(fetch(row, s, j, rstd, mean, h));
+      read_param<P, V>(ws, w_in, j, lane, w);
 #pragma unroll
       for (int i = 0; i < H; ++i) {
-        const float2 d = {dy[k][2 * i], dy[k][2 * i + 1]}, h = {xh[k][2 * i], xh[k][2 * i + 1]};
-        const float2 g = mul2(d, make_float2(w[k][2 * i], w[k][2 * i + 1]));
-        dw[j][i] = fma2(d, h, dw[j][i]);
-        db[j][i] = add2(db[j][i], d);
-        s1 = add2(s1, g);
-        s2 = fma2(g, h, s2);
+        const float2 dy = {d[2 * i], d[2 * i + 1]}, xh = mul2(make_float2(h[2 * i], h[2 * i + 1]), m);
+        g[j][i] = mul2(dy, make_float2(w[2 * i], w[2 * i + 1]));
+        dw[j][i] = fma2(dy, xh, dw[j][i]);
+        db[j][i] = add2(db[j][i], dy);
+        s1 = add2(s1, g[j][i]);
+        s2 = fma2(g[j][i], xh, s2);
       }
     }
-    float c1 = warp_sum(s1.x + s1.y), c2 = warp_sum(s2.x + s2.y);
+    // both sums over the warp: the lower half of its lanes takes c1 and the upper half c2
+    const float a = s1.x + s1.y, b = s2.x + s2.y;
+    float v = (lane < 16 ? a : b) + __shfl_xor_sync(0xFFFFFFFFu, lane < 16 ? b : a, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     if (warps > 1) {
-      if (lane == 0) red[buf][warp] = make_float2(c1, c2);
+      if ((lane & 15) == 0) red[buf][lane >> 4][warp] = v;
       group_sync(group, warps);
-      // the other buffer is written before this one is reused
-      const float2 v = lane < warps ? red[buf][group * warps + lane] : make_float2(0.0f, 0.0f);
-      c1 = warp_sum(v.x);
-      c2 = warp_sum(v.y);
+      // lane l of a half joins warps l and l + 16 (the other buffer is written before this one is reused)
+      const int l = lane & 15;
+      const float* part = red[buf][lane >> 4] + group * warps;
+      v = l < warps ? part[l] : 0.0f;
+      if (BLOCK_WARPS > 16 && l + 16 < warps) v += part[l + 16];
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     }
-    const float2 m1 = both(-c1 * inv_n), m2 = both(-c2 * inv_n), r = both(rstd);
+    const float c1 = __shfl_sync(0xFFFFFFFFu, v, 0) * inv_n, c2 = __shfl_sync(0xFFFFFFFFu, v, 16) * inv_n;
+    // dx = r g - r c1 - (r c2) xh
+    const float2 r = both(rstd), k1 = both(-rstd * c1);
+    const float k2 = -rstd * c2;
+    T* const dx0 = static_cast<T*>(p.dx) + static_cast<int64_t>(row) * lddx + c;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      constexpr bool kOne = WIDE;
-      const int k = kOne ? 0 : j;
-      if constexpr (WIDE) {
-        load_param<P, VECTOR>(p.w, p.w_f32, base + j * P::WC, lane, cols, 1.0f, w[0]);
-        fetch(row, s, j, rstd, mean, dy[0], xh[0]);
-      }
-      float out[E];
+      float h[E], out[E];
+      const float2 m = both(k2 * fetch(row, s, j, rstd, mean, h));
 #pragma unroll
       for (int i = 0; i < H; ++i) {
-        const float2 d = {dy[k][2 * i], dy[k][2 * i + 1]}, h = {xh[k][2 * i], xh[k][2 * i + 1]};
-        const float2 v = mul2(r, fma2(h, m2, fma2(d, make_float2(w[k][2 * i], w[k][2 * i + 1]), m1)));
-        out[2 * i] = v.x;
-        out[2 * i + 1] = v.y;
+        const float2 o = fma2(make_float2(h[2 * i], h[2 * i + 1]), m, fma2(g[j][i], r, k1));
+        out[2 * i] = o.x;
+        out[2 * i + 1] = o.y;
       }
-      P::store(static_cast<T*>(p.dx) + row * p.lddx, base + j * P::WC, lane, cols, out);
+      P::store(dx0 + j * P::WC, left - j * P::WC, out);
     }
     if constexpr (VECTOR) __syncwarp();   // all lanes have read the stage's scalars
     issue(row + stages * step, s);
+    s = s + 1 == stages ? 0 : s + 1;
   }
   if (p.dw == nullptr && p.db == nullptr) return;
   // the block's groups joined pairwise in shared memory (the ring is free: every copy was waited for)
   __syncthreads();
-  float2* join = reinterpret_cast<float2*>(ring);
+  float2* join = reinterpret_cast<float2*>(smem + ring);
   for (int n = n_groups; n > 1;) {
     const int half = (n + 1) / 2;
     if (group >= half && group < n) {
-      float2* out = join + ((group - half) * warps + w_in) * 512 + lane;
+      float2* out = join + ((group - half) * warps + w_in) * 32 * V + lane;
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int i = 0; i < H; ++i) {
           out[(j * H + i) * 32] = dw[j][i];
-          out[(j * H + i) * 32 + 256] = db[j][i];
+          out[(j * H + i) * 32 + 16 * V] = db[j][i];
         }
     }
     __syncthreads();
     if (group < n - half) {
-      const float2* in = join + (group * warps + w_in) * 512 + lane;
+      const float2* in = join + (group * warps + w_in) * 32 * V + lane;
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int i = 0; i < H; ++i) {
           dw[j][i] = add2(dw[j][i], in[(j * H + i) * 32]);
-          db[j][i] = add2(db[j][i], in[(j * H + i) * 32 + 256]);
+          db[j][i] = add2(db[j][i], in[(j * H + i) * 32 + 16 * V]);
         }
     }
     __syncthreads();
     n = half;
   }
   if (group != 0) return;
-  // one block's sums are the result; several leave partial sums
-  const bool last = gridDim.x == 1;
-  float* part = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * cols;
-  void* to_dw = last ? p.dw : part;
-  void* to_db = last ? p.db : part + cols;
-  const bool f32 = !last || p.w_f32;
+  if (gridDim.x > 1) {   // partial sums
+    float* part = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * cols + c;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      float* out = part + j * P::WC;
+      if constexpr (VECTOR) {   // cols is a multiple of 4, the workspace 16-byte aligned
+        if (left <= j * P::WC) continue;
+#pragma unroll
+        for (int i = 0; i < H; i += 2) {
+          reinterpret_cast<float4*>(out)[i / 2] = make_float4(dw[j][i].x, dw[j][i].y, dw[j][i + 1].x, dw[j][i + 1].y);
+          reinterpret_cast<float4*>(out + cols)[i / 2] = make_float4(db[j][i].x, db[j][i].y, db[j][i + 1].x, db[j][i + 1].y);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          if (!P::has(left - j * P::WC, i)) continue;
+          out[P::at(i)] = i % 2 ? dw[j][i / 2].y : dw[j][i / 2].x;
+          out[cols + P::at(i)] = i % 2 ? db[j][i / 2].y : db[j][i / 2].x;
+        }
+      }
+    }
+    return;
+  }
+  // one block's sums are the result
 #pragma unroll
   for (int j = 0; j < J; ++j)
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int c = P::col(base + j * P::WC, lane, i);
-      if (c >= cols) continue;
-      if (to_dw != nullptr) st_param(to_dw, f32, c, i % 2 ? dw[j][i / 2].y : dw[j][i / 2].x);
-      if (to_db != nullptr) st_param(to_db, f32, c, i % 2 ? db[j][i / 2].y : db[j][i / 2].x);
+      if (!P::has(left - j * P::WC, i)) continue;
+      const int at = c + j * P::WC + P::at(i);
+      if (p.dw != nullptr) st_param(p.dw, p.w_f32, at, i % 2 ? dw[j][i / 2].y : dw[j][i / 2].x);
+      if (p.db != nullptr) st_param(p.db, p.w_f32, at, i % 2 ? db[j][i / 2].y : db[j][i / 2].x);
     }
 }
 
-// The 2 * cols sums of the partial sums: a block takes 32 of them, warp k the partials k, k + 8,
-// ...; then the 8 warps' sums in order.
-__global__ void __launch_bounds__(kThreads) k_norm_params(const float* partial, int n, int64_t cols, bool f32, void* dw,
-                                                          void* db) {
-  __shared__ float part[kWarps][32];
+// The 2 * cols sums of the partial sums: a block takes 32 lanes' worth of them (four a lane where
+// cols % 4 == 0), warp k the partials k, k + 32, ...; then the 32 warps' sums in order.
+constexpr int kParamWarps = 32;
+template <int N>
+__global__ void __launch_bounds__(kParamWarps * 32) k_norm_params(const float* partial, int n, int cols, bool f32, void* dw, void* db) {
+  __shared__ float part[kParamWarps][32 * N];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * N, total = 2 * static_cast<int64_t>(cols);
   pdl_wait();
   pdl_launch_dependents();
-  float v = 0.0f;
-  if (c < 2 * cols)
-    for (int k = warp; k < n; k += kWarps) v += partial[static_cast<int64_t>(k) * 2 * cols + c];
-  part[warp][lane] = v;
-  __syncthreads();
-  if (warp != 0 || c >= 2 * cols) return;
-  v = 0.0f;
+  float v[N] = {};
+  if (c < total) {
+#pragma unroll 5
+    for (int k = warp; k < n; k += kParamWarps) {
+      const float* from = partial + k * total + c;
+      if constexpr (N == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(from);
+        v[0] += u.x, v[1] += u.y, v[2] += u.z, v[3] += u.w;
+      } else {
+        v[0] += *from;
+      }
+    }
+  }
 #pragma unroll
-  for (int k = 0; k < kWarps; ++k) v += part[k][lane];
-  void* out = c < cols ? dw : db;
-  if (out != nullptr) st_param(out, f32, c < cols ? c : c - cols, v);
+  for (int i = 0; i < N; ++i) part[warp][i * 32 + lane] = v[i];
+  __syncthreads();
+  if (warp >= N) return;
+  // warp i of the first N: value i of every lane
+  const int64_t at = c + warp;
+  if (c >= total) return;
+  float sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kParamWarps; ++k) sum += part[k][warp * 32 + lane];
+  void* out = at < cols ? dw : db;
+  if (out != nullptr) st_param(out, f32, at < cols ? at : at - cols, sum);
 }
 
-// number of partial sums left in p.partial (0: none)
-template <typename T, bool VECTOR, bool CODES>
+// *partials: number of partial sums left in p.partial (0: none)
+template <typename T, bool VECTOR, bool CODES, int V, int BLOCK_WARPS>
 cudaError_t run_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
   using P = Piece<T, VECTOR>;
-  const int stage = VECTOR ? 16 / P::E * 32 * (16 + (CODES ? P::E : 16)) + 32 : 0;
-  NormPlan n = norm_plan(p.rows, p.cols, kBlockWarps, stage, num_sms < kMaxNormPartials ? num_sms : kMaxNormPartials);
-  const size_t join = static_cast<size_t>(n.groups / 2) * n.warps * 1024 * sizeof(float);
+  const int stage = VECTOR ? V / P::E * 32 * (16 + (CODES ? P::E : 16)) + 48 : 0;
+  NormPlan n = norm_plan(p.rows, p.cols, 32 * V, BLOCK_WARPS, 1, stage, num_sms < kMaxNormPartials ? num_sms : kMaxNormPartials);
+  const size_t join = n.ring + static_cast<size_t>(n.groups / 2) * n.warps * 64 * V * sizeof(float);
   if (n.smem < join) n.smem = join;
-  static std::atomic<bool> done[2][kMaxDevices];
-  auto kernel = n.wide ? k_norm_backward<T, VECTOR, CODES, true> : k_norm_backward<T, VECTOR, CODES, false>;
-  const cudaError_t e = ensure_smem_limit(kernel, kNormSmem, done[n.wide]);
+  static std::atomic<bool> done[kMaxDevices];
+  auto kernel = k_norm_backward<T, VECTOR, CODES, V, BLOCK_WARPS>;
+  const cudaError_t e = ensure_smem_limit(kernel, kNormSmem, done);
   if (e != cudaSuccess) return e;
   *partials = n.blocks > 1 ? n.blocks : 0;
   return launch_pdl(kernel, dim3(n.blocks), dim3(static_cast<unsigned>(n.warps * n.groups * 32)), n.smem, s, 1, p, n.warps,
-                    n.stages);
+                    n.stages, n.ring);
+}
+
+template <typename T, bool VECTOR, bool CODES>
+cudaError_t run_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
+  if (p.cols <= 512) return run_norm_backward<T, VECTOR, CODES, 16, 24>(p, num_sms, s, partials);
+  if (p.cols <= 12288) return run_norm_backward<T, VECTOR, CODES, 32, 12>(p, num_sms, s, partials);
+  return run_norm_backward<T, VECTOR, CODES, 32, 16>(p, num_sms, s, partials);
+}
+
+template <typename T, bool VECTOR>
+cudaError_t run_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
+  return p.q != nullptr ? run_norm_backward<T, VECTOR, true>(p, num_sms, s, partials)
+                        : run_norm_backward<T, VECTOR, false>(p, num_sms, s, partials);
 }
 
 template <typename T>
@@ -357,20 +427,22 @@ cudaError_t launch_norm_backward(const NormBwdParams& p, int num_sms, cudaStream
   const int64_t size = p.f32 ? 4 : 2, e16 = 16 / size;
   int partials = 0;
   cudaError_t e;
-  if (p.cols > kNormWarpsMost * kNormWarpCols || p.rows == 0) {
+  if (p.cols > kMostCols || p.rows == 0) {
     e = p.f32 ? run_any<float>(p, num_sms, s, &partials) : run_any<uint16_t>(p, num_sms, s, &partials);
   } else {
     const bool vec = takes(p.dy, p.lddy, p.cols, size, 16) && takes(p.x, p.ldx, p.cols, size, 16) &&
                      takes(p.dx, p.lddx, p.cols, size, 16) && takes(p.q, p.ldq, p.cols, 1, e16) && takes(p.w, 0, 0, 1, 16);
-#define FP8Q_RUN(T, V) \
-  (p.q != nullptr ? run_norm_backward<T, V, true>(p, num_sms, s, &partials) : run_norm_backward<T, V, false>(p, num_sms, s, &partials))
-    e = p.f32 ? (vec ? FP8Q_RUN(float, true) : FP8Q_RUN(float, false))
-              : (vec ? FP8Q_RUN(uint16_t, true) : FP8Q_RUN(uint16_t, false));
-#undef FP8Q_RUN
+    if (p.f32)
+      e = vec ? run_norm_backward<float, true>(p, num_sms, s, &partials) : run_norm_backward<float, false>(p, num_sms, s, &partials);
+    else
+      e = vec ? run_norm_backward<uint16_t, true>(p, num_sms, s, &partials)
+              : run_norm_backward<uint16_t, false>(p, num_sms, s, &partials);
   }
   if (e != cudaSuccess || partials == 0 || (p.dw == nullptr && p.db == nullptr)) return e;
-  return launch_pdl(k_norm_params, dim3(static_cast<unsigned>((2 * p.cols + 31) / 32)), dim3(kThreads), 0, s, 1,
-                    static_cast<const float*>(p.partial), partials, p.cols, p.w_f32 != 0, p.dw, p.db);
+  const int quad = p.cols % 4 == 0 ? 4 : 1;
+  return launch_pdl(quad == 4 ? k_norm_params<4> : k_norm_params<1>,
+                    dim3(static_cast<unsigned>((2 * p.cols / quad + 31) / 32)), dim3(kParamWarps * 32), 0, s, 1,
+                    static_cast<const float*>(p.partial), partials, static_cast<int>(p.cols), p.w_f32 != 0, p.dw, p.db);
 }
 
 }  // namespace fp8q

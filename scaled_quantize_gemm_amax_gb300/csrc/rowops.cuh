@@ -1,6 +1,6 @@
 // rowops.cuh -- device helpers of the operators that work on rows of a matrix (layer norm,
-// gated activation, expert dispatch): element loads and stores of either data type, block
-// sums, and the 8-bit copy of 128 consecutive columns of a row.
+// gated activation, expert dispatch): how a warp holds a piece of a row, and the 8-bit copy of
+// 128 consecutive columns of a row.
 //
 // bf16 elements are held as their 16-bit patterns; all arithmetic is binary32.
 #pragma once
@@ -13,7 +13,7 @@ namespace fp8q {
 
 __device__ __forceinline__ float ld_elem(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
 __device__ __forceinline__ float ld_elem(const float* p) { return *p; }
-// a parameter vector (weight, bias) of either type
+// element i of a parameter vector (weight, bias) of either type
 __device__ __forceinline__ float ld_param(const void* p, bool f32, int64_t i) {
   return f32 ? static_cast<const float*>(p)[i] : ld_elem(static_cast<const uint16_t*>(p) + i);
 }
@@ -36,11 +36,6 @@ __device__ __forceinline__ void st_param(void* p, bool f32, int64_t i, float v) 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
 }
 
@@ -72,31 +67,44 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// max(|a|, |b|, |c|), NaN ignored (all NaN: NaN)
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // ------------------------------------------------------------------ a warp's piece of a row
 // How a warp holds WC consecutive columns of a row, E values a lane.
 //   VECTOR      lane l holds E = 16 bytes' worth of consecutive columns: one 16-byte access a
 //               lane.  Needs a 16-byte aligned row and cols % E == 0 (a lane is all in or all out).
 //   otherwise   lane l holds columns l, l + 32, l + 64, l + 96: consecutive lanes on consecutive
 //               columns, so any element alignment coalesces.
+// A lane works from its own first column, first(lane) after the piece's: pointers point there,
+// and `left` is the number of columns from there to the row's end (possibly none).
 // 128-column groups (the 8-bit copy's) never cross lanes' bounds: kGroupLanes lanes hold one.
 template <typename T, bool VECTOR>
 struct Piece {
+  static constexpr bool kVector = VECTOR;
   static constexpr int E = VECTOR ? 16 / static_cast<int>(sizeof(T)) : 4;
   static constexpr int WC = 32 * E;
   static constexpr int kGroupLanes = 128 / E;
+  static constexpr int kWords = E / 4;   // of codes
 
-  __device__ static __forceinline__ int col(int c0, int lane, int i) {
-    return VECTOR ? c0 + lane * E + i : c0 + lane + 32 * i;
-  }
+  __device__ static __forceinline__ int first(int lane) { return VECTOR ? lane * E : lane; }
+  // column of value i after the lane's first
+  __device__ static __forceinline__ constexpr int at(int i) { return VECTOR ? i : 32 * i; }
+  __device__ static __forceinline__ bool has(int left, int i) { return left > (VECTOR ? 0 : 32 * i); }
+
   // v = the row's values, 0 past its end
-  __device__ static __forceinline__ void load(const T* row, int c0, int lane, int cols, float (&v)[E]) {
+  __device__ static __forceinline__ void load(const T* p, int left, float (&v)[E]) {
     if constexpr (VECTOR) {
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (col(c0, lane, 0) < cols) w = __ldg(reinterpret_cast<const uint4*>(row + col(c0, lane, 0)));
+      if (left > 0) w = __ldg(reinterpret_cast<const uint4*>(p));
       unpack(w, v);
     } else {
 #pragma unroll
-      for (int i = 0; i < E; ++i) v[i] = col(c0, lane, i) < cols ? ld_elem(row + col(c0, lane, i)) : 0.0f;
+      for (int i = 0; i < E; ++i) v[i] = has(left, i) ? ld_elem(p + at(i)) : 0.0f;
     }
   }
   __device__ static __forceinline__ void unpack(const uint4& w, float (&v)[E]) {
@@ -111,9 +119,9 @@ struct Piece {
       }
     }
   }
-  __device__ static __forceinline__ void store(T* row, int c0, int lane, int cols, const float (&v)[E]) {
+  __device__ static __forceinline__ void store(T* p, int left, const float (&v)[E]) {
     if constexpr (VECTOR) {
-      if (col(c0, lane, 0) >= cols) return;
+      if (left <= 0) return;
       uint32_t u[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -122,27 +130,59 @@ struct Piece {
         else
           u[i] = __float_as_uint(v[i]);
       }
-      *reinterpret_cast<uint4*>(row + col(c0, lane, 0)) = make_uint4(u[0], u[1], u[2], u[3]);
+      *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i)
-        if (col(c0, lane, i) < cols) st_elem(row + col(c0, lane, i), v[i]);
+        if (has(left, i)) st_elem(p + at(i), v[i]);
     }
   }
-  __device__ static __forceinline__ bool valid(int c0, int lane, int cols, int i) {
-    return VECTOR ? c0 + lane * E < cols : col(c0, lane, i) < cols;
+  // The lane's part of a parameter vector (`none` without one and past its end); `c` is the
+  // lane's first column, VECTOR: the vector is 16-byte aligned.
+  __device__ static __forceinline__ void load_param(const void* vec, bool f32, int c, int left, float none, float (&v)[E]) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = none;
+    if (vec == nullptr) return;
+    if constexpr (VECTOR) {
+      if (left <= 0) return;
+      if (f32) {
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+          const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(vec) + c) + i);
+          v[4 * i] = w.x;
+          v[4 * i + 1] = w.y;
+          v[4 * i + 2] = w.z;
+          v[4 * i + 3] = w.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(vec) + c) + i);
+          v[4 * i] = bf16lo(w.x);
+          v[4 * i + 1] = bf16hi(w.x);
+          v[4 * i + 2] = bf16lo(w.y);
+          v[4 * i + 3] = bf16hi(w.y);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (has(left, i)) v[i] = ld_param(vec, f32, c + at(i));
+    }
   }
+
+  // ---- the 8-bit copy
   // max |v| of the lane's columns (NaN ignored)
-  __device__ static __forceinline__ float amax(const float (&v)[E], int c0, int lane, int cols) {
+  __device__ static __forceinline__ float amax(const float (&v)[E], int left) {
     float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      a = VECTOR ? fmaxf(a, fabsf(v[i])) : fmaxf(a, valid(c0, lane, cols, i) ? fabsf(v[i]) : 0.0f);
-    return !VECTOR || valid(c0, lane, cols, 0) ? a : 0.0f;
+    for (int i = 0; i < E; i += 2)
+      a = max_abs3(a, VECTOR || has(left, i) ? v[i] : 0.0f, VECTOR || has(left, i + 1) ? v[i + 1] : 0.0f);
+    return left > 0 ? a : 0.0f;
   }
   // codes = satRNE(v sc)
   template <bool E5>
-  __device__ static __forceinline__ void encode(uint8_t* q_row, int c0, int lane, int cols, const float (&v)[E], float sc) {
+  __device__ static __forceinline__ void encode(uint8_t* q, int left, const float (&v)[E], float sc) {
     uint32_t u[E / 2];
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) {
@@ -150,20 +190,20 @@ struct Piece {
       u[i] = E5 ? cvt_pair_e5m2(m.x, m.y) : cvt_pair_e4m3(m.x, m.y);
     }
     if constexpr (VECTOR) {
-      if (!valid(c0, lane, cols, 0)) return;
+      if (left <= 0) return;
       if constexpr (E == 8)
-        *reinterpret_cast<uint2*>(q_row + c0 + lane * E) = make_uint2(u[0] | u[1] << 16, u[2] | u[3] << 16);
+        *reinterpret_cast<uint2*>(q) = make_uint2(__byte_perm(u[0], u[1], 0x5410), __byte_perm(u[2], u[3], 0x5410));
       else
-        *reinterpret_cast<uint32_t*>(q_row + c0 + lane * E) = u[0] | u[1] << 16;
+        *reinterpret_cast<uint32_t*>(q) = __byte_perm(u[0], u[1], 0x5410);
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i)
-        if (valid(c0, lane, cols, i)) q_row[col(c0, lane, i)] = static_cast<uint8_t>(u[i / 2] >> (8 * (i % 2)));
+        if (has(left, i)) q[at(i)] = static_cast<uint8_t>(u[i / 2] >> (8 * (i % 2)));
     }
   }
-  // The codes of a lane's columns, as they lie in memory (VECTOR) or one a byte of the word.
+  // The codes of a lane's columns, value i in byte i % 4 of word i / 4 (0 past the row's end).
   struct Codes {
-    uint32_t u[E / 4];
+    uint32_t u[kWords];
   };
   __device__ static __forceinline__ Codes read_codes(const uint8_t* q) {   // E consecutive codes at q
     Codes c;
@@ -176,40 +216,42 @@ struct Piece {
     }
     return c;
   }
-  __device__ static __forceinline__ Codes load_codes(const uint8_t* q_row, int c0, int lane, int cols) {
+  __device__ static __forceinline__ Codes load_codes(const uint8_t* q, int left) {
     Codes c = {};
     if constexpr (VECTOR) {
-      if (valid(c0, lane, cols, 0)) c = read_codes(q_row + c0 + lane * E);
+      if (left > 0) c = read_codes(q);
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i)
-        if (valid(c0, lane, cols, i)) c.u[0] |= static_cast<uint32_t>(q_row[col(c0, lane, i)]) << (8 * i);
+        if (has(left, i)) c.u[0] |= static_cast<uint32_t>(q[at(i)]) << (8 * i);
     }
     return c;
   }
-  __device__ static __forceinline__ float load_multiplier(const float* s_row, int c0, int lane, int cols) {
-    return valid(c0, lane, cols, 0) ? __ldg(s_row + col(c0, lane, 0) / 128) : 0.0f;
+  // the codes' own values
+  __device__ static __forceinline__ void decode(const Codes& c, bool e5m2, float (&v)[E]) {
+    if (e5m2) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        decode_pair(c.u[i] & 0xFFFFu, true, v[4 * i], v[4 * i + 1]);
+        decode_pair(c.u[i] >> 16, true, v[4 * i + 2], v[4 * i + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        decode_pair(c.u[i] & 0xFFFFu, false, v[4 * i], v[4 * i + 1]);
+        decode_pair(c.u[i] >> 16, false, v[4 * i + 2], v[4 * i + 3]);
+      }
+    }
   }
   // the values the codes stand for, each product rounded to binary32
-  template <bool E5>
-  __device__ static __forceinline__ void decode(const Codes& c, float s, float (&v)[E]) {
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      decode_pair(c.u[i] & 0xFFFFu, E5, v[4 * i], v[4 * i + 1]);
-      decode_pair(c.u[i] >> 16, E5, v[4 * i + 2], v[4 * i + 3]);
-    }
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const float2 m = mul2(make_float2(v[2 * i], v[2 * i + 1]), both(s));
-      v[2 * i] = m.x;
-      v[2 * i + 1] = m.y;
-    }
-  }
   __device__ static __forceinline__ void decode(const Codes& c, float s, bool e5m2, float (&v)[E]) {
-    if (e5m2)
-      decode<true>(c, s, v);
-    else
-      decode<false>(c, s, v);
+    decode(c, e5m2, v);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      const float2 m = mul2(make_float2(v[i], v[i + 1]), both(s));
+      v[i] = m.x;
+      v[i + 1] = m.y;
+    }
   }
 };
 
@@ -237,29 +279,27 @@ __device__ __forceinline__ float group_max(const float (&a)[N], int lane) {
   return m;
 }
 
-// The 8-bit copies of N pieces by the blockwise recipe's rule, codes satRNE(v FMAX / amax) and
-// multiplier 1 / (FMAX / amax) per 128 columns: piece i is v[i] at column c0[i] of the row whose
-// codes and multipliers start at q[i] and s[i].  Each lane makes the two divisions of one piece
-// only (lane % N) and the others' scales come from its neighbours: the divisions would
-// otherwise be a third of the copy's instructions.
+// The 8-bit copies of N consecutive pieces of a row by the blockwise recipe's rule, codes
+// satRNE(v FMAX / amax) and multiplier 1 / (FMAX / amax) per 128 columns.  q: the lane's first
+// code of the first piece; s: the multiplier of the lane's group there; left: as for that piece.
+// Each lane makes the two divisions of one piece only (lane % N) and has the others' scales from
+// its neighbours: the divisions would otherwise be a third of the copy's instructions.
 template <typename P, int N>
-__device__ __forceinline__ void store_copies(uint8_t* const (&q)[N], float* const (&s)[N], const int (&c0)[N], int lane,
-                                             int cols, bool e5m2, const float (&v)[N][P::E]) {
+__device__ __forceinline__ void store_copies(uint8_t* q, float* s, int lane, int left, bool e5m2, const float (&v)[N][P::E]) {
   float a[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) a[i] = P::amax(v[i], c0[i], lane, cols);
+  for (int i = 0; i < N; ++i) a[i] = P::amax(v[i], left - i * P::WC);
   const float mine = scale_from_amax(group_max<N, P::kGroupLanes>(a, lane), fmax_of(e5m2));
   const float inv = recip_rn(mine);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    // lane i of the group: its first lane's column says whether the group exists
-    const int first = P::col(c0[i], lane - i, 0);
-    if (lane % P::kGroupLanes == i && first < cols) s[i][first / 128] = inv;
+    // lane i of the group, if the group's first column is in the row
+    if (lane % P::kGroupLanes == i && left + P::first(i) > i * P::WC) s[i * (P::WC / 128)] = inv;
     const float sc = N == 1 ? mine : __shfl_sync(0xFFFFFFFFu, mine, (lane & ~(N - 1)) | i);
     if (e5m2)
-      P::template encode<true>(q[i], c0[i], lane, cols, v[i], sc);
+      P::template encode<true>(q + i * P::WC, left - i * P::WC, v[i], sc);
     else
-      P::template encode<false>(q[i], c0[i], lane, cols, v[i], sc);
+      P::template encode<false>(q + i * P::WC, left - i * P::WC, v[i], sc);
   }
 }
 
@@ -282,41 +322,6 @@ struct Walk {
     }
   }
 };
-
-// A piece of a parameter vector (`none` without one and past its end); VECTOR: 16-byte aligned.
-template <typename P, bool VECTOR>
-__device__ __forceinline__ void load_param(const void* v, bool f32, int c0, int lane, int cols, float none, float (&out)[P::E]) {
-#pragma unroll
-  for (int i = 0; i < P::E; ++i) out[i] = none;
-  if (v == nullptr) return;
-  if constexpr (VECTOR) {
-    const int c = P::col(c0, lane, 0);
-    if (c >= cols) return;
-    if (f32) {
-#pragma unroll
-      for (int i = 0; i < P::E / 4; ++i) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(v) + c) + i);
-        out[4 * i] = w.x;
-        out[4 * i + 1] = w.y;
-        out[4 * i + 2] = w.z;
-        out[4 * i + 3] = w.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < P::E / 4; ++i) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(v) + c) + i);
-        out[4 * i] = bf16lo(w.x);
-        out[4 * i + 1] = bf16hi(w.x);
-        out[4 * i + 2] = bf16lo(w.y);
-        out[4 * i + 3] = bf16hi(w.y);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < P::E; ++i)
-      if (P::col(c0, lane, i) < cols) out[i] = ld_param(v, f32, P::col(c0, lane, i));
-  }
-}
 
 // Whether a [rows, cols] matrix of `size`-byte elements, row stride ld, takes accesses of
 // `bytes` bytes throughout (null matrices do).
