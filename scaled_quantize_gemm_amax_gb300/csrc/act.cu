@@ -193,8 +193,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_act_backward(const ActBwdParams
   }
 }
 
+// More blocks than the SMs hold at once (SMs that finish early take more), but not one an item:
+// 8192x11008 gated SiLU forward / backward at 4 blocks an SM 112 / 122 us, 16: 112 / 109, 32:
+// 111 / 106, one a group of 8 pieces 118 / 108.
 dim3 grid_of(int64_t rows, int64_t cols, int64_t wc, int num_sms) {
-  const int64_t want = (rows * ((cols + wc - 1) / wc) + kWarps - 1) / kWarps, cap = static_cast<int64_t>(num_sms) * 4;
+  const int64_t want = (rows * ((cols + wc - 1) / wc) + kWarps - 1) / kWarps, cap = static_cast<int64_t>(num_sms) * 32;
   return dim3(static_cast<unsigned>(want < cap ? want : cap));
 }
 

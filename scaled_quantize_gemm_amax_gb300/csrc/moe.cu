@@ -143,34 +143,37 @@ __device__ __forceinline__ bool valid_row(int pos, int64_t capacity, uint32_t* e
   return false;
 }
 
-// What a lane has in flight: two pieces of a row, and four choices.
-constexpr int kPieces = 2;
-constexpr int kFlight = 4;
+constexpr int kPieces = 2;   // pieces of a row a warp has in flight, of each of FLIGHT choices
 
 // The choices j0 .. j0 + 31 of token t, one a lane: their rows and weights (-1 and 0 for those
-// dropped, whose weights are not read).
+// dropped, whose weights count for nothing).
 struct Choices {
-  int pos;
-  float w;
-  __device__ Choices(const int* p_pos, const float* weights, int64_t t, int k, int j0, int lane, int64_t capacity, uint32_t* err) {
-    pos = -1;
-    w = 0.0f;
-    if (j0 + lane < k) {
+  int pos = -1;
+  float w = 0.0f;
+  __device__ Choices() {}
+  __device__ Choices(const int* p_pos, const float* weights, int64_t t, int64_t tokens, int k, int j0, int lane) {
+    if (t < tokens && j0 + lane < k) {
       const int64_t at = t * k + j0 + lane;
       pos = __ldg(p_pos + at);
-      if (!valid_row(pos, capacity, err)) pos = -1;
-      if (pos >= 0) w = weights != nullptr ? __ldg(weights + at) : 1.0f;
+      w = weights != nullptr ? __ldg(weights + at) : 1.0f;
+    }
+  }
+  __device__ void check(int64_t capacity, uint32_t* err) {
+    if (!valid_row(pos, capacity, err)) {
+      pos = -1;
+      w = 0.0f;
     }
   }
 };
 
 // `warps` warps per token (a block has 8 / warps tokens at a time), each holding its pieces of
 // the token's row: rows out[pos_j] = w_j in[t], and the dots <in[t], other[pos_j]>.  The token's
-// row is read once for all its choices.  After the tokens, a warp per kZeroRows rows of `out`
-// sets those that no choice fills to zero.
+// row is read once for all its choices, and the next token's choices are fetched while this
+// one's rows move.  After the tokens, a warp per kZeroRows rows of `out` sets those that no
+// choice fills to zero.
 constexpr int kZeroRows = 4;
-template <typename T, bool VECTOR, bool DOTS>
-__global__ void __launch_bounds__(kThreads) k_scatter(const ScatterParams p, const int warps) {
+template <typename T, bool VECTOR, bool DOTS, int FLIGHT>
+__global__ void __launch_bounds__(kThreads, !DOTS ? 5 : FLIGHT > 2 ? 3 : 4) k_scatter(const ScatterParams p, const int warps) {
   using P = Piece<T, VECTOR>;
   __shared__ float part[2][kWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / warps, w_in = warp - group * warps;
@@ -180,7 +183,9 @@ __global__ void __launch_bounds__(kThreads) k_scatter(const ScatterParams p, con
   int buf = 0;
   pdl_wait();
   pdl_launch_dependents();
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kWarps / warps) + group; t < items; t += step) {
+  int64_t t = static_cast<int64_t>(blockIdx.x) * (kWarps / warps) + group;
+  Choices next(p.pos, p.weights, t, p.tokens, p.k, 0, lane);
+  for (; t < items; t += step) {
     if (t >= p.tokens) {
       const int64_t r0 = ((t - p.tokens) * warps + w_in) * kZeroRows, r = r0 + lane;
       uint32_t empty = __ballot_sync(0xFFFFFFFFu, lane < kZeroRows && r < p.capacity && __ldg(p.src + r) < 0);
@@ -194,48 +199,58 @@ __global__ void __launch_bounds__(kThreads) k_scatter(const ScatterParams p, con
       continue;
     }
     const T* in = static_cast<const T*>(p.in) + t * p.ldin;
+    Choices c = next;
+    next = Choices(p.pos, p.weights, t + step, p.tokens, p.k, 0, lane);
     for (int j0 = 0; j0 < p.k; j0 += 32) {
-      const Choices c(p.pos, p.weights, t, p.k, j0, lane, p.capacity, p.err);
+      if (j0 > 0) c = Choices(p.pos, p.weights, t, p.tokens, p.k, j0, lane);
+      c.check(p.capacity, p.err);
       const int n = min(32, p.k - j0);
       float my_dot = 0.0f;   // of choice j0 + lane
       for (int cb = w_in * kPieces * P::WC; cb < cols; cb += block_cols) {
         const int first = cb + P::first(lane), left = cols - first;
-        float v[kPieces][P::E];
+        uint4 raw[kPieces];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) P::load(in + first + i * P::WC, left - i * P::WC, v[i]);
-        for (int j = 0; j < n; j += kFlight) {
-          float o[DOTS ? kFlight : 1][kPieces][P::E];
+        for (int i = 0; i < kPieces; ++i) raw[i] = P::load_raw(in + first + i * P::WC, left - i * P::WC);
+        for (int j = 0; j < n; j += FLIGHT) {
+          uint4 o[DOTS ? FLIGHT : 1][kPieces];
           if constexpr (DOTS) {
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u) {
+            for (int u = 0; u < FLIGHT; ++u) {
               const int pos = __shfl_sync(0xFFFFFFFFu, c.pos, (j + u) & 31);
               const bool on = j + u < n && pos >= 0;
               const T* other = static_cast<const T*>(p.other) + (on ? pos : 0) * p.ldother + first;
 #pragma unroll
-              for (int i = 0; i < kPieces; ++i) P::load(other + i * P::WC, on ? left - i * P::WC : 0, o[u][i]);
+              for (int i = 0; i < kPieces; ++i) o[u][i] = P::load_raw(other + i * P::WC, on ? left - i * P::WC : 0);
             }
           }
 #pragma unroll
-          for (int u = 0; u < kFlight; ++u) {
+          for (int u = 0; u < FLIGHT; ++u) {
             if (j + u >= n) break;
             const int pos = __shfl_sync(0xFFFFFFFFu, c.pos, j + u);
             const float w = __shfl_sync(0xFFFFFFFFu, c.w, j + u);
             if (pos < 0) continue;
             T* out = static_cast<T*>(p.out) + pos * p.ldout + first;
-            float dot = 0.0f;
+            float2 dot = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-              float y[P::E];
+              float v[P::E], y[P::E];
+              P::unpack(raw[i], v);
 #pragma unroll
-              for (int e = 0; e < P::E; ++e) {
-                y[e] = w * v[i][e];
-                if constexpr (DOTS) dot = fmaf(v[i][e], o[u][i][e], dot);
+              for (int e = 0; e < P::E; e += 2) {
+                const float2 m = mul2(both(w), make_float2(v[e], v[e + 1]));
+                y[e] = m.x;
+                y[e + 1] = m.y;
               }
               P::store(out + i * P::WC, left - i * P::WC, y);
+              if constexpr (DOTS) {
+                P::unpack(o[u][i], y);
+#pragma unroll
+                for (int e = 0; e < P::E; e += 2) dot = fma2(make_float2(v[e], v[e + 1]), make_float2(y[e], y[e + 1]), dot);
+              }
             }
             if constexpr (DOTS) {
-              dot = warp_sum(dot);
-              if (lane == j + u) my_dot += dot;
+              const float d = warp_sum(dot.x + dot.y);
+              if (lane == j + u) my_dot += d;
             }
           }
         }
@@ -256,50 +271,69 @@ __global__ void __launch_bounds__(kThreads) k_scatter(const ScatterParams p, con
 }
 
 // A warp per kPieces pieces of a token's row: y[t] = sum_j w_j ys[pos_j], the choices in order.
-template <typename T, bool VECTOR>
-__global__ void __launch_bounds__(kThreads) k_combine(const CombineParams p) {
+template <typename T, bool VECTOR, int FLIGHT>
+__global__ void __launch_bounds__(kThreads, FLIGHT > 2 ? 3 : 4) k_combine(const CombineParams p) {
   using P = Piece<T, VECTOR>;
   const int lane = threadIdx.x & 31, cols = static_cast<int>(p.cols);
   Walk at(static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), static_cast<int64_t>(gridDim.x) * kWarps,
-          (p.cols + kPieces * P::WC - 1) / (kPieces * P::WC));
+          (cols + kPieces * P::WC - 1) / (kPieces * P::WC));
   pdl_wait();
   pdl_launch_dependents();
-  for (; at.row < p.tokens; at.next()) {
+  Choices next(p.pos, p.weights, at.row, p.tokens, p.k, 0, lane);
+  while (at.row < p.tokens) {
+    const int64_t t = at.row;
     const int first = static_cast<int>(at.piece) * kPieces * P::WC + P::first(lane), left = cols - first;
+    Choices c = next;
+    at.next();
+    next = Choices(p.pos, p.weights, at.row, p.tokens, p.k, 0, lane);
     float acc[kPieces][P::E];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
 #pragma unroll
       for (int e = 0; e < P::E; ++e) acc[i][e] = 0.0f;
     for (int j0 = 0; j0 < p.k; j0 += 32) {
-      const Choices c(p.pos, p.weights, at.row, p.k, j0, lane, p.capacity, p.err);
+      if (j0 > 0) c = Choices(p.pos, p.weights, t, p.tokens, p.k, j0, lane);
+      c.check(p.capacity, p.err);
       const int n = min(32, p.k - j0);
-      for (int j = 0; j < n; j += kFlight) {
-        float v[kFlight][kPieces][P::E], w[kFlight];
+      for (int j = 0; j < n; j += FLIGHT) {
+        uint4 raw[FLIGHT][kPieces];
+        float w[FLIGHT];
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
+        for (int u = 0; u < FLIGHT; ++u) {
           const int pos = __shfl_sync(0xFFFFFFFFu, c.pos, (j + u) & 31);
           w[u] = __shfl_sync(0xFFFFFFFFu, c.w, (j + u) & 31);
           const bool on = j + u < n && pos >= 0;
           const T* ys = static_cast<const T*>(p.ys) + (on ? pos : 0) * p.ldys + first;
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) P::load(ys + i * P::WC, on ? left - i * P::WC : 0, v[u][i]);
+          for (int i = 0; i < kPieces; ++i) raw[u][i] = P::load_raw(ys + i * P::WC, on ? left - i * P::WC : 0);
         }
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u)
-          if (j + u < n)
+        for (int u = 0; u < FLIGHT; ++u) {
+          if (j + u >= n) break;
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i)
+          for (int i = 0; i < kPieces; ++i) {
+            float v[P::E];
+            P::unpack(raw[u][i], v);
 #pragma unroll
-              for (int e = 0; e < P::E; ++e) acc[i][e] = fmaf(w[u], v[u][i][e], acc[i][e]);
+            for (int e = 0; e < P::E; e += 2) {
+              const float2 m = fma2(both(w[u]), make_float2(v[e], v[e + 1]), make_float2(acc[i][e], acc[i][e + 1]));
+              acc[i][e] = m.x;
+              acc[i][e + 1] = m.y;
+            }
+          }
+        }
       }
     }
-    T* y = static_cast<T*>(p.y) + at.row * p.ldy + first;
+    T* y = static_cast<T*>(p.y) + t * p.ldy + first;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) P::store(y + i * P::WC, left - i * P::WC, acc[i]);
   }
 }
 
+// Blocks of a launch over `want` blocks' worth of items: more than an SM holds, so that SMs that
+// finish early take more, but each with several items, whose choices it fetches ahead.  8192
+// tokens, 2 choices, 4096 wide (dispatch / combine / combine backward): 4 blocks an SM 39.5 / 34.2
+// / 67.5 us, 8: 35.5 / 34.5 / 64.8, 16: 33.4 / 36.2 / 66.0, one block an item 42 / 41 / 73.
 unsigned grid_of(int64_t want, int num_sms, int per_sm) {
   const int64_t cap = static_cast<int64_t>(num_sms) * per_sm;
   return static_cast<unsigned>(want < 1 ? 1 : (want > cap ? cap : want));
@@ -342,15 +376,18 @@ cudaError_t run_scatter(const ScatterParams& p, int num_sms, cudaStream_t s) {
   int warps = 1;
   while (warps < kWarps && warps * wc < p.cols) warps *= 2;
   const int64_t per_item = static_cast<int64_t>(warps) * kZeroRows, items = p.tokens + (p.capacity + per_item - 1) / per_item;
-  const dim3 grid(grid_of((items + kWarps / warps - 1) / (kWarps / warps), num_sms, 8));
-  return p.dots != nullptr ? launch_pdl(k_scatter<T, VECTOR, true>, grid, dim3(kThreads), 0, s, 1, p, warps)
-                           : launch_pdl(k_scatter<T, VECTOR, false>, grid, dim3(kThreads), 0, s, 1, p, warps);
+  const bool few = p.k <= 2;
+  const dim3 grid(grid_of((items + kWarps / warps - 1) / (kWarps / warps), num_sms, p.dots == nullptr ? 16 : 8));
+  auto kernel = p.dots == nullptr ? k_scatter<T, VECTOR, false, 2> : few ? k_scatter<T, VECTOR, true, 2> : k_scatter<T, VECTOR, true, 4>;
+  return launch_pdl(kernel, grid, dim3(kThreads), 0, s, 1, p, warps);
 }
 
 template <typename T, bool VECTOR>
 cudaError_t run_combine(const CombineParams& p, int num_sms, cudaStream_t s) {
   const int64_t wc = Piece<T, VECTOR>::WC * kPieces, items = p.tokens * ((p.cols + wc - 1) / wc);
-  return launch_pdl(k_combine<T, VECTOR>, dim3(grid_of((items + kWarps - 1) / kWarps, num_sms, 8)), dim3(kThreads), 0, s, 1, p);
+  const bool few = p.k <= 2;
+  return launch_pdl(few ? k_combine<T, VECTOR, 2> : k_combine<T, VECTOR, 4>,
+                    dim3(grid_of((items + kWarps - 1) / kWarps, num_sms, 8)), dim3(kThreads), 0, s, 1, p);
 }
 
 }  // namespace

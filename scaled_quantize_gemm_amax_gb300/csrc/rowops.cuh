@@ -96,22 +96,27 @@ struct Piece {
   __device__ static __forceinline__ constexpr int at(int i) { return VECTOR ? i : 32 * i; }
   __device__ static __forceinline__ bool has(int left, int i) { return left > (VECTOR ? 0 : 32 * i); }
 
-  // v = the row's values, 0 past its end
-  __device__ static __forceinline__ void load(const T* p, int left, float (&v)[E]) {
+  // The lane's values as loaded, four registers (0 past the row's end): what waits in registers
+  // waits in this form.
+  __device__ static __forceinline__ uint4 load_raw(const T* p, int left) {
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (VECTOR) {
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
       if (left > 0) w = __ldg(reinterpret_cast<const uint4*>(p));
-      unpack(w, v);
     } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) v[i] = has(left, i) ? ld_elem(p + at(i)) : 0.0f;
+      if (has(left, 0)) w.x = __float_as_uint(ld_elem(p + at(0)));
+      if (has(left, 1)) w.y = __float_as_uint(ld_elem(p + at(1)));
+      if (has(left, 2)) w.z = __float_as_uint(ld_elem(p + at(2)));
+      if (has(left, 3)) w.w = __float_as_uint(ld_elem(p + at(3)));
     }
+    return w;
   }
+  // v = the row's values, 0 past its end
+  __device__ static __forceinline__ void load(const T* p, int left, float (&v)[E]) { unpack(load_raw(p, left), v); }
   __device__ static __forceinline__ void unpack(const uint4& w, float (&v)[E]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 2) {
+      if constexpr (VECTOR && sizeof(T) == 2) {
         v[2 * i] = bf16lo(u[i]);
         v[2 * i + 1] = bf16hi(u[i]);
       } else {
