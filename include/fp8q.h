@@ -402,8 +402,8 @@ fp8_status fp8_layer_norm_backward(const void* dy, int64_t rows, int64_t cols, i
                                    int64_t ldq, const float* s, const void* weight, fp8_dtype wdt, void* dx, int64_t lddx,
                                    void* dweight, void* dbias, void* workspace, int64_t workspace_bytes,
                                    cudaStream_t stream);
-/* *bytes (host): the workspace of fp8_layer_norm_backward for this shape; at most
- * 304 * 8 * cols.  No device call. */
+/* *bytes (host): the workspace of fp8_layer_norm_backward for this shape,
+ *   8 * cols * min(max(rows, 1), 304).  No device call. */
 fp8_status fp8_layer_norm_workspace(int64_t rows, int64_t cols, int64_t* bytes);
 
 /*
@@ -444,17 +444,14 @@ fp8_status fp8_gated_act_backward(const void* dy, int64_t rows, int64_t cols, in
  *   pos         device, [tokens, k] int32: the choice's row (its expert's choices keep
  *               their order), -1 when dropped
  *   src         device, [capacity] int32: the row's choice i, -1 for rows that pad
- *   capacity    rows, at least fp8_moe_sizes' (FP8_ERR_SHAPE below it)
- *   workspace   device, 4-byte aligned, fp8_moe_sizes' bytes (NULL when that is 0)
+ *   capacity    rows, at least fp8_moe_capacity's (FP8_ERR_SHAPE below it)
  * tokens * k and capacity must be below 2^31 (FP8_ERR_SHAPE).
  */
 fp8_status fp8_moe_route(const void* experts, int32_t id_bytes, int64_t tokens, int32_t k, int32_t n_experts, int32_t align,
-                         int32_t* offsets, int32_t* pos, int32_t* src, int64_t capacity, void* workspace,
-                         int64_t workspace_bytes, cudaStream_t stream);
-/* Host arithmetic only: *capacity = the most rows a routing of this size can use,
- * *workspace_bytes = fp8_moe_route's workspace. */
-fp8_status fp8_moe_sizes(int64_t tokens, int32_t k, int32_t n_experts, int32_t align, int64_t* capacity,
-                         int64_t* workspace_bytes);
+                         int32_t* offsets, int32_t* pos, int32_t* src, int64_t capacity, cudaStream_t stream);
+/* Host arithmetic only: *rows = the most rows a routing of this size can use,
+ *   (n + min(n, n_experts) (align - 1)) / align * align  with n = tokens * k. */
+fp8_status fp8_moe_capacity(int64_t tokens, int32_t k, int32_t n_experts, int32_t align, int64_t* rows);
 
 /*
  * fp8_moe_dispatch -- every token's row copied to its choices' rows:

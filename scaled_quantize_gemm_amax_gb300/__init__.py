@@ -15,7 +15,7 @@ Entry points with the C names take tensors (or None for NULL) and raise
 ``fp8_debug_index_check``; and the row operators between the linear layers,
 ``fp8_layer_norm``, ``fp8_layer_norm_backward``, ``fp8_gated_act``,
 ``fp8_gated_act_backward``, ``fp8_moe_route``, ``fp8_moe_dispatch``, ``fp8_moe_combine``,
-``fp8_moe_combine_backward`` (with ``fp8_layer_norm_workspace`` and ``fp8_moe_sizes``).
+``fp8_moe_combine_backward`` (with ``fp8_layer_norm_workspace`` and ``fp8_moe_capacity``).
 ``cast_transpose`` / ``dequantize`` / ``scaled_gemm`` / ``scaled_gemm_amax`` /
 ``layer_norm`` / ``gated_act`` / ``moe_route`` ... are allocation helpers
 over them; ``linear`` holds the FP8 linear layer and the autocast scope built
@@ -41,7 +41,7 @@ __all__ = [
     "DelayedScaling",
     "Activation", "MoeRoute",
     "fp8_layer_norm", "fp8_layer_norm_backward", "fp8_layer_norm_workspace", "fp8_gated_act", "fp8_gated_act_backward",
-    "fp8_moe_route", "fp8_moe_sizes", "fp8_moe_dispatch", "fp8_moe_combine", "fp8_moe_combine_backward",
+    "fp8_moe_route", "fp8_moe_capacity", "fp8_moe_dispatch", "fp8_moe_combine", "fp8_moe_combine_backward",
     "layer_norm", "layer_norm_backward", "gated_act", "gated_act_backward", "moe_route", "moe_dispatch", "moe_combine",
     "moe_combine_backward", "moe_dispatch_backward",
 ]
@@ -133,8 +133,8 @@ _SIGNATURES = {
     "fp8_gated_act": [_P, _I64, _I64, _I64, _E, _E, _P, _I64, _P, _I64, _E, _P, _P, _P, _P, _I64, _P],
     "fp8_gated_act_backward": [_P, _I64, _I64, _I64, _E, _E, _P, _I64, _P, _I64, _E, _P, _P, _P, _P, _I64, _P, _I64, _P,
                                _I64, _P],
-    "fp8_moe_route": [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P, _I64, _P, _I64, _P],
-    "fp8_moe_sizes": [_I64, _I32, _I32, _I32, _P, _P],
+    "fp8_moe_route": [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P, _I64, _P],
+    "fp8_moe_capacity": [_I64, _I32, _I32, _I32, _P],
     "fp8_moe_dispatch": [_P, _I64, _I64, _I64, _E, _I32, _P, _P, _I64, _P, _I64, _P],
     "fp8_moe_combine": [_P, _I64, _I64, _I64, _E, _I64, _I32, _P, _P, _P, _I64, _P],
     "fp8_moe_combine_backward": [_P, _I64, _I64, _I64, _E, _I32, _P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _P],
@@ -172,9 +172,12 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream, _device_index = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # torch.cuda.current_stream().cuda_stream, without making the Stream object
+        return _raw_stream(_device_index())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -306,12 +309,17 @@ def fp8_scaled_gemm_amax(a, fa, ra, sa, b, fb, rb, sb, c, out, c_amax, c_scale, 
                                                int(fc), _ptr(c_q), _ptr(c_scale_inv), _stream(stream)))
 
 
+# ---- row operators.  The fp8_* calls check every tensor; the allocation helpers below check the
+# caller's tensors and pass the outputs they have just made straight on (the _run_* functions).
 def _rows(t, what: str):
-    """(rows, cols, row stride) of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError(f"{what}: a 2-D tensor with contiguous rows is needed, not shape {tuple(t.shape)} "
-                         f"stride {t.stride()}")
-    return t.shape[0], t.shape[1], t.stride(0)
+    """(rows, cols, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
+    if t.dim() == 2:
+        rows, cols = t.shape
+        ld, one = t.stride()
+        if one == 1 or cols <= 1:
+            return rows, cols, ld
+    raise ValueError(f"{what}: a 2-D tensor with contiguous rows is needed, not shape {tuple(t.shape)} "
+                     f"stride {t.stride()}")
 
 
 _DTYPE_CODE = {torch.bfloat16: 0, torch.float32: 1}
@@ -349,6 +357,14 @@ def _codes(q, s, rows: int, cols: int, what: str) -> int:
     return _rows(q, what)[2]
 
 
+def _code_pair(qa, sa, qb, sb, rows: int, cols: int) -> int:
+    """The one row stride of both 8-bit copies (each possibly None)."""
+    lda, ldb = _codes(qa, sa, rows, cols, "qa"), _codes(qb, sb, rows, cols, "qb")
+    if qa is not None and qb is not None and lda != ldb and rows > 1:
+        raise ValueError("qa and qb: one row stride is needed for both")
+    return lda or ldb
+
+
 def _params(weight, bias, cols: int):
     """The type code of weight and bias (either may be None)."""
     p = weight if weight is not None else bias
@@ -366,16 +382,23 @@ def _on_gpu(*tensors):
             raise ValueError(f"a CUDA tensor is needed, not one on {t.device}")
 
 
-def fp8_layer_norm(x, weight, bias, eps, y, mean, rstd, fmt, q, s, stream=None):
+def _run_layer_norm(x, weight, bias, eps, y, ldy, mean, rstd, fmt, q, ldq, s, stream, outs=()):
     rows, cols, ldx = _rows(x, "x")
     dt, wdt = _dtype(x, "x"), _params(weight, bias, cols)
+    _on_gpu(x, weight, bias, *outs)
+    st = load_library().fp8_layer_norm(_ptr(x), rows, cols, ldx, dt, _ptr(weight), _ptr(bias), wdt, eps, _ptr(y), ldy,
+                                       _ptr(mean), _ptr(rstd), fmt, _ptr(q), ldq, _ptr(s), _stream(stream))
+    if st:
+        raise FP8Error("fp8_layer_norm", st)
+
+
+def fp8_layer_norm(x, weight, bias, eps, y, mean, rstd, fmt, q, s, stream=None):
+    rows, cols, _ = _rows(x, "x")
+    _dtype(x, "x")
     ldy, ldq = _like(y, x, "y"), _codes(q, s, rows, cols, "q")
     _vector(mean, rows, "mean")
     _vector(rstd, rows, "rstd")
-    _on_gpu(x, weight, bias, y, mean, rstd, q, s)
-    _check("fp8_layer_norm",
-           load_library().fp8_layer_norm(_ptr(x), rows, cols, ldx, dt, _ptr(weight), _ptr(bias), wdt, eps, _ptr(y), ldy,
-                                         _ptr(mean), _ptr(rstd), int(fmt), _ptr(q), ldq, _ptr(s), _stream(stream)))
+    _run_layer_norm(x, weight, bias, eps, y, ldy, mean, rstd, int(fmt), q, ldq, s, stream, (y, mean, rstd, q, s))
 
 
 def fp8_layer_norm_workspace(rows: int, cols: int) -> int:
@@ -385,115 +408,152 @@ def fp8_layer_norm_workspace(rows: int, cols: int) -> int:
     return n.value
 
 
-def fp8_layer_norm_backward(dy, x, mean, rstd, fmt, q, s, weight, dx, dweight, dbias, workspace, stream=None):
+def _run_layer_norm_backward(dy, x, mean, rstd, fmt, q, s, weight, wdt, dx, lddx, dweight, dbias, workspace, nbytes, stream,
+                             outs=()):
     rows, cols, lddy = _rows(dy, "dy")
-    dt = _dtype(dy, "dy")
-    wdt = _params(weight, dweight, cols)
-    wdt = wdt if weight is not None or dweight is not None else _params(None, dbias, cols)
-    ldx, lddx, ldq = _like(x, dy, "x"), _like(dx, dy, "dx"), _codes(q, s, rows, cols, "q")
-    for t in (dweight, dbias):
-        if t is not None:
-            _vector(t, cols, "dweight / dbias", (torch.bfloat16, torch.float32)[wdt])
+    dt, ldx, ldq = _dtype(dy, "dy"), _like(x, dy, "x"), _codes(q, s, rows, cols, "q")
     _vector(mean, rows, "mean")
     _vector(rstd, rows, "rstd")
+    _on_gpu(dy, x, mean, rstd, q, s, weight, *outs)
+    st = load_library().fp8_layer_norm_backward(_ptr(dy), rows, cols, lddy, dt, _ptr(x), ldx, _ptr(mean), _ptr(rstd), fmt,
+                                                _ptr(q), ldq, _ptr(s), _ptr(weight), wdt, _ptr(dx), lddx, _ptr(dweight),
+                                                _ptr(dbias), _ptr(workspace), nbytes, _stream(stream))
+    if st:
+        raise FP8Error("fp8_layer_norm_backward", st)
+
+
+def fp8_layer_norm_backward(dy, x, mean, rstd, fmt, q, s, weight, dx, dweight, dbias, workspace, stream=None):
+    cols = _rows(dy, "dy")[1]
+    wdt = _params(weight, dweight, cols) if weight is not None or dweight is not None else _params(None, dbias, cols)
+    _vector(dbias, cols, "dbias", (torch.bfloat16, torch.float32)[wdt])
+    lddx = _like(dx, dy, "dx")
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _on_gpu(dy, x, mean, rstd, q, s, weight, dx, dweight, dbias, workspace)
-    _check("fp8_layer_norm_backward",
-           load_library().fp8_layer_norm_backward(_ptr(dy), rows, cols, lddy, dt, _ptr(x), ldx, _ptr(mean), _ptr(rstd),
-                                                  int(fmt), _ptr(q), ldq, _ptr(s), _ptr(weight), wdt, _ptr(dx), lddx,
-                                                  _ptr(dweight), _ptr(dbias), _ptr(workspace), nbytes, _stream(stream)))
+    _run_layer_norm_backward(dy, x, mean, rstd, int(fmt), q, s, weight, wdt, dx, lddx, dweight, dbias, workspace, nbytes, stream,
+                             (dx, dweight, dbias, workspace))
+
+
+def _run_gated_act(a, b, act, y, ldy, fmt, qa, sa, qb, sb, ldq, stream, outs=()):
+    rows, cols, lda = _rows(a, "a")
+    ldb, dt = _like(b, a, "b"), _dtype(a, "a")
+    _on_gpu(a, b, *outs)
+    st = load_library().fp8_gated_act(_ptr(a), rows, cols, lda, dt, act, _ptr(b), ldb, _ptr(y), ldy, fmt, _ptr(qa), _ptr(sa),
+                                      _ptr(qb), _ptr(sb), ldq, _stream(stream))
+    if st:
+        raise FP8Error("fp8_gated_act", st)
 
 
 def fp8_gated_act(a, b, act, y, fmt, qa, sa, qb, sb, stream=None):
-    rows, cols, lda = _rows(a, "a")
-    ldb, ldy = _like(b, a, "b"), _like(y, a, "y")
-    ldq, ldqb = _codes(qa, sa, rows, cols, "qa"), _codes(qb, sb, rows, cols, "qb")
-    if qa is not None and qb is not None and ldq != ldqb and rows > 1:
-        raise ValueError("qa and qb: one row stride is needed for both")
-    _on_gpu(a, b, y, qa, sa, qb, sb)
-    _check("fp8_gated_act",
-           load_library().fp8_gated_act(_ptr(a), rows, cols, lda, _dtype(a, "a"), int(act), _ptr(b), ldb, _ptr(y), ldy,
-                                        int(fmt), _ptr(qa), _ptr(sa), _ptr(qb), _ptr(sb), ldq or ldqb, _stream(stream)))
+    rows, cols, _ = _rows(a, "a")
+    ldy, ldq = _like(y, a, "y"), _code_pair(qa, sa, qb, sb, rows, cols)
+    _run_gated_act(a, b, int(act), y, ldy, int(fmt), qa, sa, qb, sb, ldq, stream, (y, qa, sa, qb, sb))
+
+
+def _run_gated_act_backward(dy, act, a, b, fmt, qa, sa, qb, sb, da, ldda, db, lddb, stream, outs=()):
+    rows, cols, lddy = _rows(dy, "dy")
+    lda, ldb, dt = _like(a, dy, "a"), _like(b, dy, "b"), _dtype(dy, "dy")
+    ldq = _code_pair(qa, sa, qb, sb, rows, cols)
+    _on_gpu(dy, a, b, qa, sa, qb, sb, *outs)
+    st = load_library().fp8_gated_act_backward(_ptr(dy), rows, cols, lddy, dt, act, _ptr(a), lda, _ptr(b), ldb, fmt, _ptr(qa),
+                                               _ptr(sa), _ptr(qb), _ptr(sb), ldq, _ptr(da), ldda, _ptr(db), lddb,
+                                               _stream(stream))
+    if st:
+        raise FP8Error("fp8_gated_act_backward", st)
 
 
 def fp8_gated_act_backward(dy, act, a, b, fmt, qa, sa, qb, sb, da, db, stream=None):
-    rows, cols, lddy = _rows(dy, "dy")
-    lda, ldb = _like(a, dy, "a"), _like(b, dy, "b")
     ldda, lddb = _like(da, dy, "da"), _like(db, dy, "db")
-    ldq, ldqb = _codes(qa, sa, rows, cols, "qa"), _codes(qb, sb, rows, cols, "qb")
-    if qa is not None and qb is not None and ldq != ldqb and rows > 1:
-        raise ValueError("qa and qb: one row stride is needed for both")
-    _on_gpu(dy, a, b, qa, sa, qb, sb, da, db)
-    _check("fp8_gated_act_backward",
-           load_library().fp8_gated_act_backward(_ptr(dy), rows, cols, lddy, _dtype(dy, "dy"), int(act), _ptr(a), lda,
-                                                 _ptr(b), ldb, int(fmt), _ptr(qa), _ptr(sa), _ptr(qb), _ptr(sb), ldq,
-                                                 _ptr(da), ldda, _ptr(db), lddb, _stream(stream)))
+    _run_gated_act_backward(dy, int(act), a, b, int(fmt), qa, sa, qb, sb, da, ldda, db, lddb, stream, (da, db))
 
 
-def fp8_moe_sizes(tokens: int, k: int, n_experts: int, align: int):
-    """(rows a routing of this size can use, bytes of fp8_moe_route's workspace); host arithmetic."""
-    out = (ctypes.c_int64 * 2)()
-    at = ctypes.addressof(out)
-    _check("fp8_moe_sizes", load_library().fp8_moe_sizes(tokens, k, n_experts, align, at, at + 8))
-    return out[0], out[1]
+def fp8_moe_capacity(tokens: int, k: int, n_experts: int, align: int) -> int:
+    """Rows that a routing of this size can use (host arithmetic)."""
+    n = ctypes.c_int64()
+    _check("fp8_moe_capacity", load_library().fp8_moe_capacity(tokens, k, n_experts, align, ctypes.addressof(n)))
+    return n.value
 
 
-def fp8_moe_route(experts, n_experts: int, align: int, offsets, pos, src, workspace, stream=None):
+def _run_moe_route(experts, n_experts, align, offsets, pos, src, capacity, stream, outs=()):
     if experts.dim() != 2 or experts.dtype not in (torch.int32, torch.int64) or not experts.is_contiguous():
         raise ValueError("experts: a contiguous [tokens, k] int32 or int64 tensor is needed")
     tokens, k = experts.shape
+    _on_gpu(experts, *outs)
+    st = load_library().fp8_moe_route(_ptr(experts), 4 if experts.dtype == torch.int32 else 8, tokens, k, n_experts, align,
+                                      _ptr(offsets), _ptr(pos), _ptr(src), capacity, _stream(stream))
+    if st:
+        raise FP8Error("fp8_moe_route", st)
+
+
+def fp8_moe_route(experts, n_experts: int, align: int, offsets, pos, src, stream=None):
     _vector(offsets, n_experts + 1, "offsets", torch.int32)
-    _vector(pos, tokens * k, "pos", torch.int32)
+    _vector(pos, experts.numel(), "pos", torch.int32)
     _vector(src, src.numel(), "src", torch.int32)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _on_gpu(experts, offsets, pos, src, workspace)
-    _check("fp8_moe_route",
-           load_library().fp8_moe_route(_ptr(experts), experts.element_size(), tokens, k, n_experts, align, _ptr(offsets),
-                                        _ptr(pos), _ptr(src), src.numel(), _ptr(workspace), nbytes, _stream(stream)))
+    _run_moe_route(experts, n_experts, align, offsets, pos, src, src.numel(), stream, (offsets, pos, src))
 
 
-def _scattered(x, pos, src, out):
-    """Checks of the operators that copy [tokens, cols] rows to [capacity, cols]; (tokens, cols, ldx, k, capacity, ldout)."""
-    tokens, cols, ldx = _rows(x, "rows of tokens")
-    if pos.dim() != 2 or pos.shape[0] != tokens:
-        raise ValueError(f"pos: shape ({tokens}, k) is needed, not {tuple(pos.shape)}")
-    _vector(pos, pos.numel(), "pos", torch.int32)
+def _choices(pos, what_tokens: int | None = None):
+    """(tokens, k) of a routing's pos."""
+    if pos.dim() != 2 or pos.dtype != torch.int32 or not pos.is_contiguous() or what_tokens not in (None, pos.shape[0]):
+        raise ValueError(f"pos: a contiguous int32 [tokens, k] tensor is needed, not {pos.dtype} {tuple(pos.shape)}"
+                         + ("" if what_tokens is None else f" for {what_tokens} tokens"))
+    return pos.shape
+
+
+def _check_segments(out, ref, capacity: int, cols: int, what: str) -> int:
+    """The row stride of a [capacity, cols] matrix of `ref`'s type."""
+    if out.shape != (capacity, cols) or out.dtype != ref.dtype:
+        raise ValueError(f"{what}: {ref.dtype} ({capacity}, {cols}) is needed, not {out.dtype} {tuple(out.shape)}")
+    return _rows(out, what)[2]
+
+
+def _run_moe_dispatch(x, pos, src, xs, ldxs, stream, outs=()):
+    tokens, cols, ldx = _rows(x, "x")
+    k, dt = _choices(pos, tokens)[1], _dtype(x, "x")
     _vector(src, src.numel(), "src", torch.int32)
-    if out.shape != (src.numel(), cols) or out.dtype != x.dtype:
-        raise ValueError(f"rows of choices: {x.dtype} ({src.numel()}, {cols}) is needed, not {out.dtype} {tuple(out.shape)}")
-    return tokens, cols, ldx, pos.shape[1], src.numel(), _rows(out, "rows of choices")[2]
+    _on_gpu(x, pos, src, *outs)
+    st = load_library().fp8_moe_dispatch(_ptr(x), tokens, cols, ldx, dt, k, _ptr(pos), _ptr(src), src.numel(), _ptr(xs), ldxs,
+                                         _stream(stream))
+    if st:
+        raise FP8Error("fp8_moe_dispatch", st)
 
 
 def fp8_moe_dispatch(x, pos, src, xs, stream=None):
-    tokens, cols, ldx, k, capacity, ldxs = _scattered(x, pos, src, xs)
-    _on_gpu(x, pos, src, xs)
-    _check("fp8_moe_dispatch",
-           load_library().fp8_moe_dispatch(_ptr(x), tokens, cols, ldx, _dtype(x, "x"), k, _ptr(pos), _ptr(src), capacity,
-                                           _ptr(xs), ldxs, _stream(stream)))
+    ldxs = _check_segments(xs, x, src.numel(), x.shape[-1], "xs")
+    _run_moe_dispatch(x, pos, src, xs, ldxs, stream, (xs,))
+
+
+def _run_moe_combine(ys, pos, weights, y, ldy, stream, outs=()):
+    capacity, cols, ldys = _rows(ys, "ys")
+    (tokens, k), dt = _choices(pos), _dtype(ys, "ys")
+    _vector(weights, tokens * k, "weights")
+    _on_gpu(ys, pos, weights, *outs)
+    st = load_library().fp8_moe_combine(_ptr(ys), capacity, cols, ldys, dt, tokens, k, _ptr(pos), _ptr(weights), _ptr(y), ldy,
+                                        _stream(stream))
+    if st:
+        raise FP8Error("fp8_moe_combine", st)
 
 
 def fp8_moe_combine(ys, pos, weights, y, stream=None):
-    capacity, cols, ldys = _rows(ys, "ys")
-    tokens, k = pos.shape
-    _vector(pos, tokens * k, "pos", torch.int32)
+    ldy = _check_segments(y, ys, pos.shape[0], ys.shape[-1], "y")
+    _run_moe_combine(ys, pos, weights, y, ldy, stream, (y,))
+
+
+def _run_moe_combine_backward(dy, pos, src, weights, ys, dys, lddys, dweights, stream, outs=()):
+    tokens, cols, lddy = _rows(dy, "dy")
+    k, dt, capacity = _choices(pos, tokens)[1], _dtype(dy, "dy"), src.numel()
+    _vector(src, capacity, "src", torch.int32)
     _vector(weights, tokens * k, "weights")
-    if y.shape != (tokens, cols) or y.dtype != ys.dtype:
-        raise ValueError(f"y: {ys.dtype} ({tokens}, {cols}) is needed, not {y.dtype} {tuple(y.shape)}")
-    _on_gpu(ys, pos, weights, y)
-    _check("fp8_moe_combine",
-           load_library().fp8_moe_combine(_ptr(ys), capacity, cols, ldys, _dtype(ys, "ys"), tokens, k, _ptr(pos),
-                                          _ptr(weights), _ptr(y), _rows(y, "y")[2], _stream(stream)))
+    ldys = 0 if ys is None else _check_segments(ys, dy, capacity, cols, "ys")
+    _on_gpu(dy, pos, src, weights, ys, *outs)
+    st = load_library().fp8_moe_combine_backward(_ptr(dy), tokens, cols, lddy, dt, k, _ptr(pos), _ptr(src), _ptr(weights),
+                                                 _ptr(ys), ldys, capacity, _ptr(dys), lddys, _ptr(dweights), _stream(stream))
+    if st:
+        raise FP8Error("fp8_moe_combine_backward", st)
 
 
 def fp8_moe_combine_backward(dy, pos, src, weights, ys, dys, dweights, stream=None):
-    tokens, cols, lddy, k, capacity, lddys = _scattered(dy, pos, src, dys)
-    _vector(weights, tokens * k, "weights")
-    _vector(dweights, tokens * k, "dweights")
-    _on_gpu(dy, pos, src, weights, ys, dys, dweights)
-    _check("fp8_moe_combine_backward",
-           load_library().fp8_moe_combine_backward(_ptr(dy), tokens, cols, lddy, _dtype(dy, "dy"), k, _ptr(pos), _ptr(src),
-                                                   _ptr(weights), _ptr(ys), _like(ys, dys, "ys"), capacity, _ptr(dys),
-                                                   lddys, _ptr(dweights), _stream(stream)))
+    lddys = _check_segments(dys, dy, src.numel(), dy.shape[-1], "dys")
+    _vector(dweights, pos.numel(), "dweights")
+    _run_moe_combine_backward(dy, pos, src, weights, ys, dys, lddys, dweights, stream, (dys, dweights))
 
 
 def fp8_get_device_status(stream=None) -> Status:
@@ -612,10 +672,11 @@ def scaled_gemm_amax(a, fa, ra, sa, b, fb, rb, sb, c_scale, fc=Format.E4M3, out=
 
 # ------------------------------------------------------------------ row operators, outputs allocated
 def _codes_like(x, rows: int, cols: int):
-    """Codes and multipliers of an 8-bit copy.  The codes' row stride is padded to 16 bytes."""
+    """Codes and multipliers of an 8-bit copy, and the codes' row stride (padded to 16 bytes)."""
     ld = (cols + 15) // 16 * 16
-    q = torch.empty((rows, ld), dtype=torch.uint8, device=x.device)
-    return q if ld == cols else q[:, :cols], torch.empty((rows, (cols + 127) // 128), dtype=torch.float32, device=x.device)
+    dev = x.device
+    return (torch.empty_strided((rows, cols), (ld, 1), dtype=torch.uint8, device=dev),
+            torch.empty((rows, (cols + 127) // 128), dtype=torch.float32, device=dev), ld)
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, checkpoint=None, stats: bool = True, stream=None):
@@ -624,14 +685,16 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, checkpoint=None, st
     Returns (y, mean, rstd, q, s).  checkpoint: a Format keeps the normalised rows in 8 bits
     (q, s; else None).  stats=False skips mean and rstd (inference)."""
     rows, cols = x.shape
-    y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    dev = x.device
+    y = torch.empty((rows, cols), dtype=x.dtype, device=dev)
     mean = rstd = q = s = None
+    ldq = 0
     if stats:
-        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        mean = torch.empty(rows, dtype=torch.float32, device=dev)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     if checkpoint is not None:
-        q, s = _codes_like(x, rows, cols)
-    fp8_layer_norm(x, weight, bias, eps, y, mean, rstd, checkpoint or 0, q, s, stream)
+        q, s, ldq = _codes_like(x, rows, cols)
+    _run_layer_norm(x, weight, bias, eps, y, cols, mean, rstd, checkpoint or 0, q, ldq, s, stream)
     return y, mean, rstd, q, s
 
 
@@ -642,14 +705,19 @@ def layer_norm_backward(dy, rstd, weight=None, x=None, mean=None, q=None, s=None
     Returns (dx, dweight, dbias), the last two in the weight's type (param_dtype without a
     weight; default float32), or None with param_grads=False."""
     rows, cols = dy.shape
-    dx = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device)
+    dev = dy.device
+    dx = torch.empty((rows, cols), dtype=dy.dtype, device=dev)
+    dt = weight.dtype if weight is not None else param_dtype or torch.float32
+    if dt not in _DTYPE_CODE or (weight is not None and (weight.numel() != cols or not weight.is_contiguous())):
+        raise ValueError(f"weight: {cols} contiguous bfloat16 or float32 elements are needed, not {dt}")
     dw = db = workspace = None
+    nbytes = 0
     if param_grads:
-        dt = weight.dtype if weight is not None else param_dtype or torch.float32
-        dw = torch.empty(cols, dtype=dt, device=dy.device)
-        db = torch.empty(cols, dtype=dt, device=dy.device)
-        workspace = torch.empty(fp8_layer_norm_workspace(rows, cols), dtype=torch.uint8, device=dy.device)
-    fp8_layer_norm_backward(dy, x, mean, rstd, fmt, q, s, weight, dx, dw, db, workspace, stream)
+        dw = torch.empty(cols, dtype=dt, device=dev)
+        db = torch.empty(cols, dtype=dt, device=dev)
+        nbytes = 8 * cols * min(max(rows, 1), 304)   # fp8_layer_norm_workspace
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _run_layer_norm_backward(dy, x, mean, rstd, fmt, q, s, weight, _DTYPE_CODE[dt], dx, cols, dw, db, workspace, nbytes, stream)
     return dx, dw, db
 
 
@@ -660,11 +728,12 @@ def gated_act(a, b=None, act=Activation.SILU, checkpoint=None, stream=None):
     rows, cols = a.shape
     y = torch.empty((rows, cols), dtype=a.dtype, device=a.device)
     qa = sa = qb = sb = None
+    ldq = 0
     if checkpoint is not None:
-        qa, sa = _codes_like(a, rows, cols)
+        qa, sa, ldq = _codes_like(a, rows, cols)
         if b is not None:
-            qb, sb = _codes_like(a, rows, cols)
-    fp8_gated_act(a, b, act, y, checkpoint or 0, qa, sa, qb, sb, stream)
+            qb, sb, _ = _codes_like(a, rows, cols)
+    _run_gated_act(a, b, act, y, cols, checkpoint or 0, qa, sa, qb, sb, ldq, stream)
     return y, qa, sa, qb, sb
 
 
@@ -675,11 +744,11 @@ def gated_act_backward(dy, act=Activation.SILU, a=None, b=None, qa=None, sa=None
     Returns (da, db): the halves of one [rows, 2 cols] tensor, or (da, None) when not gated."""
     rows, cols = dy.shape
     if b is None and qb is None:
-        da, db = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device), None
+        da, db, ld = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device), None, cols
     else:
-        d = torch.empty((rows, 2 * cols), dtype=dy.dtype, device=dy.device)
-        da, db = d[:, :cols], d[:, cols:]
-    fp8_gated_act_backward(dy, act, a, b, fmt, qa, sa, qb, sb, da, db, stream)
+        da, db = torch.empty((rows, 2 * cols), dtype=dy.dtype, device=dy.device).split(cols, 1) if cols else (dy, dy)
+        ld = 2 * cols
+    _run_gated_act_backward(dy, act, a, b, fmt, qa, sa, qb, sb, da, ld, db, ld, stream)
     return da, db
 
 
@@ -695,37 +764,39 @@ def moe_route(experts, n_experts: int, align: int = 1, stream=None) -> MoeRoute:
 
     align=128 makes every expert's segment an operand of scaled_gemm."""
     tokens, k = experts.shape
-    capacity, nbytes = fp8_moe_sizes(tokens, k, n_experts, align)
+    capacity = fp8_moe_capacity(tokens, k, n_experts, align)
     dev = experts.device
     offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
     pos = torch.empty((tokens, k), dtype=torch.int32, device=dev)
     src = torch.empty(capacity, dtype=torch.int32, device=dev)
-    workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    fp8_moe_route(experts, n_experts, align, offsets, pos, src, workspace, stream)
+    _run_moe_route(experts, n_experts, align, offsets, pos, src, capacity, stream)
     return MoeRoute(offsets, pos, src)
 
 
 def moe_dispatch(x, route: MoeRoute, stream=None):
     """xs [capacity, cols]: every token's row at its choices' rows, 0 in the rows that pad."""
-    xs = torch.empty((route.src.numel(), x.shape[1]), dtype=x.dtype, device=x.device)
-    fp8_moe_dispatch(x, route.pos, route.src, xs, stream)
+    cols = x.shape[-1]
+    xs = torch.empty((route.src.numel(), cols), dtype=x.dtype, device=x.device)
+    _run_moe_dispatch(x, route.pos, route.src, xs, cols, stream)
     return xs
 
 
 def moe_combine(ys, route: MoeRoute, weights=None, stream=None):
     """y [tokens, cols]: the choices' rows of ys summed with weights [tokens, k] float32 (None: 1)."""
-    y = torch.empty((route.pos.shape[0], ys.shape[1]), dtype=ys.dtype, device=ys.device)
-    fp8_moe_combine(ys, route.pos, weights, y, stream)
+    cols = ys.shape[-1]
+    y = torch.empty((route.pos.shape[0], cols), dtype=ys.dtype, device=ys.device)
+    _run_moe_combine(ys, route.pos, weights, y, cols, stream)
     return y
 
 
 def moe_combine_backward(dy, ys, route: MoeRoute, weights=None, stream=None):
     """The gradients of moe_combine: (dys [capacity, cols], dweights [tokens, k] or None without weights)."""
-    dys = torch.empty((route.src.numel(), dy.shape[1]), dtype=dy.dtype, device=dy.device)
+    cols = dy.shape[-1]
+    dys = torch.empty((route.src.numel(), cols), dtype=dy.dtype, device=dy.device)
     dw = None
     if weights is not None:
         dw = torch.empty(route.pos.shape, dtype=torch.float32, device=dy.device)
-    fp8_moe_combine_backward(dy, route.pos, route.src, weights, ys if dw is not None else None, dys, dw, stream)
+    _run_moe_combine_backward(dy, route.pos, route.src, weights, ys if dw is not None else None, dys, cols, dw, stream)
     return dys, dw
 
 

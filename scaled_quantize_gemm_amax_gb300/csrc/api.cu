@@ -841,35 +841,28 @@ fp8_status fp8_gated_act_backward(const void* dy, int64_t rows, int64_t cols, in
   return cuda_status(launch_act_backward(p, d->num_sms, stream));
 }
 
-fp8_status fp8_moe_sizes(int64_t tokens, int32_t k, int32_t n_experts, int32_t align, int64_t* capacity,
-                         int64_t* workspace_bytes) {
-  ApiRange nvtx_range("fp8_moe_sizes");
-  if (tokens < 0 || k < 1 || n_experts < 1 || align < 1 || capacity == nullptr || workspace_bytes == nullptr)
-    return FP8_ERR_INVALID_ARG;
+fp8_status fp8_moe_capacity(int64_t tokens, int32_t k, int32_t n_experts, int32_t align, int64_t* rows) {
+  ApiRange nvtx_range("fp8_moe_capacity");
+  if (tokens < 0 || k < 1 || n_experts < 1 || align < 1 || rows == nullptr) return FP8_ERR_INVALID_ARG;
   if (n_experts > kMaxExperts || tokens > kMaxDim || tokens * k > kMaxDim) return FP8_ERR_SHAPE;
   // every expert with choices pads at most align - 1 rows, and the sum is a multiple of align
   const int64_t n = tokens * k, used = n < n_experts ? n : n_experts;
-  const int64_t rows = (n + used * (align - 1)) / align * align;
-  if (rows > kMaxDim) return FP8_ERR_SHAPE;
-  *capacity = rows;
-  const int blocks = route_blocks(n);
-  *workspace_bytes = blocks > 1 ? static_cast<int64_t>(blocks) * n_experts * static_cast<int64_t>(sizeof(int)) : 0;
+  const int64_t most = (n + used * (align - 1)) / align * align;
+  if (most > kMaxDim) return FP8_ERR_SHAPE;
+  *rows = most;
   return FP8_OK;
 }
 
 fp8_status fp8_moe_route(const void* experts, int32_t id_bytes, int64_t tokens, int32_t k, int32_t n_experts, int32_t align,
-                         int32_t* offsets, int32_t* pos, int32_t* src, int64_t capacity, void* workspace,
-                         int64_t workspace_bytes, cudaStream_t stream) {
+                         int32_t* offsets, int32_t* pos, int32_t* src, int64_t capacity, cudaStream_t stream) {
   ApiRange nvtx_range("fp8_moe_route");
-  int64_t rows = 0, need = 0;
+  int64_t rows = 0;
   if (id_bytes != 4 && id_bytes != 8) return FP8_ERR_INVALID_ARG;
-  if (fp8_status st = fp8_moe_sizes(tokens, k, n_experts, align, &rows, &need)) return st;
-  if (offsets == nullptr || (tokens > 0 && (experts == nullptr || pos == nullptr)) || (capacity > 0 && src == nullptr) ||
-      (need > 0 && workspace == nullptr))
+  if (fp8_status st = fp8_moe_capacity(tokens, k, n_experts, align, &rows)) return st;
+  if (offsets == nullptr || (tokens > 0 && (experts == nullptr || pos == nullptr)) || (capacity > 0 && src == nullptr))
     return FP8_ERR_INVALID_ARG;
-  if (capacity < rows || capacity > kMaxDim || workspace_bytes < need) return FP8_ERR_SHAPE;
-  if (!aligned(experts, static_cast<uintptr_t>(id_bytes)) || !aligned(offsets, 4) || !aligned(pos, 4) || !aligned(src, 4) ||
-      (need > 0 && !aligned(workspace, 4)))
+  if (capacity < rows || capacity > kMaxDim) return FP8_ERR_SHAPE;
+  if (!aligned(experts, static_cast<uintptr_t>(id_bytes)) || !aligned(offsets, 4) || !aligned(pos, 4) || !aligned(src, 4))
     return FP8_ERR_ALIGNMENT;
   RouteParams p{};
   p.experts = experts;
@@ -881,7 +874,6 @@ fp8_status fp8_moe_route(const void* experts, int32_t id_bytes, int64_t tokens, 
   p.offsets = offsets;
   p.pos = pos;
   p.src = src;
-  p.counts = static_cast<int*>(workspace);
   return cuda_status(launch_route(p, stream));
 }
 

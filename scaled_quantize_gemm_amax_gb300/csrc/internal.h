@@ -220,10 +220,8 @@ struct RouteParams {
   int* offsets;          // [n_experts + 1]
   int* pos;              // [n]
   int* src;              // [capacity]
-  int* counts;           // [route_blocks(n)][n_experts]
   int64_t per_block;     // set by the launcher
 };
-int route_blocks(int64_t n);
 cudaError_t launch_route(RouteParams p, cudaStream_t s);
 struct ScatterParams {
   const void* in;        // [tokens, cols]

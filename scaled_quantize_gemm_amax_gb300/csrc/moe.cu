@@ -19,59 +19,56 @@ namespace {
 // ------------------------------------------------------------------ route
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kRouteBlocks = 128;       // most blocks of a route: each adds up all blocks' counts
-constexpr int kRouteSingle = 4096;      // most choices that one block sorts alone
+constexpr int kRouteBlocks = 8;   // most blocks of the one cluster that sorts
 
 __device__ __forceinline__ int expert_of(const RouteParams& p, int64_t i) {
   const int64_t e = p.ids64 ? static_cast<const int64_t*>(p.experts)[i] : static_cast<const int32_t*>(p.experts)[i];
   return e >= 0 && e < p.n_experts ? static_cast<int>(e) : -1;
 }
-
-// counts[block][expert] of the block's choices
-__global__ void __launch_bounds__(kRouteThreads) k_route_count(const RouteParams p) {
-  extern __shared__ int hist[];
-  pdl_wait();
-  pdl_launch_dependents();
-  for (int e = threadIdx.x; e < p.n_experts; e += kRouteThreads) hist[e] = 0;
-  __syncthreads();
-  const int64_t i1 = min(p.n, (blockIdx.x + 1) * p.per_block);
-  for (int64_t i = blockIdx.x * p.per_block + threadIdx.x; i < i1; i += kRouteThreads) {
-    const int e = expert_of(p, i);
-    if (e >= 0) atomicAdd(hist + e, 1);
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.n_experts; e += kRouteThreads)
-    p.counts[static_cast<int64_t>(blockIdx.x) * p.n_experts + e] = hist[e];
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
-// Shared memory: next[E], the row of the expert's next choice (first its count, when one block
-// sorts alone), and of[kRouteWarps][E], the warps' counts within 1024 choices.
-__global__ void __launch_bounds__(kRouteThreads) k_route_place(const RouteParams p) {
+// One cluster: every block counts its contiguous part of the choices, reads the other blocks'
+// counts from their shared memory, and then places its part in order, 1024 choices at a time.
+// One launch, no workspace: bound by latency (8192 tokens with 2 choices: 5.6 us as two launches
+// that exchanged the counts through global memory).
+// Shared memory: hist[E], this block's counts; next[E], the row of the expert's next choice;
+// used[E], the row past its last; of[kRouteWarps][E], the warps' counts within 1024 choices.
+__global__ void __launch_bounds__(kRouteThreads) k_route(const RouteParams p) {
   extern __shared__ int smem[];
   __shared__ int warp_total[kRouteWarps];
   const int E = p.n_experts, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int* next = smem;
-  uint16_t* of = reinterpret_cast<uint16_t*>(smem + E);
+  const int blocks = gridDim.x, rank = blockIdx.x;
+  int *hist = smem, *next = smem + E, *used = smem + 2 * E;
+  uint16_t* of = reinterpret_cast<uint16_t*>(smem + 3 * E);
+  if (tid < E) hist[tid] = 0;
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t i0 = blockIdx.x * p.per_block, i1 = min(p.n, i0 + p.per_block);
+  const int64_t i0 = rank * p.per_block, i1 = min(p.n, i0 + p.per_block);
+  for (int64_t i = i0 + tid; i < i1; i += kRouteThreads) {
+    const int e = expert_of(p, i);
+    if (e >= 0) atomicAdd(hist + e, 1);
+  }
   // this expert's choices in all blocks, and in the blocks before this one
   int total = 0, before = 0;
-  if (p.counts == nullptr) {
-    if (tid < E) next[tid] = 0;
-    __syncthreads();
-    for (int64_t i = i0 + tid; i < i1; i += kRouteThreads) {
-      const int e = expert_of(p, i);
-      if (e >= 0) atomicAdd(next + e, 1);
+  if (blocks > 1) {
+    cluster_sync();
+    if (tid < E) {
+      const uint32_t mine = smem_u32(hist + tid);
+      for (int b = 0; b < blocks; ++b) {
+        const int c = ld_cluster(mapa_shared(mine, b));
+        total += c;
+        before += b < rank ? c : 0;
+      }
     }
+    cluster_sync();   // no block leaves while another still reads its counts
+  } else {
     __syncthreads();
-    if (tid < E) total = next[tid];
-  } else if (tid < E) {
-    for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-      const int c = p.counts[static_cast<int64_t>(b) * E + tid];
-      total += c;
-      before += b < static_cast<int>(blockIdx.x) ? c : 0;
-    }
+    if (tid < E) total = hist[tid];
   }
   // exclusive scan of the padded totals over the experts
   const int padded = static_cast<int>((static_cast<int64_t>(total) + p.align - 1) / p.align * p.align);
@@ -83,38 +80,44 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_place(const RouteParams
   }
   if (lane == 31) warp_total[warp] = incl;
   __syncthreads();
-  int off = incl - padded;
-  for (int w = 0; w < warp; ++w) off += warp_total[w];
+  int off = incl - padded, rows = 0;
+  for (int w = 0; w < kRouteWarps; ++w) {
+    off += w < warp ? warp_total[w] : 0;
+    rows += warp_total[w];
+  }
   if (tid < E) {
     next[tid] = off + before;
-    if (blockIdx.x == 0) {
+    used[tid] = off + total;
+    if (rank == 0) {
       p.offsets[tid] = off;
-      if (tid == E - 1) p.offsets[E] = off + padded;
+      if (tid == E - 1) p.offsets[E] = rows;
     }
   }
-  // rows that pad this expert's segment, shared out over the blocks by expert; then the rows
-  // past the last segment
-  if (tid < E && tid % gridDim.x == blockIdx.x) {
-    for (int r = off + total; r < off + padded; ++r) p.src[r] = -1;
+  __syncthreads();
+  // rows that pad a segment, a warp an expert; then the rows past the last segment
+  if (p.align > 1) {
+    for (int e = rank * kRouteWarps + warp; e < E; e += blocks * kRouteWarps) {
+      const int r0 = used[e], r1 = (r0 + p.align - 1) / p.align * p.align;   // segments start at multiples of align
+      for (int r = r0 + lane; r < r1; r += 32) p.src[r] = -1;
+    }
   }
-  int rows = 0;
-  for (int w = 0; w < kRouteWarps; ++w) rows += warp_total[w];
-  for (int64_t r = rows + static_cast<int64_t>(blockIdx.x) * kRouteThreads + tid; r < p.capacity;
-       r += static_cast<int64_t>(gridDim.x) * kRouteThreads)
+  for (int64_t r = rows + static_cast<int64_t>(rank) * kRouteThreads + tid; r < p.capacity;
+       r += static_cast<int64_t>(blocks) * kRouteThreads)
     p.src[r] = -1;
   // 1024 choices at a time: a choice's rank is the choices of its expert in the warps before,
   // then in the lanes before
   for (int64_t base = i0; base < i1; base += kRouteThreads) {
-    for (int i = tid; i < E * kRouteWarps / 2; i += kRouteThreads) reinterpret_cast<uint32_t*>(of)[i] = 0;
-    __syncthreads();
     const int64_t i = base + tid;
     const int e = i < i1 ? expert_of(p, i) : -1;
+    for (int k = tid; k < E * kRouteWarps / 2; k += kRouteThreads) reinterpret_cast<uint32_t*>(of)[k] = 0;
+    __syncthreads();
     const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    if (e >= 0 && rank == 0) of[warp * E + e] = static_cast<uint16_t>(__popc(same));
+    const int in_warp = __popc(same & ((1u << lane) - 1u));
+    if (e >= 0 && in_warp == 0) of[warp * E + e] = static_cast<uint16_t>(__popc(same));
     __syncthreads();
     int sum = 0;
     if (tid < E) {
+#pragma unroll 8
       for (int w = 0; w < kRouteWarps; ++w) {
         const int c = of[w * E + tid];
         of[w * E + tid] = static_cast<uint16_t>(sum);
@@ -123,7 +126,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_place(const RouteParams
     }
     __syncthreads();
     if (i < i1) {
-      const int row = e >= 0 ? next[e] + of[warp * E + e] + rank : -1;
+      const int row = e >= 0 ? next[e] + of[warp * E + e] + in_warp : -1;
       p.pos[i] = row;
       if (row >= 0) p.src[row] = static_cast<int>(i);
     }
@@ -339,32 +342,20 @@ unsigned grid_of(int64_t want, int num_sms, int per_sm) {
   return static_cast<unsigned>(want < 1 ? 1 : (want > cap ? cap : want));
 }
 
-size_t place_smem(int experts) {
-  return static_cast<size_t>(experts) * (sizeof(int) + kRouteWarps * sizeof(uint16_t));
+size_t route_smem(int experts) {
+  return static_cast<size_t>(experts) * (3 * sizeof(int) + kRouteWarps * sizeof(uint16_t));
 }
 
 }  // namespace
 
-int route_blocks(int64_t n) {
-  if (n <= kRouteSingle) return 1;
-  const int64_t b = (n + kRouteThreads - 1) / kRouteThreads;
-  return static_cast<int>(b < kRouteBlocks ? b : kRouteBlocks);
-}
-
 cudaError_t launch_route(RouteParams p, cudaStream_t s) {
   static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = ensure_smem_limit(k_route_place, static_cast<int>(place_smem(kMaxExperts)), done);
+  const cudaError_t e = ensure_smem_limit(k_route, static_cast<int>(route_smem(kMaxExperts)), done);
   if (e != cudaSuccess) return e;
-  const unsigned blocks = static_cast<unsigned>(route_blocks(p.n));
-  // whole multiples of 1024 choices a block
-  p.per_block = ((p.n + blocks - 1) / blocks + kRouteThreads - 1) / kRouteThreads * kRouteThreads;
-  if (blocks == 1) {
-    p.counts = nullptr;
-  } else {
-    e = launch_pdl(k_route_count, dim3(blocks), dim3(kRouteThreads), p.n_experts * sizeof(int), s, 1, p);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(k_route_place, dim3(blocks), dim3(kRouteThreads), place_smem(p.n_experts), s, 1, p);
+  int blocks = 1;
+  while (blocks < kRouteBlocks && static_cast<int64_t>(blocks) * kRouteThreads < p.n) blocks *= 2;
+  p.per_block = (p.n + blocks - 1) / blocks;
+  return launch_pdl(k_route, dim3(static_cast<unsigned>(blocks)), dim3(kRouteThreads), route_smem(p.n_experts), s, blocks, p);
 }
 
 namespace {

@@ -71,10 +71,10 @@ def test_route_extremes():
     assert r.src.numel() == 0 and host(r.offsets).tolist() == [0] * 5
     # more room than needed: the rows past the last segment are marked as padding too
     ids = choices(700, 2, 8, 5)
-    cap = fq.fp8_moe_sizes(700, 2, 8, 128)[0] + 1000
+    cap = fq.fp8_moe_capacity(700, 2, 8, 128) + 1000
     offsets, src = torch.empty(9, dtype=torch.int32, device="cuda"), torch.empty(cap, dtype=torch.int32, device="cuda")
     pos = torch.empty((700, 2), dtype=torch.int32, device="cuda")
-    fq.fp8_moe_route(ids, 8, 128, offsets, pos, src, None)
+    fq.fp8_moe_route(ids, 8, 128, offsets, pos, src)
     ref = route_ref(host(ids), 8, 128, cap)
     for a, b in zip((offsets, pos, src), ref):
         assert np.array_equal(host(a), b)
@@ -200,14 +200,14 @@ def test_rows_out_of_range_are_reported_not_used():
 def test_writes_stay_inside():
     tokens, k, n, cols = 77, 3, 6, 1001
     ids = choices(tokens, k, n, 750)
-    cap, nbytes = fq.fp8_moe_sizes(tokens, k, n, 16)
+    cap = fq.fp8_moe_capacity(tokens, k, n, 16)
     g = {name: Guarded(shape, dt) for name, shape, dt in (
         ("offsets", (n + 1,), torch.int32), ("pos", (tokens, k), torch.int32), ("src", (cap,), torch.int32),
         ("xs", (cap, cols), torch.bfloat16), ("y", (tokens, cols), torch.bfloat16), ("dys", (cap, cols), torch.bfloat16),
         ("dw", (tokens, k), torch.float32))}
     t = {name: v.t for name, v in g.items()}
     x, w = matrix(tokens, cols, torch.bfloat16, 751), torch.rand((tokens, k), device="cuda")
-    fq.fp8_moe_route(ids, n, 16, t["offsets"], t["pos"], t["src"], None)
+    fq.fp8_moe_route(ids, n, 16, t["offsets"], t["pos"], t["src"])
     fq.fp8_moe_dispatch(x, t["pos"], t["src"], t["xs"])
     fq.fp8_moe_combine(t["xs"], t["pos"], w, t["y"])
     fq.fp8_moe_combine_backward(x, t["pos"], t["src"], w, t["xs"], t["dys"], t["dw"])
@@ -220,12 +220,10 @@ def test_a_graph_on_another_stream():
     ids, x = choices(6000, 2, 8, 760), matrix(6000, 256, torch.bfloat16, 761)
     ref = fq.moe_route(ids, 8, 128)
     xs_ref = fq.moe_dispatch(x, ref)
-    cap, nbytes = fq.fp8_moe_sizes(6000, 2, 8, 128)
     outs = [torch.empty_like(t) for t in (*ref, xs_ref)]
-    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):          # captures on a stream of its own
-        fq.fp8_moe_route(ids, 8, 128, *outs[:3], ws)
+        fq.fp8_moe_route(ids, 8, 128, *outs[:3])
         fq.fp8_moe_dispatch(x, outs[1], outs[2], outs[3])
     for _ in range(2):
         for t in outs:
