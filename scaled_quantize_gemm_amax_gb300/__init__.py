@@ -764,7 +764,8 @@ def moe_route(experts, n_experts: int, align: int = 1, stream=None) -> MoeRoute:
 
     align=128 makes every expert's segment an operand of scaled_gemm."""
     tokens, k = experts.shape
-    capacity = fp8_moe_capacity(tokens, k, n_experts, align)
+    n = tokens * k
+    capacity = (n + min(n, n_experts) * (align - 1)) // max(align, 1) * align   # fp8_moe_capacity
     dev = experts.device
     offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
     pos = torch.empty((tokens, k), dtype=torch.int32, device=dev)

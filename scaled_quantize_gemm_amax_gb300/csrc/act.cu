@@ -96,7 +96,7 @@ __device__ __forceinline__ void act_grad2(float2 x, float2& f, float2& df) {
 constexpr int kPieces = 2;
 
 template <typename T, bool VECTOR, int ACT, bool GATED>
-__global__ void __launch_bounds__(kThreads, 4) k_act(const ActParams p) {
+__global__ void __launch_bounds__(kThreads, VECTOR ? 4 : 3) k_act(const ActParams p) {
   using P = Piece<T, VECTOR>;
   constexpr int E = P::E;
   const int lane = threadIdx.x & 31, cols = static_cast<int>(p.cols), groups = (cols + 127) / 128;
@@ -110,24 +110,26 @@ __global__ void __launch_bounds__(kThreads, 4) k_act(const ActParams p) {
     const T* pa = static_cast<const T*>(p.a) + row * p.lda + c;
     const T* pb = static_cast<const T*>(p.b) + row * p.ldb + c;
     T* py = static_cast<T*>(p.y) + row * p.ldy + c;
+    uint4 ra[kPieces], rb[kPieces];
+    P::load_raw(pa, c, left, ra);
+    if (GATED) P::load_raw(pb, c, left, rb);
     float a[kPieces][E], b[kPieces][E];
+    uint4 y[kPieces];
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
-      P::load(pa + k * P::WC, left - k * P::WC, a[k]);
-      if (GATED) P::load(pb + k * P::WC, left - k * P::WC, b[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      float y[E];
+      P::unpack(ra[k], a[k]);
+      if (GATED) P::unpack(rb[k], b[k]);
+      float v[E];
 #pragma unroll
       for (int i = 0; i < E; i += 2) {
         float2 f = act_value2<ACT>(make_float2(a[k][i], a[k][i + 1]));
         if (GATED) f = mul2(f, make_float2(b[k][i], b[k][i + 1]));
-        y[i] = f.x;
-        y[i + 1] = f.y;
+        v[i] = f.x;
+        v[i + 1] = f.y;
       }
-      P::store(py + k * P::WC, left - k * P::WC, y);
+      y[k] = P::pack(v);
     }
+    P::store_raw(py, left, y);
     const int64_t q = row * p.ldq + c, s = row * groups + c / 128;
     if (p.qa != nullptr) store_copies<P, kPieces>(p.qa + q, p.sa + s, lane, left, p.e5m2, a);
     if (GATED && p.qb != nullptr) store_copies<P, kPieces>(p.qb + q, p.sb + s, lane, left, p.e5m2, b);
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_act(const ActParams p) {
 }
 
 template <typename T, bool VECTOR, int ACT, bool GATED, bool CODES>
-__global__ void __launch_bounds__(kThreads, 4) k_act_backward(const ActBwdParams p) {
+__global__ void __launch_bounds__(kThreads, VECTOR ? 4 : 3) k_act_backward(const ActBwdParams p) {
   using P = Piece<T, VECTOR>;
   constexpr int E = P::E;
   const int lane = threadIdx.x & 31, cols = static_cast<int>(p.cols), groups = (cols + 127) / 128;
@@ -147,49 +149,55 @@ __global__ void __launch_bounds__(kThreads, 4) k_act_backward(const ActBwdParams
     const int64_t row = at.row;
     const int c = static_cast<int>(at.piece) * kPieces * P::WC + P::first(lane), left = cols - c;
     const int64_t q = row * p.ldq + c, s = row * groups + c / 128;
-    float dy[kPieces][E], a[kPieces][E], b[kPieces][E];
+    uint4 rdy[kPieces], ra[kPieces], rb[kPieces];
     typename P::Codes ca[kPieces], cb[kPieces];
     float sa[kPieces], sb[kPieces];
+    P::load_raw(static_cast<const T*>(p.dy) + row * p.lddy + c, c, left, rdy);
+    if (CODES) {
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      const int off = k * P::WC, rest = left - off;
-      P::load(static_cast<const T*>(p.dy) + row * p.lddy + c + off, rest, dy[k]);
-      if (CODES) {
-        ca[k] = P::load_codes(p.qa + q + off, rest);
+      for (int k = 0; k < kPieces; ++k) {
+        const int off = k * P::WC, rest = left - off;
+        ca[k] = P::load_codes(p.qa + q + off, c + off, rest);
         sa[k] = rest > 0 ? __ldg(p.sa + s + off / 128) : 0.0f;
         if (GATED) {
-          cb[k] = P::load_codes(p.qb + q + off, rest);
+          cb[k] = P::load_codes(p.qb + q + off, c + off, rest);
           sb[k] = rest > 0 ? __ldg(p.sb + s + off / 128) : 0.0f;
         }
-      } else {
-        P::load(static_cast<const T*>(p.a) + row * p.lda + c + off, rest, a[k]);
-        if (GATED) P::load(static_cast<const T*>(p.b) + row * p.ldb + c + off, rest, b[k]);
       }
+    } else {
+      P::load_raw(static_cast<const T*>(p.a) + row * p.lda + c, c, left, ra);
+      if (GATED) P::load_raw(static_cast<const T*>(p.b) + row * p.ldb + c, c, left, rb);
     }
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
-      const int off = k * P::WC, rest = left - off;
+      float dy[E], a[E], b[E];
+      P::unpack(rdy[k], dy);
       if (CODES) {
-        P::decode(ca[k], sa[k], p.e5m2, a[k]);
-        if (GATED) P::decode(cb[k], sb[k], p.e5m2, b[k]);
+        P::decode(ca[k], sa[k], p.e5m2, a);
+        if (GATED) P::decode(cb[k], sb[k], p.e5m2, b);
+      } else {
+        P::unpack(ra[k], a);
+        if (GATED) P::unpack(rb[k], b);
       }
 #pragma unroll
       for (int i = 0; i < E; i += 2) {
-        const float2 d = make_float2(dy[k][i], dy[k][i + 1]);
+        const float2 d = make_float2(dy[i], dy[i + 1]);
         float2 f, df, da;
-        act_grad2<ACT>(make_float2(a[k][i], a[k][i + 1]), f, df);
-        da = mul2(GATED ? mul2(d, make_float2(b[k][i], b[k][i + 1])) : d, df);
-        a[k][i] = da.x;
-        a[k][i + 1] = da.y;
+        act_grad2<ACT>(make_float2(a[i], a[i + 1]), f, df);
+        da = mul2(GATED ? mul2(d, make_float2(b[i], b[i + 1])) : d, df);
+        a[i] = da.x;
+        a[i + 1] = da.y;
         if (GATED) {
           f = mul2(d, f);
-          b[k][i] = f.x;
-          b[k][i + 1] = f.y;
+          b[i] = f.x;
+          b[i + 1] = f.y;
         }
       }
-      P::store(static_cast<T*>(p.da) + row * p.ldda + c + off, rest, a[k]);
-      if (GATED) P::store(static_cast<T*>(p.db) + row * p.lddb + c + off, rest, b[k]);
+      ra[k] = P::pack(a);
+      if (GATED) rb[k] = P::pack(b);
     }
+    P::store_raw(static_cast<T*>(p.da) + row * p.ldda + c, left, ra);
+    if (GATED) P::store_raw(static_cast<T*>(p.db) + row * p.lddb + c, left, rb);
   }
 }
 

@@ -176,7 +176,7 @@ struct Choices {
 // choice fills to zero.
 constexpr int kZeroRows = 4;
 template <typename T, bool VECTOR, bool DOTS, int FLIGHT>
-__global__ void __launch_bounds__(kThreads, !DOTS ? 5 : FLIGHT > 2 ? 3 : 4) k_scatter(const ScatterParams p, const int warps) {
+__global__ void __launch_bounds__(kThreads, VECTOR ? (!DOTS ? 5 : FLIGHT > 2 ? 3 : 4) : (!DOTS ? 3 : 2)) k_scatter(const ScatterParams p, const int warps) {
   using P = Piece<T, VECTOR>;
   __shared__ float part[2][kWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / warps, w_in = warp - group * warps;
@@ -192,12 +192,10 @@ __global__ void __launch_bounds__(kThreads, !DOTS ? 5 : FLIGHT > 2 ? 3 : 4) k_sc
     if (t >= p.tokens) {
       const int64_t r0 = ((t - p.tokens) * warps + w_in) * kZeroRows, r = r0 + lane;
       uint32_t empty = __ballot_sync(0xFFFFFFFFu, lane < kZeroRows && r < p.capacity && __ldg(p.src + r) < 0);
-      float zero[P::E];
-#pragma unroll
-      for (int i = 0; i < P::E; ++i) zero[i] = 0.0f;
+      const uint4 zero[1] = {make_uint4(0u, 0u, 0u, 0u)};
       for (; empty != 0; empty &= empty - 1) {
         T* out = static_cast<T*>(p.out) + (r0 + __ffs(empty) - 1) * p.ldout;
-        for (int c = P::first(lane); c < cols; c += P::WC) P::store(out + c, cols - c, zero);
+        for (int c0 = 0, c = P::first(lane); c0 < cols; c0 += P::WC, c += P::WC) P::store_raw(out + c, cols - c, zero);
       }
       continue;
     }
@@ -212,8 +210,7 @@ __global__ void __launch_bounds__(kThreads, !DOTS ? 5 : FLIGHT > 2 ? 3 : 4) k_sc
       for (int cb = w_in * kPieces * P::WC; cb < cols; cb += block_cols) {
         const int first = cb + P::first(lane), left = cols - first;
         uint4 raw[kPieces];
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) raw[i] = P::load_raw(in + first + i * P::WC, left - i * P::WC);
+        P::load_raw(in + first, first, left, raw);
         for (int j = 0; j < n; j += FLIGHT) {
           uint4 o[DOTS ? FLIGHT : 1][kPieces];
           if constexpr (DOTS) {
@@ -223,7 +220,8 @@ __global__ void __launch_bounds__(kThreads, !DOTS ? 5 : FLIGHT > 2 ? 3 : 4) k_sc
               const bool on = j + u < n && pos >= 0;
               const T* other = static_cast<const T*>(p.other) + (on ? pos : 0) * p.ldother + first;
 #pragma unroll
-              for (int i = 0; i < kPieces; ++i) o[u][i] = P::load_raw(other + i * P::WC, on ? left - i * P::WC : 0);
+              for (int i = 0; i < kPieces; ++i) o[u][i] = make_uint4(0u, 0u, 0u, 0u);
+              if (on) P::load_raw(other, first, left, o[u]);
             }
           }
 #pragma unroll
@@ -234,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, !DOTS ? 5 : FLIGHT > 2 ? 3 : 4) k_sc
             if (pos < 0) continue;
             T* out = static_cast<T*>(p.out) + pos * p.ldout + first;
             float2 dot = {0.0f, 0.0f};
+            uint4 moved[kPieces];
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
               float v[P::E], y[P::E];
@@ -244,13 +243,14 @@ __global__ void __launch_bounds__(kThreads, !DOTS ? 5 : FLIGHT > 2 ? 3 : 4) k_sc
                 y[e] = m.x;
                 y[e + 1] = m.y;
               }
-              P::store(out + i * P::WC, left - i * P::WC, y);
+              moved[i] = P::pack(y);
               if constexpr (DOTS) {
                 P::unpack(o[u][i], y);
 #pragma unroll
                 for (int e = 0; e < P::E; e += 2) dot = fma2(make_float2(v[e], v[e + 1]), make_float2(y[e], y[e + 1]), dot);
               }
             }
+            P::store_raw(out, left, moved);
             if constexpr (DOTS) {
               const float d = warp_sum(dot.x + dot.y);
               if (lane == j + u) my_dot += d;
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, !DOTS ? 5 : FLIGHT > 2 ? 3 : 4) k_sc
 
 // A warp per kPieces pieces of a token's row: y[t] = sum_j w_j ys[pos_j], the choices in order.
 template <typename T, bool VECTOR, int FLIGHT>
-__global__ void __launch_bounds__(kThreads, FLIGHT > 2 ? 3 : 4) k_combine(const CombineParams p) {
+__global__ void __launch_bounds__(kThreads, VECTOR ? (FLIGHT > 2 ? 3 : 4) : 2) k_combine(const CombineParams p) {
   using P = Piece<T, VECTOR>;
   const int lane = threadIdx.x & 31, cols = static_cast<int>(p.cols);
   Walk at(static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), static_cast<int64_t>(gridDim.x) * kWarps,
@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(kThreads, FLIGHT > 2 ? 3 : 4) k_combine(const 
           const bool on = j + u < n && pos >= 0;
           const T* ys = static_cast<const T*>(p.ys) + (on ? pos : 0) * p.ldys + first;
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) raw[u][i] = P::load_raw(ys + i * P::WC, on ? left - i * P::WC : 0);
+          for (int i = 0; i < kPieces; ++i) raw[u][i] = make_uint4(0u, 0u, 0u, 0u);
+          if (on) P::load_raw(ys, first, left, raw[u]);
         }
 #pragma unroll
         for (int u = 0; u < FLIGHT; ++u) {
@@ -328,8 +329,7 @@ __global__ void __launch_bounds__(kThreads, FLIGHT > 2 ? 3 : 4) k_combine(const 
       }
     }
     T* y = static_cast<T*>(p.y) + t * p.ldy + first;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) P::store(y + i * P::WC, left - i * P::WC, acc[i]);
+    P::store(y, left, acc);
   }
 }
 

@@ -65,19 +65,19 @@ __global__ void __launch_bounds__(kThreads) k_norm_any(const NormParams p) {
       if (p.rstd != nullptr) p.rstd[row] = rstd;
     }
     using P = Piece<T, false>;
-    for (int g = warp; g < groups; g += kWarps) {
-      const int c = g * 128 + lane, left = cols - c;
-      float v[4], w[4], b[4], xh[1][4];
-      P::load(x + c, left, v);
+    for (int c0 = warp * P::WC; c0 < cols; c0 += kWarps * P::WC) {
+      const int c = c0 + P::first(lane), left = cols - c;
+      float v[1][P::E], w[P::E], b[P::E], xh[1][P::E];
+      P::load(x + c, c, left, v);
       P::load_param(p.w, p.w_f32, c, left, 1.0f, w);
       P::load_param(p.b, p.w_f32, c, left, 0.0f, b);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        xh[0][i] = (v[i] - mean) * rstd;
-        v[i] = fmaf(xh[0][i], w[i], b[i]);
+      for (int i = 0; i < P::E; ++i) {
+        xh[0][i] = (v[0][i] - mean) * rstd;
+        v[0][i] = fmaf(xh[0][i], w[i], b[i]);
       }
       P::store(y + c, left, v);
-      if (p.q != nullptr) store_copies<P, 1>(p.q + row * p.ldq + c, p.s + row * groups + g, lane, left, p.e5m2, xh);
+      if (p.q != nullptr) store_copies<P, 1>(p.q + row * p.ldq + c, p.s + row * groups + c / 128, lane, left, p.e5m2, xh);
     }
   }
 }
@@ -91,33 +91,28 @@ template <typename T, bool VECTOR, int V>
 __global__ void __launch_bounds__(kBlockWarps * 32) k_norm(const NormParams p, const int warps, const int stages, const int ring) {
   using P = Piece<T, VECTOR>;
   constexpr int E = P::E, J = V / E, kCols = 32 * V;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 red[2][kBlockWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / warps, w_in = warp - group * warps;
   const int n_groups = (blockDim.x >> 5) / warps, step = gridDim.x * n_groups;
   const int rows = static_cast<int>(p.rows), cols = static_cast<int>(p.cols), groups8 = (cols + 127) / 128;
   const int ldx = static_cast<int>(p.ldx), ldy = static_cast<int>(p.ldy), ldq = static_cast<int>(p.ldq);
+  using Part = RowPart<P, kCols, VECTOR, T>;
   // this lane's first column and the columns from there to the row's end
-  const int c = w_in * kCols + P::first(lane), left = cols - c;
+  const int base = w_in * kCols, c = base + P::first(lane), left = cols - c;
   const float inv_nw = 1.0f / static_cast<float>(min(cols - w_in * kCols, kCols)), inv_n = 1.0f / static_cast<float>(cols);
   // columns of the warp that this lane joins below
   const float n_l = lane < warps ? static_cast<float>(min(cols - lane * kCols, kCols)) : 0.0f;
-  const T* const x0 = static_cast<const T*>(p.x) + (left > 0 ? c : 0);
-  // this thread's 16 bytes of piece j in stage s: slot + (s * J + j) * 512
-  uint8_t* const slot = smem + ring + (warp * stages * J * 32 + lane) * 16;
+  uint8_t* const slots = smem + ring + warp * stages * Part::kBytes;   // the warp's part of its group's next rows
   float* const ws = reinterpret_cast<float*>(smem);
   float* const bs = ws + warps * kCols;
 
   auto issue = [&](int row, int s) {
-    if constexpr (VECTOR) {
-      if (row < rows) {
-        const T* x = x0 + static_cast<int64_t>(row) * ldx;
-        const uint32_t to = smem_u32(slot) + s * J * 512;
-#pragma unroll
-        for (int j = 0; j < J; ++j) cp_async<16>(to + j * 512, left > j * P::WC ? x + j * P::WC : x, left > j * P::WC);
-      }
-      cp_async_commit();
+    if (row < rows) {
+      const int64_t before = static_cast<int64_t>(row) * ldx;
+      Part::start(slots + s * Part::kBytes, static_cast<const T*>(p.x) + before, before, base, cols, lane);
     }
+    cp_async_commit();
   };
   pdl_wait();
   pdl_launch_dependents();
@@ -126,21 +121,15 @@ __global__ void __launch_bounds__(kBlockWarps * 32) k_norm(const NormParams p, c
   start_param<P, V>(p.b, p.w_f32, cols, warps, 0.0f, bs);
   cp_async_commit();
   for (int s = 0; s < stages; ++s) issue(row + s * step, s);
-  cp_async_wait_oldest(VECTOR ? stages + 1 : 1);
+  cp_async_wait_oldest(stages + 1);
   settle_param<P, V>(p.w, p.w_f32, warps, ws);
   settle_param<P, V>(p.b, p.w_f32, warps, bs);
   __syncthreads();
   for (int s = 0, buf = 0; row < rows; row += step, buf ^= 1) {
     float x[J][E];
-    if constexpr (VECTOR) {
-      cp_async_wait_oldest(stages);
-#pragma unroll
-      for (int j = 0; j < J; ++j) P::unpack(*reinterpret_cast<const uint4*>(slot + (s * J + j) * 512), x[j]);
-    } else {
-      const T* in = x0 + static_cast<int64_t>(row) * ldx;
-#pragma unroll
-      for (int j = 0; j < J; ++j) P::load(in + j * P::WC, left - j * P::WC, x[j]);
-    }
+    cp_async_wait_oldest(stages);
+    if (!VECTOR) __syncwarp();   // other lanes copied some of this lane's elements
+    Part::read(slots + s * Part::kBytes, Part::past(static_cast<const T*>(p.x) + static_cast<int64_t>(row) * ldx + base), lane, x);
     float2 acc = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < J; ++j)
@@ -177,26 +166,31 @@ __global__ void __launch_bounds__(kBlockWarps * 32) k_norm(const NormParams p, c
       if (p.mean != nullptr) p.mean[row] = mean;
       if (p.rstd != nullptr) p.rstd[row] = rstd;
     }
+    if (!VECTOR) __syncwarp();   // other lanes have read this lane's granules
     issue(row + stages * step, s);
     s = s + 1 == stages ? 0 : s + 1;
-    T* const y0 = static_cast<T*>(p.y) + static_cast<int64_t>(row) * ldy + c;
+    uint4 y[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int off = j * P::WC, rest = left - off;
-      float y[E], w[E], b[E];
+      float v[E], w[E], b[E];
       read_param<P, V>(ws, w_in, j, lane, w);
       read_param<P, V>(bs, w_in, j, lane, b);
 #pragma unroll
       for (int i = 0; i < E; i += 2) {
         const float2 h = mul2(add2(make_float2(x[j][i], x[j][i + 1]), both(-mean)), both(rstd));
-        const float2 v = fma2(h, make_float2(w[i], w[i + 1]), make_float2(b[i], b[i + 1]));
+        const float2 o = fma2(h, make_float2(w[i], w[i + 1]), make_float2(b[i], b[i + 1]));
         x[j][i] = h.x;
         x[j][i + 1] = h.y;
-        y[i] = v.x;
-        y[i + 1] = v.y;
+        v[i] = o.x;
+        v[i + 1] = o.y;
       }
-      P::store(y0 + off, rest, y);
+      y[j] = P::pack(v);
+      if constexpr (VECTOR) {   // at once, without waiting in registers
+        const uint4 one[1] = {y[j]};
+        P::store_raw(static_cast<T*>(p.y) + static_cast<int64_t>(row) * ldy + c + j * P::WC, left - j * P::WC, one);
+      }
     }
+    if constexpr (!VECTOR) P::store_raw(static_cast<T*>(p.y) + static_cast<int64_t>(row) * ldy + c, left, y);
     if (p.q != nullptr) {
       constexpr int N = J < 4 ? J : 4;
       uint8_t* const q = p.q + static_cast<int64_t>(row) * ldq + c;
@@ -216,7 +210,8 @@ __global__ void __launch_bounds__(kBlockWarps * 32) k_norm(const NormParams p, c
 
 template <typename T, bool VECTOR, int V>
 cudaError_t run_norm(const NormParams& p, int num_sms, cudaStream_t s) {
-  const NormPlan n = norm_plan(p.rows, p.cols, 32 * V, kBlockWarps, 2, VECTOR ? 32 * V * static_cast<int>(sizeof(T)) : 0, num_sms);
+  const NormPlan n = norm_plan(p.rows, p.cols, 32 * V, kBlockWarps, 2,
+                               RowPart<Piece<T, VECTOR>, 32 * V, VECTOR, T>::kBytes, num_sms);
   static std::atomic<bool> done[kMaxDevices];
   const cudaError_t e = ensure_smem_limit(k_norm<T, VECTOR, V>, kNormSmem, done);
   if (e != cudaSuccess) return e;

@@ -1,8 +1,9 @@
 // norm.cuh -- how the layer norm kernels divide rows: a group of `warps` warps holds one row at
 // a time, each warp a fixed number of its columns, and walks the rows grid-wide.  A block holds
 // as many groups as its warps allow (what fits an SM's registers), and there is a block an SM.
-// The next rows of each group are on their way into shared memory by asynchronous copies
-// (every thread copies the bytes it will read itself, so no barrier guards them).
+// The next rows of each group are on their way into shared memory by asynchronous copies of 16
+// bytes a lane.  Rows that are not 16-byte aligned are copied by their granules and shifted into
+// place on reading; a warp reads what its own lanes copied, so no block barrier guards them.
 #pragma once
 #include "internal.h"
 #include "rowops.cuh"
@@ -41,13 +42,17 @@ inline NormPlan norm_plan(int64_t rows, int64_t cols, int warp_cols, int block_w
   return n;
 }
 
+// the first n of BYTES bytes, and zeros
 template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? BYTES : 0;   // 0: the destination is filled with zeros
+__device__ __forceinline__ void cp_async_part(uint32_t dst, const void* src, int n) {
   if constexpr (BYTES == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
+  cp_async_part<BYTES>(dst, src, valid ? BYTES : 0);
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
@@ -109,6 +114,85 @@ __device__ __forceinline__ void group_sync(int group, int warps) {
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
 }
 
+// One warp's part of a row, SPAN columns from column `base` on, in shared memory: SPAN / E granules
+// of E elements, unaligned one more.  VECTOR: granule k holds the elements from base + k E on; otherwise
+// from base + k E - m on, where row + base - m is a multiple of E elements.
+template <typename P, int SPAN, bool VECTOR, typename T>
+struct RowPart {
+  static constexpr int G = P::E * static_cast<int>(sizeof(T));   // bytes of a granule (T: the data's type, or one-byte codes)
+  static constexpr int K = SPAN / P::E;
+  // a multiple of 128: 32 lanes' 16 bytes then fill whole lines of shared memory (starting 16 bytes
+  // off them, 8192x4096 forward took 36.8 us instead of 33.6)
+  static constexpr int kBytes = VECTOR ? K * G : (K * G + G + 127) / 128 * 128;
+
+  __device__ static __forceinline__ int past(const T* p) {
+    return VECTOR ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(p) / sizeof(T) % P::E);
+  }
+  // Copies of granules lane, lane + 32, ... of the row that starts at `row`, `before` elements of
+  // whose matrix lie in front of it; zeros past its end.  What a granule holds in front of the
+  // row is never used.
+  __device__ static __forceinline__ void start(uint8_t* to, const T* row, int64_t before, int base, int cols, int lane) {
+    uint32_t at = smem_u32(to) + lane * G;
+    if constexpr (VECTOR) {
+      const int left = cols - base - lane * P::E;
+      const T* const p = row + (left > 0 ? base + lane * P::E : 0);
+#pragma unroll
+      for (int j = 0; j < K / 32; ++j) cp_async<G>(at + j * 32 * G, left > j * P::WC ? p + j * P::WC : p, left > j * P::WC);
+    } else {
+      const int m = past(row + base), c0 = base + lane * P::E - m;
+      const T* const p = row + c0;
+      if (base >= P::E && cols - base >= SPAN + P::E) {   // every granule is the row's: the whole warp takes this way
+#pragma unroll
+        for (int j = 0; j < K / 32; ++j) cp_async<G>(at + j * 32 * G, p + j * P::WC, true);
+        if (lane == 0 && m != 0) cp_async<G>(at + K * G, p + SPAN, true);
+        return;
+      }
+#pragma unroll
+      for (int k0 = 0; k0 <= K; k0 += 32) {
+        const int c = c0 + k0 * P::E;
+        if (k0 == K && (lane != 0 || m == 0)) continue;
+        const int have = min(max(cols - c, 0), P::E);   // elements in front of the row's end
+        if (have > 0 && before + c < 0) {               // a granule that starts in front of the matrix
+          T* const out = reinterpret_cast<T*>(to + (k0 + lane) * G);
+          for (int i = 0; i < P::E; ++i)
+            if (c + i >= 0) out[i] = i < have ? row[c + i] : T(0);
+        } else {
+          cp_async_part<G>(at + k0 * G, have > 0 ? row + c : row + base - m, have * static_cast<int>(sizeof(T)));
+        }
+      }
+    }
+  }
+  // The lane's values of piece j; m = past(row + base).
+  __device__ static __forceinline__ void read(const uint8_t* from, int m, int lane, int j, float (&v)[P::E]) {
+    if constexpr (P::kStrided) {
+#pragma unroll
+      for (int i = 0; i < P::E; ++i) v[i] = *reinterpret_cast<const T*>(from + (m + j * P::WC + lane + P::at(i)) * G / P::E);
+    } else {
+      const uint8_t* const at = from + (j * 32 + lane) * G;
+      uint4 raw = *reinterpret_cast<const uint4*>(at);
+      if (!VECTOR && m != 0) raw = from_byte<sizeof(T)>(raw, *reinterpret_cast<const uint4*>(at + G), m * static_cast<int>(sizeof(T)));
+      P::unpack(raw, v);
+    }
+  }
+  template <int J>
+  __device__ static __forceinline__ void read(const uint8_t* from, int m, int lane, float (&v)[J][P::E]) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) read(from, m, lane, j, v[j]);
+  }
+  // the same of one-byte codes
+  __device__ static __forceinline__ typename P::Codes read_codes(const uint8_t* from, int m, int lane, int j) {
+    if constexpr (P::kStrided) {
+      typename P::Codes c = {};
+#pragma unroll
+      for (int i = 0; i < P::E; ++i) c.u[0] |= static_cast<uint32_t>(from[m + j * P::WC + lane + P::at(i)]) << (8 * i);
+      return c;
+    } else {
+      const uint8_t* const at = from + (j * 32 + lane) * G;
+      const typename P::Codes c = P::read_codes(at);
+      return VECTOR || m == 0 ? c : P::codes_from(c, P::read_codes(at + G), m);
+    }
+  }
+};
 // until at most `stages` - 1 of the committed copies are outstanding
 __device__ __forceinline__ void cp_async_wait_oldest(int stages) {
   if (stages == 5)

@@ -98,6 +98,16 @@ __global__ void __launch_bounds__(kThreads) k_norm_partial_any(const NormBwdPara
   out[p.cols + c] = db;
 }
 
+// Shared memory of one warp's part of one row: dy, x or the codes, and 12 floats: the part's
+// multipliers, rstd and mean.
+template <typename T, bool VECTOR, bool CODES, int V>
+struct NormBackwardStage {
+  using P = Piece<T, VECTOR>;
+  static constexpr int kIn = RowPart<P, 32 * V, VECTOR, T>::kBytes;   // where x or the codes start
+  static constexpr int kScalars = kIn + (CODES ? RowPart<P, 32 * V, VECTOR, uint8_t>::kBytes : RowPart<P, 32 * V, VECTOR, T>::kBytes);
+  static constexpr int kBytes = (kScalars + 48 + 127) / 128 * 128;
+};
+
 // Rows of up to kMostCols columns, V values a lane.  The column sums take 2 V of a thread's
 // registers and g V; xh is read from shared memory twice, before and after the row's sums are
 // known.
@@ -106,10 +116,11 @@ __global__ void __launch_bounds__(BLOCK_WARPS * 32)
     k_norm_backward(const NormBwdParams p, const int warps, const int stages, const int ring) {
   using P = Piece<T, VECTOR>;
   constexpr int E = P::E, J = V / E, H = E / 2, kGroups = V / 4;   // kGroups: of 128 columns in a warp's part
-  constexpr int kIn = CODES ? E : 16;                    // a lane's bytes of x or the codes in one piece
-  constexpr int kPiece = 32 * (16 + kIn);                // a warp's bytes of dy and x / codes in one piece
-  constexpr int kStage = J * kPiece + 48;                // and in one row, with its multipliers, rstd and mean
-  extern __shared__ __align__(16) uint8_t smem[];
+  using PartDy = RowPart<P, 32 * V, VECTOR, T>;
+  using PartQ = RowPart<P, 32 * V, VECTOR, uint8_t>;
+  using Stage = NormBackwardStage<T, VECTOR, CODES, V>;
+  constexpr int kStage = Stage::kBytes, kIn = Stage::kIn, kScalars = Stage::kScalars;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[2][2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / warps, w_in = warp - group * warps;
   const int n_groups = (blockDim.x >> 5) / warps, step = gridDim.x * n_groups;
@@ -117,68 +128,44 @@ __global__ void __launch_bounds__(BLOCK_WARPS * 32)
   const int lddy = static_cast<int>(p.lddy), ldx = static_cast<int>(p.ldx), ldq = static_cast<int>(p.ldq),
             lddx = static_cast<int>(p.lddx);
   // this lane's first column and the columns from there to the row's end
-  const int c = w_in * 32 * V + P::first(lane), left = cols - c, c_in = left > 0 ? c : 0;
+  const int base = w_in * 32 * V, c = base + P::first(lane), left = cols - c;
   const float inv_n = 1.0f / static_cast<float>(cols);
   uint8_t* const mine = smem + ring + warp * stages * kStage;
   float* const ws = reinterpret_cast<float*>(smem);
-  const T* const dy0 = static_cast<const T*>(p.dy) + c_in;
-  const T* const x0 = static_cast<const T*>(p.x) + c_in;
-  const uint8_t* const q0 = p.q + c_in;
 
-  // row `row` into stage s: every lane its own bytes of dy and x / codes; the first lanes
-  // the warp's multipliers, rstd and mean
+  // row `row` into stage s: the warp's part of dy and x / codes; the first lanes the warp's
+  // multipliers, rstd and mean
   auto issue = [&](int row, int s) {
-    if constexpr (VECTOR) {
-      if (row < rows) {
-        const uint32_t to = smem_u32(mine) + s * kStage;
-        const T* dy = dy0 + static_cast<int64_t>(row) * lddy;
-        const T* x = x0 + static_cast<int64_t>(row) * ldx;
-        const uint8_t* q = q0 + static_cast<int64_t>(row) * ldq;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const bool in = left > j * P::WC;
-          const int off = in ? j * P::WC : 0;
-          cp_async<16>(to + j * kPiece + lane * 16, dy + off, in);
-          if constexpr (CODES)
-            cp_async<kIn>(to + j * kPiece + 512 + lane * kIn, q + off, in);
-          else
-            cp_async<16>(to + j * kPiece + 512 + lane * 16, x + off, in);
-        }
-        const float* scalar = (lane == kGroups ? p.rstd : p.mean) + row;
-        bool want = lane == kGroups || (lane == kGroups + 1 && !CODES);
-        if (CODES && lane < kGroups) {
-          const int g = w_in * kGroups + lane;
-          want = g < groups8;
-          scalar = p.s + static_cast<int64_t>(row) * groups8 + (want ? g : 0);
-        }
-        if (want) cp_async<4>(to + J * kPiece + lane * 4, scalar, true);
-      }
-      cp_async_commit();
-    }
-  };
-  // what piece j of a row holds beside dy: the codes' values and their multiplier, or x - mean
-  // and rstd; xh is their product.  Past the row's end dy is 0, and these are finite unless the
-  // row's own scalars are not.
-  auto fetch = [&](int row, int s, int j, float rstd, float mean, float (&h)[E]) -> float {
-    const int rest = left - j * P::WC;
-    if constexpr (CODES) {
-      float m;
-      typename P::Codes k;
-      if constexpr (VECTOR) {
-        k = P::read_codes(mine + s * kStage + j * kPiece + 512 + lane * kIn);
-        // past the row's end the codes are 0, and the multiplier was not copied
-        m = rest > 0 ? reinterpret_cast<const float*>(mine + s * kStage + J * kPiece)[(j * P::WC + P::first(lane)) / 128] : 0.0f;
-      } else {
-        k = P::load_codes(q0 + static_cast<int64_t>(row) * ldq + j * P::WC, rest);
-        m = rest > 0 ? __ldg(p.s + static_cast<int64_t>(row) * groups8 + (c + j * P::WC) / 128) : 0.0f;
-      }
-      P::decode(k, p.e5m2, h);
-      return m;
-    } else {
-      if constexpr (VECTOR)
-        P::unpack(*reinterpret_cast<const uint4*>(mine + s * kStage + j * kPiece + 512 + lane * 16), h);
+    if (row < rows) {
+      uint8_t* const to = mine + s * kStage;
+      const int64_t r = row;
+      PartDy::start(to, static_cast<const T*>(p.dy) + r * lddy, r * lddy, base, cols, lane);
+      if constexpr (CODES)
+        PartQ::start(to + kIn, p.q + r * ldq, r * ldq, base, cols, lane);
       else
-        P::load(x0 + static_cast<int64_t>(row) * ldx + j * P::WC, rest, h);
+        PartDy::start(to + kIn, static_cast<const T*>(p.x) + r * ldx, r * ldx, base, cols, lane);
+      const float* scalar = (lane == kGroups ? p.rstd : p.mean) + row;
+      bool want = lane == kGroups || (lane == kGroups + 1 && !CODES);
+      if (CODES && lane < kGroups) {
+        const int g = w_in * kGroups + lane;
+        want = g < groups8;
+        scalar = p.s + r * groups8 + (want ? g : 0);
+      }
+      if (want) cp_async<4>(smem_u32(to) + kScalars + lane * 4, scalar, true);
+    }
+    cp_async_commit();
+  };
+  // What piece j of the row in stage s holds beside dy: the codes' values and their multiplier, or
+  // x - mean and rstd; xh is their product.  Past the row's end dy is 0, and these are finite
+  // unless the row's own scalars are not.
+  auto fetch = [&](int s, int m, int j, float rstd, float mean, float (&h)[E]) -> float {
+    const uint8_t* const at = mine + s * kStage + kIn;
+    if constexpr (CODES) {
+      P::decode(PartQ::read_codes(at, m, lane, j), p.e5m2, h);
+      // past the row's end the codes are 0, and the multiplier was not copied
+      return left > j * P::WC ? reinterpret_cast<const float*>(mine + s * kStage + kScalars)[(j * P::WC + P::first(lane)) / 128] : 0.0f;
+    } else {
+      PartDy::read(at, m, lane, j, h);
 #pragma unroll
       for (int i = 0; i < E; i += 2) {
         const float2 d = add2(make_float2(h[i], h[i + 1]), both(-mean));
@@ -200,30 +187,24 @@ __global__ void __launch_bounds__(BLOCK_WARPS * 32)
   start_param<P, V>(p.w, p.w_f32, cols, warps, 1.0f, ws);
   cp_async_commit();
   for (int s = 0; s < stages; ++s) issue(row + s * step, s);
-  cp_async_wait_oldest(VECTOR ? stages + 1 : 1);
+  cp_async_wait_oldest(stages + 1);
   settle_param<P, V>(p.w, p.w_f32, warps, ws);
   __syncthreads();
   for (int s = 0, buf = 0; row < rows; row += step, buf ^= 1) {
-    float rstd, mean = 0.0f;
-    if constexpr (VECTOR) {
-      cp_async_wait_oldest(stages);
-      __syncwarp();   // the row's scalars were copied by other lanes
-      const float* scalars = reinterpret_cast<const float*>(mine + s * kStage + J * kPiece);
-      rstd = scalars[kGroups];
-      if (!CODES) mean = scalars[kGroups + 1];
-    } else {
-      rstd = __ldg(p.rstd + row);
-      if (!CODES) mean = __ldg(p.mean + row);
-    }
+    cp_async_wait_oldest(stages);
+    __syncwarp();   // the row's scalars, and unaligned a lane's last elements, were copied by other lanes
+    const float* const scalars = reinterpret_cast<const float*>(mine + s * kStage + kScalars);
+    const float rstd = scalars[kGroups], mean = CODES ? 0.0f : scalars[kGroups + 1];
+    // elements between granules and values, of dy and of x or the codes
+    const int m_dy = PartDy::past(static_cast<const T*>(p.dy) + static_cast<int64_t>(row) * lddy + base);
+    const int m_in = CODES ? PartQ::past(p.q + static_cast<int64_t>(row) * ldq + base)
+                           : PartDy::past(static_cast<const T*>(p.x) + static_cast<int64_t>(row) * ldx + base);
     float2 g[J][H], s1 = {0.0f, 0.0f}, s2 = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       float d[E], h[E], w[E];
-      if constexpr (VECTOR)
-        P::unpack(*reinterpret_cast<const uint4*>(mine + s * kStage + j * kPiece + lane * 16), d);
-      else
-        P::load(dy0 + static_cast<int64_t>(row) * lddy + j * P::WC, left - j * P::WC, d);
-      const float2 m = both(fetch(row, s, j, rstd, mean, h));
+      PartDy::read(mine + s * kStage, m_dy, lane, j, d);
+      const float2 m = both(fetch(s, m_in, j, rstd, mean, h));
       read_param<P, V>(ws, w_in, j, lane, w);
 #pragma unroll
       for (int i = 0; i < H; ++i) {
@@ -256,19 +237,26 @@ __global__ void __launch_bounds__(BLOCK_WARPS * 32)
     const float2 r = both(rstd), k1 = both(-rstd * c1);
     const float k2 = -rstd * c2;
     T* const dx0 = static_cast<T*>(p.dx) + static_cast<int64_t>(row) * lddx + c;
+    constexpr int N = VECTOR ? 1 : J;   // pieces stored together: unaligned, the fewer ends the better
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      float h[E], out[E];
-      const float2 m = both(k2 * fetch(row, s, j, rstd, mean, h));
+    for (int j0 = 0; j0 < J; j0 += N) {
+      uint4 packed[N];
 #pragma unroll
-      for (int i = 0; i < H; ++i) {
-        const float2 o = fma2(make_float2(h[2 * i], h[2 * i + 1]), m, fma2(g[j][i], r, k1));
-        out[2 * i] = o.x;
-        out[2 * i + 1] = o.y;
+      for (int k = 0; k < N; ++k) {
+        const int j = j0 + k;
+        float h[E], out[E];
+        const float2 m = both(k2 * fetch(s, m_in, j, rstd, mean, h));
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          const float2 o = fma2(make_float2(h[2 * i], h[2 * i + 1]), m, fma2(g[j][i], r, k1));
+          out[2 * i] = o.x;
+          out[2 * i + 1] = o.y;
+        }
+        packed[k] = P::pack(out);
       }
-      P::store(dx0 + j * P::WC, left - j * P::WC, out);
+      P::store_raw(dx0 + j0 * P::WC, left - j0 * P::WC, packed);
     }
-    if constexpr (VECTOR) __syncwarp();   // all lanes have read the stage's scalars
+    __syncwarp();   // all lanes have read what this one copied
     issue(row + stages * step, s);
     s = s + 1 == stages ? 0 : s + 1;
   }
@@ -378,8 +366,7 @@ __global__ void __launch_bounds__(kParamWarps * 32) k_norm_params(const float* p
 // *partials: number of partial sums left in p.partial (0: none)
 template <typename T, bool VECTOR, bool CODES, int V, int BLOCK_WARPS>
 cudaError_t run_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
-  using P = Piece<T, VECTOR>;
-  const int stage = VECTOR ? V / P::E * 32 * (16 + (CODES ? P::E : 16)) + 48 : 0;
+  const int stage = NormBackwardStage<T, VECTOR, CODES, V>::kBytes;
   NormPlan n = norm_plan(p.rows, p.cols, 32 * V, BLOCK_WARPS, 1, stage, num_sms < kMaxNormPartials ? num_sms : kMaxNormPartials);
   const size_t join = n.ring + static_cast<size_t>(n.groups / 2) * n.warps * 64 * V * sizeof(float);
   if (n.smem < join) n.smem = join;
