@@ -26,6 +26,19 @@ inline cudaError_t ensure_smem_limit(Kernel* fn, int bytes, std::atomic<bool> (&
   return e;
 }
 
+// The same for a kernel whose clusters may have 16 blocks.
+template <typename Kernel>
+inline cudaError_t ensure_wide_cluster(Kernel* fn, std::atomic<bool> (&done)[kMaxDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 // Launch with programmatic stream serialization: the kernel may be scheduled while the
 // kernel before it in the stream drains.  Every kernel of this library executes
 // griddepcontrol.wait (pdl_wait) before its first global-memory access, which returns
@@ -220,7 +233,8 @@ struct RouteParams {
   int* offsets;          // [n_experts + 1]
   int* pos;              // [n]
   int* src;              // [capacity]
-  int64_t per_block;     // set by the launcher
+  int64_t per_block;     // choices of a block and of a warp, set by the launcher
+  int64_t per_warp;
 };
 cudaError_t launch_route(RouteParams p, cudaStream_t s);
 struct ScatterParams {

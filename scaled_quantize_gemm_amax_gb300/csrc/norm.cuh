@@ -2,8 +2,8 @@
 // a time, each warp a fixed number of its columns, and walks the rows grid-wide.  A block holds
 // as many groups as its warps allow (what fits an SM's registers), and there is a block an SM.
 // The next rows of each group are on their way into shared memory by asynchronous copies of 16
-// bytes a lane.  Rows that are not 16-byte aligned are copied by their granules and shifted into
-// place on reading; a warp reads what its own lanes copied, so no block barrier guards them.
+// bytes a lane.  Rows that are not 16-byte aligned are copied by their aligned 16-byte granules
+// and read at their own offset; a warp reads what its own lanes copied, so no block barrier guards them.
 #pragma once
 #include "internal.h"
 #include "rowops.cuh"
@@ -169,9 +169,10 @@ struct RowPart {
       for (int i = 0; i < P::E; ++i) v[i] = *reinterpret_cast<const T*>(from + (m + j * P::WC + lane + P::at(i)) * G / P::E);
     } else {
       const uint8_t* const at = from + (j * 32 + lane) * G;
-      uint4 raw = *reinterpret_cast<const uint4*>(at);
-      if (!VECTOR && m != 0) raw = from_byte<sizeof(T)>(raw, *reinterpret_cast<const uint4*>(at + G), m * static_cast<int>(sizeof(T)));
-      P::unpack(raw, v);
+      if (VECTOR || m == 0)
+        P::unpack(*reinterpret_cast<const uint4*>(at), v);
+      else
+        P::unpack(P::words(reinterpret_cast<const uint32_t*>(at + (m & ~1) * static_cast<int>(sizeof(T))), (m & 1) != 0), v);
     }
   }
   template <int J>
@@ -187,9 +188,8 @@ struct RowPart {
       for (int i = 0; i < P::E; ++i) c.u[0] |= static_cast<uint32_t>(from[m + j * P::WC + lane + P::at(i)]) << (8 * i);
       return c;
     } else {
-      const uint8_t* const at = from + (j * 32 + lane) * G;
-      const typename P::Codes c = P::read_codes(at);
-      return VECTOR || m == 0 ? c : P::codes_from(c, P::read_codes(at + G), m);
+      const uint8_t* const at = from + (j * 32 + lane) * G + m;
+      return VECTOR || m == 0 ? P::read_codes(at) : P::code_words(at);
     }
   }
 };

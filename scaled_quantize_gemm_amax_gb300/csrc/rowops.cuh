@@ -75,35 +75,16 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
 }
 
 // ------------------------------------------------------------------ a warp's piece of a row
-// 16 bytes from byte m on of the 32 bytes a, b (m a multiple of `step` below 16; the whole warp's)
-template <int STEP>
-__device__ __forceinline__ uint4 from_byte(const uint4& a, const uint4& b, int m) {
-  uint32_t t[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 6; ++i) t[i] = m & 8 ? t[i + 2] : t[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) t[i] = m & 4 ? t[i + 1] : t[i];
-  if constexpr (STEP < 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = __funnelshift_r(t[i], t[i + 1], (m & 2) * 8);
-  }
-  return make_uint4(t[0], t[1], t[2], t[3]);
-}
-__device__ __forceinline__ uint4 shfl_from(const uint4& v, int lane) {
-  return make_uint4(__shfl_sync(0xFFFFFFFFu, v.x, lane), __shfl_sync(0xFFFFFFFFu, v.y, lane),
-                    __shfl_sync(0xFFFFFFFFu, v.z, lane), __shfl_sync(0xFFFFFFFFu, v.w, lane));
-}
-
 // How a warp holds WC consecutive columns of a row, E = 16 bytes' worth a lane.
 //   VECTOR           the row is 16-byte aligned and cols % E == 0 (a lane is all in or all out):
 //                    lane l the E columns from l E on, one 16-byte access.
-//   bf16 otherwise   the same columns.  A lane still moves 16 aligned bytes, a granule, and the
-//                    warp shifts the row into place: granule and lane differ by the same m
-//                    elements in every lane, so a lane's values are the end of its own granule
-//                    and the beginning of the next lane's.  Granules that are not wholly the
-//                    row's, at its ends and at those of what a warp stores, are moved element by
-//                    element; no byte outside the row is touched.  (Element by element
-//                    throughout, 8192x9001 gated SiLU took 265 us.)
+//   bf16 otherwise   the same columns, in 4-byte words: rows that start at an odd element are read
+//                    a word more and shifted by half a word; what a lane stores begins with the
+//                    lane before's last value, so that every word but the ends' is whole.  A run
+//                    of pieces that touches the row's end goes element by element; no byte outside
+//                    the row is touched.  (Element by element throughout, 8192x9001 gated SiLU took
+//                    265 us; aligned 16-byte granules shifted over the lanes 157 us: 11 selections a
+//                    lane and tensor.)
 //   binary32 otherwise  lane l columns l, l + 32, l + 64, l + 96, element by element, which
 //                    coalesces at any alignment (4096x9001 gated SiLU 84 us; granules 136).
 // A lane works from its own first column `c` of the row: pointers point there, and `left` is the
@@ -129,18 +110,13 @@ struct Piece {
     else
       return __float_as_uint(*p);
   }
-  // elements p's address is past a multiple of 16 bytes
-  __device__ static __forceinline__ int past16(const T* p) {
-    return static_cast<int>(reinterpret_cast<uintptr_t>(p) / sizeof(T) % E);
-  }
-  // elements lo <= i < hi of the granule at `a`, 0 for the others
-  __device__ static __forceinline__ uint4 granule(const T* a, int lo, int hi) {
-    if (lo <= 0 && hi >= E) return __ldg(reinterpret_cast<const uint4*>(a));
-    uint32_t u[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (i >= lo && i < hi) u[i * sizeof(T) / 4] |= bits(a + i) << (i * sizeof(T) % 4 * 8);
-    return make_uint4(u[0], u[1], u[2], u[3]);
+  // whether p is at an odd element of a 4-byte word (bf16)
+  __device__ static __forceinline__ bool odd(const T* p) { return (reinterpret_cast<uintptr_t>(p) & 2) != 0; }
+  // 16 bytes from 4-byte words at w, or from two bytes on (generic address: global or shared memory)
+  __device__ static __forceinline__ uint4 words(const uint32_t* w, bool half) {
+    const uint32_t a = w[0], b = w[1], c = w[2], d = w[3];
+    if (!half) return make_uint4(a, b, c, d);
+    return make_uint4(__funnelshift_r(a, b, 16), __funnelshift_r(b, c, 16), __funnelshift_r(c, d, 16), __funnelshift_r(d, w[4], 16));
   }
 
   // The lane's values of N consecutive pieces as they lie in memory (0 past the row's end): what
@@ -160,27 +136,22 @@ struct Piece {
                           has(rest, 3) ? bits(q + at(3)) : 0u);
       }
     } else {
-      const int lane = threadIdx.x & 31, m = past16(p), c0 = c - first(lane), row_left = left + first(lane);
-      const T* a = p - m;
-      uint4 last;   // lane 31's next granule after the last piece
-      if ((c0 > 0 || m == 0) && row_left >= N * WC + E) {   // every granule is the row's: the whole warp takes this way
+      const int lane = threadIdx.x & 31, row_left = left + first(lane);
+      const bool half = odd(p);
+      // every word is the row's: the whole warp takes this way
+      if ((c > first(lane) || !half) && row_left > N * WC) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(p - (half ? 1 : 0));
 #pragma unroll
-        for (int j = 0; j < N; ++j) r[j] = __ldg(reinterpret_cast<const uint4*>(a + j * WC));
-        if (m == 0) return;
-        if (lane == 31) last = __ldg(reinterpret_cast<const uint4*>(a + (N - 1) * WC + E));
+        for (int j = 0; j < N; ++j) r[j] = words(w + j * WC / 2, half);
       } else {
 #pragma unroll
-        for (int j = 0; j < N; ++j) r[j] = granule(a + j * WC, m - c - j * WC, left + m - j * WC);
-        if (m == 0) return;
-        if (lane == 31) last = granule(a + (N - 1) * WC + E, m - c - (N - 1) * WC - E, left + m - (N - 1) * WC - E);
-      }
+        for (int j = 0; j < N; ++j) {
+          uint32_t u[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        // lane 31's next granule is lane 0's of the piece after
-        const uint4 give = lane == 0 && j + 1 < N ? r[j + 1 < N ? j + 1 : j] : r[j];
-        uint4 n = shfl_from(give, (lane + 1) & 31);
-        if (j + 1 == N && lane == 31) n = last;
-        r[j] = from_byte<sizeof(T)>(r[j], n, m * static_cast<int>(sizeof(T)));
+          for (int i = 0; i < E; ++i)
+            if (left - j * WC > i) u[i / 2] |= bits(p + j * WC + i) << (i % 2 * 16);
+          r[j] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
       }
     }
   }
@@ -215,13 +186,6 @@ struct Piece {
     else
       *p = __uint_as_float(b);
   }
-  // elements lo <= i < hi of `w` to p + i, one by one
-  __device__ static __forceinline__ void store_some(T* p, const uint4& w, int lo, int hi) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (i >= lo && i < hi) store_bits(p + i, u[i * sizeof(T) / 4] >> (i * sizeof(T) % 4 * 8));
-  }
   // N consecutive pieces, packed
   template <int N>
   __device__ static __forceinline__ void store_raw(T* p, int left, const uint4 (&r)[N]) {
@@ -238,35 +202,40 @@ struct Piece {
           if (has(left - j * WC, i)) store_bits(p + j * WC + at(i), u[i]);
       }
     } else {
-      // a lane's granule: the last m values of the lane before, then its own first E - m
-      const int lane = threadIdx.x & 31, m = past16(p), row_left = left + first(lane);
-      if (m == 0) {
+      const int lane = threadIdx.x & 31;
+      const bool half = odd(p);
+      if (left + first(lane) < N * WC) {   // the row ends in the run: the whole warp takes this way
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          if (left - j * WC >= E)
-            *reinterpret_cast<uint4*>(p + j * WC) = r[j];
-          else
-            store_some(p + j * WC, r[j], 0, left - j * WC);
-        }
-        return;
-      }
-      const bool all = row_left >= N * WC;   // every value is the row's: the whole warp takes this way
+          if (N > 2 && left + first(lane) <= j * WC) break;
+          const uint32_t u[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        // lane 0's lane before is lane 31 of the piece before
-        const uint4 give = lane == 31 && j > 0 ? r[j > 0 ? j - 1 : 0] : r[j];
-        const uint4 w = from_byte<sizeof(T)>(shfl_from(give, (lane + 31) & 31), r[j], (E - m) * static_cast<int>(sizeof(T)));
-        const bool whole = (all || left - j * WC >= E - m) && (lane != 0 || j > 0);
-        if (whole) *reinterpret_cast<uint4*>(p + j * WC - m) = w;
-        if (!all) {
-          // values whose granule is not whole; from E - m on they are the next lane's granule's
-          const bool next = lane == 31 ? j + 1 < N && row_left - (j + 1) * WC >= E - m : left - E - j * WC >= E - m;
-          store_some(p + j * WC, r[j], whole ? E - m : 0, min(left - j * WC, next ? E - m : E));
+          for (int i = 0; i < E; ++i)
+            if (left - j * WC > i) store_bits(p + j * WC + i, u[i / 2] >> (i % 2 * 16));
         }
-      }
-      if (all) {   // the ends: lane 0's first E - m values and lane 31's last m
-        if (lane == 0) store_some(p, r[0], 0, E - m);
-        if (lane == 31) store_some(p + (N - 1) * WC, r[N - 1], E - m, E);
+      } else if (!half) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(p + j * WC);
+          w[0] = r[j].x, w[1] = r[j].y, w[2] = r[j].z, w[3] = r[j].w;
+        }
+      } else {
+        // word k: the last value before, then value 2 k; the lane before lane 0 is lane 31 of the piece before
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const uint32_t give = lane == 31 && j > 0 ? r[j > 0 ? j - 1 : 0].w : r[j].w;
+          const uint32_t before = __shfl_sync(0xFFFFFFFFu, give, (lane + 31) & 31);
+          T* q = p + j * WC;
+          uint32_t* w = reinterpret_cast<uint32_t*>(q - 1);
+          if (lane > 0 || j > 0)
+            w[0] = __funnelshift_r(before, r[j].x, 16);
+          else
+            store_bits(q, r[j].x);
+          w[1] = __funnelshift_r(r[j].x, r[j].y, 16);
+          w[2] = __funnelshift_r(r[j].y, r[j].z, 16);
+          w[3] = __funnelshift_r(r[j].z, r[j].w, 16);
+        }
+        if (lane == 31) store_bits(p + (N - 1) * WC + E - 1, r[N - 1].w >> 16);
       }
     }
   }
@@ -328,48 +297,34 @@ struct Piece {
     }
     return c;
   }
-  // E codes from byte m on of the 2 E bytes a, b
-  __device__ static __forceinline__ Codes codes_from(const Codes& a, const Codes& b, int m) {
-    Codes r;
-    if constexpr (E == 8) {
-      const bool word = (m & 4) != 0;
-      const uint32_t t0 = word ? a.u[1] : a.u[0], t1 = word ? b.u[0] : a.u[1], t2 = word ? b.u[1] : b.u[0];
-      r.u[0] = __funnelshift_r(t0, t1, (m & 3) * 8);
-      r.u[1] = __funnelshift_r(t1, t2, (m & 3) * 8);
-    } else {
-      r.u[0] = __funnelshift_r(a.u[0], b.u[0], m * 8);
-    }
-    return r;
-  }
-  __device__ static __forceinline__ Codes code_granule(const uint8_t* a, int lo, int hi) {
-    if (lo <= 0 && hi >= E) return read_codes(a);
-    Codes c = {};
+  // E codes at any byte, all of whose 4-byte words may be read
+  __device__ static __forceinline__ Codes code_words(const uint8_t* q) {
+    const int m = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 3);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(q - m);
+    Codes c;
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (i >= lo && i < hi) c.u[i / 4] |= static_cast<uint32_t>(a[i]) << (8 * (i % 4));
+    for (int i = 0; i < kWords; ++i) c.u[i] = __funnelshift_r(w[i], w[i + 1], m * 8);
     return c;
   }
   __device__ static __forceinline__ Codes load_codes(const uint8_t* q, int c, int left) {
+    Codes r = {};
     if constexpr (VECTOR) {
-      Codes none = {};
-      return left > 0 ? read_codes(q) : none;
+      if (left > 0) r = read_codes(q);
     } else if constexpr (kStrided) {
-      Codes r = {};
 #pragma unroll
       for (int i = 0; i < E; ++i)
         if (has(left, i)) r.u[0] |= static_cast<uint32_t>(q[at(i)]) << (8 * i);
-      return r;
     } else {
-      const int m = static_cast<int>(reinterpret_cast<uintptr_t>(q) % E);
-      const uint8_t* a = q - m;
-      const Codes w = code_granule(a, m - c, left + m);
-      if (m == 0) return w;
-      Codes n;
+      const int lane = threadIdx.x & 31;
+      if (c > first(lane) && left + first(lane) >= WC + 4) {   // every word is the row's: the whole warp takes this way
+        r = code_words(q);
+      } else {
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) n.u[i] = __shfl_down_sync(0xFFFFFFFFu, w.u[i], 1);
-      if ((threadIdx.x & 31) == 31) n = code_granule(a + E, m - c - E, left + m - E);
-      return codes_from(w, n, m);
+        for (int i = 0; i < E; ++i)
+          if (left > i) r.u[i / 4] |= static_cast<uint32_t>(q[i]) << (8 * (i % 4));
+      }
     }
+    return r;
   }
   // the codes' own values
   __device__ static __forceinline__ void decode(const Codes& c, bool e5m2, float (&v)[E]) {
