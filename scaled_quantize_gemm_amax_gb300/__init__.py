@@ -309,8 +309,7 @@ def fp8_scaled_gemm_amax(a, fa, ra, sa, b, fb, rb, sb, c, out, c_amax, c_scale, 
                                                int(fc), _ptr(c_q), _ptr(c_scale_inv), _stream(stream)))
 
 
-# ---- row operators.  The fp8_* calls check every tensor; the allocation helpers below check the
-# caller's tensors and pass the outputs they have just made straight on (the _run_* functions).
+# ---- row operators
 def _rows(t, what: str):
     """(rows, cols, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
     if t.dim() == 2:
@@ -382,23 +381,16 @@ def _on_gpu(*tensors):
             raise ValueError(f"a CUDA tensor is needed, not one on {t.device}")
 
 
-def _run_layer_norm(x, weight, bias, eps, y, ldy, mean, rstd, fmt, q, ldq, s, stream, outs=()):
+def fp8_layer_norm(x, weight, bias, eps, y, mean, rstd, fmt, q, s, stream=None):
     rows, cols, ldx = _rows(x, "x")
     dt, wdt = _dtype(x, "x"), _params(weight, bias, cols)
-    _on_gpu(x, weight, bias, *outs)
-    st = load_library().fp8_layer_norm(_ptr(x), rows, cols, ldx, dt, _ptr(weight), _ptr(bias), wdt, eps, _ptr(y), ldy,
-                                       _ptr(mean), _ptr(rstd), fmt, _ptr(q), ldq, _ptr(s), _stream(stream))
-    if st:
-        raise FP8Error("fp8_layer_norm", st)
-
-
-def fp8_layer_norm(x, weight, bias, eps, y, mean, rstd, fmt, q, s, stream=None):
-    rows, cols, _ = _rows(x, "x")
-    _dtype(x, "x")
     ldy, ldq = _like(y, x, "y"), _codes(q, s, rows, cols, "q")
     _vector(mean, rows, "mean")
     _vector(rstd, rows, "rstd")
-    _run_layer_norm(x, weight, bias, eps, y, ldy, mean, rstd, int(fmt), q, ldq, s, stream, (y, mean, rstd, q, s))
+    _on_gpu(x, weight, bias, y, mean, rstd, q, s)
+    _check("fp8_layer_norm",
+           load_library().fp8_layer_norm(_ptr(x), rows, cols, ldx, dt, _ptr(weight), _ptr(bias), wdt, eps, _ptr(y), ldy,
+                                         _ptr(mean), _ptr(rstd), int(fmt), _ptr(q), ldq, _ptr(s), _stream(stream)))
 
 
 def fp8_layer_norm_workspace(rows: int, cols: int) -> int:
@@ -408,61 +400,42 @@ def fp8_layer_norm_workspace(rows: int, cols: int) -> int:
     return n.value
 
 
-def _run_layer_norm_backward(dy, x, mean, rstd, fmt, q, s, weight, wdt, dx, lddx, dweight, dbias, workspace, nbytes, stream,
-                             outs=()):
-    rows, cols, lddy = _rows(dy, "dy")
-    dt, ldx, ldq = _dtype(dy, "dy"), _like(x, dy, "x"), _codes(q, s, rows, cols, "q")
-    _vector(mean, rows, "mean")
-    _vector(rstd, rows, "rstd")
-    _on_gpu(dy, x, mean, rstd, q, s, weight, *outs)
-    st = load_library().fp8_layer_norm_backward(_ptr(dy), rows, cols, lddy, dt, _ptr(x), ldx, _ptr(mean), _ptr(rstd), fmt,
-                                                _ptr(q), ldq, _ptr(s), _ptr(weight), wdt, _ptr(dx), lddx, _ptr(dweight),
-                                                _ptr(dbias), _ptr(workspace), nbytes, _stream(stream))
-    if st:
-        raise FP8Error("fp8_layer_norm_backward", st)
-
-
 def fp8_layer_norm_backward(dy, x, mean, rstd, fmt, q, s, weight, dx, dweight, dbias, workspace, stream=None):
-    cols = _rows(dy, "dy")[1]
+    rows, cols, lddy = _rows(dy, "dy")
+    dt = _dtype(dy, "dy")
     wdt = _params(weight, dweight, cols) if weight is not None or dweight is not None else _params(None, dbias, cols)
     _vector(dbias, cols, "dbias", (torch.bfloat16, torch.float32)[wdt])
-    lddx = _like(dx, dy, "dx")
+    ldx, lddx, ldq = _like(x, dy, "x"), _like(dx, dy, "dx"), _codes(q, s, rows, cols, "q")
+    _vector(mean, rows, "mean")
+    _vector(rstd, rows, "rstd")
+    _on_gpu(dy, x, mean, rstd, q, s, weight, dx, dweight, dbias, workspace)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _run_layer_norm_backward(dy, x, mean, rstd, int(fmt), q, s, weight, wdt, dx, lddx, dweight, dbias, workspace, nbytes, stream,
-                             (dx, dweight, dbias, workspace))
-
-
-def _run_gated_act(a, b, act, y, ldy, fmt, qa, sa, qb, sb, ldq, stream, outs=()):
-    rows, cols, lda = _rows(a, "a")
-    ldb, dt = _like(b, a, "b"), _dtype(a, "a")
-    _on_gpu(a, b, *outs)
-    st = load_library().fp8_gated_act(_ptr(a), rows, cols, lda, dt, act, _ptr(b), ldb, _ptr(y), ldy, fmt, _ptr(qa), _ptr(sa),
-                                      _ptr(qb), _ptr(sb), ldq, _stream(stream))
-    if st:
-        raise FP8Error("fp8_gated_act", st)
+    _check("fp8_layer_norm_backward",
+           load_library().fp8_layer_norm_backward(_ptr(dy), rows, cols, lddy, dt, _ptr(x), ldx, _ptr(mean), _ptr(rstd),
+                                                  int(fmt), _ptr(q), ldq, _ptr(s), _ptr(weight), wdt, _ptr(dx), lddx,
+                                                  _ptr(dweight), _ptr(dbias), _ptr(workspace), nbytes, _stream(stream)))
 
 
 def fp8_gated_act(a, b, act, y, fmt, qa, sa, qb, sb, stream=None):
-    rows, cols, _ = _rows(a, "a")
-    ldy, ldq = _like(y, a, "y"), _code_pair(qa, sa, qb, sb, rows, cols)
-    _run_gated_act(a, b, int(act), y, ldy, int(fmt), qa, sa, qb, sb, ldq, stream, (y, qa, sa, qb, sb))
-
-
-def _run_gated_act_backward(dy, act, a, b, fmt, qa, sa, qb, sb, da, ldda, db, lddb, stream, outs=()):
-    rows, cols, lddy = _rows(dy, "dy")
-    lda, ldb, dt = _like(a, dy, "a"), _like(b, dy, "b"), _dtype(dy, "dy")
+    rows, cols, lda = _rows(a, "a")
+    ldb, ldy, dt = _like(b, a, "b"), _like(y, a, "y"), _dtype(a, "a")
     ldq = _code_pair(qa, sa, qb, sb, rows, cols)
-    _on_gpu(dy, a, b, qa, sa, qb, sb, *outs)
-    st = load_library().fp8_gated_act_backward(_ptr(dy), rows, cols, lddy, dt, act, _ptr(a), lda, _ptr(b), ldb, fmt, _ptr(qa),
-                                               _ptr(sa), _ptr(qb), _ptr(sb), ldq, _ptr(da), ldda, _ptr(db), lddb,
-                                               _stream(stream))
-    if st:
-        raise FP8Error("fp8_gated_act_backward", st)
+    _on_gpu(a, b, y, qa, sa, qb, sb)
+    _check("fp8_gated_act",
+           load_library().fp8_gated_act(_ptr(a), rows, cols, lda, dt, int(act), _ptr(b), ldb, _ptr(y), ldy, int(fmt), _ptr(qa),
+                                        _ptr(sa), _ptr(qb), _ptr(sb), ldq, _stream(stream)))
 
 
 def fp8_gated_act_backward(dy, act, a, b, fmt, qa, sa, qb, sb, da, db, stream=None):
+    rows, cols, lddy = _rows(dy, "dy")
+    lda, ldb, dt = _like(a, dy, "a"), _like(b, dy, "b"), _dtype(dy, "dy")
     ldda, lddb = _like(da, dy, "da"), _like(db, dy, "db")
-    _run_gated_act_backward(dy, int(act), a, b, int(fmt), qa, sa, qb, sb, da, ldda, db, lddb, stream, (da, db))
+    ldq = _code_pair(qa, sa, qb, sb, rows, cols)
+    _on_gpu(dy, a, b, qa, sa, qb, sb, da, db)
+    _check("fp8_gated_act_backward",
+           load_library().fp8_gated_act_backward(_ptr(dy), rows, cols, lddy, dt, int(act), _ptr(a), lda, _ptr(b), ldb, int(fmt),
+                                                 _ptr(qa), _ptr(sa), _ptr(qb), _ptr(sb), ldq, _ptr(da), ldda, _ptr(db), lddb,
+                                                 _stream(stream)))
 
 
 def fp8_moe_capacity(tokens: int, k: int, n_experts: int, align: int) -> int:
@@ -472,22 +445,17 @@ def fp8_moe_capacity(tokens: int, k: int, n_experts: int, align: int) -> int:
     return n.value
 
 
-def _run_moe_route(experts, n_experts, align, offsets, pos, src, capacity, stream, outs=()):
+def fp8_moe_route(experts, n_experts: int, align: int, offsets, pos, src, stream=None):
     if experts.dim() != 2 or experts.dtype not in (torch.int32, torch.int64) or not experts.is_contiguous():
         raise ValueError("experts: a contiguous [tokens, k] int32 or int64 tensor is needed")
     tokens, k = experts.shape
-    _on_gpu(experts, *outs)
-    st = load_library().fp8_moe_route(_ptr(experts), 4 if experts.dtype == torch.int32 else 8, tokens, k, n_experts, align,
-                                      _ptr(offsets), _ptr(pos), _ptr(src), capacity, _stream(stream))
-    if st:
-        raise FP8Error("fp8_moe_route", st)
-
-
-def fp8_moe_route(experts, n_experts: int, align: int, offsets, pos, src, stream=None):
     _vector(offsets, n_experts + 1, "offsets", torch.int32)
-    _vector(pos, experts.numel(), "pos", torch.int32)
+    _vector(pos, tokens * k, "pos", torch.int32)
     _vector(src, src.numel(), "src", torch.int32)
-    _run_moe_route(experts, n_experts, align, offsets, pos, src, src.numel(), stream, (offsets, pos, src))
+    _on_gpu(experts, offsets, pos, src)
+    _check("fp8_moe_route",
+           load_library().fp8_moe_route(_ptr(experts), 4 if experts.dtype == torch.int32 else 8, tokens, k, n_experts, align,
+                                        _ptr(offsets), _ptr(pos), _ptr(src), src.numel(), _stream(stream)))
 
 
 def _choices(pos, what_tokens: int | None = None):
@@ -505,55 +473,40 @@ def _check_segments(out, ref, capacity: int, cols: int, what: str) -> int:
     return _rows(out, what)[2]
 
 
-def _run_moe_dispatch(x, pos, src, xs, ldxs, stream, outs=()):
-    tokens, cols, ldx = _rows(x, "x")
-    k, dt = _choices(pos, tokens)[1], _dtype(x, "x")
-    _vector(src, src.numel(), "src", torch.int32)
-    _on_gpu(x, pos, src, *outs)
-    st = load_library().fp8_moe_dispatch(_ptr(x), tokens, cols, ldx, dt, k, _ptr(pos), _ptr(src), src.numel(), _ptr(xs), ldxs,
-                                         _stream(stream))
-    if st:
-        raise FP8Error("fp8_moe_dispatch", st)
-
-
 def fp8_moe_dispatch(x, pos, src, xs, stream=None):
-    ldxs = _check_segments(xs, x, src.numel(), x.shape[-1], "xs")
-    _run_moe_dispatch(x, pos, src, xs, ldxs, stream, (xs,))
-
-
-def _run_moe_combine(ys, pos, weights, y, ldy, stream, outs=()):
-    capacity, cols, ldys = _rows(ys, "ys")
-    (tokens, k), dt = _choices(pos), _dtype(ys, "ys")
-    _vector(weights, tokens * k, "weights")
-    _on_gpu(ys, pos, weights, *outs)
-    st = load_library().fp8_moe_combine(_ptr(ys), capacity, cols, ldys, dt, tokens, k, _ptr(pos), _ptr(weights), _ptr(y), ldy,
-                                        _stream(stream))
-    if st:
-        raise FP8Error("fp8_moe_combine", st)
+    tokens, cols, ldx = _rows(x, "x")
+    k, dt, capacity = _choices(pos, tokens)[1], _dtype(x, "x"), src.numel()
+    _vector(src, capacity, "src", torch.int32)
+    ldxs = _check_segments(xs, x, capacity, cols, "xs")
+    _on_gpu(x, pos, src, xs)
+    _check("fp8_moe_dispatch",
+           load_library().fp8_moe_dispatch(_ptr(x), tokens, cols, ldx, dt, k, _ptr(pos), _ptr(src), capacity, _ptr(xs), ldxs,
+                                           _stream(stream)))
 
 
 def fp8_moe_combine(ys, pos, weights, y, stream=None):
-    ldy = _check_segments(y, ys, pos.shape[0], ys.shape[-1], "y")
-    _run_moe_combine(ys, pos, weights, y, ldy, stream, (y,))
+    capacity, cols, ldys = _rows(ys, "ys")
+    (tokens, k), dt = _choices(pos), _dtype(ys, "ys")
+    _vector(weights, tokens * k, "weights")
+    ldy = _check_segments(y, ys, tokens, cols, "y")
+    _on_gpu(ys, pos, weights, y)
+    _check("fp8_moe_combine",
+           load_library().fp8_moe_combine(_ptr(ys), capacity, cols, ldys, dt, tokens, k, _ptr(pos), _ptr(weights), _ptr(y), ldy,
+                                          _stream(stream)))
 
 
-def _run_moe_combine_backward(dy, pos, src, weights, ys, dys, lddys, dweights, stream, outs=()):
+def fp8_moe_combine_backward(dy, pos, src, weights, ys, dys, dweights, stream=None):
     tokens, cols, lddy = _rows(dy, "dy")
     k, dt, capacity = _choices(pos, tokens)[1], _dtype(dy, "dy"), src.numel()
     _vector(src, capacity, "src", torch.int32)
     _vector(weights, tokens * k, "weights")
+    _vector(dweights, tokens * k, "dweights")
     ldys = 0 if ys is None else _check_segments(ys, dy, capacity, cols, "ys")
-    _on_gpu(dy, pos, src, weights, ys, *outs)
-    st = load_library().fp8_moe_combine_backward(_ptr(dy), tokens, cols, lddy, dt, k, _ptr(pos), _ptr(src), _ptr(weights),
-                                                 _ptr(ys), ldys, capacity, _ptr(dys), lddys, _ptr(dweights), _stream(stream))
-    if st:
-        raise FP8Error("fp8_moe_combine_backward", st)
-
-
-def fp8_moe_combine_backward(dy, pos, src, weights, ys, dys, dweights, stream=None):
-    lddys = _check_segments(dys, dy, src.numel(), dy.shape[-1], "dys")
-    _vector(dweights, pos.numel(), "dweights")
-    _run_moe_combine_backward(dy, pos, src, weights, ys, dys, lddys, dweights, stream, (dys, dweights))
+    lddys = _check_segments(dys, dy, capacity, cols, "dys")
+    _on_gpu(dy, pos, src, weights, ys, dys, dweights)
+    _check("fp8_moe_combine_backward",
+           load_library().fp8_moe_combine_backward(_ptr(dy), tokens, cols, lddy, dt, k, _ptr(pos), _ptr(src), _ptr(weights),
+                                                   _ptr(ys), ldys, capacity, _ptr(dys), lddys, _ptr(dweights), _stream(stream)))
 
 
 def fp8_get_device_status(stream=None) -> Status:
@@ -671,31 +624,35 @@ def scaled_gemm_amax(a, fa, ra, sa, b, fb, rb, sb, c_scale, fc=Format.E4M3, out=
 
 
 # ------------------------------------------------------------------ row operators, outputs allocated
-def _codes_like(x, rows: int, cols: int):
-    """Codes and multipliers of an 8-bit copy, and the codes' row stride (padded to 16 bytes)."""
-    ld = (cols + 15) // 16 * 16
-    dev = x.device
-    return (torch.empty_strided((rows, cols), (ld, 1), dtype=torch.uint8, device=dev),
-            torch.empty((rows, (cols + 127) // 128), dtype=torch.float32, device=dev), ld)
+_ext = None
+
+
+def _rowops():
+    """The compiled helpers (csrc/rowops_binding.cpp), bound to the loaded library."""
+    global _ext
+    if _ext is None:
+        import importlib.machinery
+        import importlib.util
+
+        path = os.path.join(_PKG, "_rowops.so")
+        if not os.path.exists(path):
+            raise OSError(f"_rowops.so not built at {path}; run scaled_quantize_gemm_amax_gb300/build.py")
+        lib = load_library()
+        loader = importlib.machinery.ExtensionFileLoader("_rowops", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_rowops", loader))
+        loader.exec_module(module)
+        module.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _SIGNATURES}, FP8Error)
+        _ext = module
+    return _ext
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, checkpoint=None, stats: bool = True, stream=None):
     """Allocate outputs and run fp8_layer_norm on x [rows, cols].
 
     Returns (y, mean, rstd, q, s).  checkpoint: a Format keeps the normalised rows in 8 bits
-    (q, s; else None).  stats=False skips mean and rstd (inference)."""
-    rows, cols = x.shape
-    dev = x.device
-    y = torch.empty((rows, cols), dtype=x.dtype, device=dev)
-    mean = rstd = q = s = None
-    ldq = 0
-    if stats:
-        mean = torch.empty(rows, dtype=torch.float32, device=dev)
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    if checkpoint is not None:
-        q, s, ldq = _codes_like(x, rows, cols)
-    _run_layer_norm(x, weight, bias, eps, y, cols, mean, rstd, checkpoint or 0, q, ldq, s, stream)
-    return y, mean, rstd, q, s
+    (q, s; else None; the codes' row stride is padded to 16 bytes).  stats=False skips mean
+    and rstd (inference)."""
+    return (_ext or _rowops()).layer_norm(x, weight, bias, eps, checkpoint, stats, stream)
 
 
 def layer_norm_backward(dy, rstd, weight=None, x=None, mean=None, q=None, s=None, fmt=Format.E4M3, param_grads: bool = True,
@@ -704,37 +661,16 @@ def layer_norm_backward(dy, rstd, weight=None, x=None, mean=None, q=None, s=None
 
     Returns (dx, dweight, dbias), the last two in the weight's type (param_dtype without a
     weight; default float32), or None with param_grads=False."""
-    rows, cols = dy.shape
-    dev = dy.device
-    dx = torch.empty((rows, cols), dtype=dy.dtype, device=dev)
-    dt = weight.dtype if weight is not None else param_dtype or torch.float32
-    if dt not in _DTYPE_CODE or (weight is not None and (weight.numel() != cols or not weight.is_contiguous())):
-        raise ValueError(f"weight: {cols} contiguous bfloat16 or float32 elements are needed, not {dt}")
-    dw = db = workspace = None
-    nbytes = 0
-    if param_grads:
-        dw = torch.empty(cols, dtype=dt, device=dev)
-        db = torch.empty(cols, dtype=dt, device=dev)
-        nbytes = 8 * cols * min(max(rows, 1), 304)   # fp8_layer_norm_workspace
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _run_layer_norm_backward(dy, x, mean, rstd, fmt, q, s, weight, _DTYPE_CODE[dt], dx, cols, dw, db, workspace, nbytes, stream)
-    return dx, dw, db
+    return (_ext or _rowops()).layer_norm_backward(dy, rstd, weight, x, mean, q, s, fmt, param_grads,
+                                                   param_dtype or torch.float32, stream)
 
 
 def gated_act(a, b=None, act=Activation.SILU, checkpoint=None, stream=None):
     """Allocate outputs and run fp8_gated_act: f(a) * b, or f(a) without b.
 
-    Returns (y, qa, sa, qb, sb); the 8-bit copies only with checkpoint=Format (else None)."""
-    rows, cols = a.shape
-    y = torch.empty((rows, cols), dtype=a.dtype, device=a.device)
-    qa = sa = qb = sb = None
-    ldq = 0
-    if checkpoint is not None:
-        qa, sa, ldq = _codes_like(a, rows, cols)
-        if b is not None:
-            qb, sb, _ = _codes_like(a, rows, cols)
-    _run_gated_act(a, b, act, y, cols, checkpoint or 0, qa, sa, qb, sb, ldq, stream)
-    return y, qa, sa, qb, sb
+    Returns (y, qa, sa, qb, sb); the 8-bit copies only with checkpoint=Format (else None; the
+    codes' row stride is padded to 16 bytes)."""
+    return (_ext or _rowops()).gated_act(a, b, act, checkpoint, stream)
 
 
 def gated_act_backward(dy, act=Activation.SILU, a=None, b=None, qa=None, sa=None, qb=None, sb=None, fmt=Format.E4M3,
@@ -742,14 +678,7 @@ def gated_act_backward(dy, act=Activation.SILU, a=None, b=None, qa=None, sa=None
     """Allocate outputs and run fp8_gated_act_backward; a (and b), or their 8-bit copies.
 
     Returns (da, db): the halves of one [rows, 2 cols] tensor, or (da, None) when not gated."""
-    rows, cols = dy.shape
-    if b is None and qb is None:
-        da, db, ld = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device), None, cols
-    else:
-        da, db = torch.empty((rows, 2 * cols), dtype=dy.dtype, device=dy.device).split(cols, 1) if cols else (dy, dy)
-        ld = 2 * cols
-    _run_gated_act_backward(dy, act, a, b, fmt, qa, sa, qb, sb, da, ld, db, ld, stream)
-    return da, db
+    return (_ext or _rowops()).gated_act_backward(dy, act, a, b, qa, sa, qb, sb, fmt, stream)
 
 
 class MoeRoute(typing.NamedTuple):
@@ -763,47 +692,27 @@ def moe_route(experts, n_experts: int, align: int = 1, stream=None) -> MoeRoute:
     """Allocate outputs and run fp8_moe_route on experts [tokens, k] (a choice outside [0, n_experts) is dropped).
 
     align=128 makes every expert's segment an operand of scaled_gemm."""
-    tokens, k = experts.shape
-    n = tokens * k
-    capacity = (n + min(n, n_experts) * (align - 1)) // max(align, 1) * align   # fp8_moe_capacity
-    dev = experts.device
-    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
-    pos = torch.empty((tokens, k), dtype=torch.int32, device=dev)
-    src = torch.empty(capacity, dtype=torch.int32, device=dev)
-    _run_moe_route(experts, n_experts, align, offsets, pos, src, capacity, stream)
-    return MoeRoute(offsets, pos, src)
+    return MoeRoute(*(_ext or _rowops()).moe_route(experts, n_experts, align, stream))
 
 
 def moe_dispatch(x, route: MoeRoute, stream=None):
     """xs [capacity, cols]: every token's row at its choices' rows, 0 in the rows that pad."""
-    cols = x.shape[-1]
-    xs = torch.empty((route.src.numel(), cols), dtype=x.dtype, device=x.device)
-    _run_moe_dispatch(x, route.pos, route.src, xs, cols, stream)
-    return xs
+    return (_ext or _rowops()).moe_dispatch(x, route.pos, route.src, stream)
 
 
 def moe_combine(ys, route: MoeRoute, weights=None, stream=None):
     """y [tokens, cols]: the choices' rows of ys summed with weights [tokens, k] float32 (None: 1)."""
-    cols = ys.shape[-1]
-    y = torch.empty((route.pos.shape[0], cols), dtype=ys.dtype, device=ys.device)
-    _run_moe_combine(ys, route.pos, weights, y, cols, stream)
-    return y
+    return (_ext or _rowops()).moe_combine(ys, route.pos, weights, stream)
 
 
 def moe_combine_backward(dy, ys, route: MoeRoute, weights=None, stream=None):
     """The gradients of moe_combine: (dys [capacity, cols], dweights [tokens, k] or None without weights)."""
-    cols = dy.shape[-1]
-    dys = torch.empty((route.src.numel(), cols), dtype=dy.dtype, device=dy.device)
-    dw = None
-    if weights is not None:
-        dw = torch.empty(route.pos.shape, dtype=torch.float32, device=dy.device)
-    _run_moe_combine_backward(dy, route.pos, route.src, weights, ys if dw is not None else None, dys, cols, dw, stream)
-    return dys, dw
+    return (_ext or _rowops()).moe_combine_backward(dy, ys, route.pos, route.src, weights, stream)
 
 
 def moe_dispatch_backward(dxs, route: MoeRoute, stream=None):
     """The gradient of moe_dispatch: every token's choices' rows of dxs, summed."""
-    return moe_combine(dxs, route, None, stream)
+    return (_ext or _rowops()).moe_combine(dxs, route.pos, None, stream)
 
 
 class DelayedScaling:

@@ -1,5 +1,7 @@
 """Build libfp8q.so in-tree: each .cu under csrc/ compiled by nvcc for sm_103a
-(in parallel), then linked into one shared library next to this file."""
+(in parallel), then linked into one shared library next to this file; and beside it
+_rowops.so, the Python extension of the row operators' allocation helpers (g++, the
+installed torch's headers)."""
 from __future__ import annotations
 
 import glob
@@ -18,6 +20,9 @@ LIB = os.path.join(PKG, "libfp8q.so")
 # access out of range through the device error word instead of making it.
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libfp8q_debug.so")
+# The Python extension: host code only, the same for both libraries.
+EXT_SOURCE = os.path.join(CSRC, "rowops_binding.cpp")
+EXT = os.path.join(PKG, "_rowops.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
@@ -50,9 +55,42 @@ def up_to_date(debug: bool = False) -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def start_extension(force: bool = False):
+    """The compilation of _rowops.so under way: (process, temporary file), or None when it is up to date."""
+    inputs = (EXT_SOURCE, os.path.join(INCLUDE, "fp8q.h"), os.path.abspath(__file__))
+    if not force and os.path.exists(EXT) and all(os.path.getmtime(f) <= os.path.getmtime(EXT) for f in inputs):
+        return None
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    include = os.path.join(root, "include")
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", INCLUDE, "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"), EXT_SOURCE, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True), tmp
+
+
+def finish_extension(started) -> None:
+    if started is None:
+        return
+    p, tmp = started
+    out, _ = p.communicate()
+    if p.returncode != 0:
+        sys.stderr.write(out)
+        raise RuntimeError("g++ failed for rowops_binding.cpp")
+    os.replace(tmp, EXT)
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     lib = LIB_DEBUG if debug else LIB
+    extension = start_extension(force)
     if not force and up_to_date(debug):
+        finish_extension(extension)
         return lib
     build_dir = BUILD_DEBUG if debug else BUILD
     os.makedirs(build_dir, exist_ok=True)
@@ -78,6 +116,7 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     tmp = lib + f".tmp{os.getpid()}"
     subprocess.run([nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", *objs, "-o", tmp], check=True)
     os.replace(tmp, lib)
+    finish_extension(extension)
     return lib
 
 

@@ -175,3 +175,33 @@ def test_binding_refuses_what_it_cannot_describe():
         fq.fp8_moe_dispatch(x, pos, src, torch.empty((7, 64), dtype=torch.bfloat16), stream=0)
     with pytest.raises(ValueError, match="^(?!a CUDA)"):
         fq.fp8_moe_combine(x, pos, torch.ones((4, 2), dtype=torch.float64), x, stream=0)
+
+
+def test_helpers_refuse_what_they_cannot_describe(lib):
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    w = torch.ones(64)
+    route = fq.MoeRoute(*[torch.zeros(n, dtype=torch.int32) for n in (9, (4, 2), 8)])
+    for call, what in ((lambda: fq.layer_norm(x.t()), "x"), (lambda: fq.layer_norm(x[0]), "x"), (lambda: fq.layer_norm(x, w[:63]), "weight"),
+                       (lambda: fq.layer_norm(x, w.bfloat16(), w), "bias"),
+                       (lambda: fq.layer_norm_backward(x, w), "rstd"),
+                       (lambda: fq.layer_norm_backward(x, w[:4], x=x.float(), mean=w[:4]), "x"),
+                       (lambda: fq.layer_norm_backward(x, w[:4], q=x, s=w[:4]), "q"),
+                       (lambda: fq.layer_norm_backward(x, w[:4], q=x.byte(), s=w[:3]), "q"),
+                       (lambda: fq.gated_act(x, x[:, :32]), "b"), (lambda: fq.gated_act(x, x.float()), "b"),
+                       (lambda: fq.gated_act_backward(x, qa=x.byte()), "qa"),
+                       (lambda: fq.gated_act_backward(x, a=x[:2]), "a"),
+                       (lambda: fq.moe_route(torch.zeros((4, 2)), 8), "experts"),
+                       (lambda: fq.moe_route(torch.zeros(4, dtype=torch.int32), 8), "experts"),
+                       (lambda: fq.moe_dispatch(x[:3], route), "pos"),
+                       (lambda: fq.moe_combine_backward(x[:3], x, route), "pos")):
+        with pytest.raises(ValueError, match=f"^{what}:"):
+            call()
+    for call in (lambda: fq.layer_norm(None), lambda: fq.layer_norm(3), lambda: fq.layer_norm(x.half()), lambda: fq.layer_norm(x, w.half()),
+                 lambda: fq.layer_norm_backward(x, w[:4], param_dtype=torch.half),
+                 lambda: fq.gated_act(x.double()), lambda: fq.moe_combine(x.int(), route)):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: fq.layer_norm(x, w), lambda: fq.gated_act(x, x), lambda: fq.moe_route(torch.zeros((4, 2), dtype=torch.int64), 8),
+                 lambda: fq.moe_dispatch(x, route), lambda: fq.moe_combine(x, route)):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()
