@@ -124,15 +124,29 @@ Copy copy_of(PyObject* oq, PyObject* os, int64_t rows, int64_t cols, const char*
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
 }
+// Outputs that live and die together (a copy's codes and multipliers, both statistics, a routing's
+// arrays) are parts of one allocation: at::empty takes 1 us, a part 0.1.
+at::Tensor part(const at::Tensor& whole, int64_t byte, at::ScalarType type, at::IntArrayRef shape, at::IntArrayRef strides) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_sizes_and_strides(shape, strides);
+  t.unsafeGetTensorImpl()->set_storage_offset(byte / static_cast<int64_t>(c10::elementSize(type)));
+  return t;
+}
+int64_t to16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 struct NewCopy {
   at::Tensor q, s;
   int64_t ld = 0;
 };
-// codes with a row stride of whole 16 bytes
-NewCopy new_copy(int64_t rows, int64_t cols, const at::Tensor& like) {
-  const int64_t ld = (cols + 15) / 16 * 16;
-  return {at::empty_strided({rows, cols}, {ld, 1}, at::TensorOptions().dtype(at::kByte).device(like.device())),
-          make({rows, groups(cols)}, at::kFloat, like), ld};
+// N copies' codes, with a row stride of whole 16 bytes, and multipliers
+template <int N>
+void new_copies(NewCopy* const (&to)[N], int64_t rows, int64_t cols, const at::Tensor& like) {
+  const int64_t ld = to16(cols), g = groups(cols), codes = rows * ld, scales = to16(rows * g * 4);
+  const at::Tensor whole = make({N * (codes + scales)}, at::kByte, like);
+  for (int i = 0; i < N; ++i) {
+    to[i]->q = part(whole, i * codes, at::kByte, {rows, cols}, {ld, 1});
+    to[i]->s = part(whole, N * codes + i * scales, at::kFloat, {rows, g}, {g, 1});
+    to[i]->ld = ld;
+  }
 }
 template <typename T>
 T* ptr(const at::Tensor& t) {
@@ -203,10 +217,11 @@ PyObject* layer_norm(PyObject* const* a) {
     Unlocked unlocked;
     y = make({x.rows, x.cols}, x.t->scalar_type(), *x.t);
     if (stats) {
-      mean = make({x.rows}, at::kFloat, *x.t);
-      rstd = make({x.rows}, at::kFloat, *x.t);
+      const at::Tensor whole = make({2 * x.rows}, at::kFloat, *x.t);
+      mean = part(whole, 0, at::kFloat, {x.rows}, {1});
+      rstd = part(whole, 4 * x.rows, at::kFloat, {x.rows}, {1});
     }
-    if (keep) c = new_copy(x.rows, x.cols, *x.t);
+    if (keep) new_copies({&c}, x.rows, x.cols, *x.t);
     st = p_fp8_layer_norm(x.p(), x.rows, x.cols, x.ld, dt, w, b, wdt, static_cast<float>(eps), y.data_ptr(), x.cols,
                           ptr<float>(mean), ptr<float>(rstd), fmt, ptr<uint8_t>(c.q), c.ld, ptr<float>(c.s), stream);
   }
@@ -239,8 +254,10 @@ PyObject* layer_norm_backward(PyObject* const* a) {
     Unlocked unlocked;
     dx = make({dy.rows, dy.cols}, dy.t->scalar_type(), *dy.t);
     if (param_grads) {
-      dw = make({dy.cols}, scalar_type(wdt), *dy.t);
-      db = make({dy.cols}, scalar_type(wdt), *dy.t);
+      const int64_t half = to16(dy.cols * static_cast<int64_t>(c10::elementSize(scalar_type(wdt))));
+      const at::Tensor whole = make({2 * half}, at::kByte, *dy.t);
+      dw = part(whole, 0, scalar_type(wdt), {dy.cols}, {1});
+      db = part(whole, half, scalar_type(wdt), {dy.cols}, {1});
       ws = make({bytes}, at::kByte, *dy.t);
     }
     st = p_fp8_layer_norm_backward(dy.p(), dy.rows, dy.cols, dy.ld, dt, x.p(), x.ld, mean, rstd, fmt, c.q, c.ld, c.s, w, wdt,
@@ -266,8 +283,10 @@ PyObject* gated_act(PyObject* const* a) {
   {
     Unlocked unlocked;
     y = make({x.rows, x.cols}, x.t->scalar_type(), *x.t);
-    if (keep) ca = new_copy(x.rows, x.cols, *x.t);
-    if (keep && b.t != nullptr) cb = new_copy(x.rows, x.cols, *x.t);
+    if (keep && b.t != nullptr)
+      new_copies({&ca, &cb}, x.rows, x.cols, *x.t);
+    else if (keep)
+      new_copies({&ca}, x.rows, x.cols, *x.t);
     st = p_fp8_gated_act(x.p(), x.rows, x.cols, x.ld, dt, act, b.p(), b.ld, y.data_ptr(), x.cols, fmt, ptr<uint8_t>(ca.q),
                          ptr<float>(ca.s), ptr<uint8_t>(cb.q), ptr<float>(cb.s), ca.ld, stream);
   }
@@ -295,8 +314,9 @@ PyObject* gated_act_backward(PyObject* const* a) {
     Unlocked unlocked;
     da = make({dy.rows, ld}, dy.t->scalar_type(), *dy.t);
     if (gated) {   // the halves of one tensor
-      db = da.as_strided({dy.rows, dy.cols}, {ld, 1}, dy.cols);
-      da = da.as_strided({dy.rows, dy.cols}, {ld, 1}, 0);
+      const at::Tensor whole = da;
+      da = part(whole, 0, dy.t->scalar_type(), {dy.rows, dy.cols}, {ld, 1});
+      db = part(whole, dy.cols * dy.t->element_size(), dy.t->scalar_type(), {dy.rows, dy.cols}, {ld, 1});
     }
     st = p_fp8_gated_act_backward(dy.p(), dy.rows, dy.cols, dy.ld, dt, act, x.p(), x.ld, b.p(), b.ld, fmt, ca.q, ca.s, cb.q, cb.s,
                                   ca.q != nullptr ? ca.ld : cb.ld, da.data_ptr(), ld, ptr<void>(db), ld, stream);
@@ -321,9 +341,11 @@ PyObject* moe_route(PyObject* const* a) {
   fp8_status st;
   {
     Unlocked unlocked;
-    offsets = make({n_experts + 1}, at::kInt, e);
-    pos = make({tokens, k}, at::kInt, e);
-    src = make({capacity}, at::kInt, e);
+    const int64_t at_pos = to16(4 * (int64_t{n_experts} + 1)), at_src = at_pos + to16(4 * tokens * k);
+    const at::Tensor whole = make({at_src + 4 * capacity}, at::kByte, e);
+    offsets = part(whole, 0, at::kInt, {n_experts + 1}, {1});
+    pos = part(whole, at_pos, at::kInt, {tokens, k}, {k, 1});
+    src = part(whole, at_src, at::kInt, {capacity}, {1});
     st = p_fp8_moe_route(e.data_ptr(), wide ? 8 : 4, tokens, k, n_experts, align, ptr<int32_t>(offsets), ptr<int32_t>(pos),
                          ptr<int32_t>(src), capacity, stream);
   }
