@@ -13,7 +13,9 @@ namespace fp8q {
 
 namespace {
 
-constexpr int kBlockWarps = 24;   // 80 registers a thread
+// warps of a block at V values a lane: 80 registers a thread, 64 at 8 values
+template <int V>
+constexpr int kBlockWarps = V == 8 ? 32 : 24;
 constexpr int kMostCols = 16384;  // of a row held in registers, its weight and bias in shared memory
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -88,11 +90,11 @@ __global__ void __launch_bounds__(kThreads) k_norm_any(const NormParams p) {
 //   M2 = sum M2_w + n_w (mean_w - mean)^2
 // so a row costs one barrier and loses no digits to a large mean.
 template <typename T, bool VECTOR, int V>
-__global__ void __launch_bounds__(kBlockWarps * 32) k_norm(const NormParams p, const int warps, const int stages, const int ring) {
+__global__ void __launch_bounds__(kBlockWarps<V> * 32) k_norm(const NormParams p, const int warps, const int stages, const int ring) {
   using P = Piece<T, VECTOR>;
   constexpr int E = P::E, J = V / E, kCols = 32 * V;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 red[2][kBlockWarps];
+  __shared__ float2 red[2][kBlockWarps<V>];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / warps, w_in = warp - group * warps;
   const int n_groups = (blockDim.x >> 5) / warps, step = gridDim.x * n_groups;
   const int rows = static_cast<int>(p.rows), cols = static_cast<int>(p.cols), groups8 = (cols + 127) / 128;
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32) k_norm(const NormParams p, c
 
 template <typename T, bool VECTOR, int V>
 cudaError_t run_norm(const NormParams& p, int num_sms, cudaStream_t s) {
-  const NormPlan n = norm_plan(p.rows, p.cols, 32 * V, kBlockWarps, 2,
+  const NormPlan n = norm_plan(p.rows, p.cols, 32 * V, kBlockWarps<V>, 2,
                                RowPart<Piece<T, VECTOR>, 32 * V, VECTOR, T>::kBytes, num_sms);
   static std::atomic<bool> done[kMaxDevices];
   const cudaError_t e = ensure_smem_limit(k_norm<T, VECTOR, V>, kNormSmem, done);
@@ -221,10 +223,13 @@ cudaError_t run_norm(const NormParams& p, int num_sms, cudaStream_t s) {
 
 // 32 values a lane halve what a row costs besides its values (sums over lanes and warps,
 // addresses); 16 where that would leave lanes empty (rows of up to 512 columns) or where a row's
-// latency counts and there are warps to spare (no more rows than SMs).
+// latency counts and there are warps to spare (no more rows than SMs); 8 where 16 would leave half
+// of them empty (up to 256 columns: 131072x128 with codes 37 us, 53 with 16 values; 262144x256 73 and
+// 106), and there 32 warps an SM, since a row is then mostly sums over lanes (24: 40 and 78 us).
 template <typename T, bool VECTOR>
 cudaError_t run_norm(const NormParams& p, int num_sms, cudaStream_t s) {
-  if (p.cols <= 512 || (p.rows <= num_sms && p.cols <= kBlockWarps * 512)) return run_norm<T, VECTOR, 16>(p, num_sms, s);
+  if (p.cols <= 256) return run_norm<T, VECTOR, 8>(p, num_sms, s);
+  if (p.cols <= 512 || (p.rows <= num_sms && p.cols <= kBlockWarps<16> * 512)) return run_norm<T, VECTOR, 16>(p, num_sms, s);
   return run_norm<T, VECTOR, 32>(p, num_sms, s);
 }
 

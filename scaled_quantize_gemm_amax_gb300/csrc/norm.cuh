@@ -11,6 +11,10 @@
 namespace fp8q {
 
 constexpr int kNormStages = 4;        // most rows in flight a group
+// Bytes in flight that a block aims at.  Fewer leave HBM waiting (backward from codes, 65536x4096:
+// 72 KB 218 us, 108 KB 212); more lengthen the walk's end, where rows have arrived and wait for
+// their turn (forward, 8192x4096: 96 KB 32.6 us, 192 KB 34.6; 32768x1024 20.8 and 25.1).
+constexpr int kNormInFlight = 96 * 1024;
 constexpr int kNormSmem = 220 * 1024; // dynamic shared memory of a block: those rows and the parameters
 
 // How a launch divides its rows (host side).
@@ -32,10 +36,11 @@ inline NormPlan norm_plan(int64_t rows, int64_t cols, int warp_cols, int block_w
   // few rows: spread over the SMs first
   const int64_t per_sm = (rows + num_sms - 1) / num_sms;
   if (n.groups > per_sm) n.groups = static_cast<int>(per_sm);
-  const int64_t stage = static_cast<int64_t>(stage_bytes) * n.warps * n.groups;
   n.ring = params * n.warps * warp_cols * 4;
-  int64_t s = stage > 0 ? (kNormSmem - n.ring) / stage : 1;
-  n.stages = static_cast<int>(s < 1 ? 1 : (s > kNormStages ? kNormStages : s));
+  const int64_t room = kNormSmem - n.ring, stage = static_cast<int64_t>(stage_bytes) * n.warps * n.groups;
+  const int64_t want_stages = (kNormInFlight + stage - 1) / stage;
+  n.stages = static_cast<int>(want_stages < 2 ? 2 : (want_stages > kNormStages ? kNormStages : want_stages));
+  if (n.stages * stage > room) n.stages = static_cast<int>(room / stage > 1 ? room / stage : 1);
   const int64_t want = (rows + n.groups - 1) / n.groups;
   n.blocks = static_cast<int>(want < num_sms ? want : num_sms);
   n.smem = static_cast<size_t>(n.ring + stage * n.stages);

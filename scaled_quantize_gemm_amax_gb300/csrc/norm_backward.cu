@@ -5,7 +5,7 @@
 // with xh = (x - m) r, or the values of its 8-bit copy.  All sums are binary32, in an order
 // that depends on the shape alone.
 //
-// Bound by HBM: dy and x (or the codes) once in, dx once out.  A thread owns the same 16 columns
+// Bound by HBM: dy and x (or the codes) once in, dx once out.  A thread owns the same columns
 // for all the rows of its group, so the column sums stay in registers over the whole walk; they
 // leave as one partial sum a block, added up by a second, small launch.
 #include "norm.cuh"
@@ -379,8 +379,14 @@ cudaError_t run_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t 
                     n.stages, n.ring);
 }
 
+// Values a lane and warps of a block.  32 values halve what a row costs besides its values, and 12
+// warps leave a thread the 168 registers that they and the column sums take (8192x4096 from codes
+// and 2048x12288 from x, when chosen: 39.3 and 42.7 us; 24 warps of 16 values 41.5 and 52.4; 16
+// warps of 32 values in 128 registers 41.0 and 58.2, needed above 12288 columns).  Narrow rows take
+// the fewest values that hold them: 131072x128 from x 34 us, with 16 values 49.
 template <typename T, bool VECTOR, bool CODES>
 cudaError_t run_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
+  if (p.cols <= 256) return run_norm_backward<T, VECTOR, CODES, 8, 24>(p, num_sms, s, partials);
   if (p.cols <= 512) return run_norm_backward<T, VECTOR, CODES, 16, 24>(p, num_sms, s, partials);
   if (p.cols <= 12288) return run_norm_backward<T, VECTOR, CODES, 32, 12>(p, num_sms, s, partials);
   return run_norm_backward<T, VECTOR, CODES, 32, 16>(p, num_sms, s, partials);

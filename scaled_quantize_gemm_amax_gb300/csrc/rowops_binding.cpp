@@ -137,16 +137,22 @@ struct NewCopy {
   at::Tensor q, s;
   int64_t ld = 0;
 };
-// N copies' codes, with a row stride of whole 16 bytes, and multipliers
+// N copies' codes, with a row stride of whole 16 bytes, and multipliers; `more` bytes behind them
+// (where the returned place in the returned allocation starts)
+struct Whole {
+  at::Tensor t;
+  int64_t rest;
+};
 template <int N>
-void new_copies(NewCopy* const (&to)[N], int64_t rows, int64_t cols, const at::Tensor& like) {
-  const int64_t ld = to16(cols), g = groups(cols), codes = rows * ld, scales = to16(rows * g * 4);
-  const at::Tensor whole = make({N * (codes + scales)}, at::kByte, like);
+Whole new_copies(NewCopy* const (&to)[N], int64_t rows, int64_t cols, const at::Tensor& like, int64_t more = 0) {
+  const int64_t ld = to16(cols), g = groups(cols), codes = rows * ld, scales = to16(rows * g * 4), rest = N * (codes + scales);
+  const at::Tensor whole = make({rest + more}, at::kByte, like);
   for (int i = 0; i < N; ++i) {
     to[i]->q = part(whole, i * codes, at::kByte, {rows, cols}, {ld, 1});
     to[i]->s = part(whole, N * codes + i * scales, at::kFloat, {rows, g}, {g, 1});
     to[i]->ld = ld;
   }
+  return {whole, rest};
 }
 template <typename T>
 T* ptr(const at::Tensor& t) {
@@ -216,12 +222,14 @@ PyObject* layer_norm(PyObject* const* a) {
   {
     Unlocked unlocked;
     y = make({x.rows, x.cols}, x.t->scalar_type(), *x.t);
-    if (stats) {
-      const at::Tensor whole = make({2 * x.rows}, at::kFloat, *x.t);
-      mean = part(whole, 0, at::kFloat, {x.rows}, {1});
-      rstd = part(whole, 4 * x.rows, at::kFloat, {x.rows}, {1});
+    const int64_t more = stats ? 8 * x.rows : 0;
+    if (keep || stats) {
+      const Whole whole = keep ? new_copies({&c}, x.rows, x.cols, *x.t, more) : Whole{make({more}, at::kByte, *x.t), 0};
+      if (stats) {
+        mean = part(whole.t, whole.rest, at::kFloat, {x.rows}, {1});
+        rstd = part(whole.t, whole.rest + 4 * x.rows, at::kFloat, {x.rows}, {1});
+      }
     }
-    if (keep) new_copies({&c}, x.rows, x.cols, *x.t);
     st = p_fp8_layer_norm(x.p(), x.rows, x.cols, x.ld, dt, w, b, wdt, static_cast<float>(eps), y.data_ptr(), x.cols,
                           ptr<float>(mean), ptr<float>(rstd), fmt, ptr<uint8_t>(c.q), c.ld, ptr<float>(c.s), stream);
   }
