@@ -5,6 +5,9 @@ path runs in the library's CUDA kernels; this module only marshals arguments
 (torch tensors -> device pointers, the current torch stream) and allocates
 output tensors with torch.  There is no fallback: every call raises when
 ``libfp8q.so`` has not been built (``scaled_quantize_gemm_amax_gb300/build.py``).
+The row operators' allocation helpers do the same marshalling compiled
+(``_rowops.so``, built beside the library): their calls on a few tokens last
+as long as an allocation and a launch.
 
 Entry points with the C names take tensors (or None for NULL) and raise
 ``FP8Error`` on a non-OK status: ``fp8_amax``, ``fp8_amax_f32``, ``fp8_compute_scale``,

@@ -9,6 +9,10 @@
 //   combine           y_t = sum_j w_{t,j} ys_{pos_{t,j}}  over the choices not dropped, in order of j
 //   combine backward  dys_r = w_{src_r} dy_{src_r / k},  dw_{t,j} = <dy_t, ys_{pos_{t,j}}>
 //   dispatch backward = combine with w = 1
+//
+// The rows are bound by HBM: 8192 tokens, 2 choices of 8 experts, 4096 wide in bf16, dispatch 33 us
+// and combine 32 (0.93 of what a copy reaches), combine backward of finer experts 58 and
+// dispatch backward 26 (0.86 together); routing is bound by latency (6.3 us there, 1.9 for a token).
 #include "internal.h"
 #include "rowops.cuh"
 

@@ -6,7 +6,12 @@
 // which the backward pass needs neither x nor m.  All sums are binary32.
 //
 // Bound by HBM: x once in, y (and the codes) once out.  A row stays in registers between its
-// statistics and its output.
+// statistics and its output; weight and bias stay in shared memory for the whole walk.
+// 8192x4096 bf16 with codes 32.6 us (5.2 TB/s, 0.76 of what a copy reaches), 65536x4096 0.89,
+// 16384x4096 without codes 0.87, one row of 4096 3.0 us.  What is left at 8192x4096: launch, the
+// first rows' way in and the last ones' way out (5 us), and SMs that finish at different times (the
+// rows are dealt out beforehand: 26 to 32 us).  Rows handed out on demand by cluster launch control
+// took a 25th warp a block and with it registers from the others: 36.4 us.
 #include "norm.cuh"
 
 namespace fp8q {

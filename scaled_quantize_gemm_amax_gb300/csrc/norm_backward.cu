@@ -8,6 +8,10 @@
 // Bound by HBM: dy and x (or the codes) once in, dx once out.  A thread owns the same columns
 // for all the rows of its group, so the column sums stay in registers over the whole walk; they
 // leave as one partial sum a block, added up by a second, small launch.
+// 8192x4096 bf16 from codes 36.9 us (4.6 TB/s, 0.68 of what a copy reaches), 2048x12288 from x 36.6
+// (0.61), 65536x4096 from codes 0.95.  What is left at the short sizes does not grow with the rows:
+// every SM reads the same weights at the start (1.7 to 3 us at 4096 columns, 5 at 12288), and the
+// partial sums are written and added up at the end (4.4 and 8 us, the second launch included).
 #include "norm.cuh"
 
 namespace fp8q {
