@@ -116,15 +116,17 @@ __global__ void __launch_bounds__(kThreads, VECTOR ? 4 : 3) k_act(const ActParam
     const T* pa = static_cast<const T*>(p.a) + row * p.lda + c;
     const T* pb = static_cast<const T*>(p.b) + row * p.ldb + c;
     T* py = static_cast<T*>(p.y) + row * p.ldy + c;
-    uint4 ra[kPieces], rb[kPieces];
+    typename P::template Run<kPieces> ra, rb;
     P::load_raw(pa, c, left, ra);
     if (GATED) P::load_raw(pb, c, left, rb);
+    P::settle(ra);
+    if (GATED) P::settle(rb);
     float a[kPieces][E], b[kPieces][E];
     uint4 y[kPieces];
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
-      P::unpack(ra[k], a[k]);
-      if (GATED) P::unpack(rb[k], b[k]);
+      P::unpack(ra.r[k], a[k]);
+      if (GATED) P::unpack(rb.r[k], b[k]);
       float v[E];
 #pragma unroll
       for (int i = 0; i < E; i += 2) {
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, VECTOR ? 4 : 3) k_act_backward(const
     const int64_t row = at.row;
     const int c = static_cast<int>(at.piece) * kPieces * P::WC + P::first(lane), left = cols - c;
     const int64_t q = row * p.ldq + c, s = row * groups + c / 128;
-    uint4 rdy[kPieces], ra[kPieces], rb[kPieces];
+    typename P::template Run<kPieces> rdy, ra, rb;
     typename P::Codes ca[kPieces], cb[kPieces];
     float sa[kPieces], sb[kPieces];
     P::load_raw(static_cast<const T*>(p.dy) + row * p.lddy + c, c, left, rdy);
@@ -173,17 +175,20 @@ __global__ void __launch_bounds__(kThreads, VECTOR ? 4 : 3) k_act_backward(const
     } else {
       P::load_raw(static_cast<const T*>(p.a) + row * p.lda + c, c, left, ra);
       if (GATED) P::load_raw(static_cast<const T*>(p.b) + row * p.ldb + c, c, left, rb);
+      P::settle(ra);
+      if (GATED) P::settle(rb);
     }
+    P::settle(rdy);
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
       float dy[E], a[E], b[E];
-      P::unpack(rdy[k], dy);
+      P::unpack(rdy.r[k], dy);
       if (CODES) {
         P::decode(ca[k], sa[k], p.e5m2, a);
         if (GATED) P::decode(cb[k], sb[k], p.e5m2, b);
       } else {
-        P::unpack(ra[k], a);
-        if (GATED) P::unpack(rb[k], b);
+        P::unpack(ra.r[k], a);
+        if (GATED) P::unpack(rb.r[k], b);
       }
 #pragma unroll
       for (int i = 0; i < E; i += 2) {
@@ -199,11 +204,11 @@ __global__ void __launch_bounds__(kThreads, VECTOR ? 4 : 3) k_act_backward(const
           b[i + 1] = f.y;
         }
       }
-      ra[k] = P::pack(a);
-      if (GATED) rb[k] = P::pack(b);
+      ra.r[k] = P::pack(a);
+      if (GATED) rb.r[k] = P::pack(b);
     }
-    P::store_raw(static_cast<T*>(p.da) + row * p.ldda + c, left, ra);
-    if (GATED) P::store_raw(static_cast<T*>(p.db) + row * p.lddb + c, left, rb);
+    P::store_raw(static_cast<T*>(p.da) + row * p.ldda + c, left, ra.r);
+    if (GATED) P::store_raw(static_cast<T*>(p.db) + row * p.lddb + c, left, rb.r);
   }
 }
 

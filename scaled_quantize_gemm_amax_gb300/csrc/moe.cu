@@ -191,29 +191,32 @@ struct Choices {
   }
 };
 
-// `warps` warps per token (a block has 8 / warps tokens at a time), each holding its pieces of
+// `warps` warps per token (a block has one or more tokens at a time), each holding its pieces of
 // the token's row: rows out[pos_j] = w_j in[t], and the dots <in[t], other[pos_j]>.  The token's
 // row is read once for all its choices, and the next token's choices are fetched while this
-// one's rows move.  After the tokens, a warp per kZeroRows rows of `out` sets those that no
+// one's rows move.  After the tokens, a warp per `zero_rows` rows of `out` sets those that no
 // choice fills to zero.
+constexpr int kMostWarps = 11;   // of a token's row
 constexpr int kZeroRows = 4;
 template <typename T, bool VECTOR, bool DOTS, int FLIGHT>
-__global__ void __launch_bounds__(kThreads, VECTOR ? (!DOTS ? 5 : FLIGHT > 2 ? 3 : 4) : (!DOTS ? 3 : 2)) k_scatter(const ScatterParams p, const int warps) {
+__global__ void __maxnreg__(VECTOR ? (!DOTS ? 48 : FLIGHT > 2 ? 80 : 64) : (!DOTS ? 72 : 128))
+    k_scatter(const ScatterParams p, const int warps, const int zero_rows) {
   using P = Piece<T, VECTOR>;
   __shared__ float part[2][kWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / warps, w_in = warp - group * warps;
   const int cols = static_cast<int>(p.cols), block_cols = warps * kPieces * P::WC;
-  const int64_t per_item = static_cast<int64_t>(warps) * kZeroRows, items = p.tokens + (p.capacity + per_item - 1) / per_item;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kWarps / warps);
+  const int64_t per_item = static_cast<int64_t>(warps) * zero_rows, items = p.tokens + (p.capacity + per_item - 1) / per_item;
+  const int groups = static_cast<int>(blockDim.x >> 5) / warps;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   int buf = 0;
   pdl_wait();
   pdl_launch_dependents();
-  int64_t t = static_cast<int64_t>(blockIdx.x) * (kWarps / warps) + group;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * groups + group;
   Choices next(p.pos, p.weights, t, p.tokens, p.k, 0, lane);
   for (; t < items; t += step) {
     if (t >= p.tokens) {
-      const int64_t r0 = ((t - p.tokens) * warps + w_in) * kZeroRows, r = r0 + lane;
-      uint32_t empty = __ballot_sync(0xFFFFFFFFu, lane < kZeroRows && r < p.capacity && __ldg(p.src + r) < 0);
+      const int64_t r0 = ((t - p.tokens) * warps + w_in) * zero_rows, r = r0 + lane;
+      uint32_t empty = __ballot_sync(0xFFFFFFFFu, lane < zero_rows && r < p.capacity && __ldg(p.src + r) < 0);
       const uint4 zero[1] = {make_uint4(0u, 0u, 0u, 0u)};
       for (; empty != 0; empty &= empty - 1) {
         T* out = static_cast<T*>(p.out) + (r0 + __ffs(empty) - 1) * p.ldout;
@@ -231,20 +234,21 @@ __global__ void __launch_bounds__(kThreads, VECTOR ? (!DOTS ? 5 : FLIGHT > 2 ? 3
       float my_dot = 0.0f;   // of choice j0 + lane
       for (int cb = w_in * kPieces * P::WC; cb < cols; cb += block_cols) {
         const int first = cb + P::first(lane), left = cols - first;
-        uint4 raw[kPieces];
+        typename P::template Run<kPieces> raw;
         P::load_raw(in + first, first, left, raw);
+        if (!DOTS) P::settle(raw);
         for (int j = 0; j < n; j += FLIGHT) {
-          uint4 o[DOTS ? FLIGHT : 1][kPieces];
+          typename P::template Run<kPieces> o[DOTS ? FLIGHT : 1];
           if constexpr (DOTS) {
 #pragma unroll
             for (int u = 0; u < FLIGHT; ++u) {
               const int pos = __shfl_sync(0xFFFFFFFFu, c.pos, (j + u) & 31);
               const bool on = j + u < n && pos >= 0;
               const T* other = static_cast<const T*>(p.other) + (on ? pos : 0) * p.ldother + first;
-#pragma unroll
-              for (int i = 0; i < kPieces; ++i) o[u][i] = make_uint4(0u, 0u, 0u, 0u);
+              P::clear(o[u]);
               if (on) P::load_raw(other, first, left, o[u]);
             }
+            if (j == 0) P::settle(raw);
           }
 #pragma unroll
           for (int u = 0; u < FLIGHT; ++u) {
@@ -254,11 +258,12 @@ __global__ void __launch_bounds__(kThreads, VECTOR ? (!DOTS ? 5 : FLIGHT > 2 ? 3
             if (pos < 0) continue;
             T* out = static_cast<T*>(p.out) + pos * p.ldout + first;
             float2 dot = {0.0f, 0.0f};
+            if constexpr (DOTS) P::settle(o[u]);
             uint4 moved[kPieces];
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
               float v[P::E], y[P::E];
-              P::unpack(raw[i], v);
+              P::unpack(raw.r[i], v);
 #pragma unroll
               for (int e = 0; e < P::E; e += 2) {
                 const float2 m = mul2(both(w), make_float2(v[e], v[e + 1]));
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, VECTOR ? (!DOTS ? 5 : FLIGHT > 2 ? 3
               }
               moved[i] = P::pack(y);
               if constexpr (DOTS) {
-                P::unpack(o[u][i], y);
+                P::unpack(o[u].r[i], y);
 #pragma unroll
                 for (int e = 0; e < P::E; e += 2) dot = fma2(make_float2(v[e], v[e + 1]), make_float2(y[e], y[e + 1]), dot);
               }
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, VECTOR ? (FLIGHT > 2 ? 3 : 4) : 2) k
       c.check(p.capacity, p.err);
       const int n = min(32, p.k - j0);
       for (int j = 0; j < n; j += FLIGHT) {
-        uint4 raw[FLIGHT][kPieces];
+        typename P::template Run<kPieces> raw[FLIGHT];
         float w[FLIGHT];
 #pragma unroll
         for (int u = 0; u < FLIGHT; ++u) {
@@ -329,17 +334,17 @@ __global__ void __launch_bounds__(kThreads, VECTOR ? (FLIGHT > 2 ? 3 : 4) : 2) k
           w[u] = __shfl_sync(0xFFFFFFFFu, c.w, (j + u) & 31);
           const bool on = j + u < n && pos >= 0;
           const T* ys = static_cast<const T*>(p.ys) + (on ? pos : 0) * p.ldys + first;
-#pragma unroll
-          for (int i = 0; i < kPieces; ++i) raw[u][i] = make_uint4(0u, 0u, 0u, 0u);
+          P::clear(raw[u]);
           if (on) P::load_raw(ys, first, left, raw[u]);
         }
 #pragma unroll
         for (int u = 0; u < FLIGHT; ++u) {
           if (j + u >= n) break;
+          P::settle(raw[u]);
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
             float v[P::E];
-            P::unpack(raw[u][i], v);
+            P::unpack(raw[u].r[i], v);
 #pragma unroll
             for (int e = 0; e < P::E; e += 2) {
               const float2 m = fma2(both(w[u]), make_float2(v[e], v[e + 1]), make_float2(acc[i][e], acc[i][e + 1]));
@@ -391,15 +396,25 @@ namespace {
 
 template <typename T, bool VECTOR>
 cudaError_t run_scatter(const ScatterParams& p, int num_sms, cudaStream_t s) {
-  // a warp for every kPieces pieces of a row, up to a block's 8
-  const int64_t wc = Piece<T, VECTOR>::WC * kPieces;
+  // A warp for every kPieces pieces of a row, and blocks of as many tokens as 8 warps hold.  Past 8
+  // warps' pieces the block grows a little before it goes round twice (dispatch, 4099 wide: 57 us with
+  // 9 warps, 65 with 8; 12 warps, 6144 wide, are no gain and 16, 12288 wide, lose a quarter).  With
+  // dots, whose warps wait for each other, a power of two up to 8 (4099 wide: 9 warps 208 us, 8 180).
+  const int64_t wc = Piece<T, VECTOR>::WC * kPieces, runs = (p.cols + wc - 1) / wc;
   int warps = 1;
-  while (warps < kWarps && warps * wc < p.cols) warps *= 2;
-  const int64_t per_item = static_cast<int64_t>(warps) * kZeroRows, items = p.tokens + (p.capacity + per_item - 1) / per_item;
+  if (p.dots == nullptr && runs <= kMostWarps)
+    warps = static_cast<int>(runs < 1 ? 1 : runs);
+  else
+    while (warps < kWarps && warps < runs) warps *= 2;
+  const int groups = warps < kWarps ? kWarps / warps : 1;
+  // rows a warp looks through for those to set to zero: few enough that every SM has some
+  int64_t zero_rows = p.capacity / (static_cast<int64_t>(num_sms) * kWarps);
+  zero_rows = zero_rows < 1 ? 1 : zero_rows > kZeroRows ? kZeroRows : zero_rows;
+  const int64_t per_item = warps * zero_rows, items = p.tokens + (p.capacity + per_item - 1) / per_item;
   const bool few = p.k <= 2;
-  const dim3 grid(grid_of((items + kWarps / warps - 1) / (kWarps / warps), num_sms, p.dots == nullptr ? 16 : 8));
+  const dim3 grid(grid_of((items + groups - 1) / groups, num_sms, p.dots == nullptr ? 16 : 8));
   auto kernel = p.dots == nullptr ? k_scatter<T, VECTOR, false, 2> : few ? k_scatter<T, VECTOR, true, 2> : k_scatter<T, VECTOR, true, 4>;
-  return launch_pdl(kernel, grid, dim3(kThreads), 0, s, 1, p, warps);
+  return launch_pdl(kernel, grid, dim3(static_cast<unsigned>(warps * groups * 32)), 0, s, 1, p, warps, static_cast<int>(zero_rows));
 }
 
 template <typename T, bool VECTOR>

@@ -120,9 +120,33 @@ struct Piece {
   }
 
   // The lane's values of N consecutive pieces as they lie in memory (0 past the row's end): what
-  // waits in registers waits in this form.
+  // waits in registers waits in this form.  Unaligned bf16 from an odd element is held as the words
+  // around it until settle(), so that loads that nothing waits for yet stay in flight together.
   template <int N>
-  __device__ static __forceinline__ void load_raw(const T* p, int c, int left, uint4 (&r)[N]) {
+  struct Run {
+    uint4 r[N];
+    uint32_t past[N];   // the word after each piece's four
+    bool half;
+  };
+  template <int N>
+  __device__ static __forceinline__ void clear(Run<N>& x) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) x.r[j] = make_uint4(0u, 0u, 0u, 0u);
+    x.half = false;
+  }
+  template <int N>
+  __device__ static __forceinline__ void settle(Run<N>& x) {
+    if constexpr (!VECTOR && !kStrided) {
+      if (!x.half) return;
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        x.r[j] = make_uint4(__funnelshift_r(x.r[j].x, x.r[j].y, 16), __funnelshift_r(x.r[j].y, x.r[j].z, 16),
+                            __funnelshift_r(x.r[j].z, x.r[j].w, 16), __funnelshift_r(x.r[j].w, x.past[j], 16));
+    }
+  }
+  template <int N>
+  __device__ static __forceinline__ void load_raw(const T* p, int c, int left, Run<N>& x) {
+    uint4(&r)[N] = x.r;
     if constexpr (VECTOR) {
 #pragma unroll
       for (int j = 0; j < N; ++j)
@@ -141,9 +165,14 @@ struct Piece {
       // every word is the row's: the whole warp takes this way
       if ((c > first(lane) || !half) && row_left > N * WC) {
         const uint32_t* w = reinterpret_cast<const uint32_t*>(p - (half ? 1 : 0));
+        x.half = half;
 #pragma unroll
-        for (int j = 0; j < N; ++j) r[j] = words(w + j * WC / 2, half);
+        for (int j = 0; j < N; ++j) {
+          r[j] = make_uint4(__ldg(w + j * WC / 2), __ldg(w + j * WC / 2 + 1), __ldg(w + j * WC / 2 + 2), __ldg(w + j * WC / 2 + 3));
+          if (half) x.past[j] = __ldg(w + j * WC / 2 + 4);
+        }
       } else {
+        x.half = false;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           uint32_t u[4] = {0u, 0u, 0u, 0u};
@@ -157,10 +186,11 @@ struct Piece {
   }
   template <int N>
   __device__ static __forceinline__ void load(const T* p, int c, int left, float (&v)[N][E]) {
-    uint4 r[N];
-    load_raw(p, c, left, r);
+    Run<N> x;
+    load_raw(p, c, left, x);
+    settle(x);
 #pragma unroll
-    for (int j = 0; j < N; ++j) unpack(r[j], v[j]);
+    for (int j = 0; j < N; ++j) unpack(x.r[j], v[j]);
   }
   __device__ static __forceinline__ void unpack(const uint4& w, float (&v)[E]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
