@@ -355,7 +355,7 @@ fp8_status fp8_scaled_gemm_amax(const uint8_t* A, fp8_format fa, fp8_recipe ra, 
  *     elements (FP8_ERR_SHAPE below it; ignored for a single row) and may start at any
  *     element (alignment: the element's size).  Rows whose pointer and stride are
  *     multiples of 16 bytes, with cols a multiple of 16 bytes, move in 16-byte accesses;
- *     others in 4-byte words (bf16) or element by element (binary32), at 1/2 to 3/4 of
+ *     others in 4-byte words (bf16) or element by element (binary32), at 0.4 to 0.9 of
  *     the speed; binary32 sums over such a row are then taken in another order.
  *   - rows and cols are below 2^31 - 65536, strides and capacity below 2^31 (FP8_ERR_SHAPE).
  *   - outputs must not overlap inputs or each other.

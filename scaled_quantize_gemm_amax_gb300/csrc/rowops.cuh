@@ -82,9 +82,9 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
 //                    a word more and shifted by half a word; what a lane stores begins with the
 //                    lane before's last value, so that every word but the ends' is whole.  A run
 //                    of pieces that touches the row's end goes element by element; no byte outside
-//                    the row is touched.  (Element by element throughout, 8192x9001 gated SiLU took
-//                    265 us; aligned 16-byte granules shifted over the lanes 157 us: 11 selections a
-//                    lane and tensor.)
+//                    the row is touched.  (8192x9001 gated SiLU 124 us; element by element throughout
+//                    265; aligned 16-byte granules shifted over the lanes 157, 11 selections a lane
+//                    and tensor; pairs 2 l and 2 l + 64, halves exchanged between lanes, 147.)
 //   binary32 otherwise  lane l columns l, l + 32, l + 64, l + 96, element by element, which
 //                    coalesces at any alignment (4096x9001 gated SiLU 84 us; granules 136).
 // A lane works from its own first column `c` of the row: pointers point there, and `left` is the
@@ -112,7 +112,7 @@ struct Piece {
   }
   // whether p is at an odd element of a 4-byte word (bf16)
   __device__ static __forceinline__ bool odd(const T* p) { return (reinterpret_cast<uintptr_t>(p) & 2) != 0; }
-  // 16 bytes from 4-byte words at w, or from two bytes on (generic address: global or shared memory)
+  // 16 bytes from 4-byte words at w, or from two bytes on (shared memory)
   __device__ static __forceinline__ uint4 words(const uint32_t* w, bool half) {
     const uint32_t a = w[0], b = w[1], c = w[2], d = w[3];
     if (!half) return make_uint4(a, b, c, d);
