@@ -278,6 +278,29 @@ def test_another_stream_and_a_graph():
             assert torch.equal(a, c)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_given_stream_owns_the_workspace(raw):
+    # the call returns while its kernels wait behind other work of that stream; what it allocated for
+    # itself must not be handed to the current stream meanwhile
+    x, dy = matrix(64, 2048, torch.bfloat16, 542), matrix(64, 2048, torch.bfloat16, 543)
+    w, b = params(2048, torch.float32, 13)
+    _, mean, rstd, _, _ = fq.layer_norm(x, w, b)
+    ref = fq.layer_norm_backward(dy, rstd, w, x=x, mean=mean)
+    nbytes = fq.fp8_layer_norm_workspace(64, 2048)
+    side = torch.cuda.Stream()
+    big = torch.ones((4096, 4096), device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            out = big @ big
+    got = fq.layer_norm_backward(dy, rstd, w, x=x, mean=mean, stream=side.cuda_stream if raw else side)
+    junk = [torch.full((nbytes,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    for a, c in zip(ref, got):
+        assert torch.equal(a, c)
+    del out, junk
+
+
 def test_offsets_past_32_bits():
     ld = 1_200_000_000                            # the third row starts past 2^31 elements
     buf = torch.empty(2 * ld + 4096, dtype=torch.bfloat16, device="cuda")
