@@ -392,7 +392,13 @@ template <typename T, bool VECTOR, bool CODES>
 cudaError_t run_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
   if (p.cols <= 256) return run_norm_backward<T, VECTOR, CODES, 8, 24>(p, num_sms, s, partials);
   if (p.cols <= 512) return run_norm_backward<T, VECTOR, CODES, 16, 24>(p, num_sms, s, partials);
-  if (p.cols <= 12288) return run_norm_backward<T, VECTOR, CODES, 32, 12>(p, num_sms, s, partials);
+  // rows of 5, 7 or 8 warps leave 2 to 5 of 12 idle and at most 2 of 16: bf16 from codes 8192x8192 66
+  // us with 16 warps, 77 with 12, 13107x5120 67 and 73; unaligned from x 16372x4099 140 and 155;
+  // aligned from x 76 and 71 at 5120, binary32 60 and 52 at 4096x8192: these stay
+  const int64_t warps = (p.cols + 1023) / 1024;
+  const bool idle = warps <= 12 && 4 * (12 / warps) < 3 * (16 / warps);
+  if (p.cols <= 12288 && !(idle && sizeof(T) == 2 && (CODES || !VECTOR)))
+    return run_norm_backward<T, VECTOR, CODES, 32, 12>(p, num_sms, s, partials);
   return run_norm_backward<T, VECTOR, CODES, 32, 16>(p, num_sms, s, partials);
 }
 
