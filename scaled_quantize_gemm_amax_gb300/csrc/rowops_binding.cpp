@@ -63,11 +63,17 @@ const at::Tensor& needed(PyObject* o, const char* what) {
   if (t == nullptr) refuse(PyExc_TypeError, std::string(what) + ": a tensor is needed, not None");
   return *t;
 }
-// Checked last, so that what else is wrong with a tensor is named first.
+// All tensors of a call are on one GPU.  Checked last, so that what else is wrong with a tensor is named first.
 void on_gpu(std::initializer_list<PyObject*> args) {
-  for (PyObject* o : args)
-    if (o != Py_None && !THPVariable_Unpack(o).is_cuda())
-      refuse(PyExc_ValueError, "a CUDA tensor is needed, not one on " + THPVariable_Unpack(o).device().str());
+  const at::Tensor* first = nullptr;
+  for (PyObject* o : args) {
+    if (o == Py_None) continue;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda()) refuse(PyExc_ValueError, "a CUDA tensor is needed, not one on " + t.device().str());
+    if (first == nullptr) first = &t;
+    if (t.device() != first->device())
+      refuse(PyExc_ValueError, "tensors of one device are needed, not of " + first->device().str() + " and " + t.device().str());
+  }
 }
 fp8_dtype dtype_code(at::ScalarType type, const char* what) {
   if (type == at::kBFloat16) return FP8_DT_BF16;
@@ -184,17 +190,26 @@ bool truth(PyObject* o) {
 }
 // A number for an int32_t of the C ABI, which refuses what lies outside its range there too.
 int32_t small(int64_t v) { return static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(v, -1), INT32_MAX)); }
+// Where a call runs.  The tensors' device is current meanwhile: the library launches on the
+// current device, whose number need not be the tensors'.
+struct Place {
+  c10::cuda::OptionalCUDAGuard device;
+  c10::cuda::OptionalCUDAStreamGuard stream;
+};
 // The stream of a call.  None: the current stream of the tensors' device; else a raw stream or an
 // object that has one, which `on` makes current, so that outputs and workspaces are allocated for
 // the stream that writes them: a workspace is given back while its kernels may still be queued.
-cudaStream_t stream_of(PyObject* o, const at::Tensor& t, c10::cuda::OptionalCUDAStreamGuard& on) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
+cudaStream_t stream_of(PyObject* o, const at::Tensor& t, Place& on) {
+  if (o == Py_None) {
+    on.device.set_index(t.device().index());
+    return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
+  }
   PyObject* raw = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
   if (raw == nullptr) throw Failed();
   const auto s = static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(raw));
   Py_DECREF(raw);
   if (PyErr_Occurred()) throw Failed();
-  on.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(s), t.device().index()));
+  on.stream.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(s), t.device().index()));
   return reinterpret_cast<cudaStream_t>(s);
 }
 fp8_format format(PyObject* o) { return static_cast<fp8_format>(small(integer(o))); }
@@ -219,7 +234,7 @@ PyObject* layer_norm(PyObject* const* a) {
   if (PyErr_Occurred()) throw Failed();
   const bool stats = truth(a[5]), keep = a[4] != Py_None;
   const fp8_format fmt = keep ? format(a[4]) : FP8_E4M3;
-  c10::cuda::OptionalCUDAStreamGuard on;
+  Place on;
   const cudaStream_t stream = stream_of(a[6], *x.t, on);
   at::Tensor y, mean, rstd;
   NewCopy c;
@@ -258,7 +273,7 @@ PyObject* layer_norm_backward(PyObject* const* a) {
   on_gpu({a[0], a[1], a[2], a[3], a[4], a[5], a[6]});
   const fp8_format fmt = format(a[7]);
   const bool param_grads = truth(a[8]);
-  c10::cuda::OptionalCUDAStreamGuard on;
+  Place on;
   const cudaStream_t stream = stream_of(a[10], *dy.t, on);
   int64_t bytes = 0;
   if (param_grads) check(p_fp8_layer_norm_workspace(dy.rows, dy.cols, &bytes), "fp8_layer_norm_workspace");
@@ -290,7 +305,7 @@ PyObject* gated_act(PyObject* const* a) {
   const fp8_act act = activation(a[2]);
   const bool keep = a[3] != Py_None;
   const fp8_format fmt = keep ? format(a[3]) : FP8_E4M3;
-  c10::cuda::OptionalCUDAStreamGuard on;
+  Place on;
   const cudaStream_t stream = stream_of(a[4], *x.t, on);
   at::Tensor y;
   NewCopy ca, cb;
@@ -320,7 +335,7 @@ PyObject* gated_act_backward(PyObject* const* a) {
   on_gpu({a[0], a[2], a[3], a[4], a[5], a[6], a[7]});
   const fp8_act act = activation(a[1]);
   const fp8_format fmt = format(a[8]);
-  c10::cuda::OptionalCUDAStreamGuard on;
+  Place on;
   const cudaStream_t stream = stream_of(a[9], *dy.t, on);
   const bool gated = b.t != nullptr || cb.q != nullptr;
   const int64_t ld = gated ? 2 * dy.cols : dy.cols;
@@ -350,7 +365,7 @@ PyObject* moe_route(PyObject* const* a) {
   on_gpu({a[0]});
   const int64_t tokens = e.size(0);
   const int32_t k = small(e.size(1)), n_experts = small(integer(a[1])), align = small(integer(a[2]));
-  c10::cuda::OptionalCUDAStreamGuard on;
+  Place on;
   const cudaStream_t stream = stream_of(a[3], e, on);
   int64_t capacity = 0;
   check(p_fp8_moe_capacity(tokens, k, n_experts, align, &capacity), "fp8_moe_capacity");
@@ -386,7 +401,7 @@ PyObject* moe_dispatch(PyObject* const* a) {
   const int64_t capacity = needed(a[2], "src").numel();
   auto* src = static_cast<int32_t*>(vector_of(a[2], capacity, at::kInt, "src"));
   on_gpu({a[0], a[1], a[2]});
-  c10::cuda::OptionalCUDAStreamGuard on;
+  Place on;
   const cudaStream_t stream = stream_of(a[3], *x.t, on);
   at::Tensor xs;
   fp8_status st;
@@ -407,7 +422,7 @@ PyObject* moe_combine(PyObject* const* a) {
   const at::Tensor& pos = choices(a[1], -1);
   auto* w = static_cast<float*>(vector_of(a[2], pos.numel(), at::kFloat, "weights"));
   on_gpu({a[0], a[1], a[2]});
-  c10::cuda::OptionalCUDAStreamGuard on;
+  Place on;
   const cudaStream_t stream = stream_of(a[3], *ys.t, on);
   at::Tensor y;
   fp8_status st;
@@ -431,9 +446,8 @@ PyObject* moe_combine_backward(PyObject* const* a) {
   auto* w = static_cast<float*>(vector_of(a[4], pos.numel(), at::kFloat, "weights"));
   const bool weighted = a[4] != Py_None;
   const Rows ys = weighted ? rows_like(a[1], *dy.t, capacity, dy.cols, "ys") : Rows{};
-  on_gpu({a[0], a[2], a[3], a[4]});
-  if (weighted) on_gpu({a[1]});
-  c10::cuda::OptionalCUDAStreamGuard on;
+  on_gpu({a[0], a[2], a[3], a[4], weighted ? a[1] : Py_None});
+  Place on;
   const cudaStream_t stream = stream_of(a[5], *dy.t, on);
   at::Tensor dys, dw;
   fp8_status st;
