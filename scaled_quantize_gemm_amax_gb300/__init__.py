@@ -28,6 +28,7 @@ from __future__ import annotations
 
 import ctypes
 import enum
+import functools
 import os
 import typing
 
@@ -167,11 +168,19 @@ def load_library(path: str | None = None):
     return lib
 
 
+@functools.cache
+def _several_gpus() -> bool:
+    return torch.cuda.device_count() > 1
+
+
 def _ptr(t):
     if t is None:
         return None
     if isinstance(t, int):
         return t
+    # the library launches on the current device; with one GPU there is nothing to compare
+    if _several_gpus() and t.is_cuda and t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
     return t.data_ptr()
 
 

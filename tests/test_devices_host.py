@@ -34,3 +34,40 @@ def test_helpers_refuse_tensors_of_two_gpus():
                  lambda: fq.moe_combine_backward(b(4, 64), a(8, 64), route, b(4, 2))):
         with pytest.raises(ValueError, match="of one device"):
             call()
+
+
+def test_entry_points_refuse_tensors_of_another_gpu(monkeypatch):
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: calls.append(name) or 0
+
+    monkeypatch.setattr(fq, "load_library", lambda path=None: Library())
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    fq._several_gpus.cache_clear()
+    try:
+        here, there = on(1), on(0)
+        bf16, u8 = torch.bfloat16, torch.uint8
+
+        def amax(at, to):
+            fq.fp8_amax(at(4, 128, dtype=bf16), to(1), stream=0)
+
+        def cast(at, to):
+            fq.fp8_cast_transpose(at(128, 128, dtype=bf16), fq.Recipe.BLOCK_1x128, fq.Format.E4M3, None, None,
+                                  to(128, 128, dtype=u8), to(128, 1), to(128, 128, dtype=u8), to(128, 1), stream=0)
+
+        def norm(at, to):
+            fq.fp8_layer_norm(at(4, 128), None, None, 1e-5, to(4, 128), None, None, fq.Format.E4M3, None, None, stream=0)
+
+        for call in (amax, cast, norm):
+            for at, to in ((there, there), (here, there), (there, here)):
+                with pytest.raises(ValueError):
+                    call(at, to)
+            assert not calls
+            call(here, here)
+            assert len(calls) == 1
+            calls.clear()
+    finally:
+        fq._several_gpus.cache_clear()
