@@ -184,12 +184,9 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_raw_stream, _device_index = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-
-
 def _stream(stream):
-    if stream is None:   # torch.cuda.current_stream().cuda_stream, without making the Stream object
-        return _raw_stream(_device_index())
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
