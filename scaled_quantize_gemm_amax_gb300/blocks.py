@@ -17,7 +17,7 @@ the BF16 tensors; the forward values do not change.
 FP8 linear layers per expert with a gated activation between them, combine, residual.
 Every operator runs in the library's kernels; torch does the router's small product and
 top-k.  Leading dimensions are flattened; a tensor whose last dimension is not contiguous
-is copied.
+or whose rows overlap (an expanded one) is copied.
 """
 from __future__ import annotations
 
@@ -37,9 +37,10 @@ __all__ = ["layer_norm", "gated_act", "moe_dispatch", "moe_combine", "LayerNorm"
 
 
 def _flat(x):
-    """x as a matrix of rows with a contiguous last dimension."""
+    """x as a matrix of rows of their own with a contiguous last dimension (an expanded one's rows share their memory)."""
     x = x.reshape(-1, x.shape[-1])
-    return x if x.stride(1) == 1 or x.shape[1] <= 1 else x.contiguous()
+    dense = (x.stride(1) == 1 or x.shape[1] <= 1) and (x.stride(0) >= x.shape[1] or x.shape[0] <= 1)
+    return x if dense else x.contiguous()
 
 
 class _LayerNormFn(torch.autograd.Function):
