@@ -11,7 +11,7 @@ the C ABI:
 
 ``checkpoint=Format.E4M3`` keeps what the backward pass needs (layer norm: the normalised
 rows; activation: its inputs) as 8-bit codes with one multiplier per 128 columns instead of
-the BF16 tensors; the forward values do not change.
+the BF16 tensors; the forward values do not change.  A second derivative is an error.
 
 ``FP8MoEBlock`` is the pre-norm expert MLP of a transformer: norm, router, dispatch, two
 FP8 linear layers per expert with a gated activation between them, combine, residual.
@@ -22,6 +22,7 @@ or whose rows overlap (an expanded one) is copied.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (Activation, Format, MoeRoute, fp8_gated_act_backward, moe_route)
 from . import gated_act as _gated_act
@@ -57,6 +58,7 @@ class _LayerNormFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         w, rstd, a, b = ctx.saved_tensors
         checkpoint, has_weight, bias_dtype = ctx.meta
@@ -85,6 +87,7 @@ class _GatedActFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         act, gated, checkpoint, cols = ctx.meta
         dy = _flat(dy)
@@ -115,6 +118,7 @@ class _DispatchFn(torch.autograd.Function):
         return _moe_dispatch(x, ctx.route)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dxs):
         return _moe_dispatch_backward(_flat(dxs), ctx.route), None, None, None
 
@@ -133,6 +137,7 @@ class _CombineFn(torch.autograd.Function):
         return _moe_combine(ys, ctx.route, w)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         w, ys = ctx.saved_tensors
         dys, dw = _moe_combine_backward(_flat(dy), ys, ctx.route, w)

@@ -121,3 +121,14 @@ def test_expanded_inputs(name):
     ref, = torch.autograd.grad(y_ref, full, dy)
     assert torch.equal(y, y_ref)
     assert torch.allclose(got, ref.sum(0, keepdim=True), atol=1e-5)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_second_derivative_is_refused(name):
+    # the backward passes have no derivatives of their own: a gradient that should carry a graph must not pass for one
+    # that does
+    f, shape = operators()[name]
+    x = torch.randn(shape, requires_grad=True)
+    g, = torch.autograd.grad(f(x).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.square().sum().backward()
