@@ -28,7 +28,8 @@ FP32 master weight is quantized directly (fp8_cast_transpose_f32, with
 fp8_amax_f32 for current scaling), bf16 or float32 activations and gradients
 go to the cast of their own dtype, and each GEMM writes its output in the
 dtype autograd expects (Y and dX in the input's dtype, dW in FP32).  M, N and
-K must be multiples of 128 (the GEMM's tile), which the library checks.
+K must be multiples of 128 (the GEMM's tile), which the library checks.  A second
+derivative is an error.
 """
 from __future__ import annotations
 
@@ -37,6 +38,7 @@ import dataclasses
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (DelayedScaling, Format, OutDtype, Recipe, amax_history_update, cast_transpose, fp8_amax,
                fp8_amax_f32, fp8_compute_scale, fp8_scaled_gemm)
@@ -142,6 +144,7 @@ class _FP8LinearFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         qxt, sxt, qwt, swt = ctx.saved_tensors
         kx, kw, fx, fdy, st_dy, x_dtype, w_dtype = ctx.meta
