@@ -26,4 +26,4 @@ def test_a_second_derivative_is_refused():
     assert torch.allclose(gx, 2 * y @ w, atol=1e-5) and torch.allclose(gw, 2 * y.t() @ x, atol=1e-5)
     for g in (gx, gw):
         with pytest.raises(RuntimeError, match="once_differentiable"):
-            torch.autograd.grad(g.square().sum(), x, retain_graph=True)
+            g.square().sum().backward(retain_graph=True)
