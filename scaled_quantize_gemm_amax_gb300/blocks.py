@@ -114,13 +114,13 @@ def gated_act(h, act: Activation = Activation.SILU, gated: bool = True, checkpoi
 class _DispatchFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, offsets, pos, src):
-        ctx.route = MoeRoute(offsets, pos, src)
-        return _moe_dispatch(x, ctx.route)
+        ctx.save_for_backward(offsets, pos, src)
+        return _moe_dispatch(x, MoeRoute(offsets, pos, src))
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dxs):
-        return _moe_dispatch_backward(_flat(dxs), ctx.route), None, None, None
+        return _moe_dispatch_backward(_flat(dxs), MoeRoute(*ctx.saved_tensors)), None, None, None
 
 
 def moe_dispatch(x, route: MoeRoute):
@@ -131,16 +131,15 @@ def moe_dispatch(x, route: MoeRoute):
 class _CombineFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ys, weights, offsets, pos, src):
-        ctx.route = MoeRoute(offsets, pos, src)
         w = weights.detach().contiguous() if weights is not None else None
-        ctx.save_for_backward(w, ys if w is not None else None)
-        return _moe_combine(ys, ctx.route, w)
+        ctx.save_for_backward(w, ys if w is not None else None, offsets, pos, src)
+        return _moe_combine(ys, MoeRoute(offsets, pos, src), w)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        w, ys = ctx.saved_tensors
-        dys, dw = _moe_combine_backward(_flat(dy), ys, ctx.route, w)
+        w, ys, *route = ctx.saved_tensors
+        dys, dw = _moe_combine_backward(_flat(dy), ys, MoeRoute(*route), w)
         return dys, dw, None, None, None
 
 

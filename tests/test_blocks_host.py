@@ -132,3 +132,29 @@ def test_a_second_derivative_is_refused(name):
     g, = torch.autograd.grad(f(x).square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         g.square().sum().backward()
+
+
+@pytest.mark.parametrize("name", ["dispatch", "combine", "combine, no weights"])
+@pytest.mark.parametrize("changed", ["pos", "src"])
+def test_a_routing_changed_before_the_backward_pass_is_noticed(name, changed, monkeypatch):
+    monkeypatch.setitem(globals(), "ROUTE", fq.MoeRoute(*(t.clone() for t in ROUTE)))
+    f, shape = operators()[name]
+    y = f(torch.randn(shape, requires_grad=True))
+    getattr(ROUTE, changed).fill_(0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+@pytest.mark.parametrize("name", ["dispatch", "combine", "combine, no weights"])
+def test_saved_tensor_hooks_see_the_routing(name):
+    f, shape = operators()[name]
+    seen = []
+
+    def pack(t):
+        seen.append(t)
+        return t
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+        f(torch.randn(shape, requires_grad=True))
+    for t in (ROUTE.pos, ROUTE.src):
+        assert any(s.data_ptr() == t.data_ptr() for s in seen)
