@@ -133,6 +133,7 @@ class _CombineFn(torch.autograd.Function):
     def forward(ctx, ys, weights, offsets, pos, src):
         w = weights.detach().contiguous() if weights is not None else None
         ctx.save_for_backward(w, ys if w is not None else None, offsets, pos, src)
+        ctx.shape = weights.shape if weights is not None else None
         return _moe_combine(ys, MoeRoute(offsets, pos, src), w)
 
     @staticmethod
@@ -140,7 +141,7 @@ class _CombineFn(torch.autograd.Function):
     def backward(ctx, dy):
         w, ys, *route = ctx.saved_tensors
         dys, dw = _moe_combine_backward(_flat(dy), ys, MoeRoute(*route), w)
-        return dys, dw, None, None, None
+        return dys, dw.view(ctx.shape) if dw is not None else None, None, None, None
 
 
 def moe_combine(ys, route: MoeRoute, weights=None):

@@ -158,3 +158,16 @@ def test_saved_tensor_hooks_see_the_routing(name):
         f(torch.randn(shape, requires_grad=True))
     for t in (ROUTE.pos, ROUTE.src):
         assert any(s.data_ptr() == t.data_ptr() for s in seen)
+
+
+@pytest.mark.parametrize("shape", [(3, 2), (6,), (1, 3, 2)])
+def test_combine_weights_of_any_shape_have_a_gradient(shape):
+    ys = torch.randn((6, 8))
+    w = torch.rand(6)
+    ref = w.view(3, 2).clone().requires_grad_(True)
+    terms = plain_rows(ys, ROUTE) * ref[..., None]
+    dy = torch.randn((3, 8))
+    terms.sum(1).backward(dy)
+    got = w.view(shape).clone().requires_grad_(True)
+    B.moe_combine(ys, ROUTE, got).backward(dy)
+    assert got.grad.shape == shape and torch.allclose(got.grad.view(3, 2), ref.grad)
