@@ -320,11 +320,11 @@ def fp8_scaled_gemm_amax(a, fa, ra, sa, b, fb, rb, sb, c, out, c_amax, c_scale, 
 
 # ---- row operators
 def _rows(t, what: str):
-    """(rows, cols, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
+    """(rows, cols, row stride) of a 2-D CUDA tensor whose rows are contiguous (one without elements is)."""
     if t.dim() == 2:
         rows, cols = t.shape
         ld, one = t.stride()
-        if one == 1 or cols <= 1:
+        if one == 1 or cols <= 1 or rows == 0:
             return rows, cols, ld
     raise ValueError(f"{what}: a 2-D tensor with contiguous rows is needed, not shape {tuple(t.shape)} "
                      f"stride {t.stride()}")

@@ -82,14 +82,14 @@ fp8_dtype dtype_code(at::ScalarType type, const char* what) {
 }
 fp8_dtype data_type(const at::Tensor& t, const char* what) { return dtype_code(t.scalar_type(), what); }
 
-// A 2-D tensor whose rows are contiguous.
+// A 2-D tensor whose rows are contiguous (one without elements is, whatever its strides).
 struct Rows {
   const at::Tensor* t = nullptr;
   int64_t rows = 0, cols = 0, ld = 0;
   void* p() const { return t == nullptr ? nullptr : t->data_ptr(); }
 };
 Rows rows_of(const at::Tensor& t, const char* what) {
-  if (t.dim() != 2 || (t.stride(1) != 1 && t.size(1) > 1))
+  if (t.dim() != 2 || (t.stride(1) != 1 && t.size(1) > 1 && t.size(0) > 0))
     refuse(PyExc_ValueError, std::string(what) + ": a 2-D tensor with contiguous rows is needed, not " + shape_of(t));
   return {&t, t.size(0), t.size(1), t.stride(0)};
 }

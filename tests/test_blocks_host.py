@@ -9,7 +9,7 @@ from scaled_quantize_gemm_amax_gb300 import blocks as B
 
 def rows(x):
     """A matrix argument of an entry point: contiguous rows, a row stride of at least their length."""
-    assert x.dim() == 2 and (x.stride(1) == 1 or x.shape[1] <= 1), (x.shape, x.stride())
+    fq._rows(x, "x")
     assert x.shape[0] <= 1 or x.stride(0) >= x.shape[1], (x.shape, x.stride())
     return x.detach()
 
@@ -171,3 +171,12 @@ def test_combine_weights_of_any_shape_have_a_gradient(shape):
     got = w.view(shape).clone().requires_grad_(True)
     B.moe_combine(ys, ROUTE, got).backward(dy)
     assert got.grad.shape == shape and torch.allclose(got.grad.view(3, 2), ref.grad)
+
+
+
+def test_a_gradient_without_rows_that_is_expanded():
+    # the gradient of y.sum() where y has no rows: strides 0, and contiguous() leaves it so
+    for f in (lambda x: B.layer_norm(x), lambda x: B.gated_act(x, gated=False), B.gated_act):
+        x = torch.randn((0, 8), requires_grad=True)
+        f(x).sum().backward()
+        assert x.grad.shape == (0, 8)
