@@ -39,7 +39,7 @@ __all__ = ["layer_norm", "gated_act", "moe_dispatch", "moe_combine", "LayerNorm"
 
 def _flat(x):
     """x as a matrix of rows of their own with a contiguous last dimension (an expanded one's rows share their memory)."""
-    x = x.reshape(-1, x.shape[-1])
+    x = x.reshape(x.shape[:-1].numel(), x.shape[-1])   # -1 is ambiguous for rows of no columns
     dense = (x.stride(1) == 1 or x.shape[1] <= 1) and (x.stride(0) >= x.shape[1] or x.shape[0] <= 1)
     return x if dense else x.contiguous()
 

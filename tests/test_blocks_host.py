@@ -180,3 +180,13 @@ def test_a_gradient_without_rows_that_is_expanded():
         x = torch.randn((0, 8), requires_grad=True)
         f(x).sum().backward()
         assert x.grad.shape == (0, 8)
+
+
+@pytest.mark.parametrize("shape", [(0, 8), (2, 0, 8), (3, 0), (2, 3, 0), (0,), (8,)])
+def test_tensors_without_elements_and_without_leading_dimensions(shape):
+    for f in (lambda x: B.layer_norm(x), lambda x: B.gated_act(x, gated=False), B.gated_act):
+        x = torch.randn(shape, requires_grad=True)
+        y = f(x)
+        assert y.shape[:-1] == x.shape[:-1]
+        y.sum().backward()
+        assert x.grad.shape == x.shape
