@@ -56,10 +56,10 @@ def up_to_date(debug: bool = False) -> bool:
 
 
 def start_extension(force: bool = False):
-    """The compilation of _rowops.so under way: (process, temporary file), or None when it is up to date."""
-    inputs = (EXT_SOURCE, os.path.join(INCLUDE, "fp8q.h"), os.path.abspath(__file__))
-    if not force and os.path.exists(EXT) and all(os.path.getmtime(f) <= os.path.getmtime(EXT) for f in inputs):
-        return None
+    """The compilation of _rowops.so under way: (process, temporary file, stamp), or None when it is up to date.
+
+    The stamp, kept beside the object files, says what the extension was compiled against: it fits
+    one version of torch and Python only."""
     import sysconfig
 
     import torch
@@ -67,23 +67,45 @@ def start_extension(force: bool = False):
     root = os.path.dirname(torch.__file__)
     include = os.path.join(root, "include")
     cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
-    tmp = EXT + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            "-I", INCLUDE, "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"), EXT_SOURCE, "-o", tmp,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"), EXT_SOURCE,
            "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
-    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True), tmp
+    stamp = "\n".join((torch.__version__, sysconfig.get_config_var("EXT_SUFFIX") or "", *cmd))
+    inputs = (EXT_SOURCE, os.path.join(INCLUDE, "fp8q.h"), os.path.abspath(__file__))
+    if not force and os.path.exists(EXT) and all(os.path.getmtime(f) <= os.path.getmtime(EXT) for f in inputs) and \
+            _read(_stamp_path()) == stamp:
+        return None
+    tmp = EXT + f".tmp{os.getpid()}"
+    return subprocess.Popen([*cmd, "-o", tmp], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True), tmp, stamp
+
+
+def _stamp_path() -> str:
+    return os.path.join(BUILD, os.path.basename(EXT) + ".stamp")
+
+
+def _read(path: str) -> str | None:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
 
 
 def finish_extension(started) -> None:
     if started is None:
         return
-    p, tmp = started
+    p, tmp, stamp = started
     out, _ = p.communicate()
     if p.returncode != 0:
         sys.stderr.write(out)
         raise RuntimeError("g++ failed for rowops_binding.cpp")
+    os.makedirs(BUILD, exist_ok=True)
+    if os.path.exists(_stamp_path()):   # never beside an extension that it does not describe
+        os.remove(_stamp_path())
     os.replace(tmp, EXT)
+    with open(_stamp_path(), "w") as f:
+        f.write(stamp)
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
