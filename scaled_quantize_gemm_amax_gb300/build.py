@@ -92,6 +92,19 @@ def _read(path: str) -> str | None:
         return None
 
 
+def _remove(path: str) -> None:
+    if os.path.exists(path):
+        os.remove(path)
+
+
+def abandon_extension(started) -> None:
+    """Wait for a compilation whose result is not wanted, and remove it."""
+    if started is not None:
+        started[0].terminate()
+        started[0].communicate()
+        _remove(started[1])
+
+
 def finish_extension(started) -> None:
     if started is None:
         return
@@ -99,21 +112,16 @@ def finish_extension(started) -> None:
     out, _ = p.communicate()
     if p.returncode != 0:
         sys.stderr.write(out)
+        _remove(tmp)
         raise RuntimeError("g++ failed for rowops_binding.cpp")
     os.makedirs(BUILD, exist_ok=True)
-    if os.path.exists(_stamp_path()):   # never beside an extension that it does not describe
-        os.remove(_stamp_path())
+    _remove(_stamp_path())   # never beside an extension that it does not describe
     os.replace(tmp, EXT)
     with open(_stamp_path(), "w") as f:
         f.write(stamp)
 
 
-def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
-    lib = LIB_DEBUG if debug else LIB
-    extension = start_extension(force)
-    if not force and up_to_date(debug):
-        finish_extension(extension)
-        return lib
+def _build_library(lib: str, verbose: bool, debug: bool) -> None:
     build_dir = BUILD_DEBUG if debug else BUILD
     os.makedirs(build_dir, exist_ok=True)
     nvcc = _nvcc()
@@ -138,6 +146,19 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     tmp = lib + f".tmp{os.getpid()}"
     subprocess.run([nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", *objs, "-o", tmp], check=True)
     os.replace(tmp, lib)
+
+
+def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
+    lib = LIB_DEBUG if debug else LIB
+    extension = start_extension(force)
+    if not force and up_to_date(debug):
+        finish_extension(extension)
+        return lib
+    try:
+        _build_library(lib, verbose, debug)
+    except BaseException:
+        abandon_extension(extension)
+        raise
     finish_extension(extension)
     return lib
 

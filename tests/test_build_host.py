@@ -70,3 +70,22 @@ def test_the_extension_is_built_again_for_another_torch(tree, monkeypatch):
     assert extension_builds(started) == 1
     fqbuild.build()
     assert extension_builds(started) == 0
+
+
+@pytest.mark.parametrize("debug", [False, True])
+def test_a_failed_build_leaves_no_compiler_and_no_temporary_file(tree, debug):
+    started, codes, folder = tree
+    codes["nvcc"] = 1
+    with pytest.raises(RuntimeError, match="nvcc failed"):
+        fqbuild.build(debug=debug)
+    assert started and all(p.waited for p in started)
+    assert not [f for f in os.listdir(folder) if ".tmp" in f]
+
+
+def test_a_failed_extension_leaves_no_temporary_file(tree):
+    started, codes, folder = tree
+    codes["g++"] = 1
+    with pytest.raises(RuntimeError, match="g.. failed"):
+        fqbuild.build()
+    assert not [f for f in os.listdir(folder) if ".tmp" in f]
+    assert not os.path.exists(fqbuild.EXT)
