@@ -412,7 +412,7 @@ fp8_status fp8_layer_norm_workspace(int64_t rows, int64_t cols, int64_t* bytes);
  * fp8_gated_act -- y = f(a) b, or y = f(a) with b NULL; f is `act`.  With dt FP32, f and f'
  * (below) are right to a few units in the last place of their terms, however small.  With dt
  * BF16 shorter forms are used: GELU's normal distribution function is right to 2^-23 absolute,
- * so that below x = -3.8 f loses bf16 digits and below about -5.3 is 0; SiLU is 0 below -87.
+ * so that below x = -3.8 f loses bf16 digits and below about -5.3 is 0.
  *   a, b        device, [rows, cols] dt, each with its own stride (the halves of one
  *               [rows, 2 cols] product, for instance); b nullable
  *   y           device, [rows, cols] dt

@@ -9,11 +9,10 @@
 // backward pass then differentiates at the values the codes stand for.
 //
 // Bound by HBM: every element once in and once out, a warp two pieces of a row at a time, nothing
-// shared between warps.  At 8192x11008 bf16, gated SiLU with codes 110 us (0.97 of what a copy
-// reaches) and its gradient from the codes 105.5 (1.02); plain GELU's gradient at 8192x12288 88.4
-// (1.01); 8192x9001, unaligned, forward 124 (0.71).  The arithmetic must not take the issue slots
-// for that (45 to 60 % are taken, 29 instructions an output with both 8-bit copies, 20 of the
-// gradient): one exponential and one reciprocal an element, divisions shared by lanes.
+// shared between warps.  At 8192x11008 bf16, gated SiLU with codes 111.5 us (0.96 of what a copy
+// reaches) and its gradient from the codes 105.5 (1.02); plain GELU's gradient at 8192x12288 88.3
+// (1.01); 8192x9001, unaligned, forward 129 (0.68).  The arithmetic must not take the issue slots
+// for that: one exponential and one reciprocal an element, divisions shared by lanes.
 // Binary32 data have twice the bytes an element and take longer forms of f, right to the last places:
 // 4096x8192 plain GELU 47.6 us (0.83), SiLU 43.1 (0.92), gated with codes 86.5 and 73.0 (0.81, 0.95), the
 // gradients 57.5 to 96 (1.03).  With the shorter forms 40.5 to 72; with CUDA's normcdff, expf and an
@@ -41,21 +40,24 @@ __device__ __forceinline__ float rcp(float x) {
 
 constexpr float kLog2e = 1.44269504f;
 
-// s = 1 / (1 + exp(-u)) with u = x (SiLU) or GELU tanh's argument.  The base-2 exponent of
-// SiLU is the product with log2 e in two parts, so that its error is one rounding; infinite
-// exponentials give 0.
+// s = e / (1 + e), e = exp(u) with u = x (SiLU) or GELU tanh's argument.  The base-2 exponent of
+// SiLU is the product with log2 e in two parts, so that its error is one rounding.  e is the
+// square of its root, so that no subnormal passes through the approximate functions, which flush
+// them; it is held to 2^60, where s is 1.  (1 / (1 + exp(-u)) is 2 instructions an element less, 109.3
+// us instead of 111.5 above, and is 0 from u = -87 on.)
 template <int ACT>
 __device__ __forceinline__ float2 sigmoid2(float2 x, float2 x2) {
-  float2 t;
+  float2 t;   // half the exponent
   if (ACT == kActSilu) {
     constexpr float kLo = static_cast<float>(1.44269504088896341 - static_cast<double>(kLog2e));
-    t = fma2(x, both(-kLog2e), mul2(x, both(-kLo)));
+    t = fma2(x, both(0.5f * kLog2e), mul2(x, both(0.5f * kLo)));
   } else {
-    constexpr float kA = static_cast<float>(2 * 0.79788456080286536 * 1.44269504088896341);
-    t = mul2(x, fma2(x2, both(-0.044715f * kA), both(-kA)));
+    constexpr float kA = static_cast<float>(0.79788456080286536 * 1.44269504088896341);
+    t = mul2(x, fma2(x2, both(0.044715f * kA), both(kA)));
   }
-  const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.0f));
-  return make_float2(rcp(d.x), rcp(d.y));
+  const float2 h = make_float2(ex2(fminf(t.x, 30.0f)), ex2(fminf(t.y, 30.0f)));
+  const float2 d = fma2(h, h, both(1.0f));
+  return mul2(mul2(h, h), make_float2(rcp(d.x), rcp(d.y)));
 }
 
 // The normal distribution function P(x) = 1/2 + x R(x^2): R, smooth and even, by a polynomial of
@@ -77,7 +79,7 @@ __device__ __forceinline__ float2 normal_cdf2(float2 x, float2 x2) {
 
 // ---- binary32 data: f and f' to a few units in the last place of the value itself, however small.
 // (bf16 data take the shorter forms above: their error is absolute, below 2^-23 in P, so GELU loses
-// bf16's own digits below x = -3.8, where P is under 1e-4, and SiLU is 0 below -87.)
+// bf16's own digits below x = -3.8, where P is under 1e-4.)
 
 // exp(-(z + lo)) for 0 <= z <= 112, lo below half a unit in z's last place: the rounding of the
 // base-2 exponent is made up for to first order.
