@@ -9,9 +9,9 @@
 // backward pass then differentiates at the values the codes stand for.
 //
 // Bound by HBM: every element once in and once out, a warp two pieces of a row at a time, nothing
-// shared between warps.  At 8192x11008 bf16, gated SiLU with codes 111.5 us (0.96 of what a copy
+// shared between warps.  At 8192x11008 bf16, gated SiLU with codes 111.3 us (0.96 of what a copy
 // reaches) and its gradient from the codes 105.5 (1.02); plain GELU's gradient at 8192x12288 88.3
-// (1.01); 8192x9001, unaligned, forward 129 (0.68).  The arithmetic must not take the issue slots
+// (1.01); 8192x9001, unaligned, forward 127 (0.69).  The arithmetic must not take the issue slots
 // for that: one exponential and one reciprocal an element, divisions shared by lanes.
 // Binary32 data have twice the bytes an element and take longer forms of f, right to the last places:
 // 4096x8192 plain GELU 47.6 us (0.83), SiLU 43.1 (0.92), gated with codes 86.5 and 73.0 (0.81, 0.95), the
@@ -40,17 +40,15 @@ __device__ __forceinline__ float rcp(float x) {
 
 constexpr float kLog2e = 1.44269504f;
 
-// s = e / (1 + e), e = exp(u) with u = x (SiLU) or GELU tanh's argument.  The base-2 exponent of
-// SiLU is the product with log2 e in two parts, so that its error is one rounding.  e is the
-// square of its root, so that no subnormal passes through the approximate functions, which flush
-// them; it is held to 2^60, where s is 1.  (1 / (1 + exp(-u)) is 2 instructions an element less, 109.3
-// us instead of 111.5 above, and is 0 from u = -87 on.)
+// s = e / (1 + e), e = exp(u) with u = x (SiLU) or GELU tanh's argument.  e is the square of its
+// root, so that no subnormal passes through the approximate functions, which flush them; it is
+// held to 2^60, where s is 1.  (1 / (1 + exp(-u)) is 2 instructions an element less, 109.3
+// us instead of 111.3 above, and is 0 from u = -87 on.)
 template <int ACT>
 __device__ __forceinline__ float2 sigmoid2(float2 x, float2 x2) {
   float2 t;   // half the exponent
   if (ACT == kActSilu) {
-    constexpr float kLo = static_cast<float>(1.44269504088896341 - static_cast<double>(kLog2e));
-    t = fma2(x, both(0.5f * kLog2e), mul2(x, both(0.5f * kLo)));
+    t = mul2(x, both(0.5f * kLog2e));   // off by 2 roundings, |x| 2^-23 of e: nothing in bf16
   } else {
     constexpr float kA = static_cast<float>(0.79788456080286536 * 1.44269504088896341);
     t = mul2(x, fma2(x2, both(0.044715f * kA), both(kA)));
