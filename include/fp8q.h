@@ -473,7 +473,8 @@ fp8_status fp8_moe_dispatch(const void* x, int64_t tokens, int64_t cols, int64_t
  * fp8_moe_combine -- y[t] = sum over j of weights[t, j] ys[pos[t, j]], in order of j, over
  * the choices that were not dropped (neither their weights nor any row are read for those
  * that were; a token with none gives 0).  weights NULL: 1, which is also the gradient of
- * fp8_moe_dispatch (ys its output's gradient, y its input's).
+ * fp8_moe_dispatch (ys its output's gradient, y its input's).  Rows of pos outside [-1, capacity)
+ * are skipped and reported as for fp8_moe_dispatch.
  *   ys  device, [capacity, cols] dt;  y  device, [tokens, cols] dt
  *   weights  device, [tokens, k] float, nullable
  */
@@ -483,7 +484,7 @@ fp8_status fp8_moe_combine(const void* ys, int64_t capacity, int64_t cols, int64
 /*
  * fp8_moe_combine_backward -- the gradients of fp8_moe_combine:
  *   dys[r] = weights[src[r]] dy[src[r] / k], 0 where src[r] is -1
- *   dweights[t, j] = <dy[t], ys[pos[t, j]]>, 0 for a dropped choice
+ *   dweights[t, j] = <dy[t], ys[pos[t, j]]>, 0 for a dropped choice (rows out of range as above)
  *   dy  device, [tokens, cols] dt;  ys, dys  device, [capacity, cols] dt
  *   weights  device, [tokens, k] float, nullable (1)
  *   dweights  device, [tokens, k] float, nullable (ys is then not read and may be NULL)

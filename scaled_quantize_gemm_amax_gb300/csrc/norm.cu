@@ -8,7 +8,8 @@
 // Bound by HBM: x once in, y (and the codes) once out.  A row stays in registers between its
 // statistics and its output; weight and bias stay in shared memory for the whole walk.
 // 8192x4096 bf16 with codes 32.6 us (5.2 TB/s, 0.76 of what a copy reaches), 65536x4096 0.89,
-// 16384x4096 without codes 0.87, one row of 4096 3.0 us.  What is left at 8192x4096: launch, the
+// 16384x4096 without codes 0.87, one row of 4096 3.1 us; binary32 8192x4096 44.5 us (0.89), 2048x16384, one
+// row in flight a block, 46.2 (0.86).  What is left at 8192x4096: launch, the
 // first rows' way in and the last ones' way out (5 us), and SMs that finish at different times (the
 // rows are dealt out beforehand: 26 to 32 us).  Rows handed out on demand by cluster launch control
 // took a 25th warp a block and with it registers from the others: 36.4 us.
@@ -45,7 +46,8 @@ __device__ __forceinline__ float inv_sqrt(float v) {
   return v > 0.0f && !is_inf_or_nan(v) ? fmaf(0.5f * e, r, r) : r;
 }
 
-// Rows of any width: one block per row, three passes over it (sum, squared differences, output).
+// Rows of any width: one block per row, three passes over it (sum, squared differences, output), which a
+// row of more than kMostCols columns takes: 2048x20480 bf16 125 us (0.20), binary32 90 (0.55).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_norm_any(const NormParams p) {
   __shared__ float red[kWarps];
@@ -231,6 +233,7 @@ cudaError_t run_norm(const NormParams& p, int num_sms, cudaStream_t s) {
 // latency counts and there are warps to spare (no more rows than SMs); 8 where 16 would leave half
 // of them empty (up to 256 columns: 131072x128 with codes 37 us, 53 with 16 values; 262144x256 73 and
 // 106), and there 32 warps an SM, since a row is then mostly sums over lanes (24: 40 and 78 us).
+// Unaligned bf16 at 32 values spills 32 bytes a thread at its 80 registers.
 template <typename T, bool VECTOR>
 cudaError_t run_norm(const NormParams& p, int num_sms, cudaStream_t s) {
   if (p.cols <= 256) return run_norm<T, VECTOR, 8>(p, num_sms, s);

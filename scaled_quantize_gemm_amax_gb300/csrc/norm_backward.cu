@@ -9,7 +9,8 @@
 // for all the rows of its group, so the column sums stay in registers over the whole walk; they
 // leave as one partial sum a block, added up by a second, small launch.
 // 8192x4096 bf16 from codes 36.9 us (4.6 TB/s, 0.68 of what a copy reaches), 2048x12288 from x 36.6
-// (0.61), 65536x4096 from codes 0.95.  What is left at the short sizes does not grow with the rows:
+// (0.61), 65536x4096 from codes 0.94; binary32 from x 8192x4096 66 us (0.90), 2048x16384, one row in flight a
+// block, 78 (0.76); unaligned bf16 8192x4099 77 from x and 82 from codes (0.38, 0.31).  What is left at the short sizes does not grow with the rows:
 // every SM reads the same weights at the start (1.7 to 3 us at 4096 columns, 5 at 12288), and the
 // partial sums are written and added up at the end (4.4 and 8 us, the second launch included).
 #include "norm.cuh"
@@ -53,7 +54,8 @@ __device__ __forceinline__ float normalised(const NormBwdParams& p, int64_t row,
   return v * p.s[row * groups + c / 128];
 }
 
-// dx of rows of any width: one block per row, two passes.
+// dx of rows of any width: one block per row, two passes.  Rows of more than kMostCols columns, with the
+// column pass below: 2048x20480 bf16 from x 290 us (0.13), binary32 346 (0.22).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_norm_dx_any(const NormBwdParams p) {
   __shared__ float red[2 * kWarps];
@@ -393,7 +395,8 @@ cudaError_t run_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t 
 // Values a lane and warps of a block.  32 values halve what a row costs besides its values, and 12
 // warps leave a thread the 168 registers that they and the column sums take (8192x4096 from codes
 // and 2048x12288 from x, when chosen: 39.3 and 42.7 us; 24 warps of 16 values 41.5 and 52.4; 16
-// warps of 32 values in 128 registers 41.0 and 58.2, needed above 12288 columns).  Narrow rows take
+// warps of 32 values in 128 registers 41.0 and 58.2, needed above 12288 columns).  24 warps of 16 values and 16
+// of 32 spill 4 to 56 bytes a thread in 11 of their 16 forms.  Narrow rows take
 // the fewest values that hold them: 131072x128 from x 34 us, with 16 values 49.
 template <typename T, bool VECTOR, bool CODES>
 cudaError_t run_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s, int* partials) {

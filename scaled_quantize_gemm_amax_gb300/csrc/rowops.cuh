@@ -82,11 +82,11 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
 //                    a word more and shifted by half a word; what a lane stores begins with the
 //                    lane before's last value, so that every word but the ends' is whole.  A run
 //                    of pieces that touches the row's end goes element by element; no byte outside
-//                    the row is touched.  (8192x9001 gated SiLU 124 us; element by element throughout
-//                    265; aligned 16-byte granules shifted over the lanes 157, 11 selections a lane
-//                    and tensor; pairs 2 l and 2 l + 64, halves exchanged between lanes, 147.)
+//                    the row is touched.  (8192x9001 gated SiLU, when chosen, 124 us; element by element
+//                    throughout 265; aligned 16-byte granules shifted over the lanes 157, 11 selections
+//                    a lane and tensor; pairs 2 l and 2 l + 64, halves exchanged between lanes, 147.)
 //   binary32 otherwise  lane l columns l, l + 32, l + 64, l + 96, element by element, which
-//                    coalesces at any alignment (4096x9001 gated SiLU 84 us; granules 136).
+//                    coalesces at any alignment (4096x9001 gated SiLU, when chosen, 84 us; granules 136).
 // A lane works from its own first column `c` of the row: pointers point there, and `left` is the
 // number of columns from there to the row's end (possibly none).  Every function is called by
 // the whole warp, with the same values but for the lane's own c and left.
