@@ -495,6 +495,135 @@ fp8_status fp8_moe_combine_backward(const void* dy, int64_t tokens, int64_t cols
                                     cudaStream_t stream);
 
 /*
+ * fp8_rms_norm -- the residual's addition, the norm and an 8-bit output in one pass.  With
+ *   h = x + residual, rounded to dt (the stream as it is kept; x itself without a residual),
+ *   y = h r weight,  r = 1 / sqrt(mean(h^2) + eps) of a row of h
+ *   x           device, [rows, cols] dt
+ *   residual    device, [rows, cols] dt, nullable
+ *   weight      device, [cols] wdt, nullable (1)
+ *   eps         >= 0
+ *   h           device, [rows, cols] dt, nullable; needs a residual
+ *   y           device, [rows, cols] dt, nullable (then q is needed)
+ *   rstd        device, [rows] float, nullable: r, for the backward pass
+ *   recipe, fmt, scale, amax_out, q, ldq, s   q nullable: the row-wise copy of y that
+ *               fp8_cast_transpose_f32 would write for its binary32 values, so an operand of
+ *               fp8_scaled_gemm without a pass of its own: codes [rows, cols] u8 with row stride
+ *               ldq and, by recipe,
+ *                 FP8_TENSOR       scale device float[1], s device float[1] nullable: 1 / scale
+ *                 FP8_BLOCK_1x128  s device float [rows, ceil(cols / 128)] (ragged last block)
+ *                 FP8_MX_1x32(_FLOOR)        s device u8 [rows, cols / 32]; cols % 32 == 0
+ *                 FP8_MX_1x32(_FLOOR)_TILED  s as the cast's; rows and cols % 128 == 0
+ *               (FP8_BLOCK_128x128 is FP8_ERR_UNSUPPORTED; other cols and rows FP8_ERR_SHAPE)
+ *   amax_out    device float[1], nullable, with FP8_TENSOR only: max |y|, NaN ignored (0 without
+ *               rows or columns)
+ * The sum of squares is binary32: a row in which it overflows gives r = 0.  A row with a NaN
+ * gives a row of NaN.  rows or cols == 0 writes nothing but amax_out.
+ */
+fp8_status fp8_rms_norm(const void* x, int64_t rows, int64_t cols, int64_t ldx, fp8_dtype dt, const void* residual, int64_t ldr,
+                        const void* weight, fp8_dtype wdt, float eps, void* h, int64_t ldh, void* y, int64_t ldy, float* rstd,
+                        fp8_recipe recipe, fp8_format fmt, const float* scale, float* amax_out, uint8_t* q, int64_t ldq, void* s,
+                        cudaStream_t stream);
+
+/*
+ * fp8_rms_norm_backward -- with xh = h r, g = dy weight, c = mean(g xh) of a row,
+ *   dx = r (g - xh c) + dh,  dweight = sum over rows of dy xh
+ * dx is the gradient of x and of the residual.
+ *   dy          device, [rows, cols] dt
+ *   h, rstd     the forward pass's h (x without a residual) and r
+ *   dh          device, [rows, cols] dt, nullable (0): the gradient that reaches h itself
+ *   weight      device, [cols] wdt, nullable (1)
+ *   dx          device, [rows, cols] dt
+ *   dweight     device, [cols] wdt, nullable
+ *   workspace   device, 16-byte aligned, fp8_rms_norm_workspace bytes; may be NULL when dweight
+ *               is.  Its contents need no initialisation and mean nothing after the call.
+ * rows == 0 sets dweight to 0; cols == 0 is a no-op.
+ */
+fp8_status fp8_rms_norm_backward(const void* dy, int64_t rows, int64_t cols, int64_t lddy, fp8_dtype dt, const void* h, int64_t ldh,
+                                 const float* rstd, const void* dh, int64_t lddh, const void* weight, fp8_dtype wdt, void* dx,
+                                 int64_t lddx, void* dweight, void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+/* *bytes (host): the workspace of fp8_rms_norm_backward for this shape,
+ *   4 * cols * min(max(rows, 1), 304).  No device call. */
+fp8_status fp8_rms_norm_workspace(int64_t rows, int64_t cols, int64_t* bytes);
+
+/*
+ * Products grouped by expert: the three GEMMs of the experts' linear layers, all experts in one
+ * call, over rows sorted by expert (fp8_moe_route with align 128, fp8_moe_dispatch).  The segments'
+ * starts stay on the device, so no call waits for a routing and all of them can be captured.
+ *   offsets     device, [n_experts + 1] int32, ascending multiples of 128 in [0, capacity]: expert
+ *               e's rows are [offsets[e], offsets[e + 1]).  Others write nothing and are reported
+ *               as FP8_ERR_DEVICE_STATE by fp8_get_device_status.
+ *   n_experts   1..1024
+ *   capacity    rows that A (and C, or B) have; a multiple of 128
+ * Operands are FP8, row-major and dense, with the recipes (ra, rb) = (FP8_TENSOR, FP8_TENSOR) or
+ * two of FP8_MX_1x32_TILED and FP8_MX_1x32_FLOOR_TILED, scales as fp8_cast_transpose writes them
+ * (other pairings FP8_ERR_UNSUPPORTED).  Accumulation is binary32; C is rounded once.  M, N, K and
+ * capacity are multiples of 128, and they, n_experts times M, N or K and the number of 256 x 256
+ * tiles below 2^31 (FP8_ERR_SHAPE).  Matrices and tiled scales are 16-byte aligned.
+ */
+typedef enum {
+  FP8_STACKED_ROWS = 0,  /* the experts' [N, K] one below the other: [n_experts * N, K] */
+  FP8_STACKED_COLS = 1   /* side by side: [N, n_experts * K] */
+} fp8_stacked;
+
+/*
+ * fp8_grouped_gemm -- C[r, n] = sum_k deq(A)[r, k] deq(B_e)[n, k] for the rows r of expert e.
+ *   A           device, [capacity, K]
+ *   B           device, the experts' [N, K] stacked as said.  A weight [n_experts * N, K] cast as
+ *               one matrix has its row-wise copy stacked by rows (the rows' outputs) and its
+ *               column-wise copy [K, n_experts * N] stacked by columns (the rows' gradients).
+ *   sB, sB_count  FP8_TENSOR: 1 multiplier, or n_experts, one an expert; else sB_count is not used
+ *   C           device, [capacity, N] bf16 or FP32
+ *   zero_tail   not 0: the rows from offsets[n_experts] on are set to 0; 0: they are left as they
+ *               were
+ * Rows before offsets[0] are left as they were.  K == 0 sets the segments' rows to 0; capacity or
+ * N == 0 is a no-op.
+ */
+fp8_status fp8_grouped_gemm(const uint8_t* A, fp8_format fa, fp8_recipe ra, const void* sA, const uint8_t* B, fp8_format fb,
+                            fp8_recipe rb, const void* sB, int32_t sB_count, const int32_t* offsets, int32_t n_experts,
+                            int64_t capacity, int64_t N, int64_t K, fp8_stacked stacked, void* C, fp8_out_dtype out,
+                            int32_t zero_tail, cudaStream_t stream);
+
+/*
+ * fp8_grouped_wgrad -- C[e][m, n] = sum over the rows r of expert e of deq(A)[m, r] deq(B)[n, r]:
+ * every expert's weight gradient from the column-wise copies of the outputs' gradients and of the
+ * inputs; 0 for an expert without rows.
+ *   A           device, [M, capacity];  B  device, [N, capacity]
+ *   C           device, [n_experts, M, N] bf16 or FP32
+ * M or N == 0 is a no-op.
+ */
+fp8_status fp8_grouped_wgrad(const uint8_t* A, fp8_format fa, fp8_recipe ra, const void* sA, const uint8_t* B, fp8_format fb,
+                             fp8_recipe rb, const void* sB, const int32_t* offsets, int32_t n_experts, int64_t capacity,
+                             int64_t M, int64_t N, void* C, fp8_out_dtype out, cudaStream_t stream);
+
+/* One gradient of a model: n elements of dt, dense, at any element's alignment. */
+typedef struct {
+  const void* in;
+  void* out;   /* fp8_clip_grad_norm: where the clipped gradient goes (in itself, or no part of any `in`) */
+  int64_t n;
+  fp8_dtype dt;
+} fp8_gradient;
+
+/*
+ * fp8_grad_norm -- *norm = sqrt(sum over all elements of all gradients of g^2).
+ * fp8_clip_grad_norm -- that, and out = g min(1, max_norm / (norm + 1e-6)), rounded once; in place
+ * nothing is written when the factor is 1.  A NaN norm makes every output NaN, an infinite one makes
+ * finite elements 0.
+ *   grads       host, [n_grads]: read before the call returns; gradients must not overlap
+ *   max_norm    >= 0 (infinity scales nothing)
+ *   workspace   device, 8-byte aligned, fp8_grad_norm_workspace bytes; needs no initialisation
+ *   norm        device, float[1]
+ * Squares are binary32 within 64 elements and binary64 beyond, or binary64 where binary32's range
+ * ends: no element is too large or too small to count.  n_grads == 0 gives 0.  Sizes sum to less
+ * than 2^44 elements (FP8_ERR_SHAPE).
+ */
+fp8_status fp8_grad_norm(const fp8_gradient* grads, int32_t n_grads, void* workspace, int64_t workspace_bytes, float* norm,
+                         cudaStream_t stream);
+fp8_status fp8_clip_grad_norm(const fp8_gradient* grads, int32_t n_grads, float max_norm, void* workspace,
+                              int64_t workspace_bytes, float* norm, cudaStream_t stream);
+/* *bytes (host): the workspace of both for n_grads gradients.  No device call. */
+fp8_status fp8_grad_norm_workspace(int32_t n_grads, int64_t* bytes);
+
+/*
  * fp8_get_device_status -- synchronize `stream`, then read and clear the
  * device error word of the current device.  Returns FP8_OK, FP8_ERR_TIMEOUT
  * (some kernel gave up a wait), FP8_ERR_DEVICE_STATE, FP8_ERR_INDEX (debug

@@ -29,6 +29,7 @@ from __future__ import annotations
 import ctypes
 import enum
 import functools
+import math
 import os
 import typing
 
@@ -48,6 +49,9 @@ __all__ = [
     "fp8_moe_route", "fp8_moe_capacity", "fp8_moe_dispatch", "fp8_moe_combine", "fp8_moe_combine_backward",
     "layer_norm", "layer_norm_backward", "gated_act", "gated_act_backward", "moe_route", "moe_dispatch", "moe_combine",
     "moe_combine_backward", "moe_dispatch_backward",
+    "Stacked", "fp8_rms_norm", "fp8_rms_norm_backward", "fp8_rms_norm_workspace", "fp8_grouped_gemm", "fp8_grouped_wgrad",
+    "fp8_grad_norm", "fp8_clip_grad_norm", "fp8_grad_norm_workspace",
+    "rms_norm", "rms_norm_backward", "grouped_gemm", "grouped_wgrad", "grad_norm", "clip_grad_norm",
 ]
 
 
@@ -83,6 +87,12 @@ class OutDtype(enum.IntEnum):
     FP32 = 1
 
 
+class Stacked(enum.IntEnum):
+    """How the experts' matrices of a grouped product lie: [E * N, K], or side by side [N, E * K]."""
+    ROWS = 0
+    COLS = 1
+
+
 class Activation(enum.IntEnum):
     SILU = 0
     GELU = 1
@@ -108,6 +118,11 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _E = ctypes.c_int
+class Gradient(ctypes.Structure):
+    """C layout of fp8_gradient."""
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("dt", ctypes.c_int)]
+
+
 class CastJob(ctypes.Structure):
     """C layout of fp8_cast_job."""
     _fields_ = [("x", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
@@ -142,6 +157,15 @@ _SIGNATURES = {
     "fp8_moe_dispatch": [_P, _I64, _I64, _I64, _E, _I32, _P, _P, _I64, _P, _I64, _P],
     "fp8_moe_combine": [_P, _I64, _I64, _I64, _E, _I64, _I32, _P, _P, _P, _I64, _P],
     "fp8_moe_combine_backward": [_P, _I64, _I64, _I64, _E, _I32, _P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _P],
+    "fp8_rms_norm": [_P, _I64, _I64, _I64, _E, _P, _I64, _P, _E, ctypes.c_float, _P, _I64, _P, _I64, _P, _E, _E, _P, _P, _P, _I64,
+                     _P, _P],
+    "fp8_rms_norm_backward": [_P, _I64, _I64, _I64, _E, _P, _I64, _P, _P, _I64, _P, _E, _P, _I64, _P, _P, _I64, _P],
+    "fp8_rms_norm_workspace": [_I64, _I64, _P],
+    "fp8_grouped_gemm": [_P, _E, _E, _P, _P, _E, _E, _P, _I32, _P, _I32, _I64, _I64, _I64, _E, _P, _E, _I32, _P],
+    "fp8_grouped_wgrad": [_P, _E, _E, _P, _P, _E, _E, _P, _P, _I32, _I64, _I64, _I64, _P, _E, _P],
+    "fp8_grad_norm": [_P, _I32, _P, _I64, _P, _P],
+    "fp8_clip_grad_norm": [_P, _I32, ctypes.c_float, _P, _I64, _P, _P],
+    "fp8_grad_norm_workspace": [_I32, _P],
     "fp8_get_device_status": [_P],
     "fp8_debug_wait_timeout": [_P],
     "fp8_debug_gemm_plan": [_E, _E, _E, _I64, _I64, _I64, _I32, _I32, _I32, _P],
@@ -518,6 +542,149 @@ def fp8_moe_combine_backward(dy, pos, src, weights, ys, dys, dweights, stream=No
                                                    _ptr(ys), ldys, capacity, _ptr(dys), lddys, _ptr(dweights), _stream(stream)))
 
 
+def _copy_of_y(recipe, q, s, rows: int, cols: int) -> int:
+    """The row stride of RMS norm's 8-bit output, having checked codes and scales."""
+    if q is None:
+        return 0
+    recipe = Recipe(recipe)
+    if q.element_size() != 1 or q.shape != (rows, cols):
+        raise ValueError(f"q: codes [{rows}, {cols}] of one byte are needed, not {q.dtype} {tuple(q.shape)}")
+    if recipe == Recipe.TENSOR:
+        _vector(s, 1, "s")
+    elif recipe == Recipe.BLOCK_1x128:
+        _vector(s, rows * ((cols + 127) // 128), "s")
+    else:
+        shape, dtype = scale_shape(recipe, rows, cols)
+        _vector(s, math.prod(shape), "s", dtype)
+    return _rows(q, "q")[2]
+
+
+def fp8_rms_norm(x, residual, weight, eps, h, y, rstd, recipe, fmt, scale, amax_out, q, s, stream=None):
+    rows, cols, ldx = _rows(x, "x")
+    dt, wdt = _dtype(x, "x"), _params(weight, None, cols)
+    ldr, ldh, ldy = _like(residual, x, "residual"), _like(h, x, "h"), _like(y, x, "y")
+    ldq = _copy_of_y(recipe, q, s, rows, cols)
+    _vector(rstd, rows, "rstd")
+    _vector(scale, 1, "scale")
+    _vector(amax_out, 1, "amax_out")
+    _on_gpu(x, residual, weight, h, y, rstd, scale, amax_out, q, s)
+    _check("fp8_rms_norm",
+           load_library().fp8_rms_norm(_ptr(x), rows, cols, ldx, dt, _ptr(residual), ldr, _ptr(weight), wdt, eps, _ptr(h), ldh,
+                                       _ptr(y), ldy, _ptr(rstd), int(recipe), int(fmt), _ptr(scale), _ptr(amax_out), _ptr(q), ldq,
+                                       _ptr(s), _stream(stream)))
+
+
+def fp8_rms_norm_workspace(rows: int, cols: int) -> int:
+    """Bytes of fp8_rms_norm_backward's workspace (host arithmetic)."""
+    n = ctypes.c_int64()
+    _check("fp8_rms_norm_workspace", load_library().fp8_rms_norm_workspace(rows, cols, ctypes.addressof(n)))
+    return n.value
+
+
+def fp8_rms_norm_backward(dy, h, rstd, dh, weight, dx, dweight, workspace, stream=None):
+    rows, cols, lddy = _rows(dy, "dy")
+    dt, wdt = _dtype(dy, "dy"), _params(weight, dweight, cols)
+    ldh, lddh, lddx = _like(h, dy, "h"), _like(dh, dy, "dh"), _like(dx, dy, "dx")
+    _vector(rstd, rows, "rstd")
+    _on_gpu(dy, h, rstd, dh, weight, dx, dweight, workspace)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("fp8_rms_norm_backward",
+           load_library().fp8_rms_norm_backward(_ptr(dy), rows, cols, lddy, dt, _ptr(h), ldh, _ptr(rstd), _ptr(dh), lddh,
+                                                _ptr(weight), wdt, _ptr(dx), lddx, _ptr(dweight), _ptr(workspace), nbytes,
+                                                _stream(stream)))
+
+
+def _starts(offsets) -> int:
+    """The number of experts of a routing's offsets."""
+    if offsets.dim() != 1 or offsets.numel() < 2 or offsets.dtype != torch.int32 or not offsets.is_contiguous():
+        raise ValueError(f"offsets: a contiguous int32 vector of n_experts + 1 is needed, not {offsets.dtype} {tuple(offsets.shape)}")
+    return offsets.numel() - 1
+
+
+def _operand(q, recipe, s, what: str, experts: int = 1):
+    """(rows, cols) of a dense matrix of codes, having checked its multipliers."""
+    if q.dim() != 2 or q.element_size() != 1 or not q.is_contiguous():
+        raise ValueError(f"{what}: a dense matrix of one-byte codes is needed, not {q.dtype} {tuple(q.shape)}")
+    rows, cols = q.shape
+    if Recipe(recipe) == Recipe.TENSOR:
+        _vector(s, experts if s.numel() == experts else 1, f"{what}'s multipliers")
+    else:
+        n = ((rows + 127) // 128) * ((cols + 127) // 128) * 512
+        if s.numel() != n or s.element_size() != 1 or not s.is_contiguous():
+            raise ValueError(f"{what}: its {n} tiled one-byte scales are needed, not {s.dtype} {tuple(s.shape)}")
+    return rows, cols
+
+
+def _product_out(c, shape, out):
+    want = torch.float32 if OutDtype(out) == OutDtype.FP32 else torch.bfloat16
+    if c.shape != shape or c.dtype != want or not c.is_contiguous():
+        raise ValueError(f"c: dense {want} {tuple(shape)} is needed, not {c.dtype} {tuple(c.shape)}")
+
+
+def fp8_grouped_gemm(a, fa, ra, sa, b, fb, rb, sb, offsets, c, out=OutDtype.BF16, stacked=Stacked.ROWS, zero_tail=False,
+                     stream=None):
+    experts, (capacity, k) = _starts(offsets), _operand(a, ra, sa, "a")
+    rows, cols = _operand(b, rb, sb, "b", experts)
+    n = rows if Stacked(stacked) == Stacked.COLS else rows // experts
+    if (rows, cols) != ((n, experts * k) if Stacked(stacked) == Stacked.COLS else (experts * n, k)):
+        raise ValueError(f"b: {experts} experts' matrices of depth {k} are needed, not {tuple(b.shape)}")
+    _product_out(c, (capacity, n), out)
+    _on_gpu(a, sa, b, sb, offsets, c)
+    _check("fp8_grouped_gemm",
+           load_library().fp8_grouped_gemm(_ptr(a), int(fa), int(ra), _ptr(sa), _ptr(b), int(fb), int(rb), _ptr(sb), sb.numel(),
+                                           _ptr(offsets), experts, capacity, n, k, int(stacked), _ptr(c), int(out),
+                                           int(zero_tail), _stream(stream)))
+
+
+def fp8_grouped_wgrad(a, fa, ra, sa, b, fb, rb, sb, offsets, c, out=OutDtype.FP32, stream=None):
+    experts, (m, capacity) = _starts(offsets), _operand(a, ra, sa, "a")
+    n, same = _operand(b, rb, sb, "b")
+    if same != capacity:
+        raise ValueError(f"a and b: the same number of columns is needed, not {capacity} and {same}")
+    _product_out(c, (experts, m, n), out)
+    _on_gpu(a, sa, b, sb, offsets, c)
+    _check("fp8_grouped_wgrad",
+           load_library().fp8_grouped_wgrad(_ptr(a), int(fa), int(ra), _ptr(sa), _ptr(b), int(fb), int(rb), _ptr(sb), _ptr(offsets),
+                                            experts, capacity, m, n, _ptr(c), int(out), _stream(stream)))
+
+
+def fp8_grad_norm_workspace(n_grads: int) -> int:
+    """Bytes of the workspace of fp8_grad_norm and fp8_clip_grad_norm (host arithmetic)."""
+    n = ctypes.c_int64()
+    _check("fp8_grad_norm_workspace", load_library().fp8_grad_norm_workspace(n_grads, ctypes.addressof(n)))
+    return n.value
+
+
+def _gradients(grads, outs):
+    table = (Gradient * max(len(grads), 1))()
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if not (g.is_contiguous() and (o is None or o.is_contiguous() and o.shape == g.shape and o.dtype == g.dtype)):
+            raise ValueError("gradients: contiguous tensors, and outputs like them, are needed")
+        table[i] = Gradient(_ptr(g), _ptr(o), g.numel(), _dtype(g, "gradients"))
+    _on_gpu(*grads, *outs)
+    return table
+
+
+def fp8_grad_norm(grads, workspace, norm, stream=None):
+    _vector(norm, 1, "norm")
+    _on_gpu(workspace, norm)
+    table = _gradients(grads, [None] * len(grads))
+    _check("fp8_grad_norm",
+           load_library().fp8_grad_norm(ctypes.cast(table, ctypes.c_void_p), len(grads), _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(), _ptr(norm), _stream(stream)))
+
+
+def fp8_clip_grad_norm(grads, outs, max_norm, workspace, norm, stream=None):
+    if len(outs) != len(grads):
+        raise ValueError("outs: as many tensors as gradients are needed")
+    _vector(norm, 1, "norm")
+    _on_gpu(workspace, norm)
+    table = _gradients(grads, outs)
+    _check("fp8_clip_grad_norm",
+           load_library().fp8_clip_grad_norm(ctypes.cast(table, ctypes.c_void_p), len(grads), max_norm, _ptr(workspace),
+                                             workspace.numel() * workspace.element_size(), _ptr(norm), _stream(stream)))
+
+
 def fp8_get_device_status(stream=None) -> Status:
     return Status(load_library().fp8_get_device_status(_stream(stream)))
 
@@ -722,6 +889,48 @@ def moe_combine_backward(dy, ys, route: MoeRoute, weights=None, stream=None):
 def moe_dispatch_backward(dxs, route: MoeRoute, stream=None):
     """The gradient of moe_dispatch: every token's choices' rows of dxs, summed."""
     return (_ext or _rowops()).moe_combine(dxs, route.pos, None, stream)
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-5, recipe=None, fmt=Format.E4M3, scale=None, amax_out=None,
+             keep_y: bool = True, stats: bool = True, stream=None):
+    """Allocate outputs and run fp8_rms_norm on x [rows, cols], with residual on their sum.
+
+    Returns (y, h, rstd, q, s): h = x + residual (None without one); q, s the 8-bit copy of y by `recipe`
+    (else None; the codes' row stride is padded to 16 bytes).  keep_y=False (with a recipe): y leaves in
+    8 bits only.  stats=False skips rstd (inference)."""
+    return (_ext or _rowops()).rms_norm(x, weight, residual, eps, recipe, fmt, scale, amax_out, keep_y, stats, stream)
+
+
+def rms_norm_backward(dy, h, rstd, weight=None, dh=None, param_grads: bool = True, param_dtype=None, stream=None):
+    """Allocate outputs and run fp8_rms_norm_backward; dh: the gradient that reaches h itself.
+
+    Returns (dx, dweight): dx is the gradient of x and of the residual; dweight is in the weight's type
+    (param_dtype without a weight; default float32), or None with param_grads=False."""
+    return (_ext or _rowops()).rms_norm_backward(dy, h, rstd, weight, dh, param_grads, param_dtype or torch.float32, stream)
+
+
+def grouped_gemm(a, fa, ra, sa, b, fb, rb, sb, offsets, out=OutDtype.BF16, stacked=Stacked.ROWS, zero_tail: bool = True,
+                 stream=None):
+    """Allocate C [capacity, N] and run fp8_grouped_gemm: every expert's rows of a times its matrix of b.
+
+    Rows behind the last segment are 0, or with zero_tail=False whatever the allocation held."""
+    return (_ext or _rowops()).grouped_gemm(a, fa, ra, sa, b, fb, rb, sb, offsets, out, stacked, zero_tail, stream)
+
+
+def grouped_wgrad(a, fa, ra, sa, b, fb, rb, sb, offsets, out=OutDtype.FP32, stream=None):
+    """Allocate C [experts, M, N] and run fp8_grouped_wgrad: a [M, capacity] times b [N, capacity] over every expert's rows."""
+    return (_ext or _rowops()).grouped_wgrad(a, fa, ra, sa, b, fb, rb, sb, offsets, out, stream)
+
+
+def grad_norm(grads, stream=None):
+    """The 2-norm (float32 [1], on the device) over all elements of a sequence of bf16 or float32 tensors."""
+    return (_ext or _rowops()).clip_grad_norm(grads, None, None, stream)
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
+    """Scale the gradients by min(1, max_norm / (norm + 1e-6)), in place or into the tensors `out`; returns their norm
+    before (float32 [1], on the device)."""
+    return (_ext or _rowops()).clip_grad_norm(grads, max_norm, out, stream)
 
 
 class DelayedScaling:

@@ -5,6 +5,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <atomic>
+#include <cstddef>
 #include <cstring>
 #include <mutex>
 
@@ -967,6 +968,284 @@ fp8_status fp8_moe_combine_backward(const void* dy, int64_t tokens, int64_t cols
                                     cudaStream_t stream) {
   ApiRange nvtx_range("fp8_moe_combine_backward");
   return scatter_rows(dy, tokens, cols, lddy, dt, k, pos, src, weights, ys, ldys, capacity, dys, lddys, dweights, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ RMS norm
+extern "C" {
+
+fp8_status fp8_rms_norm(const void* x, int64_t rows, int64_t cols, int64_t ldx, fp8_dtype dt, const void* residual, int64_t ldr,
+                        const void* weight, fp8_dtype wdt, float eps, void* h, int64_t ldh, void* y, int64_t ldy, float* rstd,
+                        fp8_recipe recipe, fp8_format fmt, const float* scale, float* amax_out, uint8_t* q, int64_t ldq, void* s,
+                        cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_rms_norm");
+  if (rows < 0 || cols < 0 || !valid_dt(dt) || !valid_dt(wdt) || !valid_fmt(fmt) || !valid_recipe(recipe) || !(eps >= 0.0f))
+    return FP8_ERR_INVALID_ARG;
+  if (recipe == FP8_BLOCK_128x128) return FP8_ERR_UNSUPPORTED;
+  const bool empty = rows == 0 || cols == 0;
+  if (amax_out != nullptr && (recipe != FP8_TENSOR || (q == nullptr && !empty))) return FP8_ERR_INVALID_ARG;
+  if (!aligned(amax_out, 4)) return FP8_ERR_ALIGNMENT;
+  if (!empty) {
+    if (x == nullptr || (y == nullptr && q == nullptr) || (h != nullptr && residual == nullptr)) return FP8_ERR_INVALID_ARG;
+    if (q != nullptr && (recipe == FP8_TENSOR ? scale == nullptr : s == nullptr)) return FP8_ERR_INVALID_ARG;
+    if (rows > kMaxExtent || cols > kMaxExtent || !row_stride(rows, cols, &ldx) || (y != nullptr && !row_stride(rows, cols, &ldy)) ||
+        (residual != nullptr && !row_stride(rows, cols, &ldr)) || (h != nullptr && !row_stride(rows, cols, &ldh)) ||
+        (q != nullptr && !row_stride(rows, cols, &ldq)))
+      return FP8_ERR_SHAPE;
+    if (q != nullptr && is_mx(recipe) && (cols % 32 || (is_mx_tiled(recipe) && (rows % 128 || cols % 128)))) return FP8_ERR_SHAPE;
+    const uintptr_t es = elem_size(dt), ws = elem_size(wdt);
+    if (!aligned(x, es) || !aligned(residual, es) || !aligned(h, es) || !aligned(y, es) || !aligned(weight, ws) ||
+        !aligned(rstd, 4) || !aligned(scale, 4) || (!is_mx(recipe) && !aligned(s, 4)) || (is_mx_tiled(recipe) && !aligned(s, 16)))
+      return FP8_ERR_ALIGNMENT;
+  }
+  if (empty && amax_out == nullptr) return FP8_OK;
+  DeviceInfo* d;
+  if (fp8_status st = device_info(&d)) return st;
+  if (amax_out != nullptr && launch_zero_f32(amax_out, 1, stream) != cudaSuccess) return FP8_ERR_CUDA;
+  if (empty) return FP8_OK;
+  RmsParams p{};
+  p.x = x;
+  p.rows = rows;
+  p.cols = cols;
+  p.ldx = ldx;
+  p.f32 = dt == FP8_DT_FP32;
+  p.res = residual;
+  p.ldr = ldr;
+  p.w = weight;
+  p.w_f32 = wdt == FP8_DT_FP32;
+  p.eps = eps;
+  p.h = h;
+  p.ldh = ldh;
+  p.y = y;
+  p.ldy = ldy;
+  p.rstd = rstd;
+  p.recipe = is_mx(recipe) ? kMx : static_cast<int>(recipe);
+  p.mx_tiled = is_mx_tiled(recipe);
+  p.mx_floor = is_mx_floor(recipe);
+  p.e5m2 = fmt == FP8_E5M2;
+  p.scale = scale;
+  p.amax = amax_out;
+  p.q = q;
+  p.ldq = ldq;
+  p.s = s;
+  return cuda_status(launch_rms(p, d->num_sms, stream));
+}
+
+fp8_status fp8_rms_norm_workspace(int64_t rows, int64_t cols, int64_t* bytes) {
+  ApiRange nvtx_range("fp8_rms_norm_workspace");
+  if (rows < 0 || cols < 0 || bytes == nullptr) return FP8_ERR_INVALID_ARG;
+  if (rows > kMaxExtent || cols > kMaxExtent) return FP8_ERR_SHAPE;
+  *bytes = static_cast<int64_t>(norm_partials(rows)) * cols * static_cast<int64_t>(sizeof(float));
+  return FP8_OK;
+}
+
+fp8_status fp8_rms_norm_backward(const void* dy, int64_t rows, int64_t cols, int64_t lddy, fp8_dtype dt, const void* h, int64_t ldh,
+                                 const float* rstd, const void* dh, int64_t lddh, const void* weight, fp8_dtype wdt, void* dx,
+                                 int64_t lddx, void* dweight, void* workspace, int64_t workspace_bytes, cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_rms_norm_backward");
+  if (rows < 0 || cols < 0 || !valid_dt(dt) || !valid_dt(wdt)) return FP8_ERR_INVALID_ARG;
+  if (cols == 0) return FP8_OK;
+  if (rows > 0 && (dy == nullptr || dx == nullptr || h == nullptr || rstd == nullptr)) return FP8_ERR_INVALID_ARG;
+  if (dweight != nullptr && workspace == nullptr) return FP8_ERR_INVALID_ARG;
+  if (rows > kMaxExtent || cols > kMaxExtent || !row_stride(rows, cols, &lddy) || !row_stride(rows, cols, &lddx) ||
+      !row_stride(rows, cols, &ldh) || (dh != nullptr && !row_stride(rows, cols, &lddh)))
+    return FP8_ERR_SHAPE;
+  if (dweight != nullptr) {
+    int64_t need = 0;
+    if (fp8_status st = fp8_rms_norm_workspace(rows, cols, &need)) return st;
+    if (workspace_bytes < need) return FP8_ERR_SHAPE;
+    if (!aligned(workspace, 16)) return FP8_ERR_ALIGNMENT;
+  }
+  const uintptr_t es = elem_size(dt), ws = elem_size(wdt);
+  if (!aligned(dy, es) || !aligned(h, es) || !aligned(dh, es) || !aligned(dx, es) || !aligned(weight, ws) ||
+      !aligned(dweight, ws) || !aligned(rstd, 4))
+    return FP8_ERR_ALIGNMENT;
+  if (rows == 0 && dweight == nullptr) return FP8_OK;
+  DeviceInfo* d;
+  if (fp8_status st = device_info(&d)) return st;
+  RmsBwdParams p{};
+  p.dy = dy;
+  p.rows = rows;
+  p.cols = cols;
+  p.lddy = lddy;
+  p.f32 = dt == FP8_DT_FP32;
+  p.h = h;
+  p.ldh = ldh;
+  p.rstd = rstd;
+  p.dh = dh;
+  p.lddh = lddh;
+  p.w = weight;
+  p.w_f32 = wdt == FP8_DT_FP32;
+  p.dx = dx;
+  p.lddx = lddx;
+  p.dw = dweight;
+  p.partial = static_cast<float*>(workspace);
+  return cuda_status(launch_rms_backward(p, d->num_sms, stream));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ products grouped by expert
+namespace {
+
+// What both products share: checks, tensor maps and the launch.  rows x depth of A's matrix, of B's, and of
+// the output's: a_rows x a_cols, b_rows x b_cols, c_rows x N.
+fp8_status grouped(GroupedParams& p, const uint8_t* A, fp8_format fa, fp8_recipe ra, const void* sA, const uint8_t* B,
+                   fp8_format fb, fp8_recipe rb, const void* sB, int64_t a_rows, int64_t a_cols, int64_t b_rows, int64_t b_cols,
+                   int64_t c_rows, fp8_out_dtype out, cudaStream_t stream) {
+  if (a_rows > kMaxDim || a_cols > kMaxDim || b_rows > kMaxDim || b_cols > kMaxDim || c_rows > kMaxDim) return FP8_ERR_SHAPE;
+  const int64_t tiles_m = p.depth ? c_rows / 128 : p.capacity / 128 + p.n_experts;
+  if (tiles_m * (p.N / 64) > kMaxDim) return FP8_ERR_SHAPE;
+  if (p.offsets == nullptr || p.c == nullptr) return FP8_ERR_INVALID_ARG;
+  const bool loads = a_rows > 0 && a_cols > 0 && b_rows > 0 && b_cols > 0;
+  const bool mx = p.kind == kMx;
+  if (loads && (A == nullptr || B == nullptr || sA == nullptr || sB == nullptr)) return FP8_ERR_INVALID_ARG;
+  if (!aligned(p.offsets, 4) || !aligned(p.c, 16)) return FP8_ERR_ALIGNMENT;
+  if (loads && (!aligned(A, 16) || !aligned(B, 16) || !aligned(sA, mx ? 16 : 4) || !aligned(sB, mx ? 16 : 4)))
+    return FP8_ERR_ALIGNMENT;
+  DeviceInfo* d;
+  if (fp8_status st = device_info(&d)) return st;
+  p.a_cols = static_cast<int>(a_cols);
+  p.b_rows_all = static_cast<int>(b_rows);
+  p.b_cols_all = static_cast<int>(b_cols);
+  p.e5m2_a = fa == FP8_E5M2;
+  p.e5m2_b = fb == FP8_E5M2;
+  p.out_fp32 = out == FP8_OUT_FP32;
+  p.sa = static_cast<const float*>(sA);
+  p.sb = static_cast<const float*>(sB);
+  p.loads = loads;
+  p.err = d->err;
+  const int tile = grouped_tile(p, d->num_sms);
+  GroupedMaps m;
+  std::memset(&m, 0, sizeof(m));
+  if (loads) {
+    if (!make_map(&m.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, a_cols, a_rows, 128, 128) ||
+        !make_map(&m.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B, b_cols, b_rows, 128, 128))
+      return FP8_ERR_CUDA;
+    // MX: the tiled scale buffers as rows of 256 bytes, two rows (one 512-byte atom) per box
+    if (mx && (!make_map(&m.sfa, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, sA, 256, 2 * (a_rows / 128) * (a_cols / 128), 256, 2,
+                         CU_TENSOR_MAP_SWIZZLE_NONE) ||
+               !make_map(&m.sfb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, sB, 256, 2 * (b_rows / 128) * (b_cols / 128), 256, 2,
+                         CU_TENSOR_MAP_SWIZZLE_NONE)))
+      return FP8_ERR_CUDA;
+  }
+  const bool ok = p.out_fp32 ? make_map(&m.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.c, p.N, c_rows, 32, 32)
+                             : make_map(&m.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.c, p.N, c_rows, 64, 32);
+  if (!ok) return FP8_ERR_CUDA;
+  return cuda_status(launch_grouped(p, m, tile, d->num_sms, stream));
+}
+
+// The kind of a pairing, among those that the grouped products take.
+fp8_status grouped_kind(fp8_format fa, fp8_recipe ra, fp8_format fb, fp8_recipe rb, fp8_out_dtype out, int* kind) {
+  if (!valid_fmt(fa) || !valid_fmt(fb) || (out != FP8_OUT_BF16 && out != FP8_OUT_FP32)) return FP8_ERR_INVALID_ARG;
+  int b_1x128;
+  if (fp8_status st = gemm_kind(ra, rb, kind, &b_1x128)) return st;
+  return *kind == kTensor || *kind == kMx ? FP8_OK : FP8_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8_status fp8_grouped_gemm(const uint8_t* A, fp8_format fa, fp8_recipe ra, const void* sA, const uint8_t* B, fp8_format fb,
+                            fp8_recipe rb, const void* sB, int32_t sB_count, const int32_t* offsets, int32_t n_experts,
+                            int64_t capacity, int64_t N, int64_t K, fp8_stacked stacked, void* C, fp8_out_dtype out,
+                            int32_t zero_tail, cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_grouped_gemm");
+  GroupedParams p{};
+  if (capacity < 0 || N < 0 || K < 0 || n_experts < 1 || (stacked != FP8_STACKED_ROWS && stacked != FP8_STACKED_COLS))
+    return FP8_ERR_INVALID_ARG;
+  if (fp8_status st = grouped_kind(fa, ra, fb, rb, out, &p.kind)) return st;
+  if (p.kind == kTensor && sB_count != 1 && sB_count != n_experts) return FP8_ERR_INVALID_ARG;
+  if (capacity % 128 || N % 128 || K % 128 || n_experts > kMaxExperts || capacity > kMaxDim || N > kMaxDim || K > kMaxDim)
+    return FP8_ERR_SHAPE;
+  if (capacity == 0 || N == 0) return FP8_OK;
+  const bool cols = stacked == FP8_STACKED_COLS;
+  p.n_experts = n_experts;
+  p.offsets = offsets;
+  p.capacity = capacity;
+  p.N = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.b_cols = cols;
+  p.sb_step = p.kind == kTensor && sB_count > 1;
+  p.c = C;
+  p.zero_tail = zero_tail != 0;
+  return grouped(p, A, fa, ra, sA, B, fb, rb, sB, capacity, K, cols ? N : n_experts * N, cols ? n_experts * K : K, capacity, out,
+                 stream);
+}
+
+fp8_status fp8_grouped_wgrad(const uint8_t* A, fp8_format fa, fp8_recipe ra, const void* sA, const uint8_t* B, fp8_format fb,
+                             fp8_recipe rb, const void* sB, const int32_t* offsets, int32_t n_experts, int64_t capacity,
+                             int64_t M, int64_t N, void* C, fp8_out_dtype out, cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_grouped_wgrad");
+  GroupedParams p{};
+  if (capacity < 0 || M < 0 || N < 0 || n_experts < 1) return FP8_ERR_INVALID_ARG;
+  if (fp8_status st = grouped_kind(fa, ra, fb, rb, out, &p.kind)) return st;
+  if (capacity % 128 || M % 128 || N % 128 || n_experts > kMaxExperts || capacity > kMaxDim || M > kMaxDim || N > kMaxDim)
+    return FP8_ERR_SHAPE;
+  if (M == 0 || N == 0) return FP8_OK;
+  p.depth = 1;
+  p.n_experts = n_experts;
+  p.offsets = offsets;
+  p.capacity = capacity;
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.c = C;
+  return grouped(p, A, fa, ra, sA, B, fb, rb, sB, M, capacity, N, capacity, n_experts * M, out, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ the gradients' norm
+namespace {
+
+static_assert(sizeof(ClipTensor) == sizeof(fp8_gradient) && offsetof(ClipTensor, out) == offsetof(fp8_gradient, out) &&
+                  offsetof(ClipTensor, n) == offsetof(fp8_gradient, n) && offsetof(ClipTensor, f32) == offsetof(fp8_gradient, dt) &&
+                  FP8_DT_BF16 == 0 && FP8_DT_FP32 == 1,
+              "the launcher reads fp8_gradient as ClipTensor");
+
+fp8_status grad_norm(const fp8_gradient* grads, int32_t n, bool clip, float max_norm, void* workspace, int64_t bytes, float* norm,
+                     cudaStream_t stream) {
+  if (n < 0 || (n > 0 && grads == nullptr) || norm == nullptr || workspace == nullptr || !(max_norm >= 0.0f))
+    return FP8_ERR_INVALID_ARG;
+  int64_t need = 0, total = 0;
+  if (fp8_status st = fp8_grad_norm_workspace(n, &need)) return st;
+  if (bytes < need) return FP8_ERR_SHAPE;
+  if (!aligned(workspace, 8) || !aligned(norm, 4)) return FP8_ERR_ALIGNMENT;
+  for (int32_t i = 0; i < n; ++i) {
+    const fp8_gradient& g = grads[i];
+    if (g.n < 0 || !valid_dt(g.dt) || (g.n > 0 && (g.in == nullptr || (clip && g.out == nullptr)))) return FP8_ERR_INVALID_ARG;
+    if (g.n >= (int64_t{1} << 44) || (total += g.n) >= (int64_t{1} << 44)) return FP8_ERR_SHAPE;
+    if (!aligned(g.in, elem_size(g.dt)) || (clip && !aligned(g.out, elem_size(g.dt)))) return FP8_ERR_ALIGNMENT;
+  }
+  DeviceInfo* d;
+  if (fp8_status st = device_info(&d)) return st;
+  return cuda_status(launch_clip(reinterpret_cast<const ClipTensor*>(grads), n, clip, max_norm, static_cast<double*>(workspace),
+                                 norm, d->num_sms, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8_status fp8_grad_norm_workspace(int32_t n_grads, int64_t* bytes) {
+  ApiRange nvtx_range("fp8_grad_norm_workspace");
+  if (n_grads < 0 || bytes == nullptr) return FP8_ERR_INVALID_ARG;
+  *bytes = clip_partials(n_grads) * static_cast<int64_t>(sizeof(double));
+  return FP8_OK;
+}
+
+fp8_status fp8_grad_norm(const fp8_gradient* grads, int32_t n_grads, void* workspace, int64_t workspace_bytes, float* norm,
+                         cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_grad_norm");
+  return grad_norm(grads, n_grads, false, 0.0f, workspace, workspace_bytes, norm, stream);
+}
+
+fp8_status fp8_clip_grad_norm(const fp8_gradient* grads, int32_t n_grads, float max_norm, void* workspace,
+                              int64_t workspace_bytes, float* norm, cudaStream_t stream) {
+  ApiRange nvtx_range("fp8_clip_grad_norm");
+  return grad_norm(grads, n_grads, true, max_norm, workspace, workspace_bytes, norm, stream);
 }
 
 }  // extern "C"

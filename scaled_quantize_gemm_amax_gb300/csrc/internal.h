@@ -344,6 +344,89 @@ GemmPlan gemm_plan(const GemmParams& p, int num_sms, int resident_pairs);
 cudaError_t launch_gemm(const GemmParams& p, const CUtensorMap& tm_a, const CUtensorMap& tm_b, const CUtensorMap& tm_sfa,
                         const CUtensorMap& tm_sfb, const CUtensorMap& tm_c, int num_sms, cudaStream_t s);
 
+// ---- RMS norm (rms.cu, rms_backward.cu); strides (ld*) in elements, f32: binary32 data, else bf16
+struct RmsParams {
+  const void* x;
+  int64_t rows, cols, ldx;
+  int f32;
+  const void* res;       // [rows, cols] added to x, null: none
+  int64_t ldr;
+  const void* w;         // [cols], null: 1
+  int w_f32;
+  float eps;
+  void* h;               // [rows, cols] x + res as rounded, null: not stored
+  int64_t ldh;
+  void* y;               // [rows, cols], null: not stored
+  int64_t ldy;
+  float* rstd;           // [rows], null: not stored
+  int recipe;            // of q: kTensor, kBlock1x128 or kMx
+  int mx_tiled, mx_floor;
+  int e5m2;
+  const float* scale;    // kTensor: float[1]
+  float* amax;           // float[1], zeroed by the kernel launched just before; null: none
+  uint8_t* q;            // [rows, cols] codes of y, null: none
+  int64_t ldq;
+  void* s;               // kTensor: float[1]; kBlock1x128: float[rows, ceil(cols / 128)]; kMx: E8M0 bytes
+};
+struct RmsBwdParams {
+  const void* dy;
+  int64_t rows, cols, lddy;
+  int f32;
+  const void* h;
+  int64_t ldh;
+  const float* rstd;
+  const void* dh;        // added to dx, null: none
+  int64_t lddh;
+  const void* w;
+  int w_f32;
+  void* dx;
+  int64_t lddx;
+  void* dw;              // [cols], null: none
+  float* partial;        // [norm_partials(rows)][cols]
+};
+cudaError_t launch_rms(const RmsParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_rms_backward(const RmsBwdParams& p, int num_sms, cudaStream_t s);
+
+// ---- the gradients' norm and clipping (clip.cu)
+struct ClipTensor {
+  const void* in;
+  void* out;
+  int64_t n;             // elements
+  int f32;
+};
+// doubles of partial sums that n_tensors need (clip.cu's workspace)
+int64_t clip_partials(int64_t n_tensors);
+// *norm = 2-norm over all tensors; with `clip`, out = in * min(1, max_norm / (*norm + 1e-6)) too
+cudaError_t launch_clip(const ClipTensor* t, int64_t n, bool clip, float max_norm, double* partial, float* norm, int num_sms,
+                        cudaStream_t s);
+
+// ---- products grouped by expert (grouped.cu)
+struct GroupedParams {
+  int kind;              // kTensor or kMx
+  int depth;             // 0: C [capacity, N], an expert's rows; 1: C [n_experts][M, N], summed over an expert's rows
+  int n_experts;
+  const int* offsets;    // [n_experts + 1], multiples of 128
+  int64_t capacity;      // rows that the segments lie in
+  int M, N, K;           // M: depth only; K: rows only
+  int b_cols;            // rows: the experts' B are side by side, [N, n_experts * K], not [n_experts * N, K]
+  int a_cols;            // columns of A's matrix, and columns and rows of B's (where its scale atoms are)
+  int b_cols_all, b_rows_all;
+  int e5m2_a, e5m2_b, out_fp32;
+  const float* sa;       // kTensor: float[1]
+  const float* sb;       // kTensor: float[1] or (sb_step 1) one an expert
+  int sb_step;
+  void* c;
+  int zero_tail;         // rows: rows behind the last segment are set to 0
+  int loads;             // whether there is anything to multiply (the tensor maps of A and B are valid)
+  uint32_t* err;
+};
+struct GroupedMaps {
+  CUtensorMap a, b, sfa, sfb, c;
+};
+// Columns of a tile of the kernel that a call takes: 256 (CTA pairs) or 128.  Boxes of A and B have 128 rows.
+int grouped_tile(const GroupedParams& p, int num_sms);
+cudaError_t launch_grouped(const GroupedParams& p, const GroupedMaps& m, int tile, int num_sms, cudaStream_t s);
+
 // Bounded-wait self test: one CTA waits on an mbarrier nothing arrives on.
 cudaError_t launch_wait_selftest(uint32_t* err, cudaStream_t s);
 // Index-check self test: one thread checks `index` against `extent` the way the kernels

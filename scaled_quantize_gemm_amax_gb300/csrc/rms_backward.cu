@@ -1,0 +1,333 @@
+// rms_backward.cu -- RMS norm, backward.
+//
+//   g = dy w,  xh = h r,  c = sum g xh / H,  dx = r (g - xh c) + dh
+//   dw = sum over rows of dy xh
+// dh is the gradient that reaches h by the residual stream; dx is the gradient of both x and the
+// residual.  All sums are binary32, in an order that depends on the shape alone.
+//
+// Bound by HBM: dy, h and dh once in, dx once out.  A thread owns the same columns for all the rows
+// of its group, so the column sums stay in registers over the whole walk; they leave as one partial
+// sum a block, added up by a second, small launch.
+#include "norm.cuh"
+
+namespace fp8q {
+
+namespace {
+
+constexpr int kMostCols = 16384;   // of a row held in registers
+constexpr int kThreads = 256;
+
+// dx of rows of any width: one block per row, two passes.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_rms_dx_any(const RmsBwdParams p) {
+  __shared__ float red[kThreads / 32];
+  const float inv_n = 1.0f / static_cast<float>(p.cols);
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
+    const T* h = static_cast<const T*>(p.h) + row * p.ldh;
+    const T* dh = p.dh != nullptr ? static_cast<const T*>(p.dh) + row * p.lddh : nullptr;
+    T* dx = static_cast<T*>(p.dx) + row * p.lddx;
+    const float rstd = p.rstd[row];
+    float sum = 0.0f;
+    for (int64_t c = threadIdx.x; c < p.cols; c += kThreads) {
+      const float g = ld_elem(dy + c) * (p.w != nullptr ? ld_param(p.w, p.w_f32, c) : 1.0f);
+      sum = fmaf(g, ld_elem(h + c) * rstd, sum);
+    }
+    sum = warp_sum(sum);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) sum += red[i];
+    const float k = -rstd * (sum * inv_n);
+    for (int64_t c = threadIdx.x; c < p.cols; c += kThreads) {
+      const float g = ld_elem(dy + c) * (p.w != nullptr ? ld_param(p.w, p.w_f32, c) : 1.0f);
+      const float v = fmaf(ld_elem(h + c) * rstd, k, fmaf(g, rstd, dh != nullptr ? ld_elem(dh + c) : 0.0f));
+      st_elem(dx + c, v);
+    }
+  }
+}
+
+// Partial sums of dw: block (x, y) sums 256 columns over the rows of slab y, one thread per column.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_rms_partial_any(const RmsBwdParams p, int slabs) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (c >= p.cols) return;
+  const int64_t r0 = p.rows * blockIdx.y / slabs, r1 = p.rows * (blockIdx.y + 1) / slabs;
+  float dw = 0.0f;
+  for (int64_t row = r0; row < r1; ++row)
+    dw = fmaf(ld_elem(static_cast<const T*>(p.dy) + row * p.lddy + c),
+              ld_elem(static_cast<const T*>(p.h) + row * p.ldh + c) * p.rstd[row], dw);
+  p.partial[static_cast<int64_t>(blockIdx.y) * p.cols + c] = dw;
+}
+
+// Rows of up to kMostCols columns, V values a lane.  A stage holds a warp's part of a row: dy, h, dh (`ahead`;
+// otherwise dh is read when it is used) and the row's rstd.  The column sums and g take V of a thread's registers each; h and dh are read from
+// shared memory when they are used.
+template <typename T, bool VECTOR, int V, int BLOCK_WARPS>
+__global__ void __launch_bounds__(BLOCK_WARPS * 32)
+    k_rms_backward(const RmsBwdParams p, const int warps, const int stages, const int ring, const bool ahead) {
+  using P = Piece<T, VECTOR>;
+  constexpr int E = P::E, J = V / E, H = E / 2, kCols = 32 * V;
+  using Part = RowPart<P, kCols, VECTOR, T>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[2][BLOCK_WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / warps, w_in = warp - group * warps;
+  const int n_groups = (blockDim.x >> 5) / warps, step = gridDim.x * n_groups;
+  const int rows = static_cast<int>(p.rows), cols = static_cast<int>(p.cols);
+  const bool add = p.dh != nullptr;
+  const int scalar = Part::kBytes * (ahead ? 3 : 2), stage_bytes = scalar + 128;
+  // this lane's first column and the columns from there to the row's end
+  const int base = w_in * kCols, c = base + P::first(lane), left = cols - c;
+  const float inv_n = 1.0f / static_cast<float>(cols);
+  uint8_t* const mine = smem + ring + warp * stages * stage_bytes;
+  float* const ws = reinterpret_cast<float*>(smem);
+
+  auto issue = [&](int row, int s) {
+    if (row < rows) {
+      uint8_t* const to = mine + s * stage_bytes;
+      const int64_t r = row;
+      Part::start(to, static_cast<const T*>(p.dy) + r * p.lddy, r * p.lddy, base, cols, lane);
+      Part::start(to + Part::kBytes, static_cast<const T*>(p.h) + r * p.ldh, r * p.ldh, base, cols, lane);
+      if (ahead) Part::start(to + 2 * Part::kBytes, static_cast<const T*>(p.dh) + r * p.lddh, r * p.lddh, base, cols, lane);
+      if (lane == 0) cp_async<4>(smem_u32(to) + scalar, p.rstd + row, true);
+    }
+    cp_async_commit();
+  };
+  // past the row's start, in elements of a granule
+  auto past = [&](const void* m, int64_t ld, int row) {
+    return Part::past(static_cast<const T*>(m) + static_cast<int64_t>(row) * ld + base);
+  };
+
+  pdl_wait();
+  pdl_launch_dependents();
+  float2 dw[J][H];
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int i = 0; i < H; ++i) dw[j][i] = both(0.0f);
+  int row = blockIdx.x * n_groups + group;
+  start_param<P, V>(p.w, p.w_f32, cols, warps, 1.0f, ws);
+  cp_async_commit();
+  for (int s = 0; s < stages; ++s) issue(row + s * step, s);
+  cp_async_wait_oldest(stages + 1);
+  settle_param<P, V>(p.w, p.w_f32, warps, ws);
+  __syncthreads();
+  for (int s = 0, buf = 0; row < rows; row += step, buf ^= 1) {
+    cp_async_wait_oldest(stages);
+    __syncwarp();   // the row's rstd, and unaligned a lane's last elements, were copied by other lanes
+    const uint8_t* const at = mine + s * stage_bytes;
+    const float rstd = *reinterpret_cast<const float*>(at + scalar);
+    const int m_dy = past(p.dy, p.lddy, row), m_h = past(p.h, p.ldh, row);
+    float2 g[J][H], acc = both(0.0f);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      float d[E], h[E], w[E];
+      Part::read(at, m_dy, lane, j, d);
+      Part::read(at + Part::kBytes, m_h, lane, j, h);
+      read_param<P, V>(ws, w_in, j, lane, w);
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        const float2 dy = {d[2 * i], d[2 * i + 1]}, xh = mul2(make_float2(h[2 * i], h[2 * i + 1]), both(rstd));
+        g[j][i] = mul2(dy, make_float2(w[2 * i], w[2 * i + 1]));
+        dw[j][i] = fma2(dy, xh, dw[j][i]);
+        acc = fma2(g[j][i], xh, acc);
+      }
+    }
+    float sum = warp_sum(acc.x + acc.y);
+    if (warps > 1) {
+      if (lane == 0) red[buf][warp] = sum;
+      group_sync(group, warps);
+      // lane l joins warp l's part (the other buffer is written before this one is reused)
+      sum = warp_sum(lane < warps ? red[buf][group * warps + lane] : 0.0f);
+    }
+    // dx = r g - (r c r) h + dh
+    const float2 r = both(rstd), k = both(-rstd * (sum * inv_n) * rstd);
+    const int m_dh = ahead ? past(p.dh, p.lddh, row) : 0;
+    const T* const dh0 = static_cast<const T*>(p.dh) + static_cast<int64_t>(row) * p.lddh + c;
+    T* const dx0 = static_cast<T*>(p.dx) + static_cast<int64_t>(row) * p.lddx + c;
+    constexpr int N = VECTOR ? 1 : J;   // pieces stored together: unaligned, the fewer ends the better
+#pragma unroll
+    for (int j0 = 0; j0 < J; j0 += N) {
+      uint4 packed[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int j = j0 + n;
+        float h[E], a[E] = {};
+        Part::read(at + Part::kBytes, m_h, lane, j, h);
+        if (ahead) {
+          Part::read(at + 2 * Part::kBytes, m_dh, lane, j, a);
+        } else if (add) {
+          float v[1][E];
+          P::load(dh0 + j * P::WC, c + j * P::WC, left - j * P::WC, v);
+#pragma unroll
+          for (int i = 0; i < E; ++i) a[i] = v[0][i];
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          const float2 o = fma2(make_float2(h[2 * i], h[2 * i + 1]), k, fma2(g[j][i], r, make_float2(a[2 * i], a[2 * i + 1])));
+          a[2 * i] = o.x;
+          a[2 * i + 1] = o.y;
+        }
+        packed[n] = P::pack(a);
+      }
+      P::store_raw(dx0 + j0 * P::WC, left - j0 * P::WC, packed);
+    }
+    __syncwarp();   // all lanes have read what this one copied
+    issue(row + stages * step, s);
+    s = s + 1 == stages ? 0 : s + 1;
+  }
+  if (p.dw == nullptr) return;
+  // the block's groups joined pairwise in shared memory (the ring is free: every copy was waited for)
+  __syncthreads();
+  float2* join = reinterpret_cast<float2*>(smem + ring);
+  for (int n = n_groups; n > 1;) {
+    const int half = (n + 1) / 2;
+    if (group >= half && group < n) {
+      float2* out = join + ((group - half) * warps + w_in) * 16 * V + lane;
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < H; ++i) out[(j * H + i) * 32] = dw[j][i];
+    }
+    __syncthreads();
+    if (group < n - half) {
+      const float2* in = join + (group * warps + w_in) * 16 * V + lane;
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < H; ++i) dw[j][i] = add2(dw[j][i], in[(j * H + i) * 32]);
+    }
+    __syncthreads();
+    n = half;
+  }
+  if (group != 0) return;
+  float* const part = gridDim.x > 1 ? p.partial + static_cast<int64_t>(blockIdx.x) * cols : nullptr;   // else: the result
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    if (VECTOR && part != nullptr) {   // cols is a multiple of 4, the workspace 16-byte aligned
+      if (left <= j * P::WC) continue;
+#pragma unroll
+      for (int i = 0; i < H; i += 2)
+        reinterpret_cast<float4*>(part + c + j * P::WC)[i / 2] = make_float4(dw[j][i].x, dw[j][i].y, dw[j][i + 1].x, dw[j][i + 1].y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        if (!P::has(left - j * P::WC, i)) continue;
+        const int col = c + j * P::WC + P::at(i);
+        const float v = i % 2 ? dw[j][i / 2].y : dw[j][i / 2].x;
+        if (part != nullptr) part[col] = v;
+        else st_param(p.dw, p.w_f32, col, v);
+      }
+    }
+  }
+}
+
+// The cols sums of the n partial sums: a block takes 32 lanes' worth of them (N a lane), warp k the partials
+// k, k + 32, ...; then the 32 warps' sums in order.
+constexpr int kParamWarps = 32;
+template <int N>
+__global__ void __launch_bounds__(kParamWarps * 32) k_rms_params(const float* partial, int n, int cols, bool f32, void* dw) {
+  __shared__ float part[kParamWarps][32 * N];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * N;
+  pdl_wait();
+  pdl_launch_dependents();
+  float v[N] = {};
+  if (c < cols) {
+#pragma unroll 5
+    for (int k = warp; k < n; k += kParamWarps) {
+      const float* from = partial + static_cast<int64_t>(k) * cols + c;
+      if constexpr (N == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(from);
+        v[0] += u.x, v[1] += u.y, v[2] += u.z, v[3] += u.w;
+      } else {
+        v[0] += *from;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) part[warp][i * 32 + lane] = v[i];
+  __syncthreads();
+  if (warp >= N || c >= cols) return;
+  float sum = 0.0f;   // warp i of the first N: value i of every lane
+#pragma unroll
+  for (int k = 0; k < kParamWarps; ++k) sum += part[k][warp * 32 + lane];
+  st_param(dw, f32, c + warp, sum);
+}
+
+// *partials: number of partial sums left in p.partial (0: none)
+template <typename T, bool VECTOR, int V, int BLOCK_WARPS>
+cudaError_t run_rms_backward(const RmsBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
+  const int part = RowPart<Piece<T, VECTOR>, 32 * V, VECTOR, T>::kBytes;
+  const int blocks = num_sms < kMaxNormPartials ? num_sms : kMaxNormPartials;
+  bool ahead = p.dh != nullptr;
+  NormPlan n = norm_plan(p.rows, p.cols, 32 * V, BLOCK_WARPS, 1, part * (ahead ? 3 : 2) + 128, blocks);
+  if (ahead && n.smem > kNormSmem) {   // binary32 rows of over 12288 columns: three parts of a row do not fit
+    ahead = false;
+    n = norm_plan(p.rows, p.cols, 32 * V, BLOCK_WARPS, 1, part * 2 + 128, blocks);
+  }
+  const size_t join = n.ring + static_cast<size_t>(n.groups / 2) * n.warps * 32 * V * sizeof(float);
+  if (n.smem < join) n.smem = join;
+  static std::atomic<bool> done[kMaxDevices];
+  auto kernel = k_rms_backward<T, VECTOR, V, BLOCK_WARPS>;
+  const cudaError_t e = ensure_smem_limit(kernel, kNormSmem, done);
+  if (e != cudaSuccess) return e;
+  *partials = n.blocks > 1 ? n.blocks : 0;
+  return launch_pdl(kernel, dim3(n.blocks), dim3(static_cast<unsigned>(n.warps * n.groups * 32)), n.smem, s, 1, p, n.warps,
+                    n.stages, n.ring, ahead);
+}
+
+// Values a lane and warps of a block: as few values as hold a narrow row, else 32; 16 warps take every row of up to
+// kMostCols columns and leave a thread 128 registers.
+template <typename T, bool VECTOR>
+cudaError_t run_rms_backward(const RmsBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
+  if (p.cols <= 256) return run_rms_backward<T, VECTOR, 8, 24>(p, num_sms, s, partials);
+  if (p.cols <= 512) return run_rms_backward<T, VECTOR, 16, 24>(p, num_sms, s, partials);
+  return run_rms_backward<T, VECTOR, 32, 16>(p, num_sms, s, partials);
+}
+
+template <typename T>
+cudaError_t run_any(const RmsBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
+  const int64_t cap = static_cast<int64_t>(num_sms) * 8;
+  if (p.rows > 0) {
+    const cudaError_t e = launch_pdl(k_rms_dx_any<T>, dim3(static_cast<unsigned>(p.rows < cap ? p.rows : cap)), dim3(kThreads), 0,
+                                     s, 1, p);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.dw == nullptr) return cudaSuccess;
+  *partials = norm_partials(p.rows);
+  return launch_pdl(k_rms_partial_any<T>, dim3(static_cast<unsigned>((p.cols + kThreads - 1) / kThreads), *partials),
+                    dim3(kThreads), 0, s, 1, p, *partials);
+}
+
+}  // namespace
+
+cudaError_t launch_rms_backward(const RmsBwdParams& p, int num_sms, cudaStream_t s) {
+  const int64_t size = p.f32 ? 4 : 2;
+  int partials = 0;
+  cudaError_t e;
+  if (p.cols > kMostCols || p.rows == 0) {
+    e = p.f32 ? run_any<float>(p, num_sms, s, &partials) : run_any<uint16_t>(p, num_sms, s, &partials);
+  } else {
+    const bool vec = takes(p.dy, p.lddy, p.cols, size, 16) && takes(p.h, p.ldh, p.cols, size, 16) &&
+                     takes(p.dh, p.lddh, p.cols, size, 16) && takes(p.dx, p.lddx, p.cols, size, 16) && takes(p.w, 0, 0, 1, 16);
+    if (p.f32)
+      e = vec ? run_rms_backward<float, true>(p, num_sms, s, &partials) : run_rms_backward<float, false>(p, num_sms, s, &partials);
+    else
+      e = vec ? run_rms_backward<uint16_t, true>(p, num_sms, s, &partials)
+              : run_rms_backward<uint16_t, false>(p, num_sms, s, &partials);
+  }
+  if (e != cudaSuccess || partials == 0 || p.dw == nullptr) return e;
+  const int quad = p.cols % 4 == 0 ? 4 : 1;
+  return launch_pdl(quad == 4 ? k_rms_params<4> : k_rms_params<1>, dim3(static_cast<unsigned>((p.cols / quad + 31) / 32)),
+                    dim3(kParamWarps * 32), 0, s, 1, static_cast<const float*>(p.partial), partials, static_cast<int>(p.cols),
+                    p.w_f32 != 0, p.dw);
+}
+
+}  // namespace fp8q

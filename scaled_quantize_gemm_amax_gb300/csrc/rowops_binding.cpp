@@ -12,13 +12,18 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <vector>
+
 #include "fp8q.h"
 
 namespace {
 
 #define FP8Q_ENTRIES(X)                                                                                                \
   X(fp8_layer_norm) X(fp8_layer_norm_backward) X(fp8_layer_norm_workspace) X(fp8_gated_act) X(fp8_gated_act_backward) \
-  X(fp8_moe_route) X(fp8_moe_capacity) X(fp8_moe_dispatch) X(fp8_moe_combine) X(fp8_moe_combine_backward)
+  X(fp8_moe_route) X(fp8_moe_capacity) X(fp8_moe_dispatch) X(fp8_moe_combine) X(fp8_moe_combine_backward)             \
+  X(fp8_rms_norm) X(fp8_rms_norm_backward) X(fp8_rms_norm_workspace) X(fp8_grouped_gemm) X(fp8_grouped_wgrad)          \
+  X(fp8_grad_norm) X(fp8_clip_grad_norm) X(fp8_grad_norm_workspace)
 #define X(f) decltype(&::f) p_##f = nullptr;
 FP8Q_ENTRIES(X)
 #undef X
@@ -462,6 +467,279 @@ PyObject* moe_combine_backward(PyObject* const* a) {
   return wrap_all(dys, dw);
 }
 
+fp8_recipe recipe_of(PyObject* o) { return static_cast<fp8_recipe>(small(integer(o))); }
+bool is_mx(fp8_recipe r) { return r >= FP8_MX_1x32; }
+bool is_tiled(fp8_recipe r) { return r == FP8_MX_1x32_TILED || r == FP8_MX_1x32_FLOOR_TILED; }
+
+// rms_norm(x, weight, residual, eps, recipe | None, fmt, scale, amax_out, keep_y, stats, stream) -> (y, h, rstd, q, s)
+PyObject* rms_norm(PyObject* const* a) {
+  const Rows x = rows_of(needed(a[0], "x"), "x");
+  const fp8_dtype dt = data_type(*x.t, "x"), wdt = param_type(a[1], Py_None);
+  void* w = vector_of(a[1], x.cols, scalar_type(wdt), "weight");
+  const Rows res = rows_like(a[2], *x.t, x.rows, x.cols, "residual");
+  auto* scale = static_cast<float*>(vector_of(a[6], 1, at::kFloat, "scale"));
+  auto* amax = static_cast<float*>(vector_of(a[7], 1, at::kFloat, "amax_out"));
+  on_gpu({a[0], a[1], a[2], a[6], a[7]});
+  const double eps = PyFloat_AsDouble(a[3]);
+  if (PyErr_Occurred()) throw Failed();
+  const bool copy = a[4] != Py_None, keep_y = truth(a[8]), stats = truth(a[9]);
+  const fp8_recipe recipe = copy ? recipe_of(a[4]) : FP8_TENSOR;
+  const fp8_format fmt = format(a[5]);
+  Place on;
+  const cudaStream_t stream = stream_of(a[10], *x.t, on);
+  at::Tensor y, h, rstd, q, s;
+  const int64_t ldq = to16(x.cols);
+  fp8_status st;
+  {
+    Unlocked unlocked;
+    if (keep_y) y = make({x.rows, x.cols}, x.t->scalar_type(), *x.t);
+    if (res.t != nullptr) h = make({x.rows, x.cols}, x.t->scalar_type(), *x.t);
+    // the codes, their multipliers and the statistics in one allocation
+    const int64_t codes = copy ? to16(x.rows * ldq) : 0;
+    int64_t scales = 0;
+    std::vector<int64_t> shape, strides;
+    if (copy) {
+      if (recipe == FP8_TENSOR) shape = {1};
+      else if (is_tiled(recipe)) shape = {(x.rows + 127) / 128, groups(x.cols), 512};
+      else shape = {x.rows, is_mx(recipe) ? x.cols / 32 : groups(x.cols)};
+      scales = is_mx(recipe) ? 1 : 4;
+      strides.resize(shape.size());
+      int64_t n = 1;
+      for (size_t i = shape.size(); i-- > 0;) {
+        strides[i] = n;
+        n *= shape[i];
+      }
+      scales = to16(scales * n);
+    }
+    if (copy || stats) {
+      const at::Tensor whole = make({codes + scales + (stats ? 4 * x.rows : 0)}, at::kByte, *x.t);
+      if (copy) {
+        q = part(whole, 0, at::kByte, {x.rows, x.cols}, {ldq, 1});
+        s = part(whole, codes, is_mx(recipe) ? at::kByte : at::kFloat, shape, strides);
+      }
+      if (stats) rstd = part(whole, codes + scales, at::kFloat, {x.rows}, {1});
+    }
+    st = p_fp8_rms_norm(x.p(), x.rows, x.cols, x.ld, dt, res.p(), res.ld, w, wdt, static_cast<float>(eps), ptr<void>(h), x.cols,
+                        ptr<void>(y), x.cols, ptr<float>(rstd), recipe, fmt, scale, amax, ptr<uint8_t>(q), ldq, ptr<void>(s),
+                        stream);
+  }
+  check(st, "fp8_rms_norm");
+  return wrap_all(y, h, rstd, q, s);
+}
+
+// rms_norm_backward(dy, h, rstd, weight, dh, param_grads, param_dtype, stream) -> (dx, dweight)
+PyObject* rms_norm_backward(PyObject* const* a) {
+  const Rows dy = rows_of(needed(a[0], "dy"), "dy");
+  const fp8_dtype dt = data_type(*dy.t, "dy");
+  needed(a[1], "h");
+  needed(a[2], "rstd");
+  const Rows h = rows_like(a[1], *dy.t, dy.rows, dy.cols, "h"), dh = rows_like(a[4], *dy.t, dy.rows, dy.cols, "dh");
+  if (!THPDtype_Check(a[6])) refuse(PyExc_TypeError, "param_dtype: a torch.dtype is needed");
+  const at::Tensor* weight = tensor(a[3], "weight");
+  const fp8_dtype wdt = dtype_code(weight != nullptr ? weight->scalar_type() : reinterpret_cast<THPDtype*>(a[6])->scalar_type,
+                                   weight != nullptr ? "weight" : "param_dtype");
+  void* w = vector_of(a[3], dy.cols, scalar_type(wdt), "weight");
+  auto* rstd = static_cast<float*>(vector_of(a[2], dy.rows, at::kFloat, "rstd"));
+  on_gpu({a[0], a[1], a[2], a[3], a[4]});
+  const bool param_grads = truth(a[5]);
+  Place on;
+  const cudaStream_t stream = stream_of(a[7], *dy.t, on);
+  int64_t bytes = 0;
+  if (param_grads) check(p_fp8_rms_norm_workspace(dy.rows, dy.cols, &bytes), "fp8_rms_norm_workspace");
+  at::Tensor dx, dw, ws;
+  fp8_status st;
+  {
+    Unlocked unlocked;
+    dx = make({dy.rows, dy.cols}, dy.t->scalar_type(), *dy.t);
+    if (param_grads) {
+      dw = make({dy.cols}, scalar_type(wdt), *dy.t);
+      ws = make({bytes}, at::kByte, *dy.t);
+    }
+    st = p_fp8_rms_norm_backward(dy.p(), dy.rows, dy.cols, dy.ld, dt, h.p(), h.ld, rstd, dh.p(), dh.ld, w, wdt, dx.data_ptr(),
+                                 dy.cols, ptr<void>(dw), ptr<void>(ws), bytes, stream);
+  }
+  check(st, "fp8_rms_norm_backward");
+  return wrap_all(dx, dw);
+}
+
+// One operand of the grouped products: dense codes and their multipliers.
+struct Operand {
+  const at::Tensor* t;
+  int64_t rows, cols, n_scales;
+  void* s;
+  uint8_t* p() const { return static_cast<uint8_t*>(t->data_ptr()); }
+};
+Operand operand_of(PyObject* o, PyObject* os, fp8_recipe recipe, int64_t experts, const char* what) {
+  const at::Tensor& t = needed(o, what);
+  if (t.dim() != 2 || t.element_size() != 1 || !t.is_contiguous())
+    refuse(PyExc_ValueError, std::string(what) + ": a dense matrix of one-byte codes is needed, not " + shape_of(t));
+  const at::Tensor& s = needed(os, "scales");
+  Operand r{&t, t.size(0), t.size(1), s.numel(), s.data_ptr()};
+  if (is_mx(recipe)) {
+    if (s.element_size() != 1 || !s.is_contiguous() || r.n_scales != (r.rows + 127) / 128 * groups(r.cols) * 512)
+      refuse(PyExc_ValueError, std::string(what) + ": its tiled one-byte scales are needed, not " + shape_of(s));
+  } else if (s.scalar_type() != at::kFloat || !s.is_contiguous() || (r.n_scales != 1 && r.n_scales != experts)) {
+    refuse(PyExc_ValueError, std::string(what) + ": one float32 multiplier" + (experts > 1 ? " (or one an expert)" : "") +
+                                 " is needed, not " + shape_of(s));
+  }
+  return r;
+}
+const at::Tensor& starts_of(PyObject* o) {
+  const at::Tensor& t = needed(o, "offsets");
+  if (t.dim() != 1 || t.size(0) < 2 || t.scalar_type() != at::kInt || !t.is_contiguous())
+    refuse(PyExc_ValueError, "offsets: a contiguous int32 vector of n_experts + 1 is needed, not " + shape_of(t));
+  return t;
+}
+fp8_out_dtype out_of(PyObject* o) { return static_cast<fp8_out_dtype>(small(integer(o))); }
+
+// grouped_gemm(a, fa, ra, sa, b, fb, rb, sb, offsets, out, stacked, zero_tail, stream) -> c
+PyObject* grouped_gemm(PyObject* const* v) {
+  const at::Tensor& offsets = starts_of(v[8]);
+  const int64_t experts = offsets.size(0) - 1;
+  const fp8_recipe ra = recipe_of(v[2]), rb = recipe_of(v[6]);
+  const Operand a = operand_of(v[0], v[3], ra, 1, "a"), b = operand_of(v[4], v[7], rb, experts, "b");
+  const fp8_out_dtype out = out_of(v[9]);
+  const fp8_format fa = format(v[1]), fb = format(v[5]);
+  const auto stacked = static_cast<fp8_stacked>(small(integer(v[10])));
+  const bool cols = stacked == FP8_STACKED_COLS;
+  const int64_t n = cols ? b.rows : b.rows / experts, depth = a.cols;
+  if (cols ? b.cols != experts * depth : b.rows != experts * n || b.cols != depth)
+    refuse(PyExc_ValueError, "b: " + std::to_string(experts) + " experts' matrices of depth " + std::to_string(depth) +
+                                 (cols ? " side by side" : " one below the other") + " are needed, not " + shape_of(*b.t));
+  on_gpu({v[0], v[3], v[4], v[7], v[8]});
+  const bool zero_tail = truth(v[11]);
+  Place on;
+  const cudaStream_t stream = stream_of(v[12], *a.t, on);
+  at::Tensor c;
+  fp8_status st;
+  {
+    Unlocked unlocked;
+    c = make({a.rows, n}, out == FP8_OUT_FP32 ? at::kFloat : at::kBFloat16, *a.t);
+    st = p_fp8_grouped_gemm(a.p(), fa, ra, a.s, b.p(), fb, rb, b.s, small(b.n_scales), ptr<int32_t>(offsets),
+                            small(experts), a.rows, n, depth, stacked, c.data_ptr(), out, zero_tail, stream);
+  }
+  check(st, "fp8_grouped_gemm");
+  return wrap(c);
+}
+
+// grouped_wgrad(a, fa, ra, sa, b, fb, rb, sb, offsets, out, stream) -> c
+PyObject* grouped_wgrad(PyObject* const* v) {
+  const at::Tensor& offsets = starts_of(v[8]);
+  const int64_t experts = offsets.size(0) - 1;
+  const fp8_recipe ra = recipe_of(v[2]), rb = recipe_of(v[6]);
+  const Operand a = operand_of(v[0], v[3], ra, 1, "a"), b = operand_of(v[4], v[7], rb, 1, "b");
+  if (a.cols != b.cols)
+    refuse(PyExc_ValueError, "a and b: the same number of rows' columns is needed, not " + shape_of(*a.t) + " and " + shape_of(*b.t));
+  on_gpu({v[0], v[3], v[4], v[7], v[8]});
+  const fp8_out_dtype out = out_of(v[9]);
+  const fp8_format fa = format(v[1]), fb = format(v[5]);
+  Place on;
+  const cudaStream_t stream = stream_of(v[10], *a.t, on);
+  at::Tensor c;
+  fp8_status st;
+  {
+    Unlocked unlocked;
+    c = make({experts, a.rows, b.rows}, out == FP8_OUT_FP32 ? at::kFloat : at::kBFloat16, *a.t);
+    st = p_fp8_grouped_wgrad(a.p(), fa, ra, a.s, b.p(), fb, rb, b.s, ptr<int32_t>(offsets), small(experts),
+                             a.cols, a.rows, b.rows, c.data_ptr(), out, stream);
+  }
+  check(st, "fp8_grouped_wgrad");
+  return wrap(c);
+}
+
+// The elements of a list or tuple of tensors.
+struct Items {
+  PyObject* seq;
+  explicit Items(PyObject* o, const char* what) : seq(PySequence_Fast(o, what)) {
+    if (seq == nullptr) throw Failed();
+  }
+  ~Items() { Py_DECREF(seq); }
+  Items(const Items&) = delete;
+  Items& operator=(const Items&) = delete;
+  Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(seq); }
+  PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(seq, i); }
+};
+// A gradient whose elements fill their memory without gaps, in whatever order.
+const at::Tensor& dense(PyObject* o, const char* what) {
+  const at::Tensor& t = needed(o, what);
+  data_type(t, what);
+  if (t.layout() != at::kStrided || !t.is_non_overlapping_and_dense())
+    refuse(PyExc_ValueError, std::string(what) + ": dense tensors are needed, not " + shape_of(t));
+  return t;
+}
+
+// clip_grad_norm(grads, max_norm | None, out | None, stream) -> norm; max_norm None: the norm alone;
+// out None: in place
+PyObject* clip_grad_norm(PyObject* const* v) {
+  const Items grads(v[0], "grads: a sequence of tensors is needed");
+  const Py_ssize_t n = grads.size();
+  const bool clip = v[1] != Py_None, in_place = v[2] == Py_None;
+  const double max_norm = clip ? PyFloat_AsDouble(v[1]) : 0.0;
+  if (PyErr_Occurred()) throw Failed();
+  const Items outs(in_place ? v[0] : v[2], "out: a sequence of tensors is needed");
+  if (clip && outs.size() != n) refuse(PyExc_ValueError, "out: as many tensors as gradients are needed");
+  if (n == 0) refuse(PyExc_ValueError, "grads: at least one tensor is needed");
+  std::vector<fp8_gradient> table(static_cast<size_t>(n));
+  const at::Tensor& first = needed(grads[0], "grads");
+  // Memory written and read by two tensors of a call would be scaled in an order of its own.  Gradients
+  // that lie in ascending order, as views into a buffer do, are seen to be apart on the way; others are sorted.
+  struct Span {
+    uintptr_t lo, hi;
+    bool out;
+  };
+  std::vector<Span> spans;
+  spans.reserve(static_cast<size_t>(in_place || !clip ? n : 2 * n));
+  auto span = [&](const at::Tensor& t, bool out) {
+    const auto lo = reinterpret_cast<uintptr_t>(t.data_ptr());
+    if (t.numel() > 0) spans.push_back({lo, lo + static_cast<uintptr_t>(t.numel() * t.element_size()), out});
+  };
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    const at::Tensor& g = dense(grads[i], "grads");
+    if (!g.is_cuda()) refuse(PyExc_ValueError, "a CUDA tensor is needed, not one on " + g.device().str());
+    if (g.device() != first.device())
+      refuse(PyExc_ValueError, "tensors of one device are needed, not of " + first.device().str() + " and " + g.device().str());
+    fp8_gradient& to = table[static_cast<size_t>(i)];
+    to = {g.data_ptr(), nullptr, g.numel(), data_type(g, "grads")};
+    if (!clip) continue;
+    span(g, in_place);
+    const at::Tensor& o = in_place ? g : dense(outs[i], "out");
+    if (!in_place) {
+      if (o.scalar_type() != g.scalar_type() || o.sizes() != g.sizes() || o.strides() != g.strides() || o.device() != g.device())
+        refuse(PyExc_ValueError, "out: tensors like the gradients are needed, not " + shape_of(o) + " for " + shape_of(g));
+      if (o.data_ptr() != g.data_ptr()) span(o, true);
+      else if (g.numel() > 0) spans.back().out = true;
+    }
+    to.out = o.data_ptr();
+  }
+  bool sorted = true;
+  for (size_t i = 1; i < spans.size() && sorted; ++i) sorted = spans[i - 1].hi <= spans[i].lo;
+  if (!sorted) {
+    std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.lo < y.lo; });
+    uintptr_t all = 0, written = 0;   // ends of what lies in front
+    for (const Span& x : spans) {
+      if (x.lo < written || (x.out && x.lo < all)) refuse(PyExc_ValueError, "gradients and outputs must not share memory");
+      all = std::max(all, x.hi);
+      if (x.out) written = std::max(written, x.hi);
+    }
+  }
+  Place on;
+  const cudaStream_t stream = stream_of(v[3], first, on);
+  int64_t bytes = 0;
+  const auto count = small(n);
+  check(p_fp8_grad_norm_workspace(count, &bytes), "fp8_grad_norm_workspace");
+  at::Tensor whole, norm;
+  fp8_status st;
+  {
+    Unlocked unlocked;
+    whole = make({bytes}, at::kByte, first);
+    norm = make({1}, at::kFloat, first);
+    st = clip ? p_fp8_clip_grad_norm(table.data(), count, static_cast<float>(max_norm), whole.data_ptr(), bytes, ptr<float>(norm), stream)
+              : p_fp8_grad_norm(table.data(), count, whole.data_ptr(), bytes, ptr<float>(norm), stream);
+  }
+  check(st, clip ? "fp8_clip_grad_norm" : "fp8_grad_norm");
+  return wrap(norm);
+}
+
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -516,6 +794,11 @@ PyMethodDef methods[] = {
     ENTRY(moe_dispatch, 4),
     ENTRY(moe_combine, 4),
     ENTRY(moe_combine_backward, 6),
+    ENTRY(rms_norm, 11),
+    ENTRY(rms_norm_backward, 8),
+    ENTRY(grouped_gemm, 13),
+    ENTRY(grouped_wgrad, 11),
+    ENTRY(clip_grad_norm, 4),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rowops", "Allocation helpers of the row operators.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
