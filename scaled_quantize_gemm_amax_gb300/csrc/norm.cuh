@@ -27,8 +27,7 @@ struct NormPlan {
   size_t smem;
 };
 // warp_cols: columns of a warp; block_warps: most warps of a block; params: parameter vectors kept
-// in shared memory in binary32; stage_bytes: shared memory of one warp's part of one row.  A plan whose
-// single row does not fit has smem above kNormSmem.
+// in shared memory in binary32; stage_bytes: shared memory of one warp's part of one row
 inline NormPlan norm_plan(int64_t rows, int64_t cols, int warp_cols, int block_warps, int params, int stage_bytes, int num_sms) {
   NormPlan n{};
   n.warps = static_cast<int>((cols + warp_cols - 1) / warp_cols);
@@ -38,9 +37,7 @@ inline NormPlan norm_plan(int64_t rows, int64_t cols, int warp_cols, int block_w
   const int64_t per_sm = (rows + num_sms - 1) / num_sms;
   if (n.groups > per_sm) n.groups = static_cast<int>(per_sm);
   n.ring = params * n.warps * warp_cols * 4;
-  const int64_t room = kNormSmem - n.ring;
-  while (n.groups > 1 && static_cast<int64_t>(stage_bytes) * n.warps * n.groups > room) --n.groups;
-  const int64_t stage = static_cast<int64_t>(stage_bytes) * n.warps * n.groups;
+  const int64_t room = kNormSmem - n.ring, stage = static_cast<int64_t>(stage_bytes) * n.warps * n.groups;
   const int64_t want_stages = (kNormInFlight + stage - 1) / stage;
   n.stages = static_cast<int>(want_stages < 2 ? 2 : (want_stages > kNormStages ? kNormStages : want_stages));
   if (n.stages * stage > room) n.stages = static_cast<int>(room / stage > 1 ? room / stage : 1);

@@ -7,7 +7,7 @@
 //
 // Bound by HBM: x and the residual once in, h and y (or the codes) once out.  A row stays in
 // registers between its sum and its output; the weight stays in shared memory for the whole walk.
-#include "norm.cuh"
+#include "rms.cuh"
 
 namespace fp8q {
 
@@ -16,6 +16,12 @@ namespace {
 // warps of a block at V values a lane: 80 registers a thread, 64 at 8 values
 template <int V>
 constexpr int kBlockWarps = V == 8 ? 32 : 24;
+// Bytes of a block's rows and of its stages (rms_plan).  With a residual, bf16 and 1x128 codes, 65536x4096: 64 KB 275 us,
+// 96 KB 300, two stages of 96 KB 319; 8192x4096 39.7, 39.8 and 43.5.  Unaligned rows are bound by their instructions and take
+// the warps that fit: 8192x4099 65 us with 96 KB, 73 with 64.
+template <bool VECTOR>
+constexpr int kMost = (VECTOR ? 64 : 96) * 1024;
+constexpr int kInFlight = 64 * 1024;
 constexpr int kMostCols = 16384;   // of a row held in registers, its weight in shared memory
 constexpr int kThreads = 256;
 
@@ -302,7 +308,8 @@ __global__ void __launch_bounds__(kBlockWarps<V> * 32) k_rms(const RmsParams p, 
 template <typename T, bool VECTOR, int V>
 cudaError_t run_rms(const RmsParams& p, int num_sms, cudaStream_t s) {
   const int part = RowPart<Piece<T, VECTOR>, 32 * V, VECTOR, T>::kBytes;
-  const NormPlan n = norm_plan(p.rows, p.cols, 32 * V, kBlockWarps<V>, 1, part * (p.res != nullptr ? 2 : 1), num_sms);
+  const NormPlan n = rms_plan(p.rows, p.cols, 32 * V, kBlockWarps<V>, part * (p.res != nullptr ? 2 : 1), kMost<VECTOR>, kInFlight, 1,
+                              num_sms);
   static std::atomic<bool> done[kMaxDevices];
   const cudaError_t e = ensure_smem_limit(k_rms<T, VECTOR, V>, kNormSmem, done);
   if (e != cudaSuccess) return e;

@@ -8,7 +8,7 @@
 // Bound by HBM: dy, h and dh once in, dx once out.  A thread owns the same columns for all the rows
 // of its group, so the column sums stay in registers over the whole walk; they leave as one partial
 // sum a block, added up by a second, small launch.
-#include "norm.cuh"
+#include "rms.cuh"
 
 namespace fp8q {
 
@@ -16,6 +16,11 @@ namespace {
 
 constexpr int kMostCols = 16384;   // of a row held in registers
 constexpr int kThreads = 256;
+// Bytes of a block's rows and of its stages (rms_plan): bf16 with dh, 8192x4096: 46.1 us, with twice as much 49.1; 65536x4096 308
+// and 323.  Unaligned rows are bound by their instructions and take the warps that fit: 8192x4099 90 us, with 52 KB 168.
+template <bool VECTOR>
+constexpr int kMost = (VECTOR ? 56 : 96) * 1024;
+constexpr int kInFlight = 104 * 1024;
 
 // dx of rows of any width: one block per row, two passes.
 template <typename T>
@@ -267,10 +272,10 @@ cudaError_t run_rms_backward(const RmsBwdParams& p, int num_sms, cudaStream_t s,
   const int part = RowPart<Piece<T, VECTOR>, 32 * V, VECTOR, T>::kBytes;
   const int blocks = num_sms < kMaxNormPartials ? num_sms : kMaxNormPartials;
   bool ahead = p.dh != nullptr;
-  NormPlan n = norm_plan(p.rows, p.cols, 32 * V, BLOCK_WARPS, 1, part * (ahead ? 3 : 2) + 128, blocks);
+  NormPlan n = rms_plan(p.rows, p.cols, 32 * V, BLOCK_WARPS, part * (ahead ? 3 : 2) + 128, kMost<VECTOR>, kInFlight, 2, blocks);
   if (ahead && n.smem > kNormSmem) {   // binary32 rows of over 12288 columns: three parts of a row do not fit
     ahead = false;
-    n = norm_plan(p.rows, p.cols, 32 * V, BLOCK_WARPS, 1, part * 2 + 128, blocks);
+    n = rms_plan(p.rows, p.cols, 32 * V, BLOCK_WARPS, part * 2 + 128, kMost<VECTOR>, kInFlight, 2, blocks);
   }
   const size_t join = n.ring + static_cast<size_t>(n.groups / 2) * n.warps * 32 * V * sizeof(float);
   if (n.smem < join) n.smem = join;
@@ -283,12 +288,13 @@ cudaError_t run_rms_backward(const RmsBwdParams& p, int num_sms, cudaStream_t s,
                     n.stages, n.ring, ahead);
 }
 
-// Values a lane and warps of a block: as few values as hold a narrow row, else 32; 16 warps take every row of up to
-// kMostCols columns and leave a thread 128 registers.
+// Values a lane and warps of a block: as few as hold a narrow row; 16 values leave two warps for each of a row's 1024 columns
+// (6000x5120 43.7 us, with 32 values 50.4; 8192x4096 46.1 and 46.3); 32 where 24 warps of 16 would hold one row and
+// leave its registers short (2048x12288 33.3 us, 34.1) or not hold it.
 template <typename T, bool VECTOR>
 cudaError_t run_rms_backward(const RmsBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
   if (p.cols <= 256) return run_rms_backward<T, VECTOR, 8, 24>(p, num_sms, s, partials);
-  if (p.cols <= 512) return run_rms_backward<T, VECTOR, 16, 24>(p, num_sms, s, partials);
+  if (p.cols <= 8192) return run_rms_backward<T, VECTOR, 16, 24>(p, num_sms, s, partials);
   return run_rms_backward<T, VECTOR, 32, 16>(p, num_sms, s, partials);
 }
 
