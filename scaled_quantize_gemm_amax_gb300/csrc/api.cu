@@ -1116,12 +1116,12 @@ fp8_status grouped(GroupedParams& p, const uint8_t* A, fp8_format fa, fp8_recipe
   p.sb = static_cast<const float*>(sB);
   p.loads = loads;
   p.err = d->err;
-  const int tile = grouped_tile(p, d->num_sms);
+  const int width = grouped_width(p, d->num_sms);
   GroupedMaps m;
   std::memset(&m, 0, sizeof(m));
   if (loads) {
     if (!make_map(&m.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, a_cols, a_rows, 128, 128) ||
-        !make_map(&m.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B, b_cols, b_rows, 128, 128))
+        !make_map(&m.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B, b_cols, b_rows, 128, width == 0 ? 128 : static_cast<uint32_t>(width)))
       return FP8_ERR_CUDA;
     // MX: the tiled scale buffers as rows of 256 bytes, two rows (one 512-byte atom) per box
     if (mx && (!make_map(&m.sfa, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, sA, 256, 2 * (a_rows / 128) * (a_cols / 128), 256, 2,
@@ -1130,10 +1130,12 @@ fp8_status grouped(GroupedParams& p, const uint8_t* A, fp8_format fa, fp8_recipe
                          CU_TENSOR_MAP_SWIZZLE_NONE)))
       return FP8_ERR_CUDA;
   }
-  const bool ok = p.out_fp32 ? make_map(&m.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.c, p.N, c_rows, 32, 32)
-                             : make_map(&m.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.c, p.N, c_rows, 64, 32);
+  const CUtensorMapSwizzle swizzle = width == 0 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
+  const bool ok = p.out_fp32
+                      ? make_map(&m.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.c, p.N, c_rows, 32, 32, swizzle)
+                      : make_map(&m.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.c, p.N, c_rows, width == 0 ? 64 : 32, 32, swizzle);
   if (!ok) return FP8_ERR_CUDA;
-  return cuda_status(launch_grouped(p, m, tile, d->num_sms, stream));
+  return cuda_status(launch_grouped(p, m, width, d->num_sms, stream));
 }
 
 // The kind of a pairing, among those that the grouped products take.

@@ -31,36 +31,41 @@ constexpr int kUmmaDepth = 32;         // K of one MMA of 8-bit operands
 constexpr int kEpi = 8;                // epilogue warps
 constexpr uint32_t kTmemAll = 512;
 
-// PAIR: two CTAs share a 256 x 256 tile (cta_group::2), each with its 128 rows of A and half of B's.
-// Otherwise one CTA a 128 x BN tile.
-template <int KIND, bool PAIR, int BN>
-struct GroupedLayout {
-  static constexpr bool MX = KIND == kMx;
-  static constexpr int S = 5;   // stages
-  static constexpr int ACC = MX && BN == 256 ? 1 : 2;   // accumulators; a wide MX one leaves TMEM for one and the scale factors
-  static constexpr uint32_t A_BYTES = kRows * kDepth, B_BYTES = (PAIR ? BN / 2 : BN) * kDepth;
-  static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
-  static constexpr int B_ATOMS = BN / 128;
-  static constexpr uint32_t SF = MX ? 512 * (1 + B_ATOMS) : 0;
-  static constexpr uint32_t OFF_SF = S * STAGE;
-  static constexpr uint32_t OFF_STG = (OFF_SF + S * SF + 1023) & ~1023u;   // a 4 KB box an epilogue warp
-  static constexpr uint32_t OFF_FULL = OFF_STG + kEpi * 4096, OFF_EMPTY = OFF_FULL + 8 * S, OFF_SFR = OFF_EMPTY + 8 * S;
-  static constexpr uint32_t OFF_TFULL = OFF_SFR + 8 * S, OFF_TEMPTY = OFF_TFULL + 16, OFF_FINAL = OFF_TEMPTY + 16;
-  static constexpr uint32_t OFF_TMEM = OFF_FINAL + 8, OFF_ABORT = OFF_TMEM + 4;
-  static constexpr uint32_t OFF_TABLE = OFF_ABORT + 8;   // offsets [E + 1], first tiles [E + 1]
-  static constexpr uint32_t FIXED = OFF_TABLE + 1024;    // + alignment slack
-  static constexpr uint32_t TX = (PAIR ? 2 : 1) * (STAGE + SF);   // bytes that complete a stage
-  static constexpr uint32_t SF_COL = BN * ACC;           // first TMEM column of the scale factors
-  static constexpr uint32_t SF_COLS = 4 + 4 * B_ATOMS;   // of a stage
-  static_assert(SF_COL + (MX ? S * SF_COLS : 0) <= kTmemAll, "TMEM");
-};
-constexpr uint32_t table_bytes(int n_experts) { return 8u * static_cast<uint32_t>(n_experts + 1); }
-static_assert(GroupedLayout<kTensor, true, 256>::FIXED + table_bytes(kMaxExperts) <= 232448, "shared memory");
-static_assert(GroupedLayout<kMx, true, 256>::FIXED + table_bytes(kMaxExperts) <= 232448, "shared memory");
-
-// warps: producer, MMA issuer, kEpi epilogue warps, and with MXFP8 the scale factors' copier
-template <int KIND>
-constexpr int grouped_threads() { return 32 * (2 + kEpi + (KIND == kMx ? 1 : 0)); }
+// ------------------------------------------------------------------ the list of tiles
+// The offsets checked and the experts' tiles summed up by one warp, 32 experts at a time: offs
+// [E + 1] the offsets, first [E + 1] the experts' first tiles.  Offsets that are not ascending
+// multiples of 128 within the capacity make the list empty.
+__device__ __forceinline__ void list_tiles(const GroupedParams& p, int tile_rows, int tiles_n, int* offs, int* first, int lane) {
+  bool good = true;
+  int sum = 0;
+  for (int e0 = 0; e0 <= p.n_experts; e0 += 32) {
+    const int e = e0 + lane;
+    const int64_t lo = e <= p.n_experts ? p.offsets[e] : 0, hi = e < p.n_experts ? p.offsets[e + 1] : lo;
+    const bool fine = lo >= 0 && lo <= hi && hi <= p.capacity && lo % kRows == 0 && hi % kRows == 0;
+    good = __all_sync(0xFFFFFFFFu, fine) && good;
+    const int64_t rows = p.depth ? p.M : hi - lo;
+    const int n = e < p.n_experts && fine ? static_cast<int>((rows + tile_rows - 1) / tile_rows) * tiles_n : 0;
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (e <= p.n_experts) {
+      offs[e] = static_cast<int>(lo);
+      first[e] = sum + upto - n;
+    }
+    sum += __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+  if (!good) {
+    __syncwarp();
+    for (int e = lane; e <= p.n_experts; e += 32) first[e] = 0;
+    if (lane == 0) {
+      offs[p.n_experts] = static_cast<int>(p.capacity);   // no rows behind the last segment either
+      if (blockIdx.x == 0) atomicOr(p.err, kErrBadState);
+    }
+  }
+}
 
 // One tile of the list.
 struct Tile {
@@ -69,18 +74,88 @@ struct Tile {
   int b_row, b_kb;   // the tile's first row of B and its first block
   int nkb;           // blocks
   int c_row, c_col;  // this CTA's first row of C, the tile's first column
-  bool held;         // whether this CTA's rows belong to the expert (of the last half tile, the second CTA's do not)
+  bool held;         // whether this CTA's rows belong to the expert (of a pair's last half tile, the second CTA's do not)
 };
 
-template <int KIND, bool PAIR, int BN>
+// Tile t for CTA `rank` of its unit; `e` moves on from the expert of the tile before.
+template <int TILE_ROWS>
+__device__ __forceinline__ Tile tile_of(const GroupedParams& p, const int* offs, const int* first, int tile_cols, int tiles_n, int rank,
+                                        int t, int& e) {
+  while (t >= first[e + 1]) ++e;
+  const int lo = offs[e], seg = offs[e + 1] - lo, rows = p.depth ? p.M : seg;
+  int tm, tn;
+  tile_coords<16>(t - first[e], (rows + TILE_ROWS - 1) / TILE_ROWS, tiles_n, tm, tn);
+  const int row = tm * TILE_ROWS + rank * kRows;
+  Tile w;
+  w.e = e;
+  w.held = row < rows;
+  const int from = w.held ? row : row - kRows;   // rows that are not the expert's: the peer's once more, from L2
+  w.c_col = tn * tile_cols;
+  if (p.depth) {
+    w.a_row = from;
+    w.a_kb = w.b_kb = lo / kDepth;
+    w.nkb = seg / kDepth;
+    w.b_row = w.c_col;
+    w.c_row = e * p.M + row;
+  } else {
+    w.a_row = lo + from;
+    w.a_kb = 0;
+    w.nkb = p.K / kDepth;
+    w.b_kb = p.b_cols ? e * w.nkb : 0;
+    w.b_row = (p.b_cols ? 0 : e * p.N) + w.c_col;
+    w.c_row = lo + row;
+  }
+  return w;
+}
+
+// Rows behind the last segment set to 0, by the 32 * kEpi epilogue threads of every CTA.
+__device__ __forceinline__ void zero_tail(const GroupedParams& p, int from, int thread) {
+  const int64_t row_bytes = static_cast<int64_t>(p.N) * (p.out_fp32 ? 4 : 2), total = p.capacity * row_bytes;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (32 * kEpi) * 16;
+  for (int64_t at = from * row_bytes + (static_cast<int64_t>(blockIdx.x) * (32 * kEpi) + thread) * 16; at < total; at += step)
+    FP8Q_GUARD(at, 16, total, p.err) { stg128(static_cast<uint8_t*>(p.c) + at, 0u, 0u, 0u, 0u); }
+}
+
+__host__ __device__ constexpr uint32_t table_bytes(int n_experts) { return 8u * static_cast<uint32_t>(n_experts + 1); }   // offs, first
+constexpr uint32_t kSmem = 232448;
+
+// warps: producer, MMA issuer, kEpi epilogue warps, and with MXFP8 the scale factors' copier
+template <int KIND>
+constexpr int grouped_threads() { return 32 * (2 + kEpi + (KIND == kMx ? 1 : 0)); }
+constexpr int kCopier = 2 + kEpi;
+
+// ------------------------------------------------------------------ many rows: CTA pairs
+// Two CTAs share a 256 x 256 tile (cta_group::2), each with its 128 rows of A and half of B's.
+constexpr int kPairCols = 256;
+template <int KIND>
+struct PairLayout {
+  static constexpr bool MX = KIND == kMx;
+  static constexpr int S = 5;            // stages
+  static constexpr int ACC = MX ? 1 : 2; // accumulators; MXFP8's scale factors leave TMEM for one
+  static constexpr uint32_t A_BYTES = kRows * kDepth, B_BYTES = kPairCols / 2 * kDepth, STAGE = A_BYTES + B_BYTES;
+  static constexpr int B_ATOMS = kPairCols / 128;
+  static constexpr uint32_t SF = MX ? 512 * (1 + B_ATOMS) : 0;
+  static constexpr uint32_t OFF_SF = S * STAGE;
+  static constexpr uint32_t OFF_STG = (OFF_SF + S * SF + 1023) & ~1023u;   // a 4 KB box an epilogue warp
+  static constexpr uint32_t OFF_FULL = OFF_STG + kEpi * 4096, OFF_EMPTY = OFF_FULL + 8 * S, OFF_SFR = OFF_EMPTY + 8 * S;
+  static constexpr uint32_t OFF_TFULL = OFF_SFR + 8 * S, OFF_TEMPTY = OFF_TFULL + 16, OFF_FINAL = OFF_TEMPTY + 16;
+  static constexpr uint32_t OFF_TMEM = OFF_FINAL + 8, OFF_ABORT = OFF_TMEM + 4, OFF_TABLE = OFF_ABORT + 4;
+  static constexpr uint32_t FIXED = OFF_TABLE + 1024;    // + alignment slack
+  static constexpr uint32_t TX = 2 * (STAGE + SF);       // bytes of both CTAs that complete a stage
+  static constexpr uint32_t SF_COL = kPairCols * ACC;    // first TMEM column of the scale factors
+  static constexpr uint32_t SF_COLS = 4 + 4 * B_ATOMS;   // of a stage
+  static_assert(SF_COL + (MX ? S * SF_COLS : 0) <= kTmemAll, "TMEM");
+  static_assert(FIXED + table_bytes(kMaxExperts) <= kSmem, "shared memory");
+};
+
+template <int KIND>
 __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
     k_grouped(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
               const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfb,
               const __grid_constant__ CUtensorMap tm_c, const GroupedParams p) {
-  using L = GroupedLayout<KIND, PAIR, BN>;
+  using L = PairLayout<KIND>;
   constexpr bool MX = L::MX;
-  constexpr int S = L::S, ACC = L::ACC, TM = PAIR ? 2 * kRows : kRows;
-  constexpr int kCopier = 2 + kEpi;
+  constexpr int S = L::S, ACC = L::ACC, TM = 2 * kRows, BN = kPairCols;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - smem_u32(smem_raw));
@@ -88,11 +163,10 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
   int* const offs = reinterpret_cast<int*>(base_ptr + L::OFF_TABLE);
   int* const first = offs + p.n_experts + 1;   // the experts' first tiles
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  const int unit = static_cast<int>(blockIdx.x) / (PAIR ? 2 : 1), units = static_cast<int>(gridDim.x) / (PAIR ? 2 : 1);
+  const int unit = static_cast<int>(blockIdx.x) / 2, units = static_cast<int>(gridDim.x) / 2;
   const int tiles_n = (p.N + BN - 1) / BN;
-  const bool depth = p.depth != 0;
 
   if (threadIdx.x == 0) {
     if (p.loads) {
@@ -106,87 +180,27 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(base + L::OFF_TFULL + 8 * a, 1);
-      mbar_init(base + L::OFF_TEMPTY + 8 * a, PAIR ? 2 * kEpi : kEpi);
+      mbar_init(base + L::OFF_TEMPTY + 8 * a, 2 * kEpi);
     }
     mbar_init(base + L::OFF_FINAL, MX ? 2 : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    if (PAIR) {
-      tmem_alloc_pair(base + L::OFF_TMEM, kTmemAll);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(base + L::OFF_TMEM, kTmemAll);
-      tmem_relinquish();
-    }
+    tmem_alloc_pair(base + L::OFF_TMEM, kTmemAll);
+    tmem_relinquish_pair();
   }
   pdl_wait();   // the offsets may come from the previous kernel in the stream
-  if (warp == 2) {
-    // The offsets checked and the experts' tiles summed up, 32 experts at a time.  Offsets that
-    // are not ascending multiples of 128 within the capacity make the list empty.
-    bool good = true;
-    int sum = 0;
-    for (int e0 = 0; e0 <= p.n_experts; e0 += 32) {
-      const int e = e0 + lane;
-      const int64_t lo = e <= p.n_experts ? p.offsets[e] : 0, hi = e < p.n_experts ? p.offsets[e + 1] : lo;
-      const bool fine = lo >= 0 && lo <= hi && hi <= p.capacity && lo % kRows == 0 && hi % kRows == 0;
-      good = __all_sync(0xFFFFFFFFu, fine) && good;
-      int n = e < p.n_experts && fine ? (depth ? (p.M + TM - 1) / TM : static_cast<int>((hi - lo + TM - 1) / TM)) * tiles_n : 0;
-      int before = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, before, o);
-        if (lane >= o) before += v;
-      }
-      if (e <= p.n_experts) {
-        offs[e] = static_cast<int>(lo);
-        first[e] = sum + before - n;
-      }
-      sum += __shfl_sync(0xFFFFFFFFu, before, 31);
-    }
-    if (!good) {
-      for (int e = lane; e <= p.n_experts; e += 32) first[e] = 0;
-      if (lane == 0 && blockIdx.x == 0) atomicOr(p.err, kErrBadState);
-      if (lane == 0) offs[p.n_experts] = static_cast<int>(p.capacity);   // no rows behind the last segment either
-    }
-  }
+  if (warp == 2) list_tiles(p, TM, tiles_n, offs, first, lane);
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync();   // the peer's barriers are initialised before anyone signals them
+  cluster_sync();   // the peer's barriers are initialised before anyone signals them
   tc_fence_after();
   pdl_launch_dependents();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base_ptr + L::OFF_TMEM);
   const int ntiles = first[p.n_experts];
 
-  // Tile t; `e` moves on from the expert of the tile before.
-  auto tile_at = [&](int t, int& e) -> Tile {
-    while (t >= first[e + 1]) ++e;
-    const int lo = offs[e], rows = offs[e + 1] - lo, tiles_m = depth ? (p.M + TM - 1) / TM : (rows + TM - 1) / TM;
-    int tm, tn;
-    tile_coords<16>(t - first[e], tiles_m, tiles_n, tm, tn);
-    const int row = tm * TM + static_cast<int>(rank) * kRows;
-    Tile w;
-    w.e = e;
-    w.held = row < (depth ? p.M : rows);
-    const int from = w.held ? row : row - kRows;   // rows that are not the expert's: the peer's once more, from L2
-    w.c_col = tn * BN;
-    if (depth) {
-      w.a_row = from;
-      w.a_kb = w.b_kb = lo / kDepth;
-      w.nkb = rows / kDepth;
-      w.b_row = tn * BN;
-      w.c_row = e * p.M + row;
-    } else {
-      w.a_row = lo + from;
-      w.a_kb = 0;
-      w.nkb = p.K / kDepth;
-      w.b_kb = p.b_cols ? e * w.nkb : 0;
-      w.b_row = (p.b_cols ? 0 : e * p.N) + tn * BN;
-      w.c_row = lo + row;
-    }
-    return w;
-  };
+  auto tile_at = [&](int t, int& e) { return tile_of<TM>(p, offs, first, BN, tiles_n, static_cast<int>(rank), t, e); };
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------ producer
@@ -202,27 +216,20 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
           ok = false;
           break;
         }
-        const uint32_t full = base + L::OFF_FULL + 8 * stage, sig = PAIR ? mapa_shared(full, 0) : full;
+        const uint32_t full = base + L::OFF_FULL + 8 * stage, sig = mapa_shared(full, 0);
         const uint32_t sa = base + stage * L::STAGE, sf = base + L::OFF_SF + stage * L::SF;
         const int ak = w.a_kb + kb, bk = w.b_kb + kb;
         if (leader) mbar_arrive_expect_tx(full, L::TX);
-        if (PAIR) {
-          tma_load_2d_pair(sa, &tm_a, ak * kDepth, w.a_row, sig);
-          tma_load_2d_pair(sa + L::A_BYTES, &tm_b, bk * kDepth, w.b_row + static_cast<int>(rank) * (BN / 2), sig);
-        } else {
-          tma_load_2d(sa, &tm_a, ak * kDepth, w.a_row, sig);
-          tma_load_2d(sa + L::A_BYTES, &tm_b, bk * kDepth, w.b_row, sig);
-        }
+        tma_load_2d_pair(sa, &tm_a, ak * kDepth, w.a_row, sig);
+        tma_load_2d_pair(sa + L::A_BYTES, &tm_b, bk * kDepth, w.b_row + static_cast<int>(rank) * (BN / 2), sig);
         if (MX) {
           const int atom_a = w.a_row / kRows * a_atoms + ak;
-          if (PAIR) tma_load_2d_pair(sf, &tm_sfa, 0, 2 * atom_a, sig);
-          else tma_load_2d(sf, &tm_sfa, 0, 2 * atom_a, sig);
+          tma_load_2d_pair(sf, &tm_sfa, 0, 2 * atom_a, sig);
 #pragma unroll
           for (int h = 0; h < L::B_ATOMS; ++h) {
             // a tile that hangs over B's last row takes its last atoms (those columns are not stored)
             const int atom_b = min(w.b_row / kRows + h, b_last) * b_atoms + bk;
-            if (PAIR) tma_load_2d_pair(sf + 512 + 512 * h, &tm_sfb, 0, 2 * atom_b, sig);
-            else tma_load_2d(sf + 512 + 512 * h, &tm_sfb, 0, 2 * atom_b, sig);
+            tma_load_2d_pair(sf + 512 + 512 * h, &tm_sfb, 0, 2 * atom_b, sig);
           }
         }
         ++issued;
@@ -233,14 +240,10 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
       }
     }
     // this CTA's loads land before it exits: awaited through the stages' release by the MMAs that
-    // follow them (a pair's land on the leader's barrier)
+    // follow them (they land on the leader's barrier)
     for (int s = 0; s < S; ++s) {
       const int n = issued / S + (s < issued % S ? 1 : 0);
-      if (n == 0) continue;
-      if (PAIR)
-        mbar_wait(base + L::OFF_EMPTY + 8 * s, static_cast<uint32_t>(n - 1) & 1u, p.err, kErrTimeoutStage, abort_flag);
-      else
-        mbar_wait(base + L::OFF_FULL + 8 * s, static_cast<uint32_t>(n - 1) & 1u, p.err, kErrTimeoutTmaLoad, nullptr);
+      if (n > 0) mbar_wait(base + L::OFF_EMPTY + 8 * s, static_cast<uint32_t>(n - 1) & 1u, p.err, kErrTimeoutStage, abort_flag);
     }
   } else if ((warp == 1 || (MX && warp == kCopier)) && lane == 0 && !leader) {
     // ------------------------------------------------ the peer issues no MMAs: it waits for the leader's last
@@ -262,29 +265,23 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
         const uint32_t sf = base + L::OFF_SF + stage * L::SF, col = tmem + L::SF_COL + static_cast<uint32_t>(stage) * L::SF_COLS;
 #pragma unroll
         for (int h = 0; h <= L::B_ATOMS; ++h) {
-          if (PAIR) tc_cp_32x128b_warpx4_pair(col + 4 * h, sdesc_rows16(sf + 512 * h));
-          else tc_cp_32x128b_warpx4(col + 4 * h, sdesc_rows16(sf + 512 * h));
+          tc_cp_32x128b_warpx4_pair(col + 4 * h, sdesc_rows16(sf + 512 * h));
         }
-        if (PAIR) tc_commit_pair_mc(base + L::OFF_SFR + 8 * stage, 1);
-        else tc_commit(base + L::OFF_SFR + 8 * stage);
+        tc_commit_pair_mc(base + L::OFF_SFR + 8 * stage, 1);
         if (++stage == S) {
           stage = 0;
           phase ^= 1u;
         }
       }
     }
-    if (PAIR) tc_commit_pair_mc(base + L::OFF_FINAL, 3);
-    else tc_commit(base + L::OFF_FINAL);
+    tc_commit_pair_mc(base + L::OFF_FINAL, 3);
     mbar_wait(base + L::OFF_FINAL, 0, p.err, kErrTimeoutMma, nullptr);
   } else if (warp == 1 && lane == 0) {
     // ------------------------------------------------ MMA issuer (leader)
     const uint32_t shape = (static_cast<uint32_t>(p.e5m2_a) << 7) | (static_cast<uint32_t>(p.e5m2_b) << 10) |
                            (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
     const uint32_t idesc = shape | (MX ? 1u << 23 : 1u << 4);
-    auto commit = [&](uint32_t bar) {
-      if (PAIR) tc_commit_pair_mc(bar, 3);
-      else tc_commit(bar);
-    };
+    auto commit = [&](uint32_t bar) { tc_commit_pair_mc(bar, 3); };
     int stage = 0, e = 0;
     uint32_t phase = 0, acc_it = 0;
     bool ok = true;
@@ -293,9 +290,7 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
       if (w.nkb == 0) continue;   // the epilogue stores 0 without an accumulator
       const uint32_t a = acc_it % ACC, parity = ((acc_it / ACC) & 1u) ^ 1u;
       const uint32_t bar = base + L::OFF_TEMPTY + 8 * a;
-      if (!(PAIR ? mbar_wait_cluster(bar, parity, p.err, kErrTimeoutMma, abort_flag)
-                 : mbar_wait(bar, parity, p.err, kErrTimeoutMma, abort_flag)))
-        break;
+      if (!mbar_wait_cluster(bar, parity, p.err, kErrTimeoutMma, abort_flag)) break;
       tc_fence_after();
       const uint32_t d = tmem + a * BN;
       for (int kb = 0; kb < w.nkb; ++kb) {
@@ -313,11 +308,9 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
           const uint32_t more = (kb | k) != 0 ? 1u : 0u;
           if (MX) {
             const uint32_t id = idesc | (static_cast<uint32_t>(k) << 4) | (static_cast<uint32_t>(k) << 29);
-            if (PAIR) tc_mma_mxf8f6f4_pair(d, da, db, id, sfa, sfb, more);
-            else tc_mma_mxf8f6f4(d, da, db, id, sfa, sfb, more);
+            tc_mma_mxf8f6f4_pair(d, da, db, id, sfa, sfb, more);
           } else {
-            if (PAIR) tc_mma_f8f6f4_pair(d, da, db, idesc, more);
-            else tc_mma_f8f6f4(d, da, db, idesc, more);
+            tc_mma_f8f6f4_pair(d, da, db, idesc, more);
           }
         }
         commit(base + L::OFF_EMPTY + 8 * stage);
@@ -375,101 +368,367 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
     for (int t = unit; t < ntiles; t += units) {
       const Tile w = tile_at(t, e);
       const int col = w.c_col + h * COLS, row = w.c_row + 32 * q;
-      uint32_t r[CH][32];
       if (w.nkb > 0) {
-        const uint32_t a = acc_it % ACC;
         // warp-uniform decision: the TMEM loads that follow are .sync.aligned
-        if (!__all_sync(0xFFFFFFFFu,
-                        mbar_wait(base + L::OFF_TFULL + 8 * a, (acc_it / ACC) & 1u, p.err, kErrTimeoutMma, abort_flag)))
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(base + L::OFF_TFULL + 8 * (acc_it % ACC), (acc_it / ACC) & 1u, p.err, kErrTimeoutMma,
+                                               abort_flag)))
           break;
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < CH; ++c) tc_ld_32x32b_x32(lane_base + a * BN + h * COLS + 32 * c, r[c]);
-#pragma unroll
-        for (int c = 0; c < CH; ++c) tc_wait_ld(r[c]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {   // the accumulator goes back before its values are stored
-          const uint32_t bar = base + L::OFF_TEMPTY + 8 * a;
-          if (PAIR && !leader) mbar_arrive_remote(mapa_shared(bar, 0));
-          else mbar_arrive(bar);
-        }
-        ++acc_it;
-      } else {
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[c][j] = 0u;
       }
-      if (!w.held) continue;
+      // A lone accumulator goes back before its values are stored, so all of them wait in registers;
+      // one of two can take its time and the registers of half of them.
+      constexpr int HOLD = ACC == 1 ? CH : CH / 2;
       float scale = 1.0f;
       if (!MX && w.nkb > 0) scale = __fmul_rn(*p.sa, p.sb[p.sb_step * w.e]);
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        if (col + 32 * (c & ~1) >= p.N) break;   // N is a multiple of 128, a pair of chunks inside or outside
-        float v[32];
+      for (int c0 = 0; c0 < CH; c0 += HOLD) {
+        uint32_t r[HOLD][32];
+        if (w.nkb > 0) {
+          const uint32_t a = acc_it % ACC;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = MX ? __uint_as_float(r[c][j]) : __fmul_rn(__uint_as_float(r[c][j]), scale);
-        store_chunk(v, c, col, row);
+          for (int c = 0; c < HOLD; ++c) tc_ld_32x32b_x32(lane_base + a * BN + h * COLS + 32 * (c0 + c), r[c]);
+#pragma unroll
+          for (int c = 0; c < HOLD; ++c) tc_wait_ld(r[c]);
+          if (c0 + HOLD == CH) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              const uint32_t bar = base + L::OFF_TEMPTY + 8 * a;
+              if (!leader) mbar_arrive_remote(mapa_shared(bar, 0));
+              else mbar_arrive(bar);
+            }
+            ++acc_it;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < HOLD; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[c][j] = 0u;
+        }
+        if (!w.held) continue;
+#pragma unroll
+        for (int c = 0; c < HOLD; ++c) {
+          if (col + 32 * ((c0 + c) & ~1) >= p.N) break;   // N is a multiple of 128, a pair of chunks inside or outside
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = MX ? __uint_as_float(r[c][j]) : __fmul_rn(__uint_as_float(r[c][j]), scale);
+          store_chunk(v, c0 + c, col, row);
+        }
       }
     }
-    if (p.zero_tail && !depth) {
-      // rows behind the last segment
-      const int64_t row_bytes = static_cast<int64_t>(p.N) * (fp32 ? 4 : 2), total = p.capacity * row_bytes;
-      const int64_t step = static_cast<int64_t>(gridDim.x) * (32 * kEpi) * 16;
-      for (int64_t at = offs[p.n_experts] * row_bytes + (static_cast<int64_t>(blockIdx.x) * (32 * kEpi) + threadIdx.x - 64) * 16;
-           at < total; at += step)
-        FP8Q_GUARD(at, 16, total, p.err) { stg128(static_cast<uint8_t*>(p.c) + at, 0u, 0u, 0u, 0u); }
-    }
+    if (p.zero_tail) zero_tail(p, offs[p.n_experts], static_cast<int>(threadIdx.x) - 64);
     if (lane == 0) bulk_wait_all<0>();   // this warp's stores have finished
   }
 
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync();   // no CTA leaves while its peer may still signal its barriers
+  cluster_sync();   // no CTA leaves while its peer may still signal its barriers
   if (warp == 1) {
     tc_fence_after();
-    if (PAIR) tmem_dealloc_pair(tmem, kTmemAll);
-    else tmem_dealloc(tmem, kTmemAll);
+    tmem_dealloc_pair(tmem, kTmemAll);
   }
 }
 
-template <int KIND, bool PAIR, int BN>
-cudaError_t run_grouped(const GroupedParams& p, const GroupedMaps& m, int64_t tiles, int num_sms, cudaStream_t s) {
-  using L = GroupedLayout<KIND, PAIR, BN>;
-  auto kern = k_grouped<KIND, PAIR, BN>;
-  static std::atomic<bool> attr_done[kMaxDevices] = {};
-  cudaError_t e = ensure_smem_limit(kern, static_cast<int>(L::FIXED + table_bytes(kMaxExperts)), attr_done);
-  if (e != cudaSuccess) return e;
-  const size_t smem = L::FIXED + table_bytes(p.n_experts);
-  int64_t units = num_sms;
-  if (PAIR) {
-    // resident pairs, queried once per device
-    static std::atomic<int> resident[kMaxDevices] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (resident[dev].load(std::memory_order_relaxed) == 0) {
-      cudaLaunchConfig_t cfg = {};
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.gridDim = dim3(static_cast<unsigned>(num_sms / 2 * 2));
-      cfg.blockDim = dim3(grouped_threads<KIND>());
-      cfg.dynamicSmemBytes = L::FIXED + table_bytes(kMaxExperts);
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) n = num_sms / 2;
-      resident[dev].store(n < num_sms / 2 ? n : num_sms / 2, std::memory_order_relaxed);
-    }
-    units = resident[dev].load(std::memory_order_relaxed);
+// ------------------------------------------------------------------ few rows: one CTA a tile
+// With few tiles the product is bound by streaming the experts' weights once, by every SM: a CTA takes a
+// 128 x width tile, and the host picks the width for which the tiles divide evenly: a multiple of 32, with MXFP8 of
+// 64, since a tile's scale factors then start at an even column of TMEM.
+struct FewLayout {
+  static constexpr uint32_t A_BYTES = kRows * kDepth;
+  static constexpr int MAX_S = 8, SF_ATOMS = 3;          // A's atom and up to two of B's, of a stage
+  static constexpr uint32_t OFF_STG = 0;                 // a 4 KB box an epilogue warp
+  static constexpr uint32_t OFF_SF = kEpi * 4096, OFF_FULL = OFF_SF + MAX_S * SF_ATOMS * 512, OFF_EMPTY = OFF_FULL + 8 * MAX_S;
+  static constexpr uint32_t OFF_SFR = OFF_EMPTY + 8 * MAX_S, OFF_TFULL = OFF_SFR + 8 * MAX_S, OFF_TEMPTY = OFF_TFULL + 16;
+  static constexpr uint32_t OFF_FINAL = OFF_TEMPTY + 16, OFF_TMEM = OFF_FINAL + 8, OFF_ABORT = OFF_TMEM + 4;
+  static constexpr uint32_t OFF_TABLE = OFF_ABORT + 4;   // and behind it, on 1024 bytes, the stages
+  static constexpr uint32_t SF_COL = 384, SF_COLS = 12;  // TMEM with MXFP8: accumulators below, scale factors from there on
+  static_assert(SF_COL + MAX_S * SF_COLS <= kTmemAll, "TMEM");
+  __host__ __device__ static constexpr int accumulators(bool mx, int width) { return 2 * width <= static_cast<int>(mx ? SF_COL : kTmemAll) ? 2 : 1; }
+  __host__ __device__ static constexpr uint32_t stages_at(int n_experts) { return (OFF_TABLE + table_bytes(n_experts) + 1023) & ~1023u; }
+  __host__ __device__ static constexpr uint32_t stage_bytes(int width) { return A_BYTES + static_cast<uint32_t>(width) * kDepth; }
+  static int stages(int width, int n_experts) {
+    const uint32_t n = (kSmem - 1024 - stages_at(n_experts)) / stage_bytes(width);
+    return static_cast<int>(n < MAX_S ? n : MAX_S);
   }
-  if (tiles < units) units = tiles;
-  if (units < 1) units = 1;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(units * (PAIR ? 2 : 1))), dim3(grouped_threads<KIND>()), smem, s, PAIR ? 2 : 1,
-                    m.a, m.b, m.sfa, m.sfb, m.c, p);
+};
+
+template <int KIND>
+__global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
+    k_grouped_few(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                  const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfb,
+                  const __grid_constant__ CUtensorMap tm_c, const GroupedParams p, const int width, const int S) {
+  using L = FewLayout;
+  constexpr bool MX = KIND == kMx;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - smem_u32(smem_raw));
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(base_ptr + L::OFF_ABORT);
+  int* const offs = reinterpret_cast<int*>(base_ptr + L::OFF_TABLE);
+  int* const first = offs + p.n_experts + 1;
+  const uint32_t stages = base + L::stages_at(p.n_experts), stage_bytes = L::stage_bytes(width);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int unit = static_cast<int>(blockIdx.x), units = static_cast<int>(gridDim.x);
+  const int tiles_n = (p.N + width - 1) / width, ACC = L::accumulators(MX, width);
+
+  if (threadIdx.x == 0) {
+    if (p.loads) {
+      prefetch_tmap(&tm_a);
+      prefetch_tmap(&tm_b);
+    }
+    for (int s = 0; s < S; ++s) {
+      mbar_init(base + L::OFF_FULL + 8 * s, 1);
+      mbar_init(base + L::OFF_EMPTY + 8 * s, 1);
+      mbar_init(base + L::OFF_SFR + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(base + L::OFF_TFULL + 8 * a, 1);
+      mbar_init(base + L::OFF_TEMPTY + 8 * a, kEpi);
+    }
+    mbar_init(base + L::OFF_FINAL, MX ? 2 : 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(base + L::OFF_TMEM, kTmemAll);
+    tmem_relinquish();
+  }
+  pdl_wait();   // the offsets may come from the previous kernel in the stream
+  if (warp == 2) list_tiles(p, kRows, tiles_n, offs, first, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base_ptr + L::OFF_TMEM);
+  const int ntiles = first[p.n_experts];
+  auto tile_at = [&](int t, int& e) { return tile_of<kRows>(p, offs, first, width, tiles_n, 0, t, e); };
+  auto next = [&](int& stage, uint32_t& phase) {
+    if (++stage == S) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  };
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------ producer
+    int issued = 0, stage = 0, e = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const int a_atoms = p.a_cols / kDepth, b_atoms = p.b_cols_all / kDepth, b_last = p.b_rows_all / kRows - 1;
+    for (int t = unit; t < ntiles && ok; t += units) {
+      const Tile w = tile_at(t, e);
+      // atoms of B's scales: 128 rows each, from the one that holds the tile's first row
+      const int atom = w.b_row / kRows, n_atoms = (w.b_row % kRows + width + kRows - 1) / kRows;
+      const uint32_t tx = stage_bytes + (MX ? 512u * static_cast<uint32_t>(1 + n_atoms) : 0u);
+      for (int kb = 0; kb < w.nkb; ++kb) {
+        if (!mbar_wait(base + L::OFF_EMPTY + 8 * stage, phase ^ 1u, p.err, kErrTimeoutStage, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t full = base + L::OFF_FULL + 8 * stage, sa = stages + stage * stage_bytes;
+        const int ak = w.a_kb + kb, bk = w.b_kb + kb;
+        mbar_arrive_expect_tx(full, tx);
+        tma_load_2d(sa + L::A_BYTES, &tm_b, bk * kDepth, w.b_row, full);
+        tma_load_2d(sa, &tm_a, ak * kDepth, w.a_row, full);
+        if (MX) {
+          const uint32_t sf = base + L::OFF_SF + static_cast<uint32_t>(stage) * (L::SF_ATOMS * 512);
+          tma_load_2d(sf, &tm_sfa, 0, 2 * (w.a_row / kRows * a_atoms + ak), full);
+          for (int h = 0; h < n_atoms; ++h)   // past B's last row: its last atoms (those columns are not stored)
+            tma_load_2d(sf + 512 + 512 * h, &tm_sfb, 0, 2 * (min(atom + h, b_last) * b_atoms + bk), full);
+        }
+        ++issued;
+        next(stage, phase);
+      }
+    }
+    // the loads land before the CTA exits
+    for (int s = 0; s < S; ++s) {
+      const int n = issued / S + (s < issued % S ? 1 : 0);
+      if (n > 0) mbar_wait(base + L::OFF_FULL + 8 * s, static_cast<uint32_t>(n - 1) & 1u, p.err, kErrTimeoutTmaLoad, nullptr);
+    }
+  } else if (MX && warp == kCopier && lane == 0) {
+    // ------------------------------------------------ scale factors into TMEM
+    int stage = 0, e = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = unit; t < ntiles && ok; t += units) {
+      const Tile w = tile_at(t, e);
+      const int n_atoms = (w.b_row % kRows + width + kRows - 1) / kRows;
+      for (int kb = 0; kb < w.nkb; ++kb) {
+        if (!mbar_wait(base + L::OFF_FULL + 8 * stage, phase, p.err, kErrTimeoutTmaLoad, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // the stage's columns were last read by MMAs that finished before the stage was refilled
+        const uint32_t sf = base + L::OFF_SF + static_cast<uint32_t>(stage) * (L::SF_ATOMS * 512);
+        const uint32_t col = tmem + L::SF_COL + static_cast<uint32_t>(stage) * L::SF_COLS;
+        for (int h = 0; h <= n_atoms; ++h) tc_cp_32x128b_warpx4(col + 4 * h, sdesc_rows16(sf + 512 * h));
+        tc_commit(base + L::OFF_SFR + 8 * stage);
+        next(stage, phase);
+      }
+    }
+    tc_commit(base + L::OFF_FINAL);
+    mbar_wait(base + L::OFF_FINAL, 0, p.err, kErrTimeoutMma, nullptr);
+  } else if (warp == 1 && lane == 0) {
+    // ------------------------------------------------ MMA issuer
+    const uint32_t idesc = (static_cast<uint32_t>(p.e5m2_a) << 7) | (static_cast<uint32_t>(p.e5m2_b) << 10) |
+                           (static_cast<uint32_t>(width >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24) |
+                           (MX ? 1u << 23 : 1u << 4);
+    int stage = 0, e = 0;
+    uint32_t phase = 0, acc_it = 0;
+    bool ok = true;
+    for (int t = unit; t < ntiles && ok; t += units) {
+      const Tile w = tile_at(t, e);
+      if (w.nkb == 0) continue;   // the epilogue stores 0 without an accumulator
+      const uint32_t a = ACC == 2 ? acc_it & 1u : 0u, use = ACC == 2 ? acc_it >> 1 : acc_it;
+      if (!mbar_wait(base + L::OFF_TEMPTY + 8 * a, (use & 1u) ^ 1u, p.err, kErrTimeoutMma, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + a * static_cast<uint32_t>(width);
+      for (int kb = 0; kb < w.nkb; ++kb) {
+        // MXFP8: the copier's signal stands for the stage's data too
+        if (!mbar_wait(base + (MX ? L::OFF_SFR : L::OFF_FULL) + 8 * stage, phase, p.err, kErrTimeoutTmaLoad, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sa = stages + stage * stage_bytes, sb = sa + L::A_BYTES;
+        // B's first row may be the middle one of its first atom: 32 rows are one column of scale factors
+        const uint32_t sfa = tmem + L::SF_COL + static_cast<uint32_t>(stage) * L::SF_COLS;
+        const uint32_t sfb = sfa + 4 + static_cast<uint32_t>(w.b_row % kRows / 32);
+#pragma unroll
+        for (int k = 0; k < kDepth / kUmmaDepth; ++k) {
+          const uint64_t da = sdesc_k_sw128(sa + k * kUmmaDepth), db = sdesc_k_sw128(sb + k * kUmmaDepth);
+          const uint32_t more = (kb | k) != 0 ? 1u : 0u;
+          if (MX)
+            tc_mma_mxf8f6f4(d, da, db, idesc | (static_cast<uint32_t>(k) << 4) | (static_cast<uint32_t>(k) << 29), sfa, sfb, more);
+          else
+            tc_mma_f8f6f4(d, da, db, idesc, more);
+        }
+        tc_commit(base + L::OFF_EMPTY + 8 * stage);
+        next(stage, phase);
+      }
+      if (!ok) break;
+      tc_commit(base + L::OFF_TFULL + 8 * a);
+      ++acc_it;
+    }
+    tc_commit(base + L::OFF_FINAL);   // every MMA has finished before TMEM is released
+    mbar_wait(base + L::OFF_FINAL, 0, p.err, kErrTimeoutMma, nullptr);
+  } else if (warp >= 2 && warp < 2 + kEpi) {
+    // ------------------------------------------------ epilogue
+    const int q = warp & 3, h = (warp - 2) >> 2;   // TMEM lane quarter; chunks h, h + 2, ... of 32 columns
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const uint32_t stg = base + L::OFF_STG + static_cast<uint32_t>(warp - 2) * 4096u;
+    const bool fp32 = p.out_fp32 != 0;
+    uint32_t acc_it = 0;
+    int e = 0;
+    for (int t = unit; t < ntiles; t += units) {
+      const Tile w = tile_at(t, e);
+      const uint32_t a = ACC == 2 ? acc_it & 1u : 0u, use = ACC == 2 ? acc_it >> 1 : acc_it;
+      const int chunks = min(width, p.N - w.c_col) / 32;   // N and the width are multiples of 32
+      float scale = 1.0f;
+      if (w.nkb > 0) {
+        if (!MX) scale = __fmul_rn(*p.sa, p.sb[p.sb_step * w.e]);
+        // warp-uniform decision: the TMEM loads that follow are .sync.aligned
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(base + L::OFF_TFULL + 8 * a, use & 1u, p.err, kErrTimeoutMma, abort_flag))) break;
+        tc_fence_after();
+      }
+      for (int c = h; c < chunks; c += 2) {
+        uint32_t r[32];
+        if (w.nkb > 0) {
+          tc_ld_32x32b_x32(lane_base + a * static_cast<uint32_t>(width) + 32 * c, r);
+          tc_wait_ld(r);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = 0u;
+        }
+        // this warp's 32 rows x 32 columns staged for one TMA store, rows of 64 (bf16) or 128 bytes
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = MX ? __uint_as_float(r[j]) : __fmul_rn(__uint_as_float(r[j]), scale);
+        if (lane == 0) bulk_wait_read<0>();   // the box's previous store has read it
+        __syncwarp();
+        if (fp32) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            sts128(stg + static_cast<uint32_t>(lane) * 128u + 16 * k, __float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]),
+                   __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            sts128(stg + static_cast<uint32_t>(lane) * 64u + 16 * k, pack_bf16(v[8 * k], v[8 * k + 1]),
+                   pack_bf16(v[8 * k + 2], v[8 * k + 3]), pack_bf16(v[8 * k + 4], v[8 * k + 5]), pack_bf16(v[8 * k + 6], v[8 * k + 7]));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&tm_c, stg, w.c_col + 32 * c, w.c_row + 32 * q);
+          bulk_commit();
+        }
+      }
+      if (w.nkb > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(base + L::OFF_TEMPTY + 8 * a);
+        ++acc_it;
+      }
+    }
+    if (p.zero_tail) zero_tail(p, offs[p.n_experts], static_cast<int>(threadIdx.x) - 64);
+    if (lane == 0) bulk_wait_all<0>();   // this warp's stores have finished
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemAll);
+  }
+}
+
+// ------------------------------------------------------------------ launches
+template <int KIND>
+cudaError_t run_pairs(const GroupedParams& p, const GroupedMaps& m, int64_t tiles, int num_sms, cudaStream_t s) {
+  using L = PairLayout<KIND>;
+  constexpr int kMostSmem = static_cast<int>(L::FIXED + table_bytes(kMaxExperts));
+  auto kern = k_grouped<KIND>;
+  static std::atomic<bool> attr_done[kMaxDevices] = {};
+  cudaError_t e = ensure_smem_limit(kern, kMostSmem, attr_done);
+  if (e != cudaSuccess) return e;
+  // resident pairs, queried once per device
+  static std::atomic<int> resident[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (resident[dev].load(std::memory_order_relaxed) == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms / 2 * 2));
+    cfg.blockDim = dim3(grouped_threads<KIND>());
+    cfg.dynamicSmemBytes = kMostSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) n = num_sms / 2;
+    resident[dev].store(n < num_sms / 2 ? n : num_sms / 2, std::memory_order_relaxed);
+  }
+  int64_t pairs = resident[dev].load(std::memory_order_relaxed);
+  if (tiles < pairs) pairs = tiles < 1 ? 1 : tiles;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(grouped_threads<KIND>()), L::FIXED + table_bytes(p.n_experts), s,
+                    2, m.a, m.b, m.sfa, m.sfb, m.c, p);
+}
+
+template <int KIND>
+cudaError_t run_few(const GroupedParams& p, const GroupedMaps& m, int width, int64_t tiles, int num_sms, cudaStream_t s) {
+  auto kern = k_grouped_few<KIND>;
+  static std::atomic<bool> attr_done[kMaxDevices] = {};
+  const cudaError_t e = ensure_smem_limit(kern, static_cast<int>(kSmem), attr_done);
+  if (e != cudaSuccess) return e;
+  const int stages = FewLayout::stages(width, p.n_experts);
+  const size_t smem = FewLayout::stages_at(p.n_experts) + static_cast<size_t>(stages) * FewLayout::stage_bytes(width) + 1024;
+  const int64_t units = tiles < num_sms ? (tiles < 1 ? 1 : tiles) : num_sms;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(units)), dim3(grouped_threads<KIND>()), smem, s, 1, m.a, m.b, m.sfa, m.sfb, m.c, p,
+                    width, stages);
 }
 
 // the most tiles that a call can have, whatever its offsets are
@@ -483,19 +742,49 @@ int64_t most_tiles(const GroupedParams& p, int tile_rows, int tile_cols) {
 
 }  // namespace
 
-// CTA pairs halve what the tensor core reads of B from shared memory; with fewer than two tiles a pair
-// the smaller tiles spread the work over more SMs (one token at 2 experts, 4096 -> 11008: 28.9 us
-// against 33.3; 8192 tokens: 747 against 537).
-int grouped_tile(const GroupedParams& p, int num_sms) { return most_tiles(p, 2 * kRows, 256) < num_sms ? 128 : 256; }
-
-cudaError_t launch_grouped(const GroupedParams& p, const GroupedMaps& m, int tile, int num_sms, cudaStream_t s) {
-  const bool mx = p.kind == kMx;
-  if (tile == 256) {
-    const int64_t tiles = most_tiles(p, 2 * kRows, 256);
-    return mx ? run_grouped<kMx, true, 256>(p, m, tiles, num_sms, s) : run_grouped<kTensor, true, 256>(p, m, tiles, num_sms, s);
+// The tile width of a call: 0 for CTA pairs, else that of one CTA's 128-row tiles: what takes the fewest cycles a
+// 128-deep block, rounds of tiles times a tile's.  A pair's tile is bound by its four MMAs (~175 each); a tile of
+// one CTA by what it fetches, A's 128 rows and its width of B's at 48 bytes a cycle, and where TMEM holds one
+// accumulator, by a seventh more.  One segment of 128 rows each (us, pairs | one CTA at the best width and at 128;
+// MXFP8, K = 4096): 2 x 11008 columns 32.5 | 22.2, 29.1; 8 x 11008 78 | 72, 72; 16 x 4096 63 | 57, 58.  Segments of 256:
+// 16 x 4096 65 | 78, 82; of 384: 3 x 4096 29.5 | 23.6, 25.7; one of 1024, 4096 columns 17.3 | 21.9, 24.9.
+int grouped_width(const GroupedParams& p, int num_sms) {
+  int64_t blocks, pairs;   // tiles of 128 and of 256 rows, for each of tile columns
+  if (p.depth) {
+    blocks = static_cast<int64_t>(p.n_experts) * (p.M / kRows);
+    pairs = static_cast<int64_t>(p.n_experts) * ((p.M / kRows + 1) / 2);
+  } else {
+    // the capacity has room for 127 rows of padding an expert, of which half are expected; so are as many odd
+    // segments as even ones
+    const int64_t room = p.capacity / kRows, used = p.n_experts < room ? p.n_experts : room;
+    blocks = room - (room - used < used / 2 ? room - used : used / 2);
+    pairs = (blocks + used / 2) / 2 > used ? (blocks + used / 2) / 2 : used;
   }
-  const int64_t tiles = most_tiles(p, kRows, tile);
-  return mx ? run_grouped<kMx, false, 128>(p, m, tiles, num_sms, s) : run_grouped<kTensor, false, 128>(p, m, tiles, num_sms, s);
+  auto rounds = [&](int64_t tiles, int cols, int units) { return (tiles * ((p.N + cols - 1) / cols) + units - 1) / units; };
+  const bool mx = p.kind == kMx;
+  int best = 0;
+  int64_t least = rounds(pairs, kPairCols, num_sms < 2 ? 1 : num_sms / 2) * 700;
+  const int step = mx ? 64 : 32;
+  for (int width = step; width <= 256; width += step) {
+    const int64_t n = rounds(blocks, width, num_sms);
+    int64_t cost = n * (width + kRows) * 8 / 3;
+    if (n > 1 && FewLayout::accumulators(mx, width) == 1) cost += cost / 7;
+    if (cost < least) {
+      least = cost;
+      best = width;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_grouped(const GroupedParams& p, const GroupedMaps& m, int width, int num_sms, cudaStream_t s) {
+  const bool mx = p.kind == kMx;
+  if (width == 0) {
+    const int64_t tiles = most_tiles(p, 2 * kRows, kPairCols);
+    return mx ? run_pairs<kMx>(p, m, tiles, num_sms, s) : run_pairs<kTensor>(p, m, tiles, num_sms, s);
+  }
+  const int64_t tiles = most_tiles(p, kRows, width);
+  return mx ? run_few<kMx>(p, m, width, tiles, num_sms, s) : run_few<kTensor>(p, m, width, tiles, num_sms, s);
 }
 
 }  // namespace fp8q

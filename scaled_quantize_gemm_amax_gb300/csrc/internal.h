@@ -423,9 +423,10 @@ struct GroupedParams {
 struct GroupedMaps {
   CUtensorMap a, b, sfa, sfb, c;
 };
-// Columns of a tile of the kernel that a call takes: 256 (CTA pairs) or 128.  Boxes of A and B have 128 rows.
-int grouped_tile(const GroupedParams& p, int num_sms);
-cudaError_t launch_grouped(const GroupedParams& p, const GroupedMaps& m, int tile, int num_sms, cudaStream_t s);
+// Columns of a CTA's tile, 0 for CTA pairs.  Boxes have 128 rows of A; 128 of B for pairs, else the width; of C 32 rows,
+// swizzled 128 bytes of them for pairs, else 32 plain columns.
+int grouped_width(const GroupedParams& p, int num_sms);
+cudaError_t launch_grouped(const GroupedParams& p, const GroupedMaps& m, int width, int num_sms, cudaStream_t s);
 
 // Bounded-wait self test: one CTA waits on an mbarrier nothing arrives on.
 cudaError_t launch_wait_selftest(uint32_t* err, cudaStream_t s);

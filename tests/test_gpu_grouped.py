@@ -35,7 +35,8 @@ SHAPES = [  # blocks of 128 rows an expert, blocks before and behind, N, K
     ([1], 0, 0, 128, 128), ([2, 1, 3], 0, 2, 256, 256), ([0, 3, 0, 1, 0], 1, 1, 384, 640), ([1] * 9, 0, 0, 128, 1152),
     ([5, 0, 2], 0, 0, 1280, 384), ([0, 0], 0, 3, 256, 128), ([17], 2, 1, 640, 256), ([1, 2] * 20, 0, 5, 256, 128),
     ([3, 4, 1, 2], 0, 0, 2176, 2048), ([1, 1], 0, 0, 4096, 4096), ([3, 4, 0, 1, 2, 5] * 4, 0, 3, 2176, 384),
-    ([1, 9, 0, 6], 1, 2, 10112, 256),
+    ([1, 9, 0, 6], 1, 2, 10112, 256), ([1], 0, 0, 11008, 256), ([1, 0, 1], 0, 0, 11008, 512), ([1, 1, 1], 0, 0, 11008, 128),
+    ([1, 0, 1, 1], 0, 0, 12288, 256), ([2], 1, 1, 9600, 384), ([2, 1, 1], 0, 0, 11008, 256), ([3], 0, 0, 16384, 640),
 ]
 
 
