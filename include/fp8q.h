@@ -614,7 +614,7 @@ typedef struct {
  *   norm        device, float[1]
  * Squares are binary32 within 64 elements and binary64 beyond, or binary64 where binary32's range
  * ends: no element is too large or too small to count.  n_grads == 0 gives 0.  Sizes sum to less
- * than 2^44 elements (FP8_ERR_SHAPE).
+ * than 2^40 elements (FP8_ERR_SHAPE).
  */
 fp8_status fp8_grad_norm(const fp8_gradient* grads, int32_t n_grads, void* workspace, int64_t workspace_bytes, float* norm,
                          cudaStream_t stream);

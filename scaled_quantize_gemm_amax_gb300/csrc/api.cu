@@ -1218,7 +1218,7 @@ fp8_status grad_norm(const fp8_gradient* grads, int32_t n, bool clip, float max_
   for (int32_t i = 0; i < n; ++i) {
     const fp8_gradient& g = grads[i];
     if (g.n < 0 || !valid_dt(g.dt) || (g.n > 0 && (g.in == nullptr || (clip && g.out == nullptr)))) return FP8_ERR_INVALID_ARG;
-    if (g.n >= (int64_t{1} << 44) || (total += g.n) >= (int64_t{1} << 44)) return FP8_ERR_SHAPE;
+    if (g.n >= (int64_t{1} << 40) || (total += g.n) >= (int64_t{1} << 40)) return FP8_ERR_SHAPE;
     if (!aligned(g.in, elem_size(g.dt)) || (clip && !aligned(g.out, elem_size(g.dt)))) return FP8_ERR_ALIGNMENT;
   }
   DeviceInfo* d;

@@ -668,6 +668,58 @@ const at::Tensor& dense(PyObject* o, const char* what) {
   return t;
 }
 
+// The memory of a call's tensors: what one of them writes must not be part of another, whose turn may come first
+// or last.  Tensors of different storages are apart, and those of one storage are seen to be apart on the way when
+// they come in ascending order, as views into a buffer do; only others are sorted.
+class Spans {
+ public:
+  explicit Spans(size_t n) {
+    all_.reserve(n);
+    size_t slots = 16;
+    while (slots < 2 * n) slots *= 2;
+    ends_.resize(slots);
+  }
+  void add(const at::Tensor& t, bool written) {
+    if (t.numel() == 0) return;
+    const auto lo = reinterpret_cast<uintptr_t>(t.const_data_ptr());
+    const uintptr_t hi = lo + static_cast<uintptr_t>(t.numel() * t.element_size());
+    all_.push_back({lo, hi, written});
+    const void* storage = t.unsafeGetTensorImpl()->unsafe_storage().unsafeGetStorageImpl();
+    size_t i = (reinterpret_cast<uintptr_t>(storage) >> 4) * 0x9E3779B97F4A7C15ull >> 20;
+    while (true) {
+      End& e = ends_[i++ & (ends_.size() - 1)];
+      if (e.storage != nullptr && e.storage != storage) continue;
+      if (e.storage != nullptr && lo < e.hi) sorted_ = false;
+      e = {storage, hi};
+      return;
+    }
+  }
+  bool meet() {
+    if (sorted_) return false;
+    std::sort(all_.begin(), all_.end(), [](const Span& x, const Span& y) { return x.lo < y.lo; });
+    uintptr_t any = 0, written = 0;   // ends of what lies in front
+    for (const Span& x : all_) {
+      if (x.lo < written || (x.written && x.lo < any)) return true;
+      any = std::max(any, x.hi);
+      if (x.written) written = std::max(written, x.hi);
+    }
+    return false;
+  }
+
+ private:
+  struct Span {
+    uintptr_t lo, hi;
+    bool written;
+  };
+  struct End {
+    const void* storage = nullptr;
+    uintptr_t hi = 0;
+  };
+  std::vector<Span> all_;
+  std::vector<End> ends_;   // by storage, open addressing
+  bool sorted_ = true;
+};
+
 // clip_grad_norm(grads, max_norm | None, out | None, stream) -> norm; max_norm None: the norm alone;
 // out None: in place
 PyObject* clip_grad_norm(PyObject* const* v) {
@@ -681,18 +733,7 @@ PyObject* clip_grad_norm(PyObject* const* v) {
   if (n == 0) refuse(PyExc_ValueError, "grads: at least one tensor is needed");
   std::vector<fp8_gradient> table(static_cast<size_t>(n));
   const at::Tensor& first = needed(grads[0], "grads");
-  // Memory written and read by two tensors of a call would be scaled in an order of its own.  Gradients
-  // that lie in ascending order, as views into a buffer do, are seen to be apart on the way; others are sorted.
-  struct Span {
-    uintptr_t lo, hi;
-    bool out;
-  };
-  std::vector<Span> spans;
-  spans.reserve(static_cast<size_t>(in_place || !clip ? n : 2 * n));
-  auto span = [&](const at::Tensor& t, bool out) {
-    const auto lo = reinterpret_cast<uintptr_t>(t.data_ptr());
-    if (t.numel() > 0) spans.push_back({lo, lo + static_cast<uintptr_t>(t.numel() * t.element_size()), out});
-  };
+  Spans spans(static_cast<size_t>(in_place ? n : 2 * n));
   for (Py_ssize_t i = 0; i < n; ++i) {
     const at::Tensor& g = dense(grads[i], "grads");
     if (!g.is_cuda()) refuse(PyExc_ValueError, "a CUDA tensor is needed, not one on " + g.device().str());
@@ -701,27 +742,16 @@ PyObject* clip_grad_norm(PyObject* const* v) {
     fp8_gradient& to = table[static_cast<size_t>(i)];
     to = {g.data_ptr(), nullptr, g.numel(), data_type(g, "grads")};
     if (!clip) continue;
-    span(g, in_place);
     const at::Tensor& o = in_place ? g : dense(outs[i], "out");
     if (!in_place) {
       if (o.scalar_type() != g.scalar_type() || o.sizes() != g.sizes() || o.strides() != g.strides() || o.device() != g.device())
         refuse(PyExc_ValueError, "out: tensors like the gradients are needed, not " + shape_of(o) + " for " + shape_of(g));
-      if (o.data_ptr() != g.data_ptr()) span(o, true);
-      else if (g.numel() > 0) spans.back().out = true;
+      if (o.data_ptr() != g.data_ptr()) spans.add(o, true);
     }
     to.out = o.data_ptr();
+    spans.add(g, to.out == to.in);
   }
-  bool sorted = true;
-  for (size_t i = 1; i < spans.size() && sorted; ++i) sorted = spans[i - 1].hi <= spans[i].lo;
-  if (!sorted) {
-    std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.lo < y.lo; });
-    uintptr_t all = 0, written = 0;   // ends of what lies in front
-    for (const Span& x : spans) {
-      if (x.lo < written || (x.out && x.lo < all)) refuse(PyExc_ValueError, "gradients and outputs must not share memory");
-      all = std::max(all, x.hi);
-      if (x.out) written = std::max(written, x.hi);
-    }
-  }
+  if (spans.meet()) refuse(PyExc_ValueError, "gradients and outputs must not share memory");
   Place on;
   const cudaStream_t stream = stream_of(v[3], first, on);
   int64_t bytes = 0;

@@ -114,7 +114,7 @@ def test_grad_norm_rejects(lib):
         assert f([good], **args) == INVALID, args
     for e in ((None, FAKE, 10, 1), (FAKE, None, 10, 1), (FAKE, FAKE, -1, 1), (FAKE, FAKE, 10, 2)):
         assert f([good, e]) == INVALID, e
-    assert f([(FAKE, FAKE, 2 ** 44, 0)]) == SHAPE and f([(FAKE, FAKE, 2 ** 43, 0)] * 2) == SHAPE and f([good], nbytes=8) == SHAPE
+    assert f([(FAKE, FAKE, 2 ** 40, 0)]) == SHAPE and f([(FAKE, FAKE, 2 ** 39, 0)] * 2) == SHAPE and f([good], nbytes=8) == SHAPE
     for e in ((FAKE + 2, FAKE, 10, 1), (FAKE, FAKE + 1, 10, 0)):
         assert f([e]) == ALIGN, e
     assert f([good], ws=FAKE + 4) == ALIGN and f([good], norm=FAKE + 2) == ALIGN
