@@ -1106,6 +1106,7 @@ fp8_status grouped(GroupedParams& p, const uint8_t* A, fp8_format fa, fp8_recipe
     return FP8_ERR_ALIGNMENT;
   DeviceInfo* d;
   if (fp8_status st = device_info(&d)) return st;
+  p.a_rows = static_cast<int>(a_rows);
   p.a_cols = static_cast<int>(a_cols);
   p.b_rows_all = static_cast<int>(b_rows);
   p.b_cols_all = static_cast<int>(b_cols);

@@ -89,22 +89,24 @@ __device__ __forceinline__ Tile tile_of(const GroupedParams& p, const int* offs,
   Tile w;
   w.e = e;
   w.held = row < rows;
-  const int from = w.held ? row : row - kRows;   // rows that are not the expert's: the peer's once more, from L2
   w.c_col = tn * tile_cols;
   if (p.depth) {
-    w.a_row = from;
+    w.a_row = row;
     w.a_kb = w.b_kb = lo / kDepth;
     w.nkb = seg / kDepth;
     w.b_row = w.c_col;
     w.c_row = e * p.M + row;
   } else {
-    w.a_row = lo + from;
+    w.a_row = lo + row;
     w.a_kb = 0;
     w.nkb = p.K / kDepth;
     w.b_kb = p.b_cols ? e * w.nkb : 0;
     w.b_row = (p.b_cols ? 0 : e * p.N) + w.c_col;
     w.c_row = lo + row;
   }
+  // in the place of rows that are not the expert's, rows behind A's last: TMA makes them zeros without reading, and
+  // zeros cost the tensor core little power
+  if (!w.held) w.a_row = p.a_rows;
   return w;
 }
 

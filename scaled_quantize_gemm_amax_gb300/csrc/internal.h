@@ -409,7 +409,7 @@ struct GroupedParams {
   int64_t capacity;      // rows that the segments lie in
   int M, N, K;           // M: depth only; K: rows only
   int b_cols;            // rows: the experts' B are side by side, [N, n_experts * K], not [n_experts * N, K]
-  int a_cols;            // columns of A's matrix, and columns and rows of B's (where its scale atoms are)
+  int a_rows, a_cols;    // A's matrix, and B's (where its scale atoms are)
   int b_cols_all, b_rows_all;
   int e5m2_a, e5m2_b, out_fp32;
   const float* sa;       // kTensor: float[1]

@@ -467,6 +467,8 @@ PyObject* moe_combine_backward(PyObject* const* a) {
   return wrap_all(dys, dw);
 }
 
+constexpr int64_t kTogether = 64 * 1024;   // bytes
+
 fp8_recipe recipe_of(PyObject* o) { return static_cast<fp8_recipe>(small(integer(o))); }
 bool is_mx(fp8_recipe r) { return r >= FP8_MX_1x32; }
 bool is_tiled(fp8_recipe r) { return r == FP8_MX_1x32_TILED || r == FP8_MX_1x32_FLOOR_TILED; }
@@ -492,33 +494,38 @@ PyObject* rms_norm(PyObject* const* a) {
   fp8_status st;
   {
     Unlocked unlocked;
-    if (keep_y) y = make({x.rows, x.cols}, x.t->scalar_type(), *x.t);
-    if (res.t != nullptr) h = make({x.rows, x.cols}, x.t->scalar_type(), *x.t);
-    // the codes, their multipliers and the statistics in one allocation
-    const int64_t codes = copy ? to16(x.rows * ldq) : 0;
-    int64_t scales = 0;
-    std::vector<int64_t> shape, strides;
+    // the codes, their multipliers and the statistics in one allocation; with little data (a few tokens) all outputs are
+    int64_t shape[3] = {1, 1, 1}, dims = 1, scales = 0;
     if (copy) {
-      if (recipe == FP8_TENSOR) shape = {1};
-      else if (is_tiled(recipe)) shape = {(x.rows + 127) / 128, groups(x.cols), 512};
-      else shape = {x.rows, is_mx(recipe) ? x.cols / 32 : groups(x.cols)};
-      scales = is_mx(recipe) ? 1 : 4;
-      strides.resize(shape.size());
-      int64_t n = 1;
-      for (size_t i = shape.size(); i-- > 0;) {
-        strides[i] = n;
-        n *= shape[i];
+      if (is_tiled(recipe)) {
+        dims = 3, shape[0] = (x.rows + 127) / 128, shape[1] = groups(x.cols), shape[2] = 512;
+      } else if (recipe != FP8_TENSOR) {
+        dims = 2, shape[0] = x.rows, shape[1] = is_mx(recipe) ? x.cols / 32 : groups(x.cols);
       }
-      scales = to16(scales * n);
+      scales = to16(shape[0] * shape[1] * shape[2] * (is_mx(recipe) ? 1 : 4));
     }
-    if (copy || stats) {
-      const at::Tensor whole = make({codes + scales + (stats ? 4 * x.rows : 0)}, at::kByte, *x.t);
-      if (copy) {
-        q = part(whole, 0, at::kByte, {x.rows, x.cols}, {ldq, 1});
-        s = part(whole, codes, is_mx(recipe) ? at::kByte : at::kFloat, shape, strides);
-      }
-      if (stats) rstd = part(whole, codes + scales, at::kFloat, {x.rows}, {1});
+    const int64_t codes = copy ? to16(x.rows * ldq) : 0, rest = stats ? to16(4 * x.rows) : 0;
+    const int64_t data = to16(x.rows * x.cols * static_cast<int64_t>(x.t->element_size()));
+    const int64_t wide = (keep_y ? data : 0) + (res.t != nullptr ? data : 0);
+    const bool together = wide + codes + scales + rest <= kTogether;
+    at::Tensor whole;
+    if (together || codes + scales + rest > 0) whole = make({(together ? wide : 0) + codes + scales + rest}, at::kByte, *x.t);
+    int64_t at = 0;
+    auto matrix = [&](bool wanted) -> at::Tensor {
+      if (!wanted) return {};
+      if (!together) return make({x.rows, x.cols}, x.t->scalar_type(), *x.t);
+      at += data;
+      return part(whole, at - data, x.t->scalar_type(), {x.rows, x.cols}, {x.cols, 1});
+    };
+    y = matrix(keep_y);
+    h = matrix(res.t != nullptr);
+    if (copy) {
+      const int64_t strides[3] = {dims == 1 ? 1 : shape[1] * shape[2], dims == 2 ? 1 : shape[2], 1};
+      q = part(whole, at, at::kByte, {x.rows, x.cols}, {ldq, 1});
+      s = part(whole, at + codes, is_mx(recipe) ? at::kByte : at::kFloat, {shape, static_cast<size_t>(dims)},
+               {strides, static_cast<size_t>(dims)});
     }
+    if (stats) rstd = part(whole, at + codes + scales, at::kFloat, {x.rows}, {1});
     st = p_fp8_rms_norm(x.p(), x.rows, x.cols, x.ld, dt, res.p(), res.ld, w, wdt, static_cast<float>(eps), ptr<void>(h), x.cols,
                         ptr<void>(y), x.cols, ptr<float>(rstd), recipe, fmt, scale, amax, ptr<uint8_t>(q), ldq, ptr<void>(s),
                         stream);
