@@ -129,10 +129,12 @@ constexpr int kCopier = 2 + kEpi;
 // ------------------------------------------------------------------ many rows: CTA pairs
 // Two CTAs share a 256 x 256 tile (cta_group::2), each with its 128 rows of A and half of B's.
 constexpr int kPairCols = 256;
-template <int KIND>
+// S stages: 6 with per-tensor scales and up to 200 experts (their table of segments shares the memory), else 5.  (8192
+// tokens at 2 of 8 experts 452 -> 443 us, 64 experts of 256 rows 112 -> 110.6; with 4 stages 478 and 121.)
+constexpr int kSixStageExperts = 200;
+template <int KIND, int S>
 struct PairLayout {
   static constexpr bool MX = KIND == kMx;
-  static constexpr int S = 5;            // stages
   static constexpr int ACC = MX ? 1 : 2; // accumulators; MXFP8's scale factors leave TMEM for one
   static constexpr uint32_t A_BYTES = kRows * kDepth, B_BYTES = kPairCols / 2 * kDepth, STAGE = A_BYTES + B_BYTES;
   static constexpr int B_ATOMS = kPairCols / 128;
@@ -147,25 +149,25 @@ struct PairLayout {
   static constexpr uint32_t SF_COL = kPairCols * ACC;    // first TMEM column of the scale factors
   static constexpr uint32_t SF_COLS = 4 + 4 * B_ATOMS;   // of a stage
   static_assert(SF_COL + (MX ? S * SF_COLS : 0) <= kTmemAll, "TMEM");
-  static_assert(FIXED + table_bytes(kMaxExperts) <= kSmem, "shared memory");
+
 };
 
-template <int KIND>
+template <int KIND, int S>
 __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
     k_grouped(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
               const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfb,
               const __grid_constant__ CUtensorMap tm_c, const GroupedParams p) {
-  using L = PairLayout<KIND>;
+  using L = PairLayout<KIND, S>;
   constexpr bool MX = L::MX;
-  constexpr int S = L::S, ACC = L::ACC, TM = 2 * kRows, BN = kPairCols;
+  constexpr int ACC = L::ACC, TM = 2 * kRows, BN = kPairCols;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - smem_u32(smem_raw));
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(base_ptr + L::OFF_ABORT);
   int* const offs = reinterpret_cast<int*>(base_ptr + L::OFF_TABLE);
   int* const first = offs + p.n_experts + 1;   // the experts' first tiles
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const int warp = warp_uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  const uint32_t rank = warp_uniform(cluster_ctarank());
   const bool leader = rank == 0;
   const int unit = static_cast<int>(blockIdx.x) / 2, units = static_cast<int>(gridDim.x) / 2;
   const int tiles_n = (p.N + BN - 1) / BN;
@@ -199,8 +201,8 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
   cluster_sync();   // the peer's barriers are initialised before anyone signals them
   tc_fence_after();
   pdl_launch_dependents();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base_ptr + L::OFF_TMEM);
-  const int ntiles = first[p.n_experts];
+  const uint32_t tmem = warp_uniform(*reinterpret_cast<volatile uint32_t*>(base_ptr + L::OFF_TMEM));
+  const int ntiles = warp_uniform(first[p.n_experts]);
 
   auto tile_at = [&](int t, int& e) { return tile_of<TM>(p, offs, first, BN, tiles_n, static_cast<int>(rank), t, e); };
 
@@ -247,60 +249,55 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
       const int n = issued / S + (s < issued % S ? 1 : 0);
       if (n > 0) mbar_wait(base + L::OFF_EMPTY + 8 * s, static_cast<uint32_t>(n - 1) & 1u, p.err, kErrTimeoutStage, abort_flag);
     }
-  } else if ((warp == 1 || (MX && warp == kCopier)) && lane == 0 && !leader) {
+  } else if ((warp == 1 || (MX && warp == kCopier)) && !leader) {
     // ------------------------------------------------ the peer issues no MMAs: it waits for the leader's last
-    mbar_wait(base + L::OFF_FINAL, 0, p.err, kErrTimeoutMma, abort_flag);
-  } else if (MX && warp == kCopier && lane == 0) {
-    // ------------------------------------------------ scale factors into TMEM (leader)
+    if (lane == 0) mbar_wait(base + L::OFF_FINAL, 0, p.err, kErrTimeoutMma, abort_flag);
+  } else if (MX && warp == kCopier) {
+    // ------------------------------------------------ scale factors into TMEM (leader; the whole warp)
     int stage = 0, e = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int t = unit; t < ntiles && ok; t += units) {
-      const Tile w = tile_at(t, e);
-      for (int kb = 0; kb < w.nkb; ++kb) {
-        if (!mbar_wait(base + L::OFF_FULL + 8 * stage, phase, p.err, kErrTimeoutTmaLoad, abort_flag)) {
-          ok = false;
-          break;
-        }
+      const int nkb = warp_uniform(tile_at(t, e).nkb);
+      for (int kb = 0; kb < nkb; ++kb) {
+        ok = warp_uniform(mbar_wait(base + L::OFF_FULL + 8 * stage, phase, p.err, kErrTimeoutTmaLoad, abort_flag));
+        if (!ok) break;
         tc_fence_after();
         // the stage's columns were last read by MMAs that finished before the stage was refilled
         const uint32_t sf = base + L::OFF_SF + stage * L::SF, col = tmem + L::SF_COL + static_cast<uint32_t>(stage) * L::SF_COLS;
 #pragma unroll
-        for (int h = 0; h <= L::B_ATOMS; ++h) {
-          tc_cp_32x128b_warpx4_pair(col + 4 * h, sdesc_rows16(sf + 512 * h));
-        }
-        tc_commit_pair_mc(base + L::OFF_SFR + 8 * stage, 1);
+        for (int h = 0; h <= L::B_ATOMS; ++h) tc_cp_32x128b_warpx4_pair_warp(col + 4 * h, sdesc_rows16(sf + 512 * h));
+        tc_commit_pair_mc_warp(base + L::OFF_SFR + 8 * stage, 1);
         if (++stage == S) {
           stage = 0;
           phase ^= 1u;
         }
       }
     }
-    tc_commit_pair_mc(base + L::OFF_FINAL, 3);
+    tc_commit_pair_mc_warp(base + L::OFF_FINAL, 3);
     mbar_wait(base + L::OFF_FINAL, 0, p.err, kErrTimeoutMma, nullptr);
-  } else if (warp == 1 && lane == 0) {
-    // ------------------------------------------------ MMA issuer (leader)
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer (leader; the whole warp)
     const uint32_t shape = (static_cast<uint32_t>(p.e5m2_a) << 7) | (static_cast<uint32_t>(p.e5m2_b) << 10) |
                            (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
     const uint32_t idesc = shape | (MX ? 1u << 23 : 1u << 4);
-    auto commit = [&](uint32_t bar) { tc_commit_pair_mc(bar, 3); };
+    auto commit = [&](uint32_t bar) { tc_commit_pair_mc_warp(bar, 3); };
     int stage = 0, e = 0;
     uint32_t phase = 0, acc_it = 0;
     bool ok = true;
     for (int t = unit; t < ntiles && ok; t += units) {
-      const Tile w = tile_at(t, e);
-      if (w.nkb == 0) continue;   // the epilogue stores 0 without an accumulator
+      const int nkb = warp_uniform(tile_at(t, e).nkb);
+      if (nkb == 0) continue;   // the epilogue stores 0 without an accumulator
       const uint32_t a = acc_it % ACC, parity = ((acc_it / ACC) & 1u) ^ 1u;
-      const uint32_t bar = base + L::OFF_TEMPTY + 8 * a;
-      if (!mbar_wait_cluster(bar, parity, p.err, kErrTimeoutMma, abort_flag)) break;
+      ok = warp_uniform(mbar_wait_cluster(base + L::OFF_TEMPTY + 8 * a, parity, p.err, kErrTimeoutMma, abort_flag));
+      if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + a * BN;
-      for (int kb = 0; kb < w.nkb; ++kb) {
+      for (int kb = 0; kb < nkb; ++kb) {
         // MXFP8: the copier's signal stands for the stage's data too
-        if (!mbar_wait(base + (MX ? L::OFF_SFR : L::OFF_FULL) + 8 * stage, phase, p.err, kErrTimeoutTmaLoad, abort_flag)) {
-          ok = false;
-          break;
-        }
+        ok = warp_uniform(
+            mbar_wait(base + (MX ? L::OFF_SFR : L::OFF_FULL) + 8 * stage, phase, p.err, kErrTimeoutTmaLoad, abort_flag));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t sa = base + stage * L::STAGE, sb = sa + L::A_BYTES;
         const uint32_t sfa = tmem + L::SF_COL + static_cast<uint32_t>(stage) * L::SF_COLS, sfb = sfa + 4;
@@ -310,9 +307,9 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
           const uint32_t more = (kb | k) != 0 ? 1u : 0u;
           if (MX) {
             const uint32_t id = idesc | (static_cast<uint32_t>(k) << 4) | (static_cast<uint32_t>(k) << 29);
-            tc_mma_mxf8f6f4_pair(d, da, db, id, sfa, sfb, more);
+            tc_mma_mxf8f6f4_pair_warp(d, da, db, id, sfa, sfb, more);
           } else {
-            tc_mma_f8f6f4_pair(d, da, db, idesc, more);
+            tc_mma_f8f6f4_pair_warp(d, da, db, idesc, more);
           }
         }
         commit(base + L::OFF_EMPTY + 8 * stage);
@@ -468,7 +465,7 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
   int* const offs = reinterpret_cast<int*>(base_ptr + L::OFF_TABLE);
   int* const first = offs + p.n_experts + 1;
   const uint32_t stages = base + L::stages_at(p.n_experts), stage_bytes = L::stage_bytes(width);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int unit = static_cast<int>(blockIdx.x), units = static_cast<int>(gridDim.x);
   const int tiles_n = (p.N + width - 1) / width, ACC = L::accumulators(MX, width);
 
@@ -500,8 +497,8 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
   __syncthreads();
   tc_fence_after();
   pdl_launch_dependents();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base_ptr + L::OFF_TMEM);
-  const int ntiles = first[p.n_experts];
+  const uint32_t tmem = warp_uniform(*reinterpret_cast<volatile uint32_t*>(base_ptr + L::OFF_TMEM));
+  const int ntiles = warp_uniform(first[p.n_experts]);
   auto tile_at = [&](int t, int& e) { return tile_of<kRows>(p, offs, first, width, tiles_n, 0, t, e); };
   auto next = [&](int& stage, uint32_t& phase) {
     if (++stage == S) {
@@ -546,32 +543,30 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
       const int n = issued / S + (s < issued % S ? 1 : 0);
       if (n > 0) mbar_wait(base + L::OFF_FULL + 8 * s, static_cast<uint32_t>(n - 1) & 1u, p.err, kErrTimeoutTmaLoad, nullptr);
     }
-  } else if (MX && warp == kCopier && lane == 0) {
-    // ------------------------------------------------ scale factors into TMEM
+  } else if (MX && warp == kCopier) {
+    // ------------------------------------------------ scale factors into TMEM (the whole warp)
     int stage = 0, e = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int t = unit; t < ntiles && ok; t += units) {
       const Tile w = tile_at(t, e);
-      const int n_atoms = (w.b_row % kRows + width + kRows - 1) / kRows;
-      for (int kb = 0; kb < w.nkb; ++kb) {
-        if (!mbar_wait(base + L::OFF_FULL + 8 * stage, phase, p.err, kErrTimeoutTmaLoad, abort_flag)) {
-          ok = false;
-          break;
-        }
+      const int n_atoms = warp_uniform((w.b_row % kRows + width + kRows - 1) / kRows), nkb = warp_uniform(w.nkb);
+      for (int kb = 0; kb < nkb; ++kb) {
+        ok = warp_uniform(mbar_wait(base + L::OFF_FULL + 8 * stage, phase, p.err, kErrTimeoutTmaLoad, abort_flag));
+        if (!ok) break;
         tc_fence_after();
         // the stage's columns were last read by MMAs that finished before the stage was refilled
         const uint32_t sf = base + L::OFF_SF + static_cast<uint32_t>(stage) * (L::SF_ATOMS * 512);
         const uint32_t col = tmem + L::SF_COL + static_cast<uint32_t>(stage) * L::SF_COLS;
-        for (int h = 0; h <= n_atoms; ++h) tc_cp_32x128b_warpx4(col + 4 * h, sdesc_rows16(sf + 512 * h));
-        tc_commit(base + L::OFF_SFR + 8 * stage);
+        for (int h = 0; h <= n_atoms; ++h) tc_cp_32x128b_warpx4_warp(col + 4 * h, sdesc_rows16(sf + 512 * h));
+        tc_commit_warp(base + L::OFF_SFR + 8 * stage);
         next(stage, phase);
       }
     }
-    tc_commit(base + L::OFF_FINAL);
+    tc_commit_warp(base + L::OFF_FINAL);
     mbar_wait(base + L::OFF_FINAL, 0, p.err, kErrTimeoutMma, nullptr);
-  } else if (warp == 1 && lane == 0) {
-    // ------------------------------------------------ MMA issuer
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer (the whole warp)
     const uint32_t idesc = (static_cast<uint32_t>(p.e5m2_a) << 7) | (static_cast<uint32_t>(p.e5m2_b) << 10) |
                            (static_cast<uint32_t>(width >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24) |
                            (MX ? 1u << 23 : 1u << 4);
@@ -580,39 +575,40 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
     bool ok = true;
     for (int t = unit; t < ntiles && ok; t += units) {
       const Tile w = tile_at(t, e);
-      if (w.nkb == 0) continue;   // the epilogue stores 0 without an accumulator
+      const int nkb = warp_uniform(w.nkb);
+      if (nkb == 0) continue;   // the epilogue stores 0 without an accumulator
+      // B's first row may be the middle one of its first atom: 32 rows are one column of scale factors
+      const uint32_t sfb_col = warp_uniform(4u + static_cast<uint32_t>(w.b_row % kRows / 32));
       const uint32_t a = ACC == 2 ? acc_it & 1u : 0u, use = ACC == 2 ? acc_it >> 1 : acc_it;
-      if (!mbar_wait(base + L::OFF_TEMPTY + 8 * a, (use & 1u) ^ 1u, p.err, kErrTimeoutMma, abort_flag)) break;
+      ok = warp_uniform(mbar_wait(base + L::OFF_TEMPTY + 8 * a, (use & 1u) ^ 1u, p.err, kErrTimeoutMma, abort_flag));
+      if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + a * static_cast<uint32_t>(width);
-      for (int kb = 0; kb < w.nkb; ++kb) {
+      for (int kb = 0; kb < nkb; ++kb) {
         // MXFP8: the copier's signal stands for the stage's data too
-        if (!mbar_wait(base + (MX ? L::OFF_SFR : L::OFF_FULL) + 8 * stage, phase, p.err, kErrTimeoutTmaLoad, abort_flag)) {
-          ok = false;
-          break;
-        }
+        ok = warp_uniform(
+            mbar_wait(base + (MX ? L::OFF_SFR : L::OFF_FULL) + 8 * stage, phase, p.err, kErrTimeoutTmaLoad, abort_flag));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t sa = stages + stage * stage_bytes, sb = sa + L::A_BYTES;
-        // B's first row may be the middle one of its first atom: 32 rows are one column of scale factors
-        const uint32_t sfa = tmem + L::SF_COL + static_cast<uint32_t>(stage) * L::SF_COLS;
-        const uint32_t sfb = sfa + 4 + static_cast<uint32_t>(w.b_row % kRows / 32);
+        const uint32_t sfa = tmem + L::SF_COL + static_cast<uint32_t>(stage) * L::SF_COLS, sfb = sfa + sfb_col;
 #pragma unroll
         for (int k = 0; k < kDepth / kUmmaDepth; ++k) {
           const uint64_t da = sdesc_k_sw128(sa + k * kUmmaDepth), db = sdesc_k_sw128(sb + k * kUmmaDepth);
           const uint32_t more = (kb | k) != 0 ? 1u : 0u;
           if (MX)
-            tc_mma_mxf8f6f4(d, da, db, idesc | (static_cast<uint32_t>(k) << 4) | (static_cast<uint32_t>(k) << 29), sfa, sfb, more);
+            tc_mma_mxf8f6f4_warp(d, da, db, idesc | (static_cast<uint32_t>(k) << 4) | (static_cast<uint32_t>(k) << 29), sfa, sfb, more);
           else
-            tc_mma_f8f6f4(d, da, db, idesc, more);
+            tc_mma_f8f6f4_warp(d, da, db, idesc, more);
         }
-        tc_commit(base + L::OFF_EMPTY + 8 * stage);
+        tc_commit_warp(base + L::OFF_EMPTY + 8 * stage);
         next(stage, phase);
       }
       if (!ok) break;
-      tc_commit(base + L::OFF_TFULL + 8 * a);
+      tc_commit_warp(base + L::OFF_TFULL + 8 * a);
       ++acc_it;
     }
-    tc_commit(base + L::OFF_FINAL);   // every MMA has finished before TMEM is released
+    tc_commit_warp(base + L::OFF_FINAL);   // every MMA has finished before TMEM is released
     mbar_wait(base + L::OFF_FINAL, 0, p.err, kErrTimeoutMma, nullptr);
   } else if (warp >= 2 && warp < 2 + kEpi) {
     // ------------------------------------------------ epilogue
@@ -686,11 +682,12 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
 }
 
 // ------------------------------------------------------------------ launches
-template <int KIND>
+template <int KIND, int S>
 cudaError_t run_pairs(const GroupedParams& p, const GroupedMaps& m, int64_t tiles, int num_sms, cudaStream_t s) {
-  using L = PairLayout<KIND>;
-  constexpr int kMostSmem = static_cast<int>(L::FIXED + table_bytes(kMaxExperts));
-  auto kern = k_grouped<KIND>;
+  using L = PairLayout<KIND, S>;
+  constexpr int kMostSmem = static_cast<int>(L::FIXED + table_bytes(S == 6 ? kSixStageExperts : kMaxExperts));
+  static_assert(kMostSmem <= static_cast<int>(kSmem), "shared memory");
+  auto kern = k_grouped<KIND, S>;
   static std::atomic<bool> attr_done[kMaxDevices] = {};
   cudaError_t e = ensure_smem_limit(kern, kMostSmem, attr_done);
   if (e != cudaSuccess) return e;
@@ -783,7 +780,8 @@ cudaError_t launch_grouped(const GroupedParams& p, const GroupedMaps& m, int wid
   const bool mx = p.kind == kMx;
   if (width == 0) {
     const int64_t tiles = most_tiles(p, 2 * kRows, kPairCols);
-    return mx ? run_pairs<kMx>(p, m, tiles, num_sms, s) : run_pairs<kTensor>(p, m, tiles, num_sms, s);
+    if (mx) return run_pairs<kMx, 5>(p, m, tiles, num_sms, s);
+    return p.n_experts <= kSixStageExperts ? run_pairs<kTensor, 6>(p, m, tiles, num_sms, s) : run_pairs<kTensor, 5>(p, m, tiles, num_sms, s);
   }
   const int64_t tiles = most_tiles(p, kRows, width);
   return mx ? run_few<kMx>(p, m, width, tiles, num_sms, s) : run_few<kTensor>(p, m, width, tiles, num_sms, s);

@@ -164,6 +164,17 @@ def test_many_experts():
     assert_status_ok()
 
 
+def test_many_experts_of_many_rows():
+    """More experts than the deepest ring of stages leaves room for."""
+    blocks = [(e * 7) % 4 for e in range(260)]
+    starts, offsets = offsets_of(blocks)
+    q, s, a = operand(spread(starts[-1], 256, 20), R.TENSOR, F.E4M3)
+    qb, sb, b = operand(spread(260 * 256, 256, 21), R.TENSOR, F.E4M3)
+    c = fq.grouped_gemm(q, F.E4M3, R.TENSOR, s, qb, F.E4M3, R.TENSOR, sb, offsets, out=O.FP32)
+    _check_rows(c, a, lambda e: b[256 * e:256 * (e + 1)], starts, 256, O.FP32, None)
+    assert_status_ok()
+
+
 def test_two_at_once_and_captured():
     """The routing made inside a captured graph, replayed for another one; two calls on two streams at once."""
     tokens, k, experts, cols, n = 200, 2, 5, 256, 384
