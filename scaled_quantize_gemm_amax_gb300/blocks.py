@@ -5,6 +5,7 @@ the layers around the three GEMMs stay in BF16 / FP32), each as an autograd func
 the C ABI:
 
   layer_norm(x, weight, bias)    fp8_layer_norm / fp8_layer_norm_backward
+  rms_norm(x, weight, residual)  fp8_rms_norm / fp8_rms_norm_backward
   gated_act(h)                   fp8_gated_act / fp8_gated_act_backward; h's halves are a and b
   moe_dispatch(x, route)         fp8_moe_dispatch / fp8_moe_combine
   moe_combine(ys, route, w)      fp8_moe_combine / fp8_moe_combine_backward
@@ -14,7 +15,8 @@ rows; activation: its inputs) as 8-bit codes with one multiplier per 128 columns
 the BF16 tensors; the forward values do not change.  A second derivative is an error.
 
 ``FP8MoEBlock`` is the pre-norm expert MLP of a transformer: norm, router, dispatch, two
-FP8 linear layers per expert with a gated activation between them, combine, residual.
+FP8 linear layers per expert with a gated activation between them, combine, residual; with
+``grouped`` the experts' layers are grouped products and no step waits for the routing.
 Every operator runs in the library's kernels; torch does the router's small product and
 top-k.  Leading dimensions are flattened; a tensor whose last dimension is not contiguous
 or whose rows overlap (an expanded one) is copied.
@@ -32,9 +34,11 @@ from . import moe_combine as _moe_combine
 from . import moe_combine_backward as _moe_combine_backward
 from . import moe_dispatch as _moe_dispatch
 from . import moe_dispatch_backward as _moe_dispatch_backward
-from .linear import FP8Linear
+from . import rms_norm as _rms_norm
+from . import rms_norm_backward as _rms_norm_backward
+from .linear import FP8GroupedLinear, FP8Linear
 
-__all__ = ["layer_norm", "gated_act", "moe_dispatch", "moe_combine", "LayerNorm", "FP8MoEBlock"]
+__all__ = ["layer_norm", "rms_norm", "gated_act", "moe_dispatch", "moe_combine", "LayerNorm", "RMSNorm", "FP8MoEBlock"]
 
 
 def _flat(x):
@@ -71,6 +75,43 @@ class _LayerNormFn(torch.autograd.Function):
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, checkpoint: Format | None = None):
     """Layer norm over the last dimension of x (bf16 or float32); weight and bias of one type, bf16 or float32."""
     return _LayerNormFn.apply(_flat(x), weight, bias, eps, checkpoint).reshape(x.shape)
+
+
+class _RMSNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps, apart):
+        ctx.set_materialize_grads(False)
+        w = weight.detach() if weight is not None else None
+        y, h, rstd, _, _ = _rms_norm(x, w, residual, eps)
+        ctx.save_for_backward(w, x if residual is None else h, rstd)
+        ctx.has_residual, ctx.apart = residual is not None, apart
+        return (y, h) if residual is not None else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        w, h, rstd = ctx.saved_tensors
+        dw = None
+        if dy is None:   # only h was used
+            dx = dh
+        else:
+            need = w is not None and ctx.needs_input_grad[1]
+            dx, dw = _rms_norm_backward(_flat(dy), h, rstd, w, dh=_flat(dh) if dh is not None else None, param_grads=need)
+        dres = (dx.clone() if ctx.apart else dx) if ctx.has_residual else None
+        return dx, dw, dres, None, None
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-5):
+    """RMS norm over the last dimension of x (bf16 or float32); weight bf16 or float32.
+
+    With residual (like x) the norm of their sum h, rounded to x's type; returns (y, h) then."""
+    if residual is None:
+        return _RMSNormFn.apply(_flat(x), weight, None, eps, False).reshape(x.shape)
+    if residual.shape != x.shape:
+        raise ValueError(f"rms_norm: a residual of x's shape {tuple(x.shape)} is needed, not {tuple(residual.shape)}")
+    # both inputs have one gradient; two leaves keep it, each in memory of its own
+    y, h = _RMSNormFn.apply(_flat(x), weight, _flat(residual), eps, x.is_leaf and residual.is_leaf)
+    return y.reshape(x.shape), h.reshape(x.shape)
 
 
 class _GatedActFn(torch.autograd.Function):
@@ -162,21 +203,42 @@ class LayerNorm(torch.nn.Module):
         return layer_norm(x, self.weight, self.bias, self.eps, self.checkpoint)
 
 
+class RMSNorm(torch.nn.Module):
+    """RMS norm with a float32 weight; with a residual it returns (y, x + residual)."""
+
+    def __init__(self, cols: int, eps: float = 1e-5, device=None):
+        super().__init__()
+        self.eps = eps
+        self.weight = torch.nn.Parameter(torch.ones(cols, device=device))
+
+    def forward(self, x, residual=None):
+        return rms_norm(x, self.weight, residual, self.eps)
+
+
 class FP8MoEBlock(torch.nn.Module):
     """x + sum over a token's k experts of w_e down_e(act(up_e(norm(x)))), a gated MLP an expert.
 
     hidden and ffn are multiples of 128 (the FP8 GEMM's tile); every expert's tokens are
     padded to 128 rows.  The experts' linear layers follow the fp8_autocast scope's recipe.
-    checkpoint keeps the norm's rows and the activations' inputs in 8 bits.  One host read
-    of the segment starts per pass: they are the GEMMs' row counts."""
+    checkpoint keeps the norm's rows (of a layer norm) and the activations' inputs in 8 bits.
+    norm: "layer" or "rms".  grouped=False: a pair of FP8Linear an expert, and one host read of
+    the segment starts per pass, which are the GEMMs' row counts.  grouped=True: two
+    FP8GroupedLinear (per-tensor or MXFP8 recipes), without a host read, so that a pass can be
+    captured into a CUDA graph."""
 
     def __init__(self, hidden: int, ffn: int, n_experts: int, k: int, act: Activation = Activation.SILU,
-                 checkpoint: Format | None = Format.E4M3, device=None):
+                 checkpoint: Format | None = Format.E4M3, device=None, norm: str = "layer", grouped: bool = False):
         super().__init__()
-        self.n_experts, self.k, self.act, self.checkpoint = n_experts, k, act, checkpoint
-        self.norm = LayerNorm(hidden, checkpoint=checkpoint, device=device)
+        if norm not in ("layer", "rms"):
+            raise ValueError(f'norm: "layer" or "rms" is needed, not {norm!r}')
+        self.n_experts, self.k, self.act, self.checkpoint, self.grouped = n_experts, k, act, checkpoint, grouped
+        self.norm = RMSNorm(hidden, device=device) if norm == "rms" else LayerNorm(hidden, checkpoint=checkpoint, device=device)
         self.router = torch.nn.Parameter(torch.empty((n_experts, hidden), device=device))
         torch.nn.init.normal_(self.router, std=0.02)
+        if grouped:
+            self.up = FP8GroupedLinear(n_experts, hidden, 2 * ffn, device=device)
+            self.down = FP8GroupedLinear(n_experts, ffn, hidden, device=device)
+            return
         self.up = torch.nn.ModuleList(FP8Linear(hidden, 2 * ffn, device=device) for _ in range(n_experts))
         self.down = torch.nn.ModuleList(FP8Linear(ffn, hidden, device=device) for _ in range(n_experts))
 
@@ -187,6 +249,10 @@ class FP8MoEBlock(torch.nn.Module):
         weights = torch.softmax(top.values, dim=1)
         route = moe_route(top.indices, self.n_experts, align=128)
         xs = moe_dispatch(n, route)
+        if self.grouped:
+            h = gated_act(self.up(xs, route.offsets), self.act, checkpoint=self.checkpoint)
+            y = moe_combine(self.down(h, route.offsets), route, weights)
+            return x + y.reshape(x.shape)
         starts = route.offsets.tolist()
         parts = []
         for e in range(self.n_experts):

@@ -30,6 +30,12 @@ go to the cast of their own dtype, and each GEMM writes its output in the
 dtype autograd expects (Y and dX in the input's dtype, dW in FP32).  M, N and
 K must be multiples of 128 (the GEMM's tile), which the library checks.  A second
 derivative is an error.
+
+``FP8GroupedLinear`` is the layer of all experts at once: one [experts, N, K] weight, rows
+sorted by expert (``moe_route(..., align=128)``, ``moe_dispatch``), and three grouped products
+whose segments stay on the device.  It takes the per-tensor and MXFP8 recipes; under blockwise
+scaling it is an error (its 128-deep partial sums have no grouped kernel): an ``FP8Linear``
+an expert does that.
 """
 from __future__ import annotations
 
@@ -40,11 +46,11 @@ import threading
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (DelayedScaling, Format, OutDtype, Recipe, amax_history_update, cast_transpose, fp8_amax,
-               fp8_amax_f32, fp8_compute_scale, fp8_scaled_gemm)
+from . import (DelayedScaling, Format, OutDtype, Recipe, Stacked, amax_history_update, cast_transpose, fp8_amax,
+               fp8_amax_f32, fp8_compute_scale, fp8_scaled_gemm, grouped_gemm, grouped_wgrad)
 
 __all__ = ["Float8CurrentScaling", "Float8DelayedScaling", "Float8BlockScaling", "MXFP8BlockScaling", "fp8_autocast",
-           "get_fp8_recipe", "FP8Linear", "fp8_linear"]
+           "get_fp8_recipe", "FP8Linear", "fp8_linear", "FP8GroupedLinear", "fp8_grouped_linear"]
 
 
 @dataclasses.dataclass(frozen=True)
@@ -172,20 +178,59 @@ def fp8_linear(x, weight, recipe=None, states=None):
     return y.reshape(*lead, weight.shape[0])
 
 
-class FP8Linear(torch.nn.Module):
-    """Linear layer (no bias) whose GEMMs run in FP8 under the active recipe.
+def _out_type(dtype):
+    return OutDtype.FP32 if dtype == torch.float32 else OutDtype.BF16
 
-    The FP32 master weight is quantized directly every step (the guide's "weight
-    dual copy": FP8 weights come from a higher-precision copy).  Under a
-    Float8DelayedScaling recipe the layer keeps one delayed-scaling state per
-    tensor role (X and W in E4M3, dY in the backward format)."""
 
-    def __init__(self, in_features: int, out_features: int, device=None, dtype=torch.float32):
-        super().__init__()
-        self.in_features, self.out_features = in_features, out_features
-        self.weight = torch.nn.Parameter(torch.empty((out_features, in_features), device=device, dtype=dtype))
-        torch.nn.init.normal_(self.weight, std=0.02)
-        self._delayed = None
+class _FP8GroupedLinearFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, xs, weight, offsets, recipe, states):
+        kx, kw = _kinds(recipe)
+        if kx == Recipe.BLOCK_1x128:
+            raise TypeError("FP8GroupedLinear takes per-tensor or MXFP8 scaling; under blockwise scaling use an FP8Linear an expert")
+        experts, n, k = weight.shape
+        if offsets.numel() != experts + 1:
+            raise ValueError(f"offsets: {experts + 1} segment starts are needed, not {offsets.numel()}")
+        fx, fdy = recipe.fwd_format, recipe.bwd_format
+        qx, sx, qxt, sxt = _quantize(xs, kx, fx, states.get("x"))
+        # the experts' weights as one matrix: the row copy is stacked by rows, the column copy [K, experts * N] by columns
+        qw, sw, qwt, swt = _quantize(weight.detach().contiguous().view(experts * n, k), kw, fx, states.get("w"))
+        y = grouped_gemm(qx, fx, kx, sx, qw, fx, kw, sw, offsets, out=_out_type(xs.dtype))
+        ctx.save_for_backward(qxt, sxt, qwt, swt, offsets)
+        ctx.meta = (kx, kw, fx, fdy, states.get("dy"), xs.dtype, weight.dtype)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        qxt, sxt, qwt, swt, offsets = ctx.saved_tensors
+        kx, kw, fx, fdy, st_dy, x_dtype, w_dtype = ctx.meta
+        qdy, sdy, qdyt, sdyt = _quantize(dy.contiguous(), kx, fdy, st_dy)
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            dx = grouped_gemm(qdy, fdy, kx, sdy, qwt, fx, kw, swt, offsets, out=_out_type(x_dtype), stacked=Stacked.COLS)
+        if ctx.needs_input_grad[1]:
+            dw = grouped_wgrad(qdyt, fdy, kx, sdyt, qxt, fx, kx, sxt, offsets, out=_out_type(w_dtype))
+        return dx, dw, None, None, None
+
+
+def fp8_grouped_linear(xs, weight, offsets, recipe=None, states=None):
+    """Every expert's rows of xs [capacity, K] (bf16 or float32) times its weight of [experts, N, K] (float32), through
+    three grouped FP8 products; offsets [experts + 1] as ``moe_route`` with align 128 gives them.
+
+    Rows behind the last segment give 0; those of xs, and of the output's gradient, must be finite (per-tensor scaling takes
+    its amax over them; ``moe_dispatch`` and the gradient of ``moe_combine`` set them to 0)."""
+    recipe = recipe if recipe is not None else get_fp8_recipe()
+    if xs.dim() != 2 or weight.dim() != 3 or xs.shape[1] != weight.shape[2]:
+        raise ValueError(f"fp8_grouped_linear: [capacity, K] rows and [experts, N, K] weights are needed, not {tuple(xs.shape)} and "
+                         f"{tuple(weight.shape)}")
+    return _FP8GroupedLinearFn.apply(xs.contiguous(), weight, offsets, recipe, states or {})
+
+
+class _DelayedStates:
+    """The delayed-scaling states of a layer's tensor roles, made under the first recipe that needs them."""
+
+    _delayed = None
 
     def _states(self, recipe):
         if not isinstance(recipe, Float8DelayedScaling):
@@ -199,6 +244,37 @@ class FP8Linear(torch.nn.Module):
             })
         return self._delayed[1]
 
+
+class FP8Linear(_DelayedStates, torch.nn.Module):
+    """Linear layer (no bias) whose GEMMs run in FP8 under the active recipe.
+
+    The FP32 master weight is quantized directly every step (the guide's "weight
+    dual copy": FP8 weights come from a higher-precision copy).  Under a
+    Float8DelayedScaling recipe the layer keeps one delayed-scaling state per
+    tensor role (X and W in E4M3, dY in the backward format)."""
+
+    def __init__(self, in_features: int, out_features: int, device=None, dtype=torch.float32):
+        super().__init__()
+        self.in_features, self.out_features = in_features, out_features
+        self.weight = torch.nn.Parameter(torch.empty((out_features, in_features), device=device, dtype=dtype))
+        torch.nn.init.normal_(self.weight, std=0.02)
+
     def forward(self, x):
         recipe = get_fp8_recipe()
         return fp8_linear(x, self.weight, recipe, self._states(recipe))
+
+
+class FP8GroupedLinear(_DelayedStates, torch.nn.Module):
+    """The linear layers (no bias) of all experts as grouped FP8 products under the active recipe: weight
+    [experts, out_features, in_features] in FP32, quantized directly every step; per-tensor scales are shared by the
+    experts.  Delayed-scaling states as FP8Linear's."""
+
+    def __init__(self, n_experts: int, in_features: int, out_features: int, device=None, dtype=torch.float32):
+        super().__init__()
+        self.n_experts, self.in_features, self.out_features = n_experts, in_features, out_features
+        self.weight = torch.nn.Parameter(torch.empty((n_experts, out_features, in_features), device=device, dtype=dtype))
+        torch.nn.init.normal_(self.weight, std=0.02)
+
+    def forward(self, xs, offsets):
+        recipe = get_fp8_recipe()
+        return fp8_grouped_linear(xs, self.weight, offsets, recipe, self._states(recipe))
