@@ -429,33 +429,53 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
 }
 
 // ------------------------------------------------------------------ few rows: one CTA a tile
+// the pairs' warps, and one more that fetches A
+template <int KIND>
+constexpr int few_threads() { return grouped_threads<KIND>() + 32; }
 // With few tiles the product is bound by streaming the experts' weights once, by every SM: a CTA takes a
 // 128 x width tile, and the host picks the width for which the tiles divide evenly: a multiple of 32, with MXFP8 of
 // 64, since a tile's scale factors then start at an even column of TMEM.
+//
+// What the stream of weights needs is bytes on their way (13 MB over all SMs), so B's blocks have a ring of
+// their own, as deep as shared memory allows, and A's, which every tile reads from L2, a short one.  Each has a warp that
+// fetches it; both complete the barrier of B's stage.
 struct FewLayout {
   static constexpr uint32_t A_BYTES = kRows * kDepth;
-  static constexpr int MAX_S = 8, SF_ATOMS = 3;          // A's atom and up to two of B's, of a stage
-  static constexpr uint32_t OFF_STG = 0;                 // a 4 KB box an epilogue warp
-  static constexpr uint32_t OFF_SF = kEpi * 4096, OFF_FULL = OFF_SF + MAX_S * SF_ATOMS * 512, OFF_EMPTY = OFF_FULL + 8 * MAX_S;
-  static constexpr uint32_t OFF_SFR = OFF_EMPTY + 8 * MAX_S, OFF_TFULL = OFF_SFR + 8 * MAX_S, OFF_TEMPTY = OFF_TFULL + 16;
-  static constexpr uint32_t OFF_FINAL = OFF_TEMPTY + 16, OFF_TMEM = OFF_FINAL + 8, OFF_ABORT = OFF_TMEM + 4;
-  static constexpr uint32_t OFF_TABLE = OFF_ABORT + 4;   // and behind it, on 1024 bytes, the stages
+  static constexpr int MAX_SB = 8;                       // blocks of B's ring at most
+  static constexpr uint32_t SF_BYTES = 3 * 512;          // A's atom and up to two of B's, of a block
+  static constexpr uint32_t OFF_FULL = 0, OFF_EMPTY = OFF_FULL + 8 * MAX_SB, OFF_SFR = OFF_EMPTY + 8 * MAX_SB;
+  static constexpr uint32_t OFF_TFULL = OFF_SFR + 8 * MAX_SB, OFF_TEMPTY = OFF_TFULL + 16, OFF_FINAL = OFF_TEMPTY + 16;
+  static constexpr uint32_t OFF_TMEM = OFF_FINAL + 8, OFF_ABORT = OFF_TMEM + 4, OFF_TABLE = OFF_ABORT + 4;
   static constexpr uint32_t SF_COL = 384, SF_COLS = 12;  // TMEM with MXFP8: accumulators below, scale factors from there on
-  static_assert(SF_COL + MAX_S * SF_COLS <= kTmemAll, "TMEM");
+  static_assert(SF_COL + MAX_SB * SF_COLS <= kTmemAll, "TMEM");
   __host__ __device__ static constexpr int accumulators(bool mx, int width) { return 2 * width <= static_cast<int>(mx ? SF_COL : kTmemAll) ? 2 : 1; }
-  __host__ __device__ static constexpr uint32_t stages_at(int n_experts) { return (OFF_TABLE + table_bytes(n_experts) + 1023) & ~1023u; }
-  __host__ __device__ static constexpr uint32_t stage_bytes(int width) { return A_BYTES + static_cast<uint32_t>(width) * kDepth; }
-  static int stages(int width, int n_experts) {
-    const uint32_t n = (kSmem - 1024 - stages_at(n_experts)) / stage_bytes(width);
-    return static_cast<int>(n < MAX_S ? n : MAX_S);
+
+  // Where the rest lies: scale factors, a box of 32 x 32 elements an epilogue warp, A's ring, B's ring.
+  int width, sa, sb;
+  uint32_t sf, stg, a, b, total;
+  FewLayout(int width_, bool mx, bool fp32, int n_experts) : width(width_) {
+    auto up = [](uint32_t v) { return (v + 1023) & ~1023u; };
+    const uint32_t block = static_cast<uint32_t>(width) * kDepth + (mx ? SF_BYTES : 0), box = kEpi * (fp32 ? 4096 : 2048);
+    sf = up(OFF_TABLE + table_bytes(n_experts));
+    const uint32_t room = kSmem - 1024 - sf - box - 1024;   // alignment of the base and behind the scale factors
+    // B's ring as deep as leaves A's at most one block less (with three of A's, tiles narrower than 192 columns wait for A:
+    // 8 x 128 rows, 11008 columns, tiles of 128, 83 us instead of 72)
+    sb = MAX_SB;
+    while (sb > 4 && room < sb * block + (sb - 1) * A_BYTES) --sb;
+    sa = static_cast<int>((room - sb * block) / A_BYTES);
+    if (sa > sb) sa = sb;
+    stg = up(sf + (mx ? static_cast<uint32_t>(sb) * SF_BYTES : 0));
+    a = stg + box;
+    b = a + static_cast<uint32_t>(sa) * A_BYTES;
+    total = b + static_cast<uint32_t>(sb * width) * kDepth + 1024;
   }
 };
 
 template <int KIND>
-__global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
+__global__ void __launch_bounds__(few_threads<KIND>(), 1)
     k_grouped_few(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                   const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfb,
-                  const __grid_constant__ CUtensorMap tm_c, const GroupedParams p, const int width, const int S) {
+                  const __grid_constant__ CUtensorMap tm_c, const GroupedParams p, const FewLayout l) {
   using L = FewLayout;
   constexpr bool MX = KIND == kMx;
   extern __shared__ uint8_t smem_raw[];
@@ -464,10 +484,12 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(base_ptr + L::OFF_ABORT);
   int* const offs = reinterpret_cast<int*>(base_ptr + L::OFF_TABLE);
   int* const first = offs + p.n_experts + 1;
-  const uint32_t stages = base + L::stages_at(p.n_experts), stage_bytes = L::stage_bytes(width);
+  const int width = l.width, S = l.sb, SA = l.sa;
+  const uint32_t b_bytes = static_cast<uint32_t>(width) * kDepth;
   const int warp = warp_uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int unit = static_cast<int>(blockIdx.x), units = static_cast<int>(gridDim.x);
   const int tiles_n = (p.N + width - 1) / width, ACC = L::accumulators(MX, width);
+  constexpr int kFetchA = kCopier + (MX ? 1 : 0);
 
   if (threadIdx.x == 0) {
     if (p.loads) {
@@ -507,41 +529,68 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
     }
   };
 
-  if (warp == 0 && lane == 0) {
-    // ------------------------------------------------ producer
-    int issued = 0, stage = 0, e = 0;
+  if (warp == 0) {
+    // ------------------------------------------------ B and its scale factors (the whole warp)
+    int uses = 0, stage = 0, e = 0;
     uint32_t phase = 0;
     bool ok = true;
-    const int a_atoms = p.a_cols / kDepth, b_atoms = p.b_cols_all / kDepth, b_last = p.b_rows_all / kRows - 1;
+    const int b_atoms = p.b_cols_all / kDepth, b_last = p.b_rows_all / kRows - 1;
     for (int t = unit; t < ntiles && ok; t += units) {
       const Tile w = tile_at(t, e);
-      // atoms of B's scales: 128 rows each, from the one that holds the tile's first row
-      const int atom = w.b_row / kRows, n_atoms = (w.b_row % kRows + width + kRows - 1) / kRows;
-      const uint32_t tx = stage_bytes + (MX ? 512u * static_cast<uint32_t>(1 + n_atoms) : 0u);
-      for (int kb = 0; kb < w.nkb; ++kb) {
-        if (!mbar_wait(base + L::OFF_EMPTY + 8 * stage, phase ^ 1u, p.err, kErrTimeoutStage, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const uint32_t full = base + L::OFF_FULL + 8 * stage, sa = stages + stage * stage_bytes;
-        const int ak = w.a_kb + kb, bk = w.b_kb + kb;
-        mbar_arrive_expect_tx(full, tx);
-        tma_load_2d(sa + L::A_BYTES, &tm_b, bk * kDepth, w.b_row, full);
-        tma_load_2d(sa, &tm_a, ak * kDepth, w.a_row, full);
+      const int nkb = warp_uniform(w.nkb), b_row = warp_uniform(w.b_row);
+      // atoms of B's scales: 128 rows each, from the one that holds the tile's first row; past B's last row its last atoms
+      // (those columns are not stored)
+      const bool two = b_row % kRows + width > kRows;
+      int atom = warp_uniform(2 * (b_row / kRows * b_atoms + w.b_kb)), x = warp_uniform(w.b_kb) * kDepth;
+      const int second = b_row / kRows < b_last ? 2 * b_atoms : 0;
+      const uint32_t tx = L::A_BYTES + b_bytes + (MX ? (two ? 1536u : 1024u) : 0u);
+      for (int kb = 0; kb < nkb; ++kb) {
+        ok = warp_uniform(mbar_wait(base + L::OFF_EMPTY + 8 * stage, phase ^ 1u, p.err, kErrTimeoutStage, abort_flag));
+        if (!ok) break;
+        const uint32_t full = base + L::OFF_FULL + 8 * stage, sf = base + l.sf + static_cast<uint32_t>(stage) * L::SF_BYTES;
+        mbar_arrive_expect_tx_warp(full, tx);
+        tma_load_2d_warp(base + l.b + static_cast<uint32_t>(stage) * b_bytes, &tm_b, x, b_row, full);
         if (MX) {
-          const uint32_t sf = base + L::OFF_SF + static_cast<uint32_t>(stage) * (L::SF_ATOMS * 512);
-          tma_load_2d(sf, &tm_sfa, 0, 2 * (w.a_row / kRows * a_atoms + ak), full);
-          for (int h = 0; h < n_atoms; ++h)   // past B's last row: its last atoms (those columns are not stored)
-            tma_load_2d(sf + 512 + 512 * h, &tm_sfb, 0, 2 * (min(atom + h, b_last) * b_atoms + bk), full);
+          tma_load_2d_warp(sf + 512, &tm_sfb, 0, atom, full);
+          if (two) tma_load_2d_warp(sf + 1024, &tm_sfb, 0, atom + second, full);
         }
-        ++issued;
+        x += kDepth;
+        atom += 2;
+        ++uses;
         next(stage, phase);
       }
     }
-    // the loads land before the CTA exits
+    // the loads land before the CTA exits, A's of the same blocks too
     for (int s = 0; s < S; ++s) {
-      const int n = issued / S + (s < issued % S ? 1 : 0);
+      const int n = uses / S + (s < uses % S ? 1 : 0);
       if (n > 0) mbar_wait(base + L::OFF_FULL + 8 * s, static_cast<uint32_t>(n - 1) & 1u, p.err, kErrTimeoutTmaLoad, nullptr);
+    }
+  } else if (warp == kFetchA) {
+    // ------------------------------------------------ A and its scale factors (the whole warp)
+    int stage = 0, slot = 0, old = 0, fill = 0, e = 0;   // old: the stage of the block whose MMAs make room
+    uint32_t phase = 0, old_phase = 0;
+    bool ok = true;
+    const int a_atoms = p.a_cols / kDepth;
+    for (int t = unit; t < ntiles && ok; t += units) {
+      const Tile w = tile_at(t, e);
+      const int nkb = warp_uniform(w.nkb), a_row = warp_uniform(w.a_row);
+      int atom = warp_uniform(2 * (a_row / kRows * a_atoms + w.a_kb)), x = warp_uniform(w.a_kb) * kDepth;
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (fill < SA) {
+          ++fill;
+        } else {
+          ok = warp_uniform(mbar_wait(base + L::OFF_EMPTY + 8 * old, old_phase, p.err, kErrTimeoutStage, abort_flag));
+          if (!ok) break;
+          next(old, old_phase);
+        }
+        const uint32_t full = base + L::OFF_FULL + 8 * stage;
+        tma_load_2d_warp(base + l.a + static_cast<uint32_t>(slot) * L::A_BYTES, &tm_a, x, a_row, full);
+        if (MX) tma_load_2d_warp(base + l.sf + static_cast<uint32_t>(stage) * L::SF_BYTES, &tm_sfa, 0, atom, full);
+        x += kDepth;
+        atom += 2;
+        slot = slot + 1 == SA ? 0 : slot + 1;
+        next(stage, phase);
+      }
     }
   } else if (MX && warp == kCopier) {
     // ------------------------------------------------ scale factors into TMEM (the whole warp)
@@ -556,7 +605,7 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
         if (!ok) break;
         tc_fence_after();
         // the stage's columns were last read by MMAs that finished before the stage was refilled
-        const uint32_t sf = base + L::OFF_SF + static_cast<uint32_t>(stage) * (L::SF_ATOMS * 512);
+        const uint32_t sf = base + l.sf + static_cast<uint32_t>(stage) * L::SF_BYTES;
         const uint32_t col = tmem + L::SF_COL + static_cast<uint32_t>(stage) * L::SF_COLS;
         for (int h = 0; h <= n_atoms; ++h) tc_cp_32x128b_warpx4_warp(col + 4 * h, sdesc_rows16(sf + 512 * h));
         tc_commit_warp(base + L::OFF_SFR + 8 * stage);
@@ -570,7 +619,7 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
     const uint32_t idesc = (static_cast<uint32_t>(p.e5m2_a) << 7) | (static_cast<uint32_t>(p.e5m2_b) << 10) |
                            (static_cast<uint32_t>(width >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24) |
                            (MX ? 1u << 23 : 1u << 4);
-    int stage = 0, e = 0;
+    int stage = 0, slot_a = 0, e = 0;
     uint32_t phase = 0, acc_it = 0;
     bool ok = true;
     for (int t = unit; t < ntiles && ok; t += units) {
@@ -590,7 +639,7 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
             mbar_wait(base + (MX ? L::OFF_SFR : L::OFF_FULL) + 8 * stage, phase, p.err, kErrTimeoutTmaLoad, abort_flag));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sa = stages + stage * stage_bytes, sb = sa + L::A_BYTES;
+        const uint32_t sa = base + l.a + static_cast<uint32_t>(slot_a) * L::A_BYTES, sb = base + l.b + static_cast<uint32_t>(stage) * b_bytes;
         const uint32_t sfa = tmem + L::SF_COL + static_cast<uint32_t>(stage) * L::SF_COLS, sfb = sfa + sfb_col;
 #pragma unroll
         for (int k = 0; k < kDepth / kUmmaDepth; ++k) {
@@ -602,6 +651,7 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
             tc_mma_f8f6f4_warp(d, da, db, idesc, more);
         }
         tc_commit_warp(base + L::OFF_EMPTY + 8 * stage);
+        slot_a = slot_a + 1 == SA ? 0 : slot_a + 1;
         next(stage, phase);
       }
       if (!ok) break;
@@ -614,8 +664,8 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
     // ------------------------------------------------ epilogue
     const int q = warp & 3, h = (warp - 2) >> 2;   // TMEM lane quarter; chunks h, h + 2, ... of 32 columns
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    const uint32_t stg = base + L::OFF_STG + static_cast<uint32_t>(warp - 2) * 4096u;
     const bool fp32 = p.out_fp32 != 0;
+    const uint32_t stg = base + l.stg + static_cast<uint32_t>(warp - 2) * (fp32 ? 4096u : 2048u);
     uint32_t acc_it = 0;
     int e = 0;
     for (int t = unit; t < ntiles; t += units) {
@@ -723,11 +773,10 @@ cudaError_t run_few(const GroupedParams& p, const GroupedMaps& m, int width, int
   static std::atomic<bool> attr_done[kMaxDevices] = {};
   const cudaError_t e = ensure_smem_limit(kern, static_cast<int>(kSmem), attr_done);
   if (e != cudaSuccess) return e;
-  const int stages = FewLayout::stages(width, p.n_experts);
-  const size_t smem = FewLayout::stages_at(p.n_experts) + static_cast<size_t>(stages) * FewLayout::stage_bytes(width) + 1024;
+  const FewLayout l(width, KIND == kMx, p.out_fp32 != 0, p.n_experts);
   const int64_t units = tiles < num_sms ? (tiles < 1 ? 1 : tiles) : num_sms;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(units)), dim3(grouped_threads<KIND>()), smem, s, 1, m.a, m.b, m.sfa, m.sfb, m.c, p,
-                    width, stages);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(units)), dim3(few_threads<KIND>()), l.total, s, 1, m.a, m.b, m.sfa, m.sfb, m.c, p,
+                    l);
 }
 
 // the most tiles that a call can have, whatever its offsets are

@@ -445,7 +445,7 @@ __device__ __forceinline__ void tc_commit_pair_mc(uint32_t bar, uint16_t cta_mas
                : "memory");
 }
 
-// ------------------------------------------------------------------ tcgen05 from a whole warp
+// ------------------------------------------------------------------ tcgen05 and TMA from a whole warp
 // The same operations issued by a converged warp, of which one elected lane acts.  Their operands are then the
 // same for the whole warp and stay in uniform registers; issued from a branch that only one lane takes, every
 // operand is moved there first, and a thread needs ~75 cycles an MMA.
@@ -517,6 +517,22 @@ __device__ __forceinline__ void tc_commit_pair_mc_warp(uint32_t bar, uint16_t ct
       "elect.sync _|q, 0xffffffff;\n\t"
       "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(bar),
       "h"(cta_mask)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_warp(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}\n" ::"r"(dst),
+      "l"(tm), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_warp(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}\n" ::"r"(bar),
+      "r"(bytes)
       : "memory");
 }
 // What lane 0 has, as a value that the compiler knows to be the whole warp's.
