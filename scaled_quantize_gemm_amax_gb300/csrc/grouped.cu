@@ -9,9 +9,10 @@
 // Per-tensor scales multiply the accumulator in the epilogue; MXFP8's are applied by the tensor
 // core (kind::mxf8f6f4.block_scale).  Accumulation is binary32 in TMEM.
 //
-// Structure of a CTA, as the ungrouped product's: warp 0 fetches tiles by TMA into a ring of
-// stages, warp 1 issues the MMAs, with MXFP8 a further warp copies scale factors into TMEM, eight
-// warps drain the accumulator.  Every wait is bounded (ptx.cuh).
+// Structure of a CTA: two warps fetch A's and B's blocks by TMA into a ring of stages, one issues the
+// MMAs, with MXFP8 a further one copies scale factors into TMEM, eight drain the accumulator.  The four work
+// as converged warps with uniform operands: a 128-deep block issued by single lanes of a branch took 510 cycles, so
+// 405 (per-tensor; its four MMAs 256 to 550).  Every wait is bounded (ptx.cuh).
 #include <atomic>
 #include <cstring>
 
@@ -121,10 +122,10 @@ __device__ __forceinline__ void zero_tail(const GroupedParams& p, int from, int 
 __host__ __device__ constexpr uint32_t table_bytes(int n_experts) { return 8u * static_cast<uint32_t>(n_experts + 1); }   // offs, first
 constexpr uint32_t kSmem = 232448;
 
-// warps: producer, MMA issuer, kEpi epilogue warps, and with MXFP8 the scale factors' copier
+// warps: B's producer, MMA issuer, kEpi epilogue warps, A's producer, and with MXFP8 the scale factors' copier
 template <int KIND>
-constexpr int grouped_threads() { return 32 * (2 + kEpi + (KIND == kMx ? 1 : 0)); }
-constexpr int kCopier = 2 + kEpi;
+constexpr int grouped_threads() { return 32 * (3 + kEpi + (KIND == kMx ? 1 : 0)); }
+constexpr int kFetchA = 2 + kEpi, kCopier = 3 + kEpi;
 
 // ------------------------------------------------------------------ many rows: CTA pairs
 // Two CTAs share a 256 x 256 tile (cta_group::2), each with its 128 rows of A and half of B's.
@@ -206,8 +207,9 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
 
   auto tile_at = [&](int t, int& e) { return tile_of<TM>(p, offs, first, BN, tiles_n, static_cast<int>(rank), t, e); };
 
-  if (warp == 0 && lane == 0) {
-    // ------------------------------------------------ producer
+  if (warp == 0 || warp == kFetchA) {
+    // ------------------------------------------------ producers (whole warps): B, and A, each with its scale factors
+    const bool fetch_b = warp == 0;
     int issued = 0, stage = 0, e = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -215,27 +217,29 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
     const int a_atoms = p.a_cols / kDepth, b_atoms = p.b_cols_all / kDepth, b_last = p.b_rows_all / kRows - 1;
     for (int t = unit; t < ntiles && ok; t += units) {
       const Tile w = tile_at(t, e);
-      for (int kb = 0; kb < w.nkb; ++kb) {
-        if (!mbar_wait(base + L::OFF_EMPTY + 8 * stage, phase ^ 1u, p.err, kErrTimeoutStage, abort_flag)) {
-          ok = false;
-          break;
-        }
+      const int nkb = warp_uniform(w.nkb), a_row = warp_uniform(w.a_row), b_row = warp_uniform(w.b_row);
+      int x = warp_uniform(fetch_b ? w.b_kb : w.a_kb) * kDepth;
+      int atom = warp_uniform(2 * (fetch_b ? b_row / kRows * b_atoms + w.b_kb : a_row / kRows * a_atoms + w.a_kb));
+      // a tile that hangs over B's last row takes its last atoms twice (those columns are not stored)
+      const int second = b_row / kRows < b_last ? 2 * b_atoms : 0;
+      for (int kb = 0; kb < nkb; ++kb) {
+        ok = warp_uniform(mbar_wait(base + L::OFF_EMPTY + 8 * stage, phase ^ 1u, p.err, kErrTimeoutStage, abort_flag));
+        if (!ok) break;
         const uint32_t full = base + L::OFF_FULL + 8 * stage, sig = mapa_shared(full, 0);
         const uint32_t sa = base + stage * L::STAGE, sf = base + L::OFF_SF + stage * L::SF;
-        const int ak = w.a_kb + kb, bk = w.b_kb + kb;
-        if (leader) mbar_arrive_expect_tx(full, L::TX);
-        tma_load_2d_pair(sa, &tm_a, ak * kDepth, w.a_row, sig);
-        tma_load_2d_pair(sa + L::A_BYTES, &tm_b, bk * kDepth, w.b_row + static_cast<int>(rank) * (BN / 2), sig);
-        if (MX) {
-          const int atom_a = w.a_row / kRows * a_atoms + ak;
-          tma_load_2d_pair(sf, &tm_sfa, 0, 2 * atom_a, sig);
-#pragma unroll
-          for (int h = 0; h < L::B_ATOMS; ++h) {
-            // a tile that hangs over B's last row takes its last atoms (those columns are not stored)
-            const int atom_b = min(w.b_row / kRows + h, b_last) * b_atoms + bk;
-            tma_load_2d_pair(sf + 512 + 512 * h, &tm_sfb, 0, 2 * atom_b, sig);
+        if (fetch_b) {
+          if (leader) mbar_arrive_expect_tx_warp(full, L::TX);
+          tma_load_2d_pair_warp(sa + L::A_BYTES, &tm_b, x, b_row + static_cast<int>(rank) * (BN / 2), sig);
+          if (MX) {
+            tma_load_2d_pair_warp(sf + 512, &tm_sfb, 0, atom, sig);
+            tma_load_2d_pair_warp(sf + 1024, &tm_sfb, 0, atom + second, sig);
           }
+        } else {
+          tma_load_2d_pair_warp(sa, &tm_a, x, a_row, sig);
+          if (MX) tma_load_2d_pair_warp(sf, &tm_sfa, 0, atom, sig);
         }
+        x += kDepth;
+        atom += 2;
         ++issued;
         if (++stage == S) {
           stage = 0;
@@ -429,9 +433,6 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
 }
 
 // ------------------------------------------------------------------ few rows: one CTA a tile
-// the pairs' warps, and one more that fetches A
-template <int KIND>
-constexpr int few_threads() { return grouped_threads<KIND>() + 32; }
 // With few tiles the product is bound by streaming the experts' weights once, by every SM: a CTA takes a
 // 128 x width tile, and the host picks the width for which the tiles divide evenly: a multiple of 32, with MXFP8 of
 // 64, since a tile's scale factors then start at an even column of TMEM.
@@ -472,7 +473,7 @@ struct FewLayout {
 };
 
 template <int KIND>
-__global__ void __launch_bounds__(few_threads<KIND>(), 1)
+__global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
     k_grouped_few(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                   const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfb,
                   const __grid_constant__ CUtensorMap tm_c, const GroupedParams p, const FewLayout l) {
@@ -489,7 +490,6 @@ __global__ void __launch_bounds__(few_threads<KIND>(), 1)
   const int warp = warp_uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int unit = static_cast<int>(blockIdx.x), units = static_cast<int>(gridDim.x);
   const int tiles_n = (p.N + width - 1) / width, ACC = L::accumulators(MX, width);
-  constexpr int kFetchA = kCopier + (MX ? 1 : 0);
 
   if (threadIdx.x == 0) {
     if (p.loads) {
@@ -775,7 +775,7 @@ cudaError_t run_few(const GroupedParams& p, const GroupedMaps& m, int width, int
   if (e != cudaSuccess) return e;
   const FewLayout l(width, KIND == kMx, p.out_fp32 != 0, p.n_experts);
   const int64_t units = tiles < num_sms ? (tiles < 1 ? 1 : tiles) : num_sms;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(units)), dim3(few_threads<KIND>()), l.total, s, 1, m.a, m.b, m.sfa, m.sfb, m.c, p,
+  return launch_pdl(kern, dim3(static_cast<unsigned>(units)), dim3(grouped_threads<KIND>()), l.total, s, 1, m.a, m.b, m.sfa, m.sfb, m.c, p,
                     l);
 }
 
