@@ -557,8 +557,8 @@ fp8_status fp8_rms_norm_workspace(int64_t rows, int64_t cols, int64_t* bytes);
  * Operands are FP8, row-major and dense, with the recipes (ra, rb) = (FP8_TENSOR, FP8_TENSOR) or
  * two of FP8_MX_1x32_TILED and FP8_MX_1x32_FLOOR_TILED, scales as fp8_cast_transpose writes them
  * (other pairings FP8_ERR_UNSUPPORTED).  Accumulation is binary32; C is rounded once.  M, N, K and
- * capacity are multiples of 128, and they, n_experts times M, N or K and the number of 256 x 256
- * tiles below 2^31 (FP8_ERR_SHAPE).  Matrices and tiled scales are 16-byte aligned.
+ * capacity are multiples of 128, and they, n_experts times M, N or K and the number of 128 x 32
+ * tiles that the outputs could have below 2^31 (FP8_ERR_SHAPE).  Matrices and tiled scales are 16-byte aligned.
  */
 typedef enum {
   FP8_STACKED_ROWS = 0,  /* the experts' [N, K] one below the other: [n_experts * N, K] */
@@ -612,8 +612,8 @@ typedef struct {
  *   max_norm    >= 0 (infinity scales nothing)
  *   workspace   device, 8-byte aligned, fp8_grad_norm_workspace bytes; needs no initialisation
  *   norm        device, float[1]
- * Squares are binary32 within 64 elements and binary64 beyond, or binary64 where binary32's range
- * ends: no element is too large or too small to count.  n_grads == 0 gives 0.  Sizes sum to less
+ * Squares are summed in binary32 within 32 elements and in binary64 beyond, or throughout where
+ * binary32's range ends: no element is too large or too small to count.  n_grads == 0 gives 0.  Sizes sum to less
  * than 2^40 elements (FP8_ERR_SHAPE).
  */
 fp8_status fp8_grad_norm(const fp8_gradient* grads, int32_t n_grads, void* workspace, int64_t workspace_bytes, float* norm,

@@ -1096,7 +1096,7 @@ fp8_status grouped(GroupedParams& p, const uint8_t* A, fp8_format fa, fp8_recipe
                    int64_t c_rows, fp8_out_dtype out, cudaStream_t stream) {
   if (a_rows > kMaxDim || a_cols > kMaxDim || b_rows > kMaxDim || b_cols > kMaxDim || c_rows > kMaxDim) return FP8_ERR_SHAPE;
   const int64_t tiles_m = p.depth ? c_rows / 128 : p.capacity / 128 + p.n_experts;
-  if (tiles_m * (p.N / 64) > kMaxDim) return FP8_ERR_SHAPE;
+  if (tiles_m * (p.N / 32) > kMaxDim) return FP8_ERR_SHAPE;   // the narrowest tiles are counted in 32 bits
   if (p.offsets == nullptr || p.c == nullptr) return FP8_ERR_INVALID_ARG;
   const bool loads = a_rows > 0 && a_cols > 0 && b_rows > 0 && b_cols > 0;
   const bool mx = p.kind == kMx;

@@ -1,7 +1,7 @@
 // clip.cu -- the 2-norm over many tensors, and the tensors scaled so that it stays below a limit.
 //
 //   norm = sqrt(sum over all elements of g^2),  out = g min(1, max_norm / (norm + 1e-6))
-// The tensors' addresses and sizes travel in the launch's parameters, a table of up to kTable tensors.
+// The tensors' addresses and sizes travel in the launch's parameters, a table of up to kMostTensors.
 // The tensors, one behind the other, are cut into pieces of a few KB, and every block takes a run of
 // consecutive ones, so of most tensors a whole stretch; the host says at which tensor a run starts.  The
 // second pass takes a run from its end, of which the first has left the most in L2.

@@ -13,9 +13,10 @@ namespace fp8q {
 
 namespace {
 
-// warps of a block at V values a lane: 80 registers a thread, 64 at 8 values
-template <int V>
-constexpr int kBlockWarps = V == 8 ? 32 : 24;
+// warps of a block at V values a lane: 80 registers a thread, 64 at 8 values; unaligned binary32 at 32 values, which
+// only the widest rows take, spills at 80 and has 128
+template <typename T, bool VECTOR, int V>
+constexpr int kBlockWarps = V == 8 ? 32 : (V == 32 && !VECTOR && sizeof(T) == 4 ? 16 : 24);
 // Bytes of a block's rows and of its stages (rms_plan).  With a residual, bf16 and 1x128 codes, 65536x4096: 64 KB 275 us,
 // 96 KB 300, two stages of 96 KB 319; 8192x4096 39.7, 39.8 and 43.5.  Unaligned rows are bound by their instructions and take
 // the warps that fit: 8192x4099 65 us with 96 KB, 73 with 64.
@@ -191,12 +192,12 @@ __global__ void __launch_bounds__(kThreads) k_rms_any(const RmsParams p) {
 // Rows of up to kMostCols columns, V values a lane; a group of `warps` warps holds a row, and a row costs
 // one barrier.
 template <typename T, bool VECTOR, int V>
-__global__ void __launch_bounds__(kBlockWarps<V> * 32) k_rms(const RmsParams p, const int warps, const int stages, const int ring) {
+__global__ void __launch_bounds__(kBlockWarps<T, VECTOR, V> * 32) k_rms(const RmsParams p, const int warps, const int stages, const int ring) {
   using P = Piece<T, VECTOR>;
   constexpr int E = P::E, J = V / E, kCols = 32 * V;
   using Part = RowPart<P, kCols, VECTOR, T>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float red[2][kBlockWarps<V>];
+  __shared__ float red[2][kBlockWarps<T, VECTOR, V>];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / warps, w_in = warp - group * warps;
   const int n_groups = (blockDim.x >> 5) / warps, step = gridDim.x * n_groups;
   const int rows = static_cast<int>(p.rows), cols = static_cast<int>(p.cols);
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kBlockWarps<V> * 32) k_rms(const RmsParams p, 
 template <typename T, bool VECTOR, int V>
 cudaError_t run_rms(const RmsParams& p, int num_sms, cudaStream_t s) {
   const int part = RowPart<Piece<T, VECTOR>, 32 * V, VECTOR, T>::kBytes;
-  const NormPlan n = rms_plan(p.rows, p.cols, 32 * V, kBlockWarps<V>, part * (p.res != nullptr ? 2 : 1), kMost<VECTOR>, kInFlight, 1,
+  const NormPlan n = rms_plan(p.rows, p.cols, 32 * V, kBlockWarps<T, VECTOR, V>, part * (p.res != nullptr ? 2 : 1), kMost<VECTOR>, kInFlight, 1,
                               num_sms);
   static std::atomic<bool> done[kMaxDevices];
   const cudaError_t e = ensure_smem_limit(k_rms<T, VECTOR, V>, kNormSmem, done);
@@ -317,13 +318,16 @@ cudaError_t run_rms(const RmsParams& p, int num_sms, cudaStream_t s) {
                     n.warps, n.stages, n.ring);
 }
 
-// Values a lane as the layer norm's: 32 halve what a row costs besides its values; 16 where that would
-// leave lanes empty (up to 512 columns) or where a row's latency counts and there are warps to spare;
-// 8 for rows of up to 256 columns.
+// Values a lane: 8 for rows of up to 256 columns; 32 halve what a row costs besides its values; 16 where that would leave
+// lanes empty (up to 512 columns) or where a row's latency counts and there are warps to spare, and for unaligned rows,
+// bound by their instructions, while a row's ends cost more than its middle: binary32 (4096x4099 with a residual 45 us, 73 with
+// 32 values; 2048x9001 50 and 77) and bf16 up to 3584 columns (16384x1003 42 and 52, 8192x3001 50 and 51; 8192x4099 74 and 65).
 template <typename T, bool VECTOR>
 cudaError_t run_rms(const RmsParams& p, int num_sms, cudaStream_t s) {
+  constexpr int64_t kMost16 = kBlockWarps<T, VECTOR, 16> * 512, kMostUnaligned = sizeof(T) == 4 ? kMost16 : 7 * 512;
   if (p.cols <= 256) return run_rms<T, VECTOR, 8>(p, num_sms, s);
-  if (p.cols <= 512 || (p.rows <= num_sms && p.cols <= kBlockWarps<16> * 512)) return run_rms<T, VECTOR, 16>(p, num_sms, s);
+  if (p.cols <= 512 || (p.rows <= num_sms && p.cols <= kMost16) || (!VECTOR && p.cols <= kMostUnaligned))
+    return run_rms<T, VECTOR, 16>(p, num_sms, s);
   return run_rms<T, VECTOR, 32>(p, num_sms, s);
 }
 
