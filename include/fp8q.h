@@ -609,7 +609,7 @@ typedef struct {
  * nothing is written when the factor is 1.  A NaN norm makes every output NaN, an infinite one makes
  * finite elements 0.
  *   grads       host, [n_grads]: read before the call returns; gradients must not overlap
- *   max_norm    >= 0 (infinity scales nothing)
+ *   max_norm    >= 0 (infinity scales nothing, where the norm is finite)
  *   workspace   device, 8-byte aligned, fp8_grad_norm_workspace bytes; needs no initialisation
  *   norm        device, float[1]
  * Squares are summed in binary32 within 32 elements and in binary64 beyond, or throughout where

@@ -369,6 +369,7 @@ int fill(Table<N>& t, const ClipTensor* tensors, int64_t from, int64_t n, int le
     }
   } while (pieces >= (int64_t{1} << 30));
   t.of[count] = {nullptr, nullptr, 0, pieces};
+  if (count == 0) t.of[1] = t.of[0];   // a block reads its first tensor's entry and the next
   t.pieces = static_cast<int>(pieces);
   const int64_t blocks = pieces < least ? least : (pieces < most ? pieces : most);
   int k = 0;

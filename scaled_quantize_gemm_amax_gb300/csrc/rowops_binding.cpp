@@ -774,6 +774,11 @@ PyObject* clip_grad_norm(PyObject* const* v) {
               : p_fp8_grad_norm(table.data(), count, whole.data_ptr(), bytes, ptr<float>(norm), stream);
   }
   check(st, clip ? "fp8_clip_grad_norm" : "fp8_grad_norm");
+  // autograd learns of what was written, as of any operation in place
+  for (Py_ssize_t i = 0; clip && i < n; ++i) {
+    const at::Tensor& o = needed(outs[i], "out");
+    if (!o.is_inference()) o.unsafeGetTensorImpl()->bump_version();
+  }
   return wrap(norm);
 }
 

@@ -184,3 +184,32 @@ def test_refuses_shared_memory():
         assert torch.equal(b, was)
     fq.clip_grad_norm([b[500:], b[:500]], 0.1, out=[b[500:], b[:500]])   # in place, in another order
     assert abs(float(fq.grad_norm([b, b])) - math.sqrt(2) * float(b.double().norm())) < 1e-5   # reading twice is fine
+
+
+def test_a_write_is_seen_by_autograd():
+    """A tensor that a backward pass still needs and that was clipped meanwhile is an error there, not a wrong gradient."""
+    for out in (False, True):
+        w, g, o = torch.randn(50, device="cuda", requires_grad=True), torch.randn(50, device="cuda"), torch.randn(50, device="cuda")
+        loss = (w * (o if out else g)).sum()
+        fq.grad_norm([g])
+        fq.clip_grad_norm([g], 0.1, out=[o] if out else None)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with torch.inference_mode():
+        g = torch.ones(50, device="cuda")
+    assert abs(float(fq.clip_grad_norm([g], 1.0)) - math.sqrt(50)) < 1e-5 and float(g[0]) < 0.2
+
+
+def test_none_and_empty():
+    """No gradient, and only ones without elements, at both sizes of a launch's table."""
+    norm = torch.ones(1, device="cuda")
+    ws = torch.empty(fq.fp8_grad_norm_workspace(200), dtype=torch.uint8, device="cuda")
+    for n in (0, 1, 64, 200):
+        grads = [torch.empty(0, device="cuda") for _ in range(n)]
+        for _ in range(3):
+            norm.fill_(1.0)
+            fq.fp8_clip_grad_norm(grads, grads, 0.1, ws, norm)
+            assert float(norm) == 0
+            norm.fill_(1.0)
+            fq.fp8_grad_norm(grads, ws, norm)
+            assert float(norm) == 0
