@@ -18,7 +18,9 @@ Entry points with the C names take tensors (or None for NULL) and raise
 ``fp8_debug_index_check``; and the row operators between the linear layers,
 ``fp8_layer_norm``, ``fp8_layer_norm_backward``, ``fp8_gated_act``,
 ``fp8_gated_act_backward``, ``fp8_moe_route``, ``fp8_moe_dispatch``, ``fp8_moe_combine``,
-``fp8_moe_combine_backward`` (with ``fp8_layer_norm_workspace`` and ``fp8_moe_capacity``).
+``fp8_moe_combine_backward`` (with ``fp8_layer_norm_workspace`` and ``fp8_moe_capacity``);
+and the operators of an expert step, ``fp8_rms_norm``, ``fp8_rms_norm_backward``, ``fp8_grouped_gemm``,
+``fp8_grouped_wgrad``, ``fp8_grad_norm``, ``fp8_clip_grad_norm``.
 ``cast_transpose`` / ``dequantize`` / ``scaled_gemm`` / ``scaled_gemm_amax`` /
 ``layer_norm`` / ``gated_act`` / ``moe_route`` ... are allocation helpers
 over them; ``linear`` holds the FP8 linear layer and the autocast scope built

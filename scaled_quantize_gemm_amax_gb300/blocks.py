@@ -224,7 +224,8 @@ class FP8MoEBlock(torch.nn.Module):
     norm: "layer" or "rms".  grouped=False: a pair of FP8Linear an expert, and one host read of
     the segment starts per pass, which are the GEMMs' row counts.  grouped=True: two
     FP8GroupedLinear (per-tensor or MXFP8 recipes), without a host read, so that a pass can be
-    captured into a CUDA graph."""
+    captured into a CUDA graph (as torch asks of any backward pass, after a few eager steps on another
+    stream and while nothing keeps an eager graph of the same parameters alive: drop its outputs first)."""
 
     def __init__(self, hidden: int, ffn: int, n_experts: int, k: int, act: Activation = Activation.SILU,
                  checkpoint: Format | None = Format.E4M3, device=None, norm: str = "layer", grouped: bool = False):

@@ -12,7 +12,7 @@
 // Structure of a CTA: two warps fetch A's and B's blocks by TMA into a ring of stages, one issues the
 // MMAs, with MXFP8 a further one copies scale factors into TMEM, eight drain the accumulator.  The four work
 // as converged warps with uniform operands: a 128-deep block issued by single lanes of a branch took 510 cycles, so
-// 405 (per-tensor; its four MMAs 256 to 550).  Every wait is bounded (ptx.cuh).
+// 405 (128 rows, per-tensor; its four MMAs 256 to 550), and 64 experts of few rows 163 us, so 145.  Every wait is bounded (ptx.cuh).
 #include <atomic>
 #include <cstring>
 
@@ -128,7 +128,12 @@ constexpr int grouped_threads() { return 32 * (3 + kEpi + (KIND == kMx ? 1 : 0))
 constexpr int kFetchA = 2 + kEpi, kCopier = 3 + kEpi;
 
 // ------------------------------------------------------------------ many rows: CTA pairs
-// Two CTAs share a 256 x 256 tile (cta_group::2), each with its 128 rows of A and half of B's.
+// Two CTAs share a 256 x 256 tile (cta_group::2), each with its 128 rows of A and half of B's.  Tiles go round the pairs in
+// the order of the list, 16 of an expert's row tiles walking its columns together.
+// Bound by the tensor core: 8 x 2176 rows, 4096 -> 11008, MXFP8 477 us (3290 TFLOP/s, 0.87 of twice the measured BF16
+// rate), per-tensor 450 (3490); a pair's 128-deep block takes 560 to 620 cycles
+// with all pairs at work, 490 alone.  An expert whose rows are an odd number of 128s leaves half of its last tile empty.
+// 64 experts of 256 rows, 2048 -> 4096, per-tensor 109 us (0.96 of HBM).
 constexpr int kPairCols = 256;
 // S stages: 6 with per-tensor scales and up to 200 experts (their table of segments shares the memory), else 5.  (8192
 // tokens at 2 of 8 experts 452 -> 443 us, 64 experts of 256 rows 112 -> 110.6; with 4 stages 478 and 121.)
@@ -433,8 +438,9 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
 }
 
 // ------------------------------------------------------------------ few rows: one CTA a tile
-// With few tiles the product is bound by streaming the experts' weights once, by every SM: a CTA takes a
-// 128 x width tile, and the host picks the width for which the tiles divide evenly: a multiple of 32, with MXFP8 of
+// With few tiles the product is bound by streaming the experts' weights once, by every SM (one token at 2 of 8
+// experts, 4096 -> 11008, MXFP8 20.7 us, 4.7 TB/s; 8 x 128 rows 67, 5.8 TB/s; 4 us are launch, first loads and the way out):
+// a CTA takes a 128 x width tile, and the host picks the width for which the tiles divide evenly: a multiple of 32, with MXFP8 of
 // 64, since a tile's scale factors then start at an even column of TMEM.
 //
 // What the stream of weights needs is bytes on their way (13 MB over all SMs), so B's blocks have a ring of
@@ -793,9 +799,10 @@ int64_t most_tiles(const GroupedParams& p, int tile_rows, int tile_cols) {
 // The tile width of a call: 0 for CTA pairs, else that of one CTA's 128-row tiles: what takes the fewest cycles a
 // 128-deep block, rounds of tiles times a tile's.  A pair's tile is bound by its four MMAs (~175 each); a tile of
 // one CTA by what it fetches, A's 128 rows and its width of B's at 48 bytes a cycle, and where TMEM holds one
-// accumulator, by a seventh more.  One segment of 128 rows each (us, pairs | one CTA at the best width and at 128;
-// MXFP8, K = 4096): 2 x 11008 columns 32.5 | 22.2, 29.1; 8 x 11008 78 | 72, 72; 16 x 4096 63 | 57, 58.  Segments of 256:
-// 16 x 4096 65 | 78, 82; of 384: 3 x 4096 29.5 | 23.6, 25.7; one of 1024, 4096 columns 17.3 | 21.9, 24.9.
+// accumulator, by a seventh more.  One segment of 128 rows each (us, pairs | one CTA at the rule's width and at 128;
+// MXFP8, K = 4096): 2 x 11008 columns 32.5 | 20.7, 25.3; 8 x 11008 73 | 66, 65; 16 x 4096 63 | 53, 53.  Pairs by the rule (us,
+// pairs | one CTA at the best width): 16 segments of 256, 4096 columns 62 | 64; one of 1024 16.2 | 17.1; 64 of 128 to 384,
+// K = 2048, 127 | 126; three of 384, all odd where the rule expects half of them to be, 27.8 | 18.9.
 int grouped_width(const GroupedParams& p, int num_sms) {
   int64_t blocks, pairs;   // tiles of 128 and of 256 rows, for each of tile columns
   if (p.depth) {
@@ -803,7 +810,7 @@ int grouped_width(const GroupedParams& p, int num_sms) {
     pairs = static_cast<int64_t>(p.n_experts) * ((p.M / kRows + 1) / 2);
   } else {
     // the capacity has room for 127 rows of padding an expert, of which half are expected; so are as many odd
-    // segments as even ones
+    // segments as even ones (what they are is known on the device only)
     const int64_t room = p.capacity / kRows, used = p.n_experts < room ? p.n_experts : room;
     blocks = room - (room - used < used / 2 ? room - used : used / 2);
     pairs = (blocks + used / 2) / 2 > used ? (blocks + used / 2) / 2 : used;
