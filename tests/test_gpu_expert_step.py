@@ -94,6 +94,25 @@ def test_block_is_the_chain_of_its_operators(recipe, tokens):
     assert_status_ok()
 
 
+@pytest.mark.parametrize("recipe", [L.Float8CurrentScaling(), L.MXFP8BlockScaling(), L.Float8DelayedScaling()])
+@pytest.mark.parametrize("tokens", [0, 1])
+def test_gradients_of_few_tokens(recipe, tokens):
+    """No token gives no gradient, one token gradients of its two experts alone."""
+    torch.manual_seed(8)
+    block = B.FP8MoEBlock(256, 384, n_experts=6, k=2, device="cuda", norm="rms", grouped=True)
+    x = normal(tokens, 256, seed=9).requires_grad_(True)
+    with L.fp8_autocast(fp8_recipe=recipe):
+        y = block(x)
+    y.backward(normal(tokens, 256, seed=10))
+    assert x.grad.shape == x.shape and bool(x.grad.isfinite().all())
+    for w in (block.up.weight, block.down.weight):
+        used = w.grad.abs().amax((1, 2)) > 0
+        assert int(used.sum()) == 2 * tokens and bool(w.grad.isfinite().all())
+    assert block.norm.weight.grad.shape == (256,) and bool((block.norm.weight.grad != 0).any()) == (tokens > 0)
+    assert bool(block.router.grad.isfinite().all()) and bool((block.router.grad != 0).any()) == (tokens > 0)
+    assert_status_ok()
+
+
 @pytest.mark.parametrize("norm", ["layer", "rms"])
 def test_block_against_an_expert_at_a_time(norm):
     """MXFP8 scales lie in the experts' own rows, so both forms of the block multiply the same codes."""
