@@ -1124,6 +1124,8 @@ fp8_status grouped(GroupedParams& p, const uint8_t* A, fp8_format fa, fp8_recipe
     if (!make_map(&m.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, a_cols, a_rows, 128, 128) ||
         !make_map(&m.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B, b_cols, b_rows, 128, width == 0 ? 128 : static_cast<uint32_t>(width)))
       return FP8_ERR_CUDA;
+    // in the place of MX's scales of A: A by boxes of 64 rows, for tiles of 64 rows a CTA
+    if (!mx && width == 0 && !make_map(&m.sfa, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, a_cols, a_rows, 128, 64)) return FP8_ERR_CUDA;
     // MX: the tiled scale buffers as rows of 256 bytes, two rows (one 512-byte atom) per box
     if (mx && (!make_map(&m.sfa, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, sA, 256, 2 * (a_rows / 128) * (a_cols / 128), 256, 2,
                          CU_TENSOR_MAP_SWIZZLE_NONE) ||

@@ -75,19 +75,21 @@ struct Tile {
   int b_row, b_kb;   // the tile's first row of B and its first block
   int nkb;           // blocks
   int c_row, c_col;  // this CTA's first row of C, the tile's first column
-  bool held;         // whether this CTA's rows belong to the expert (of a pair's last half tile, the second CTA's do not)
+  bool held;         // whether this CTA's rows belong to the expert
+  bool half;         // a pair's tile has 128 rows only: 64 a CTA (HALVES), or those of the first CTA alone
 };
 
 // Tile t for CTA `rank` of its unit; `e` moves on from the expert of the tile before.
-template <int TILE_ROWS>
+template <int TILE_ROWS, bool HALVES>
 __device__ __forceinline__ Tile tile_of(const GroupedParams& p, const int* offs, const int* first, int tile_cols, int tiles_n, int rank,
                                         int t, int& e) {
   while (t >= first[e + 1]) ++e;
   const int lo = offs[e], seg = offs[e + 1] - lo, rows = p.depth ? p.M : seg;
   int tm, tn;
   tile_coords<16>(t - first[e], (rows + TILE_ROWS - 1) / TILE_ROWS, tiles_n, tm, tn);
-  const int row = tm * TILE_ROWS + rank * kRows;
   Tile w;
+  w.half = TILE_ROWS > kRows && tm * TILE_ROWS + kRows >= rows;
+  const int row = tm * TILE_ROWS + rank * (HALVES && w.half ? kRows / 2 : kRows);
   w.e = e;
   w.held = row < rows;
   w.c_col = tn * tile_cols;
@@ -132,8 +134,10 @@ constexpr int kFetchA = 2 + kEpi, kCopier = 3 + kEpi;
 // the order of the list, 16 of an expert's row tiles walking its columns together.
 // Bound by the tensor core: 8 x 2176 rows, 4096 -> 11008, MXFP8 477 us (3290 TFLOP/s, 0.87 of twice the measured BF16
 // rate), per-tensor 450 (3490); a pair's 128-deep block takes 560 to 620 cycles
-// with all pairs at work, 490 alone.  An expert whose rows are an odd number of 128s leaves half of its last tile empty.
-// 64 experts of 256 rows, 2048 -> 4096, per-tensor 109 us (0.96 of HBM).
+// with all pairs at work, 490 alone.  64 experts of 256 rows, 2048 -> 4096, per-tensor 109 us (0.96 of HBM).
+// An expert whose rows are an odd number of 128s has a last tile of 128: per-tensor one of 64 rows a CTA (64 experts, 4096 ->
+// 2048, of 384 rows 151 us, with 256 rows, of which half are zeros, 161; of 256 and 384 in turn 128 and 133); MXFP8's scale
+// factors come by atoms of 128 rows, and its tile keeps 256, zeros in the place of those that are not the expert's.
 constexpr int kPairCols = 256;
 // S stages: 6 with per-tensor scales and up to 200 experts (their table of segments shares the memory), else 5.  (8192
 // tokens at 2 of 8 experts 452 -> 443 us, 64 experts of 256 rows 112 -> 110.6; with 4 stages 478 and 121.)
@@ -152,6 +156,7 @@ struct PairLayout {
   static constexpr uint32_t OFF_TMEM = OFF_FINAL + 8, OFF_ABORT = OFF_TMEM + 4, OFF_TABLE = OFF_ABORT + 4;
   static constexpr uint32_t FIXED = OFF_TABLE + 1024;    // + alignment slack
   static constexpr uint32_t TX = 2 * (STAGE + SF);       // bytes of both CTAs that complete a stage
+  static constexpr uint32_t TX_HALF = TX - (MX ? 0 : A_BYTES);   // of a tile of 128 rows
   static constexpr uint32_t SF_COL = kPairCols * ACC;    // first TMEM column of the scale factors
   static constexpr uint32_t SF_COLS = 4 + 4 * B_ATOMS;   // of a stage
   static_assert(SF_COL + (MX ? S * SF_COLS : 0) <= kTmemAll, "TMEM");
@@ -182,6 +187,7 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
     if (p.loads) {
       prefetch_tmap(&tm_a);
       prefetch_tmap(&tm_b);
+      prefetch_tmap(&tm_sfa);
     }
     for (int s = 0; s < S; ++s) {
       mbar_init(base + L::OFF_FULL + 8 * s, 1);
@@ -210,7 +216,7 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
   const uint32_t tmem = warp_uniform(*reinterpret_cast<volatile uint32_t*>(base_ptr + L::OFF_TMEM));
   const int ntiles = warp_uniform(first[p.n_experts]);
 
-  auto tile_at = [&](int t, int& e) { return tile_of<TM>(p, offs, first, BN, tiles_n, static_cast<int>(rank), t, e); };
+  auto tile_at = [&](int t, int& e) { return tile_of<TM, !MX>(p, offs, first, BN, tiles_n, static_cast<int>(rank), t, e); };
 
   if (warp == 0 || warp == kFetchA) {
     // ------------------------------------------------ producers (whole warps): B, and A, each with its scale factors
@@ -227,20 +233,22 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
       int atom = warp_uniform(2 * (fetch_b ? b_row / kRows * b_atoms + w.b_kb : a_row / kRows * a_atoms + w.a_kb));
       // a tile that hangs over B's last row takes its last atoms twice (those columns are not stored)
       const int second = b_row / kRows < b_last ? 2 * b_atoms : 0;
+      const uint32_t tx = warp_uniform(w.half ? L::TX_HALF : L::TX);
+      const CUtensorMap* const map_a = !MX && w.half ? &tm_sfa : &tm_a;
       for (int kb = 0; kb < nkb; ++kb) {
         ok = warp_uniform(mbar_wait(base + L::OFF_EMPTY + 8 * stage, phase ^ 1u, p.err, kErrTimeoutStage, abort_flag));
         if (!ok) break;
         const uint32_t full = base + L::OFF_FULL + 8 * stage, sig = mapa_shared(full, 0);
         const uint32_t sa = base + stage * L::STAGE, sf = base + L::OFF_SF + stage * L::SF;
         if (fetch_b) {
-          if (leader) mbar_arrive_expect_tx_warp(full, L::TX);
+          if (leader) mbar_arrive_expect_tx_warp(full, tx);
           tma_load_2d_pair_warp(sa + L::A_BYTES, &tm_b, x, b_row + static_cast<int>(rank) * (BN / 2), sig);
           if (MX) {
             tma_load_2d_pair_warp(sf + 512, &tm_sfb, 0, atom, sig);
             tma_load_2d_pair_warp(sf + 1024, &tm_sfb, 0, atom + second, sig);
           }
         } else {
-          tma_load_2d_pair_warp(sa, &tm_a, x, a_row, sig);
+          tma_load_2d_pair_warp(sa, map_a, x, a_row, sig);
           if (MX) tma_load_2d_pair_warp(sf, &tm_sfa, 0, atom, sig);
         }
         x += kDepth;
@@ -289,14 +297,16 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
     // ------------------------------------------------ MMA issuer (leader; the whole warp)
     const uint32_t shape = (static_cast<uint32_t>(p.e5m2_a) << 7) | (static_cast<uint32_t>(p.e5m2_b) << 10) |
                            (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
-    const uint32_t idesc = shape | (MX ? 1u << 23 : 1u << 4);
+    const uint32_t full_tile = shape | (MX ? 1u << 23 : 1u << 4);
     auto commit = [&](uint32_t bar) { tc_commit_pair_mc_warp(bar, 3); };
     int stage = 0, e = 0;
     uint32_t phase = 0, acc_it = 0;
     bool ok = true;
     for (int t = unit; t < ntiles && ok; t += units) {
-      const int nkb = warp_uniform(tile_at(t, e).nkb);
+      const Tile w = tile_at(t, e);
+      const int nkb = warp_uniform(w.nkb);
       if (nkb == 0) continue;   // the epilogue stores 0 without an accumulator
+      const uint32_t idesc = warp_uniform(full_tile - (!MX && w.half ? static_cast<uint32_t>(kRows >> 4) << 24 : 0u));
       const uint32_t a = acc_it % ACC, parity = ((acc_it / ACC) & 1u) ^ 1u;
       ok = warp_uniform(mbar_wait_cluster(base + L::OFF_TEMPTY + 8 * a, parity, p.err, kErrTimeoutMma, abort_flag));
       if (!ok) break;
@@ -375,7 +385,11 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
     int e = 0;
     for (int t = unit; t < ntiles; t += units) {
       const Tile w = tile_at(t, e);
-      const int col = w.c_col + h * COLS, row = w.c_row + 32 * q;
+      // of 64 rows a CTA, TMEM has the first 128 columns in its lanes 0..63 and the others in 64..127
+      const bool half = !MX && w.half;
+      const int col = half ? w.c_col + (q >> 1) * (BN / 2) + h * (COLS / 2) : w.c_col + h * COLS;
+      const int row = w.c_row + 32 * (half ? q & 1 : q), chunks = half ? CH / 2 : CH;
+      const uint32_t from = lane_base + static_cast<uint32_t>(h * (half ? COLS / 2 : COLS));
       if (w.nkb > 0) {
         // warp-uniform decision: the TMEM loads that follow are .sync.aligned
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(base + L::OFF_TFULL + 8 * (acc_it % ACC), (acc_it / ACC) & 1u, p.err, kErrTimeoutMma,
@@ -394,7 +408,7 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
         if (w.nkb > 0) {
           const uint32_t a = acc_it % ACC;
 #pragma unroll
-          for (int c = 0; c < HOLD; ++c) tc_ld_32x32b_x32(lane_base + a * BN + h * COLS + 32 * (c0 + c), r[c]);
+          for (int c = 0; c < HOLD; ++c) tc_ld_32x32b_x32(from + a * BN + 32 * (c0 + c), r[c]);
 #pragma unroll
           for (int c = 0; c < HOLD; ++c) tc_wait_ld(r[c]);
           if (c0 + HOLD == CH) {
@@ -416,7 +430,8 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
         if (!w.held) continue;
 #pragma unroll
         for (int c = 0; c < HOLD; ++c) {
-          if (col + 32 * ((c0 + c) & ~1) >= p.N) break;   // N is a multiple of 128, a pair of chunks inside or outside
+          // N is a multiple of 128, a pair of chunks inside or outside
+          if (c0 + c >= chunks || col + 32 * ((c0 + c) & ~1) >= p.N) break;
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = MX ? __uint_as_float(r[c][j]) : __fmul_rn(__uint_as_float(r[c][j]), scale);
@@ -527,7 +542,7 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
   pdl_launch_dependents();
   const uint32_t tmem = warp_uniform(*reinterpret_cast<volatile uint32_t*>(base_ptr + L::OFF_TMEM));
   const int ntiles = warp_uniform(first[p.n_experts]);
-  auto tile_at = [&](int t, int& e) { return tile_of<kRows>(p, offs, first, width, tiles_n, 0, t, e); };
+  auto tile_at = [&](int t, int& e) { return tile_of<kRows, false>(p, offs, first, width, tiles_n, 0, t, e); };
   auto next = [&](int& stage, uint32_t& phase) {
     if (++stage == S) {
       stage = 0;
