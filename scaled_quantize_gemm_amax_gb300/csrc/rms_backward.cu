@@ -7,7 +7,7 @@
 //
 // Bound by HBM: dy, h and dh once in, dx once out.  A thread owns the same columns for all the rows
 // of its group, so the column sums stay in registers over the whole walk; they leave as one partial
-// sum a block, added up by a second, small launch.
+// sum a block, added up by a second, small launch.  Few rows take one launch of another kind (k_rms_backward_few).
 // bf16 with dh: 8192x4096 44 to 46 us (6.0 TB/s, 0.89 of what a copy reaches), 65536x4096 307 (1.03), 4096x8192 46; without
 // dh 2048x12288 32 (0.69), 8192x12288 95 (0.94): what does not grow with the rows is the weights' way to every SM (1.8
 // us) and the column sums (4.4 us, the second launch included).  binary32 8192x4096 81 (0.97); 2048x16384, whose dh
@@ -73,6 +73,115 @@ __global__ void __launch_bounds__(kThreads) k_rms_partial_any(const RmsBwdParams
     dw = fmaf(ld_elem(static_cast<const T*>(p.dy) + row * p.lddy + c),
               ld_elem(static_cast<const T*>(p.h) + row * p.ldh + c) * p.rstd[row], dw);
   p.partial[static_cast<int64_t>(blockIdx.y) * p.cols + c] = dw;
+}
+
+// Few rows (no more than SMs; half as many if unaligned binary32), of any width: one launch for both results, which need only the
+// rstd of the forward pass.  Block r < rows takes row r, in two passes; the blocks behind them sum dw over all rows, kFewCols columns
+// each, warp w the rows w, w + kFewWarps, ...  bf16 with dh, us, and by partial sums and a second launch: 1x4096 2.1 and 3.9,
+// 16x12288 3.8 and 7.1, 64x4096 2.2 and 4.9, 152x8192 4.8 and 7.9; binary32 152x12288 9.8 and 10.8; 256x1024 4.0 and 4.6, but
+// 512x1024 7.6 and 4.8; unaligned binary32 64x5849 5.6 and 7.9, 128x5849 11.4 and 8.9.
+constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32, kFewLane = 4, kFewCols = 32 * kFewLane;
+__device__ __forceinline__ void load4(const float* m, float* v) {
+  const float4 u = __ldg(reinterpret_cast<const float4*>(m));
+  v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+}
+__device__ __forceinline__ void load4(const uint16_t* m, float* v) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(m));
+  v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+  v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+}
+template <typename T, bool VECTOR>
+__global__ void __launch_bounds__(kFewThreads) k_rms_backward_few(const RmsBwdParams p) {
+  constexpr int E = VECTOR ? 16 / static_cast<int>(sizeof(T)) : 1;
+  __shared__ float red[kFewWarps][kFewCols];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = static_cast<int>(p.rows), cols = static_cast<int>(p.cols);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (static_cast<int>(blockIdx.x) >= rows) {
+    // the lane's kFewLane columns
+    const int c0 = (static_cast<int>(blockIdx.x) - rows) * kFewCols, c = c0 + kFewLane * lane;
+    float dw[kFewLane] = {};
+#pragma unroll 4
+    for (int64_t row = warp; row < rows; row += kFewWarps) {
+      const T* const dy = static_cast<const T*>(p.dy) + row * p.lddy + c;
+      const T* const h = static_cast<const T*>(p.h) + row * p.ldh + c;
+      float a[kFewLane] = {}, b[kFewLane] = {};
+      if (VECTOR) {   // cols is a multiple of kFewLane
+        if (c < cols) {
+          load4(dy, a);
+          load4(h, b);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kFewLane; ++i)
+          if (c + i < cols) a[i] = ld_elem(dy + i), b[i] = ld_elem(h + i);
+      }
+      const float rstd = p.rstd[row];
+#pragma unroll
+      for (int i = 0; i < kFewLane; ++i) dw[i] = fmaf(a[i], b[i] * rstd, dw[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kFewLane; ++i) red[warp][i * 32 + lane] = dw[i];
+    __syncthreads();
+    const int mine = c0 + static_cast<int>(threadIdx.x);
+    if (threadIdx.x >= kFewCols || mine >= cols) return;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) sum += red[w][threadIdx.x % kFewLane * 32 + threadIdx.x / kFewLane];
+    st_param(p.dw, p.w_f32, mine, sum);
+    return;
+  }
+  const int64_t row = blockIdx.x;
+  const T* const dy = static_cast<const T*>(p.dy) + row * p.lddy;
+  const T* const h = static_cast<const T*>(p.h) + row * p.ldh;
+  const T* const dh = p.dh != nullptr ? static_cast<const T*>(p.dh) + row * p.lddh : nullptr;
+  T* const dx = static_cast<T*>(p.dx) + row * p.lddx;
+  const float rstd = p.rstd[row];
+  // dy w and h of E elements at column c
+  auto load = [&](int c, float (&g)[E], float (&x)[E]) {
+    if constexpr (VECTOR) {
+      float w[E];
+      Piece<T, true>::unpack(__ldg(reinterpret_cast<const uint4*>(dy + c)), g);
+      Piece<T, true>::unpack(__ldg(reinterpret_cast<const uint4*>(h + c)), x);
+#pragma unroll
+      for (int i = 0; i < E; i += 4) {
+        if (p.w == nullptr) w[i] = w[i + 1] = w[i + 2] = w[i + 3] = 1.0f;
+        else if (p.w_f32) load4(static_cast<const float*>(p.w) + c + i, w + i);
+        else load4(static_cast<const uint16_t*>(p.w) + c + i, w + i);
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) g[i] *= w[i];
+    } else {
+      g[0] = ld_elem(dy + c) * (p.w != nullptr ? ld_param(p.w, p.w_f32, c) : 1.0f);
+      x[0] = ld_elem(h + c);
+    }
+  };
+  float sum = 0.0f;
+#pragma unroll 4
+  for (int c = static_cast<int>(threadIdx.x) * E; c < cols; c += kFewThreads * E) {
+    float g[E], x[E];
+    load(c, g, x);
+#pragma unroll
+    for (int i = 0; i < E; ++i) sum = fmaf(g[i], x[i] * rstd, sum);
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) red[0][warp] = sum;
+  __syncthreads();
+  sum = warp_sum(lane < kFewWarps ? red[0][lane] : 0.0f);
+  const float k = -rstd * (sum / static_cast<float>(cols)) * rstd;
+#pragma unroll 2
+  for (int c = static_cast<int>(threadIdx.x) * E; c < cols; c += kFewThreads * E) {
+    float g[E], x[E], a[E] = {};
+    if (dh != nullptr) {
+      if constexpr (VECTOR) Piece<T, true>::unpack(__ldg(reinterpret_cast<const uint4*>(dh + c)), a);
+      else a[0] = ld_elem(dh + c);
+    }
+    load(c, g, x);
+#pragma unroll
+    for (int i = 0; i < E; ++i) a[i] = fmaf(x[i], k, fmaf(g[i], rstd, a[i]));
+    if constexpr (VECTOR) *reinterpret_cast<uint4*>(dx + c) = Piece<T, true>::pack(a);
+    else st_elem(dx + c, a[0]);
+  }
 }
 
 // Rows of up to kMostCols columns, V values a lane.  A stage holds a warp's part of a row: dy, h, dh (`ahead`;
@@ -216,10 +325,10 @@ __global__ void __launch_bounds__(BLOCK_WARPS * 32)
     n = half;
   }
   if (group != 0) return;
-  float* const part = gridDim.x > 1 ? p.partial + static_cast<int64_t>(blockIdx.x) * cols : nullptr;   // else: the result
+  float* const part = p.partial + static_cast<int64_t>(blockIdx.x) * cols;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    if (VECTOR && part != nullptr) {   // cols is a multiple of 4, the workspace 16-byte aligned
+    if (VECTOR) {   // cols is a multiple of 4, the workspace 16-byte aligned
       if (left <= j * P::WC) continue;
 #pragma unroll
       for (int i = 0; i < H; i += 2)
@@ -228,10 +337,7 @@ __global__ void __launch_bounds__(BLOCK_WARPS * 32)
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         if (!P::has(left - j * P::WC, i)) continue;
-        const int col = c + j * P::WC + P::at(i);
-        const float v = i % 2 ? dw[j][i / 2].y : dw[j][i / 2].x;
-        if (part != nullptr) part[col] = v;
-        else st_param(p.dw, p.w_f32, col, v);
+        part[c + j * P::WC + P::at(i)] = i % 2 ? dw[j][i / 2].y : dw[j][i / 2].x;
       }
     }
   }
@@ -270,7 +376,7 @@ __global__ void __launch_bounds__(kParamWarps * 32) k_rms_params(const float* pa
   st_param(dw, f32, c + warp, sum);
 }
 
-// *partials: number of partial sums left in p.partial (0: none)
+// *partials: number of partial sums left in p.partial
 template <typename T, bool VECTOR, int V, int BLOCK_WARPS>
 cudaError_t run_rms_backward(const RmsBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
   const int part = RowPart<Piece<T, VECTOR>, 32 * V, VECTOR, T>::kBytes;
@@ -287,7 +393,7 @@ cudaError_t run_rms_backward(const RmsBwdParams& p, int num_sms, cudaStream_t s,
   auto kernel = k_rms_backward<T, VECTOR, V, BLOCK_WARPS>;
   const cudaError_t e = ensure_smem_limit(kernel, kNormSmem, done);
   if (e != cudaSuccess) return e;
-  *partials = n.blocks > 1 ? n.blocks : 0;
+  *partials = n.blocks;
   return launch_pdl(kernel, dim3(n.blocks), dim3(static_cast<unsigned>(n.warps * n.groups * 32)), n.smem, s, 1, p, n.warps,
                     n.stages, n.ring, ahead);
 }
@@ -300,6 +406,12 @@ cudaError_t run_rms_backward(const RmsBwdParams& p, int num_sms, cudaStream_t s,
   if (p.cols <= 256) return run_rms_backward<T, VECTOR, 8, 24>(p, num_sms, s, partials);
   if (p.cols <= 8192) return run_rms_backward<T, VECTOR, 16, 24>(p, num_sms, s, partials);
   return run_rms_backward<T, VECTOR, 32, 16>(p, num_sms, s, partials);
+}
+
+template <typename T, bool VECTOR>
+cudaError_t run_few(const RmsBwdParams& p, cudaStream_t s) {
+  const int64_t blocks = p.rows + (p.dw != nullptr ? (p.cols + kFewCols - 1) / kFewCols : 0);
+  return launch_pdl(k_rms_backward_few<T, VECTOR>, dim3(static_cast<unsigned>(blocks)), dim3(kFewThreads), 0, s, 1, p);
 }
 
 template <typename T>
@@ -322,18 +434,21 @@ cudaError_t launch_rms_backward(const RmsBwdParams& p, int num_sms, cudaStream_t
   const int64_t size = p.f32 ? 4 : 2;
   int partials = 0;
   cudaError_t e;
+  const bool vec = takes(p.dy, p.lddy, p.cols, size, 16) && takes(p.h, p.ldh, p.cols, size, 16) &&
+                   takes(p.dh, p.lddh, p.cols, size, 16) && takes(p.dx, p.lddx, p.cols, size, 16) && takes(p.w, 0, 0, 1, 16);
+  const int few = p.f32 && !vec ? num_sms / 2 : num_sms;
+  if (p.rows > 0 && p.rows <= few)
+    return p.f32 ? (vec ? run_few<float, true>(p, s) : run_few<float, false>(p, s))
+                 : (vec ? run_few<uint16_t, true>(p, s) : run_few<uint16_t, false>(p, s));
   if (p.cols > kMostCols || p.rows == 0) {
     e = p.f32 ? run_any<float>(p, num_sms, s, &partials) : run_any<uint16_t>(p, num_sms, s, &partials);
+  } else if (p.f32) {
+    e = vec ? run_rms_backward<float, true>(p, num_sms, s, &partials) : run_rms_backward<float, false>(p, num_sms, s, &partials);
   } else {
-    const bool vec = takes(p.dy, p.lddy, p.cols, size, 16) && takes(p.h, p.ldh, p.cols, size, 16) &&
-                     takes(p.dh, p.lddh, p.cols, size, 16) && takes(p.dx, p.lddx, p.cols, size, 16) && takes(p.w, 0, 0, 1, 16);
-    if (p.f32)
-      e = vec ? run_rms_backward<float, true>(p, num_sms, s, &partials) : run_rms_backward<float, false>(p, num_sms, s, &partials);
-    else
-      e = vec ? run_rms_backward<uint16_t, true>(p, num_sms, s, &partials)
-              : run_rms_backward<uint16_t, false>(p, num_sms, s, &partials);
+    e = vec ? run_rms_backward<uint16_t, true>(p, num_sms, s, &partials)
+            : run_rms_backward<uint16_t, false>(p, num_sms, s, &partials);
   }
-  if (e != cudaSuccess || partials == 0 || p.dw == nullptr) return e;
+  if (e != cudaSuccess || p.dw == nullptr) return e;
   const int quad = p.cols % 4 == 0 ? 4 : 1;
   return launch_pdl(quad == 4 ? k_rms_params<4> : k_rms_params<1>, dim3(static_cast<unsigned>((p.cols / quad + 31) / 32)),
                     dim3(kParamWarps * 32), 0, s, 1, static_cast<const float*>(p.partial), partials, static_cast<int>(p.cols),

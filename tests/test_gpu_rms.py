@@ -294,3 +294,49 @@ def test_graph_and_streams():
     y = fq.rms_norm(x, w, res, EPS, stream=other)[0]
     other.synchronize()
     assert torch.equal(y, want[0])
+
+
+MORE_ROWS = [  # rows, cols, pad, offset: above and at the rows that one launch takes
+    (152, 5849, 0, 0), (153, 5849, 1, 1), (76, 1003, 6, 5), (77, 1003, 6, 5), (77, 9, 0, 0), (153, 8, 0, 0), (160, 1, 0, 0),
+    (152, 8192, 0, 0), (153, 8192, 8, 0), (170, 12288, 0, 0), (155, 16383, 0, 1), (160, 16384, 0, 0), (154, 16392, 0, 0), (152, 20480, 0, 0),
+    (200, 250, 6, 0), (400, 4099, 0, 0), (1300, 130, 2, 2),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("stream", [False, True])
+@pytest.mark.parametrize("rows,cols,pad,offset", MORE_ROWS)
+def test_backward_of_more_rows(rows, cols, pad, offset, stream, dtype):
+    test_backward(rows, cols, pad, offset, stream, dtype)
+
+
+def test_backward_stays_inside_of_more_rows():
+    for rows, cols, dt in ((170, 1003, torch.bfloat16), (160, 640, torch.float32), (153, 20011, torch.float32), (152, 130, torch.bfloat16)):
+        dy, h, dh = (matrix(rows, cols, dt, 90 + i) for i in range(3))
+        w = _weight(cols, torch.float32, 93)
+        rstd = torch.rand(rows, generator=gen(94), device="cuda")
+        dx, dw = Guarded((rows, cols), dt), Guarded((cols,), torch.float32)
+        ws = Guarded((fq.fp8_rms_norm_workspace(rows, cols),), torch.uint8)
+        fq.fp8_rms_norm_backward(dy, h, rstd, dh, w, dx.t, dw.t, ws.t)
+        for got, what in ((dx, "dx"), (dw, "dweight"), (ws, "workspace")):
+            got.check(what)
+        want = fq.rms_norm_backward(dy, h, rstd, w, dh=dh)
+        assert torch.equal(dx.t, want[0]) and torch.equal(dw.t, want[1])
+
+
+@pytest.mark.parametrize("rows,cols", [(170, 96), (160, 99)])
+def test_backward_of_more_rows_against_differences(rows, cols):
+    x, w = matrix(rows, cols, torch.float32, 101), _weight(cols, torch.float32, 102)
+    dy = matrix(rows, cols, torch.float32, 103)
+    _, _, rstd, _, _ = fq.rms_norm(x, w, None, EPS)
+    dx, dw = fq.rms_norm_backward(dy, x, rstd, w)
+
+    def loss(h64, w64):
+        return float((h64 / (h64.square().mean(1, keepdim=True) + EPS).sqrt() * w64 * dy.double()).sum())
+
+    h64, w64, step = x.double(), w.double(), 1e-4
+    v = torch.randn((rows, cols), generator=gen(104), device="cuda").double()
+    u = torch.randn(cols, generator=gen(105), device="cuda").double()
+    for got, plus, minus in ((float((dx.double() * v).sum()), loss(h64 + step * v, w64), loss(h64 - step * v, w64)),
+                             (float((dw.double() * u).sum()), loss(h64, w64 + step * u), loss(h64, w64 - step * u))):
+        assert abs(got - (plus - minus) / (2 * step)) <= 1e-5 * (1 + abs(got)) + 64 * U * rows * cols
