@@ -10,7 +10,7 @@
 // With a residual, bf16: 8192x4096 to tiled MXFP8 codes 39 us (6.0 TB/s, 0.89 of what a copy reaches), 65536x4096 to 1x128 codes
 // 275 (1.01), 131072x256 38, 2048x16384 40; binary32 8192x4096 70 (0.92); without a residual 8192x4096 21 (0.70), 65536x4096 140
 // (0.85); one row of 4096 3.  Unaligned, to y: bf16 8192x4099 64 (0.62), binary32 4096x4099 48 (0.83).  Rows of more than
-// kMostCols columns are read twice, element by element.
+// kMostCols columns are read twice: bf16 1x16512 9, 2048x16512 72 (0.49).
 #include "rms.cuh"
 
 namespace fp8q {
@@ -28,7 +28,7 @@ template <bool VECTOR>
 constexpr int kMost = (VECTOR ? 64 : 96) * 1024;
 constexpr int kInFlight = 64 * 1024;
 constexpr int kMostCols = 16384;   // of a row held in registers, its weight in shared memory
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 
 // 1 / sqrt(v): the approximate reciprocal root and one Newton step (no step at 0 and infinity,
 // where it would make a NaN)
@@ -141,9 +141,9 @@ __device__ __forceinline__ uint4 add_residual(float (&x)[P::E], const float (&r)
 }
 
 // Rows of any width: one block per row, two passes over it.
-template <typename T>
+template <typename T, bool VECTOR>
 __global__ void __launch_bounds__(kThreads) k_rms_any(const RmsParams p) {
-  using P = Piece<T, false>;
+  using P = Piece<T, VECTOR>;
   __shared__ float red[kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cols = static_cast<int>(p.cols);
   const float inv_n = 1.0f / static_cast<float>(cols);
@@ -339,15 +339,15 @@ cudaError_t run_rms(const RmsParams& p, int num_sms, cudaStream_t s) {
 
 cudaError_t launch_rms(const RmsParams& p, int num_sms, cudaStream_t s) {
   const int64_t size = p.f32 ? 4 : 2;
-  if (p.cols > kMostCols) {
-    const int64_t cap = static_cast<int64_t>(num_sms) * 8;
-    const dim3 grid(static_cast<unsigned>(p.rows < cap ? p.rows : cap));
-    return p.f32 ? launch_pdl(k_rms_any<float>, grid, dim3(kThreads), 0, s, 1, p)
-                 : launch_pdl(k_rms_any<uint16_t>, grid, dim3(kThreads), 0, s, 1, p);
-  }
   const bool vec = takes(p.x, p.ldx, p.cols, size, 16) && takes(p.res, p.ldr, p.cols, size, 16) &&
                    takes(p.h, p.ldh, p.cols, size, 16) && takes(p.y, p.ldy, p.cols, size, 16) &&
                    takes(p.q, p.ldq, p.cols, 1, 16 / size) && takes(p.w, 0, 0, 1, 16);
+  if (p.cols > kMostCols) {
+    const int64_t cap = static_cast<int64_t>(num_sms) * 8;
+    const dim3 grid(static_cast<unsigned>(p.rows < cap ? p.rows : cap));
+    if (p.f32) return launch_pdl(vec ? k_rms_any<float, true> : k_rms_any<float, false>, grid, dim3(kThreads), 0, s, 1, p);
+    return launch_pdl(vec ? k_rms_any<uint16_t, true> : k_rms_any<uint16_t, false>, grid, dim3(kThreads), 0, s, 1, p);
+  }
   if (p.f32) return vec ? run_rms<float, true>(p, num_sms, s) : run_rms<float, false>(p, num_sms, s);
   return vec ? run_rms<uint16_t, true>(p, num_sms, s) : run_rms<uint16_t, false>(p, num_sms, s);
 }

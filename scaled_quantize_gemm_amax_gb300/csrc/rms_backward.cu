@@ -12,6 +12,7 @@
 // dh 2048x12288 32 (0.69), 8192x12288 95 (0.94): what does not grow with the rows is the weights' way to every SM (1.8
 // us) and the column sums (4.4 us, the second launch included).  binary32 8192x4096 81 (0.97); 2048x16384, whose dh
 // does not fit beside dy and h and is read late, 123 (0.65).  Unaligned bf16 8192x4099 90 (0.44), binary32 4096x4099 67 (0.59).
+// Rows of more than kMostCols columns are read three times, once for dw: bf16 2048x16512 90 (0.44).
 #include "rms.cuh"
 
 namespace fp8q {
@@ -19,65 +20,15 @@ namespace fp8q {
 namespace {
 
 constexpr int kMostCols = 16384;   // of a row held in registers
-constexpr int kThreads = 256;
 // Bytes of a block's rows and of its stages (rms_plan): bf16 with dh, 8192x4096: 46.1 us, with twice as much 49.1; 65536x4096 308
 // and 323.  Unaligned rows are bound by their instructions and take the warps that fit: 8192x4099 90 us, with 52 KB 168.
 template <bool VECTOR>
 constexpr int kMost = (VECTOR ? 56 : 96) * 1024;
 constexpr int kInFlight = 104 * 1024;
 
-// dx of rows of any width: one block per row, two passes.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_rms_dx_any(const RmsBwdParams p) {
-  __shared__ float red[kThreads / 32];
-  const float inv_n = 1.0f / static_cast<float>(p.cols);
-  pdl_wait();
-  pdl_launch_dependents();
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
-    const T* h = static_cast<const T*>(p.h) + row * p.ldh;
-    const T* dh = p.dh != nullptr ? static_cast<const T*>(p.dh) + row * p.lddh : nullptr;
-    T* dx = static_cast<T*>(p.dx) + row * p.lddx;
-    const float rstd = p.rstd[row];
-    float sum = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.cols; c += kThreads) {
-      const float g = ld_elem(dy + c) * (p.w != nullptr ? ld_param(p.w, p.w_f32, c) : 1.0f);
-      sum = fmaf(g, ld_elem(h + c) * rstd, sum);
-    }
-    sum = warp_sum(sum);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) sum += red[i];
-    const float k = -rstd * (sum * inv_n);
-    for (int64_t c = threadIdx.x; c < p.cols; c += kThreads) {
-      const float g = ld_elem(dy + c) * (p.w != nullptr ? ld_param(p.w, p.w_f32, c) : 1.0f);
-      const float v = fmaf(ld_elem(h + c) * rstd, k, fmaf(g, rstd, dh != nullptr ? ld_elem(dh + c) : 0.0f));
-      st_elem(dx + c, v);
-    }
-  }
-}
-
-// Partial sums of dw: block (x, y) sums 256 columns over the rows of slab y, one thread per column.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_rms_partial_any(const RmsBwdParams p, int slabs) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (c >= p.cols) return;
-  const int64_t r0 = p.rows * blockIdx.y / slabs, r1 = p.rows * (blockIdx.y + 1) / slabs;
-  float dw = 0.0f;
-  for (int64_t row = r0; row < r1; ++row)
-    dw = fmaf(ld_elem(static_cast<const T*>(p.dy) + row * p.lddy + c),
-              ld_elem(static_cast<const T*>(p.h) + row * p.ldh + c) * p.rstd[row], dw);
-  p.partial[static_cast<int64_t>(blockIdx.y) * p.cols + c] = dw;
-}
-
 // Few rows (no more than SMs; half as many if unaligned binary32), of any width: one launch for both results, which need only the
 // rstd of the forward pass.  Block r < rows takes row r, in two passes; the blocks behind them sum dw over all rows, kFewCols columns
-// each, warp w the rows w, w + kFewWarps, ...  bf16 with dh, us, and by partial sums and a second launch: 1x4096 2.1 and 3.9,
+// each, warp w the rows w, w + kFewWarps, ...  Without the latter, dx of rows that registers cannot hold.  bf16 with dh, us, and by partial sums and a second launch: 1x4096 2.1 and 3.9,
 // 16x12288 3.8 and 7.1, 64x4096 2.2 and 4.9, 152x8192 4.8 and 7.9; binary32 152x12288 9.8 and 10.8; 256x1024 4.0 and 4.6, but
 // 512x1024 7.6 and 4.8; unaligned binary32 64x5849 5.6 and 7.9, 128x5849 11.4 and 8.9.
 constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32, kFewLane = 4, kFewCols = 32 * kFewLane;
@@ -90,6 +41,42 @@ __device__ __forceinline__ void load4(const uint16_t* m, float* v) {
   v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
   v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xFFFF0000u);
 }
+// dw of the columns from c0 on over the rows [from, to); whether this thread has one of them, *col, and its sum.
+template <typename T, bool VECTOR>
+__device__ __forceinline__ bool sum_columns(const RmsBwdParams& p, int c0, int64_t from, int64_t to, float (&red)[kFewWarps][kFewCols],
+                                            int* col, float* sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cols = static_cast<int>(p.cols), c = c0 + kFewLane * lane;
+  float dw[kFewLane] = {};
+#pragma unroll 4
+  for (int64_t row = from + warp; row < to; row += kFewWarps) {
+    const T* const dy = static_cast<const T*>(p.dy) + row * p.lddy + c;
+    const T* const h = static_cast<const T*>(p.h) + row * p.ldh + c;
+    float a[kFewLane] = {}, b[kFewLane] = {};
+    if (VECTOR) {   // cols is a multiple of kFewLane
+      if (c < cols) {
+        load4(dy, a);
+        load4(h, b);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kFewLane; ++i)
+        if (c + i < cols) a[i] = ld_elem(dy + i), b[i] = ld_elem(h + i);
+    }
+    const float rstd = p.rstd[row];
+#pragma unroll
+    for (int i = 0; i < kFewLane; ++i) dw[i] = fmaf(a[i], b[i] * rstd, dw[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kFewLane; ++i) red[warp][i * 32 + lane] = dw[i];
+  __syncthreads();
+  *col = c0 + static_cast<int>(threadIdx.x);
+  if (threadIdx.x >= kFewCols || *col >= cols) return false;
+  *sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kFewWarps; ++w) *sum += red[w][threadIdx.x % kFewLane * 32 + threadIdx.x / kFewLane];
+  return true;
+}
+
 template <typename T, bool VECTOR>
 __global__ void __launch_bounds__(kFewThreads) k_rms_backward_few(const RmsBwdParams p) {
   constexpr int E = VECTOR ? 16 / static_cast<int>(sizeof(T)) : 1;
@@ -98,37 +85,9 @@ __global__ void __launch_bounds__(kFewThreads) k_rms_backward_few(const RmsBwdPa
   pdl_wait();
   pdl_launch_dependents();
   if (static_cast<int>(blockIdx.x) >= rows) {
-    // the lane's kFewLane columns
-    const int c0 = (static_cast<int>(blockIdx.x) - rows) * kFewCols, c = c0 + kFewLane * lane;
-    float dw[kFewLane] = {};
-#pragma unroll 4
-    for (int64_t row = warp; row < rows; row += kFewWarps) {
-      const T* const dy = static_cast<const T*>(p.dy) + row * p.lddy + c;
-      const T* const h = static_cast<const T*>(p.h) + row * p.ldh + c;
-      float a[kFewLane] = {}, b[kFewLane] = {};
-      if (VECTOR) {   // cols is a multiple of kFewLane
-        if (c < cols) {
-          load4(dy, a);
-          load4(h, b);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kFewLane; ++i)
-          if (c + i < cols) a[i] = ld_elem(dy + i), b[i] = ld_elem(h + i);
-      }
-      const float rstd = p.rstd[row];
-#pragma unroll
-      for (int i = 0; i < kFewLane; ++i) dw[i] = fmaf(a[i], b[i] * rstd, dw[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kFewLane; ++i) red[warp][i * 32 + lane] = dw[i];
-    __syncthreads();
-    const int mine = c0 + static_cast<int>(threadIdx.x);
-    if (threadIdx.x >= kFewCols || mine >= cols) return;
-    float sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) sum += red[w][threadIdx.x % kFewLane * 32 + threadIdx.x / kFewLane];
-    st_param(p.dw, p.w_f32, mine, sum);
+    int c;
+    float sum;
+    if (sum_columns<T, VECTOR>(p, (static_cast<int>(blockIdx.x) - rows) * kFewCols, 0, rows, red, &c, &sum)) st_param(p.dw, p.w_f32, c, sum);
     return;
   }
   const int64_t row = blockIdx.x;
@@ -182,6 +141,18 @@ __global__ void __launch_bounds__(kFewThreads) k_rms_backward_few(const RmsBwdPa
     if constexpr (VECTOR) *reinterpret_cast<uint4*>(dx + c) = Piece<T, true>::pack(a);
     else st_elem(dx + c, a[0]);
   }
+}
+
+// Partial sums of dw, of rows that registers cannot hold: block (x, y) sums kFewCols columns over the rows of slab y.
+template <typename T, bool VECTOR>
+__global__ void __launch_bounds__(kFewThreads) k_rms_partial_any(const RmsBwdParams p) {
+  __shared__ float red[kFewWarps][kFewCols];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t slabs = gridDim.y, from = p.rows * blockIdx.y / slabs, to = p.rows * (blockIdx.y + 1) / slabs;
+  int c;
+  float sum;
+  if (sum_columns<T, VECTOR>(p, static_cast<int>(blockIdx.x) * kFewCols, from, to, red, &c, &sum)) p.partial[blockIdx.y * p.cols + c] = sum;
 }
 
 // Rows of up to kMostCols columns, V values a lane.  A stage holds a warp's part of a row: dy, h, dh (`ahead`;
@@ -376,7 +347,7 @@ __global__ void __launch_bounds__(kParamWarps * 32) k_rms_params(const float* pa
   st_param(dw, f32, c + warp, sum);
 }
 
-// *partials: number of partial sums left in p.partial
+// *partials: number of partial sums left in p.partial (0: the result stands)
 template <typename T, bool VECTOR, int V, int BLOCK_WARPS>
 cudaError_t run_rms_backward(const RmsBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
   const int part = RowPart<Piece<T, VECTOR>, 32 * V, VECTOR, T>::kBytes;
@@ -414,18 +385,27 @@ cudaError_t run_few(const RmsBwdParams& p, cudaStream_t s) {
   return launch_pdl(k_rms_backward_few<T, VECTOR>, dim3(static_cast<unsigned>(blocks)), dim3(kFewThreads), 0, s, 1, p);
 }
 
-template <typename T>
+template <typename T, bool VECTOR>
 cudaError_t run_any(const RmsBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
-  const int64_t cap = static_cast<int64_t>(num_sms) * 8;
   if (p.rows > 0) {
-    const cudaError_t e = launch_pdl(k_rms_dx_any<T>, dim3(static_cast<unsigned>(p.rows < cap ? p.rows : cap)), dim3(kThreads), 0,
-                                     s, 1, p);
+    RmsBwdParams q = p;
+    q.dw = nullptr;
+    const cudaError_t e = run_few<T, VECTOR>(q, s);
     if (e != cudaSuccess) return e;
   }
   if (p.dw == nullptr) return cudaSuccess;
-  *partials = norm_partials(p.rows);
-  return launch_pdl(k_rms_partial_any<T>, dim3(static_cast<unsigned>((p.cols + kThreads - 1) / kThreads), *partials),
-                    dim3(kThreads), 0, s, 1, p, *partials);
+  // as many slabs as keep the SMs busy
+  const int64_t blocks = (p.cols + kFewCols - 1) / kFewCols, want = (3 * num_sms + blocks - 1) / blocks;
+  *partials = static_cast<int>(want < norm_partials(p.rows) ? want : norm_partials(p.rows));
+  return launch_pdl(k_rms_partial_any<T, VECTOR>, dim3(static_cast<unsigned>(blocks), *partials), dim3(kFewThreads), 0, s, 1, p);
+}
+
+template <typename T, bool VECTOR>
+cudaError_t run(const RmsBwdParams& p, int num_sms, cudaStream_t s, int* partials) {
+  const int few = sizeof(T) == 4 && !VECTOR ? num_sms / 2 : num_sms;
+  if (p.rows > 0 && p.rows <= few) return run_few<T, VECTOR>(p, s);
+  if (p.cols > kMostCols || p.rows == 0) return run_any<T, VECTOR>(p, num_sms, s, partials);
+  return run_rms_backward<T, VECTOR>(p, num_sms, s, partials);
 }
 
 }  // namespace
@@ -436,19 +416,11 @@ cudaError_t launch_rms_backward(const RmsBwdParams& p, int num_sms, cudaStream_t
   cudaError_t e;
   const bool vec = takes(p.dy, p.lddy, p.cols, size, 16) && takes(p.h, p.ldh, p.cols, size, 16) &&
                    takes(p.dh, p.lddh, p.cols, size, 16) && takes(p.dx, p.lddx, p.cols, size, 16) && takes(p.w, 0, 0, 1, 16);
-  const int few = p.f32 && !vec ? num_sms / 2 : num_sms;
-  if (p.rows > 0 && p.rows <= few)
-    return p.f32 ? (vec ? run_few<float, true>(p, s) : run_few<float, false>(p, s))
-                 : (vec ? run_few<uint16_t, true>(p, s) : run_few<uint16_t, false>(p, s));
-  if (p.cols > kMostCols || p.rows == 0) {
-    e = p.f32 ? run_any<float>(p, num_sms, s, &partials) : run_any<uint16_t>(p, num_sms, s, &partials);
-  } else if (p.f32) {
-    e = vec ? run_rms_backward<float, true>(p, num_sms, s, &partials) : run_rms_backward<float, false>(p, num_sms, s, &partials);
-  } else {
-    e = vec ? run_rms_backward<uint16_t, true>(p, num_sms, s, &partials)
-            : run_rms_backward<uint16_t, false>(p, num_sms, s, &partials);
-  }
-  if (e != cudaSuccess || p.dw == nullptr) return e;
+  if (p.f32)
+    e = vec ? run<float, true>(p, num_sms, s, &partials) : run<float, false>(p, num_sms, s, &partials);
+  else
+    e = vec ? run<uint16_t, true>(p, num_sms, s, &partials) : run<uint16_t, false>(p, num_sms, s, &partials);
+  if (e != cudaSuccess || partials == 0 || p.dw == nullptr) return e;
   const int quad = p.cols % 4 == 0 ? 4 : 1;
   return launch_pdl(quad == 4 ? k_rms_params<4> : k_rms_params<1>, dim3(static_cast<unsigned>((p.cols / quad + 31) / 32)),
                     dim3(kParamWarps * 32), 0, s, 1, static_cast<const float*>(p.partial), partials, static_cast<int>(p.cols),
