@@ -1133,10 +1133,10 @@ fp8_status grouped(GroupedParams& p, const uint8_t* A, fp8_format fa, fp8_recipe
                          CU_TENSOR_MAP_SWIZZLE_NONE)))
       return FP8_ERR_CUDA;
   }
-  const CUtensorMapSwizzle swizzle = width == 0 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
-  const bool ok = p.out_fp32
-                      ? make_map(&m.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.c, p.N, c_rows, 32, 32, swizzle)
-                      : make_map(&m.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.c, p.N, c_rows, width == 0 ? 64 : 32, 32, swizzle);
+  const bool ok = p.out_fp32 ? make_map(&m.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.c, p.N, c_rows, 32, 32)
+                  : width == 0
+                      ? make_map(&m.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.c, p.N, c_rows, 64, 32)
+                      : make_map(&m.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.c, p.N, c_rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (!ok) return FP8_ERR_CUDA;
   return cuda_status(launch_grouped(p, m, width, d->num_sms, stream));
 }

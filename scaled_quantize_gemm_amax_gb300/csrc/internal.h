@@ -423,8 +423,8 @@ struct GroupedParams {
 struct GroupedMaps {
   CUtensorMap a, b, sfa, sfb, c;
 };
-// Columns of a CTA's tile, 0 for CTA pairs.  Boxes have 128 rows of A; 128 of B for pairs, else the width; of C 32 rows,
-// swizzled 128 bytes of them for pairs, else 32 plain columns.  Pairs with per-tensor scales have A by boxes of 64 rows in sfa.
+// Columns of a CTA's tile, 0 for CTA pairs.  Boxes have 128 rows of A; 128 of B for pairs, else the width; of C 32 rows of
+// 128 bytes, or of 64 with bf16 and no pairs, swizzled as wide.  Pairs with per-tensor scales have A by boxes of 64 rows in sfa.
 int grouped_width(const GroupedParams& p, int num_sms);
 cudaError_t launch_grouped(const GroupedParams& p, const GroupedMaps& m, int width, int num_sms, cudaStream_t s);
 
