@@ -90,6 +90,8 @@ class _RMSNormFn(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dh=None):
+        if dy is None and dh is None:   # what used the outputs has no gradient for them
+            return None, None, None, None, None
         w, h, rstd = ctx.saved_tensors
         dw = None
         if dy is None:   # only h was used
