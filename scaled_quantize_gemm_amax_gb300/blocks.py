@@ -78,29 +78,32 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, checkpoint: Format 
 
 
 class _RMSNormFn(torch.autograd.Function):
+    # The inputs are flattened in here and both get one tensor as their gradient, as of torch's own sum: whoever keeps it sees
+    # that others hold it too.  Views of it, which flattening outside would make, hide that.
     @staticmethod
-    def forward(ctx, x, weight, residual, eps, apart):
+    def forward(ctx, x, weight, residual, eps):
         ctx.set_materialize_grads(False)
         w = weight.detach() if weight is not None else None
-        y, h, rstd, _, _ = _rms_norm(x, w, residual, eps)
-        ctx.save_for_backward(w, x if residual is None else h, rstd)
-        ctx.has_residual, ctx.apart = residual is not None, apart
+        rows = _flat(x)
+        y, h, rstd, _, _ = _rms_norm(rows, w, _flat(residual) if residual is not None else None, eps)
+        ctx.save_for_backward(w, rows if residual is None else h, rstd)
+        ctx.has_residual, ctx.shape = residual is not None, x.shape
         return (y, h) if residual is not None else y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dh=None):
         if dy is None and dh is None:   # what used the outputs has no gradient for them
-            return None, None, None, None, None
+            return None, None, None, None
         w, h, rstd = ctx.saved_tensors
         dw = None
-        if dy is None:   # only h was used
-            dx = dh
+        if dy is None:   # only h was used; its gradient may be kept elsewhere
+            dx = dh.clone(memory_format=torch.contiguous_format)
         else:
             need = w is not None and ctx.needs_input_grad[1]
             dx, dw = _rms_norm_backward(_flat(dy), h, rstd, w, dh=_flat(dh) if dh is not None else None, param_grads=need)
-        dres = (dx.clone() if ctx.apart else dx) if ctx.has_residual else None
-        return dx, dw, dres, None, None
+        dx = dx.view(ctx.shape)
+        return dx, dw, dx if ctx.has_residual else None, None
 
 
 def rms_norm(x, weight=None, residual=None, eps: float = 1e-5):
@@ -108,11 +111,10 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-5):
 
     With residual (like x) the norm of their sum h, rounded to x's type; returns (y, h) then."""
     if residual is None:
-        return _RMSNormFn.apply(_flat(x), weight, None, eps, False).reshape(x.shape)
+        return _RMSNormFn.apply(x, weight, None, eps).reshape(x.shape)
     if residual.shape != x.shape:
         raise ValueError(f"rms_norm: a residual of x's shape {tuple(x.shape)} is needed, not {tuple(residual.shape)}")
-    # both inputs have one gradient; two leaves keep it, each in memory of its own
-    y, h = _RMSNormFn.apply(_flat(x), weight, _flat(residual), eps, x.is_leaf and residual.is_leaf)
+    y, h = _RMSNormFn.apply(x, weight, residual, eps)
     return y.reshape(x.shape), h.reshape(x.shape)
 
 

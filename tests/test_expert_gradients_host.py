@@ -1,4 +1,5 @@
-"""Gradients of the differentiable RMS norm with a residual, without a GPU: where there is none at all."""
+"""Gradients of the differentiable RMS norm with a residual, without a GPU: none at all, and memory of their own."""
+import itertools
 
 import pytest
 import torch
@@ -29,3 +30,60 @@ def test_no_gradient_at_all(used, through):
     out.sum().backward()
     for t in (x, res, w):
         assert t.grad is None or bool((t.grad == 0).all())
+
+
+# ways from leaves to an input of the norm
+WAYS = {
+    "leaf": lambda ts: ts[0],
+    "product": lambda ts: ts[0] * 1.0,
+    "sum": lambda ts: ts[0] + ts[1],
+    "sum of a leaf": lambda ts: ts[0] + 0.0,
+}
+
+
+@pytest.mark.parametrize("used", ["y", "h", "both"])
+@pytest.mark.parametrize("shape", [(6, 8), (2, 3, 8)])
+@pytest.mark.parametrize("a,b", list(itertools.product(WAYS, WAYS)))
+def test_gradients_do_not_share_memory(a, b, shape, used):
+    """Both inputs have one gradient; every leaf behind them keeps it in memory of its own, so that one can be scaled or added to
+    in place without another."""
+    x0, x1, r0, r1 = ts = leaves(shape, shape, shape, shape)
+    y, h = B.rms_norm(WAYS[a]((x0, x1)), None, WAYS[b]((r0, r1)))
+    ry, rh = reference(WAYS[a]((x0, x1)), None, WAYS[b]((r0, r1)))
+    dy, dh = torch.randn(shape, dtype=torch.float64), torch.randn(shape, dtype=torch.float64)
+    pick = {"y": ((y, ry), (dy,)), "h": ((h, rh), (dh,)), "both": ((y, ry, h, rh), (dy, dh))}[used]
+    outs, refs, grads = pick[0][::2], pick[0][1::2], pick[1]
+    want = torch.autograd.grad(refs, ts, grads, allow_unused=True)
+    torch.autograd.backward(outs, grads)
+    have = [t for t in ts if t.grad is not None]
+    for t, g in zip(ts, want):
+        assert (t.grad is None) == (g is None)
+        assert g is None or torch.allclose(t.grad, g)
+    places = [t.grad.untyped_storage().data_ptr() for t in have] + [dy.untyped_storage().data_ptr(), dh.untyped_storage().data_ptr()]
+    assert len(set(places)) == len(places)
+    torch.autograd.backward(B.rms_norm(WAYS[a]((x0, x1)), None, WAYS[b]((r0, r1)))[:1], (dy,))   # added to what is there
+    more = torch.autograd.grad(reference(WAYS[a]((x0, x1)), None, WAYS[b]((r0, r1)))[0], ts, dy, allow_unused=True)
+    for t, g, m in zip(ts, want, more):
+        assert g is None or torch.allclose(t.grad, g + m)
+
+
+@pytest.mark.parametrize("shape", [(6, 8), (2, 3, 8)])
+def test_outputs_can_be_changed_in_place(shape):
+    """y is no part of what the backward pass needs."""
+    x, res = leaves(shape, shape)
+    y, h = B.rms_norm(x, None, res)
+    y += 1
+    y.sum().backward()
+    ref = torch.autograd.grad(reference(x, None, res)[0].sum(), x)[0]
+    assert torch.allclose(x.grad, ref) and torch.allclose(res.grad, ref)
+
+
+@pytest.mark.parametrize("shape", [(6, 8), (2, 3, 8)])
+def test_an_input_changed_before_the_backward_pass_is_noticed(shape):
+    """Without a residual the backward pass needs x itself."""
+    x, = leaves(shape)
+    y = B.rms_norm(x)
+    with torch.no_grad():
+        x += 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
