@@ -84,9 +84,8 @@ class _RMSNormFn(torch.autograd.Function):
     def forward(ctx, x, weight, residual, eps):
         ctx.set_materialize_grads(False)
         w = weight.detach() if weight is not None else None
-        rows = _flat(x)
-        y, h, rstd, _, _ = _rms_norm(rows, w, _flat(residual) if residual is not None else None, eps)
-        ctx.save_for_backward(w, rows if residual is None else h, rstd)
+        y, h, rstd, _, _ = _rms_norm(_flat(x), w, _flat(residual) if residual is not None else None, eps)
+        ctx.save_for_backward(w, x if residual is None else h, rstd)
         ctx.has_residual, ctx.shape = residual is not None, x.shape
         return (y, h) if residual is not None else y
 
@@ -101,7 +100,7 @@ class _RMSNormFn(torch.autograd.Function):
             dx = dh.clone(memory_format=torch.contiguous_format)
         else:
             need = w is not None and ctx.needs_input_grad[1]
-            dx, dw = _rms_norm_backward(_flat(dy), h, rstd, w, dh=_flat(dh) if dh is not None else None, param_grads=need)
+            dx, dw = _rms_norm_backward(_flat(dy), _flat(h), rstd, w, dh=_flat(dh) if dh is not None else None, param_grads=need)
         dx = dx.view(ctx.shape)
         return dx, dw, dx if ctx.has_residual else None, None
 
