@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kFewThreads) k_rms_backward_few(const RmsBwdPa
   if (lane == 0) red[0][warp] = sum;
   __syncthreads();
   sum = warp_sum(lane < kFewWarps ? red[0][lane] : 0.0f);
-  const float k = -rstd * (sum / static_cast<float>(cols)) * rstd;
+  const float k = -rstd * (sum / static_cast<float>(cols));
 #pragma unroll 2
   for (int c = static_cast<int>(threadIdx.x) * E; c < cols; c += kFewThreads * E) {
     float g[E], x[E], a[E] = {};
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kFewThreads) k_rms_backward_few(const RmsBwdPa
     }
     load(c, g, x);
 #pragma unroll
-    for (int i = 0; i < E; ++i) a[i] = fmaf(x[i], k, fmaf(g[i], rstd, a[i]));
+    for (int i = 0; i < E; ++i) a[i] = fmaf(x[i] * rstd, k, fmaf(g[i], rstd, a[i]));
     if constexpr (VECTOR) *reinterpret_cast<uint4*>(dx + c) = Piece<T, true>::pack(a);
     else st_elem(dx + c, a[0]);
   }
@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(BLOCK_WARPS * 32)
       // lane l joins warp l's part (the other buffer is written before this one is reused)
       sum = warp_sum(lane < warps ? red[buf][group * warps + lane] : 0.0f);
     }
-    // dx = r g - (r c r) h + dh
-    const float2 r = both(rstd), k = both(-rstd * (sum * inv_n) * rstd);
+    // dx = r g - (r c) xh + dh; r meets h first, since its square may leave binary32's range where r is in it (a row near 1e-20)
+    const float2 r = both(rstd), k = both(-rstd * (sum * inv_n));
     const int m_dh = ahead ? past(p.dh, p.lddh, row) : 0;
     const T* const dh0 = static_cast<const T*>(p.dh) + static_cast<int64_t>(row) * p.lddh + c;
     T* const dx0 = static_cast<T*>(p.dx) + static_cast<int64_t>(row) * p.lddx + c;
@@ -259,7 +259,8 @@ __global__ void __launch_bounds__(BLOCK_WARPS * 32)
         }
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-          const float2 o = fma2(make_float2(h[2 * i], h[2 * i + 1]), k, fma2(g[j][i], r, make_float2(a[2 * i], a[2 * i + 1])));
+          const float2 xh = mul2(make_float2(h[2 * i], h[2 * i + 1]), r);
+          const float2 o = fma2(xh, k, fma2(g[j][i], r, make_float2(a[2 * i], a[2 * i + 1])));
           a[2 * i] = o.x;
           a[2 * i + 1] = o.y;
         }
