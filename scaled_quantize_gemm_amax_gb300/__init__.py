@@ -668,6 +668,7 @@ def _gradients(grads, outs):
 
 
 def fp8_grad_norm(grads, workspace, norm, stream=None):
+    grads = tuple(grads)   # held for the call, whatever becomes of the caller's list
     _vector(norm, 1, "norm")
     _on_gpu(workspace, norm)
     table = _gradients(grads, [None] * len(grads))
@@ -677,6 +678,7 @@ def fp8_grad_norm(grads, workspace, norm, stream=None):
 
 
 def fp8_clip_grad_norm(grads, outs, max_norm, workspace, norm, stream=None):
+    grads, outs = tuple(grads), tuple(outs)   # held for the call, whatever becomes of the caller's lists
     if len(outs) != len(grads):
         raise ValueError("outs: as many tensors as gradients are needed")
     _vector(norm, 1, "norm")

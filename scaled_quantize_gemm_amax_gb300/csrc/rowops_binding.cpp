@@ -654,17 +654,22 @@ PyObject* grouped_wgrad(PyObject* const* v) {
   return wrap(c);
 }
 
-// The elements of a list or tuple of tensors.
+// The elements of a sequence of tensors, held until the call returns: the caller's list may change meanwhile, in another thread
+// while the interpreter is unlocked or in Python code that an argument runs, and its tensors may be dropped.
 struct Items {
-  PyObject* seq;
-  explicit Items(PyObject* o, const char* what) : seq(PySequence_Fast(o, what)) {
+  PyObject* tuple;
+  Items(PyObject* o, const char* what) {
+    PyObject* const seq = PySequence_Fast(o, what);
     if (seq == nullptr) throw Failed();
+    tuple = PySequence_Tuple(seq);
+    Py_DECREF(seq);
+    if (tuple == nullptr) throw Failed();
   }
-  ~Items() { Py_DECREF(seq); }
+  ~Items() { Py_DECREF(tuple); }
   Items(const Items&) = delete;
   Items& operator=(const Items&) = delete;
-  Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(seq); }
-  PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(seq, i); }
+  Py_ssize_t size() const { return PyTuple_GET_SIZE(tuple); }
+  PyObject* operator[](Py_ssize_t i) const { return PyTuple_GET_ITEM(tuple, i); }
 };
 // A gradient whose elements fill their memory without gaps, in whatever order.
 const at::Tensor& dense(PyObject* o, const char* what) {
