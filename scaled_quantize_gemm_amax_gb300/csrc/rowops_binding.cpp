@@ -13,6 +13,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
+#include <optional>
 #include <vector>
 
 #include "fp8q.h"
@@ -740,7 +741,9 @@ PyObject* clip_grad_norm(PyObject* const* v) {
   const bool clip = v[1] != Py_None, in_place = v[2] == Py_None;
   const double max_norm = clip ? PyFloat_AsDouble(v[1]) : 0.0;
   if (PyErr_Occurred()) throw Failed();
-  const Items outs(in_place ? v[0] : v[2], "out: a sequence of tensors is needed");
+  std::optional<Items> out;   // in place the gradients themselves: a generator gives its tensors once
+  if (!in_place) out.emplace(v[2], "out: a sequence of tensors is needed");
+  const Items& outs = in_place ? grads : *out;
   if (clip && outs.size() != n) refuse(PyExc_ValueError, "out: as many tensors as gradients are needed");
   if (n == 0) refuse(PyExc_ValueError, "grads: at least one tensor is needed");
   std::vector<fp8_gradient> table(static_cast<size_t>(n));

@@ -78,3 +78,16 @@ def test_through_the_c_names():
     fq.fp8_grad_norm(grads, ws, got, stream=Emptying(grads))
     assert torch.equal(got, norm)
     assert abs(float(got) / math.sqrt(sum(float(g.double().square().sum()) for g in gradients())) - 1) < 1e-6
+
+
+def test_generators():
+    """Every kind of sequence gives what a list gives, in place and not."""
+    norm, want = expected(gradients(), 0.5)
+    for make in (lambda ts: (t for t in ts), tuple, lambda ts: {i: t for i, t in enumerate(ts)}.values()):
+        grads = gradients()
+        assert torch.equal(fq.grad_norm(make(grads)), norm)
+        outs = [torch.empty_like(g) for g in grads]
+        assert torch.equal(fq.clip_grad_norm(make(grads), 0.5, out=make(outs)), norm)
+        assert torch.equal(fq.clip_grad_norm(make(grads), 0.5), norm)
+        for a, b, c in zip(outs, grads, want):
+            assert torch.equal(a, c) and torch.equal(b, c)
