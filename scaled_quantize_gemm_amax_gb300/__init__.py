@@ -934,6 +934,8 @@ def grad_norm(grads, stream=None):
 def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
     """Scale the gradients by min(1, max_norm / (norm + 1e-6)), in place or into the tensors `out`; returns their norm
     before (float32 [1], on the device)."""
+    if max_norm is None:   # what the compiled helper takes for the norm alone
+        raise TypeError("max_norm: a number is needed, not None")
     return (_ext or _rowops()).clip_grad_norm(grads, max_norm, out, stream)
 
 

@@ -32,3 +32,10 @@ def test_refusals_name_what_is_wrong():
         fq.clip_grad_norm(3, 1.0)
     with pytest.raises(TypeError, match="out: a sequence"):
         fq.clip_grad_norm([torch.ones(3)], 1.0, out=3)
+
+
+def test_a_limit_is_needed():
+    """Without one nothing would be clipped, and nothing said."""
+    for bad in (None, "1", [1.0]):
+        with pytest.raises(TypeError):
+            fq.clip_grad_norm([torch.ones(3)], bad)
