@@ -495,7 +495,8 @@ PyObject* rms_norm(PyObject* const* a) {
   fp8_status st;
   {
     Unlocked unlocked;
-    // the codes, their multipliers and the statistics in one allocation; with little data (a few tokens) all outputs are
+    // the codes and their multipliers in one allocation; with little data (a few tokens) all outputs are.  The statistics, which
+    // a backward pass holds long after the codes were used, are apart from much of them.
     int64_t shape[3] = {1, 1, 1}, dims = 1, scales = 0;
     if (copy) {
       if (is_tiled(recipe)) {
@@ -510,7 +511,7 @@ PyObject* rms_norm(PyObject* const* a) {
     const int64_t wide = (keep_y ? data : 0) + (res.t != nullptr ? data : 0);
     const bool together = wide + codes + scales + rest <= kTogether;
     at::Tensor whole;
-    if (together || codes + scales + rest > 0) whole = make({(together ? wide : 0) + codes + scales + rest}, at::kByte, *x.t);
+    if (together || codes + scales > 0) whole = make({(together ? wide + rest : 0) + codes + scales}, at::kByte, *x.t);
     int64_t at = 0;
     auto matrix = [&](bool wanted) -> at::Tensor {
       if (!wanted) return {};
@@ -526,7 +527,7 @@ PyObject* rms_norm(PyObject* const* a) {
       s = part(whole, at + codes, is_mx(recipe) ? at::kByte : at::kFloat, {shape, static_cast<size_t>(dims)},
                {strides, static_cast<size_t>(dims)});
     }
-    if (stats) rstd = part(whole, at + codes + scales, at::kFloat, {x.rows}, {1});
+    if (stats) rstd = together ? part(whole, at + codes + scales, at::kFloat, {x.rows}, {1}) : make({x.rows}, at::kFloat, *x.t);
     st = p_fp8_rms_norm(x.p(), x.rows, x.cols, x.ld, dt, res.p(), res.ld, w, wdt, static_cast<float>(eps), ptr<void>(h), x.cols,
                         ptr<void>(y), x.cols, ptr<float>(rstd), recipe, fmt, scale, amax, ptr<uint8_t>(q), ldq, ptr<void>(s),
                         stream);
