@@ -573,10 +573,9 @@ typedef enum {
  *               column-wise copy [K, n_experts * N] stacked by columns (the rows' gradients).
  *   sB, sB_count  FP8_TENSOR: 1 multiplier, or n_experts, one an expert; else sB_count is not used
  *   C           device, [capacity, N] bf16 or FP32
- *   zero_tail   not 0: the rows from offsets[n_experts] on are set to 0; 0: they are left as they
- *               were
- * Rows before offsets[0] are left as they were.  K == 0 sets the segments' rows to 0; capacity or
- * N == 0 is a no-op.
+ *   zero_tail   0: rows outside the segments are left as they were; 2: they are set to 0; others:
+ *               those from offsets[n_experts] on are set to 0, those before offsets[0] are left
+ * K == 0 sets the segments' rows to 0; capacity or N == 0 is a no-op.
  */
 fp8_status fp8_grouped_gemm(const uint8_t* A, fp8_format fa, fp8_recipe ra, const void* sA, const uint8_t* B, fp8_format fb,
                             fp8_recipe rb, const void* sB, int32_t sB_count, const int32_t* offsets, int32_t n_experts,

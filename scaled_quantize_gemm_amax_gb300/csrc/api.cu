@@ -1175,7 +1175,7 @@ fp8_status fp8_grouped_gemm(const uint8_t* A, fp8_format fa, fp8_recipe ra, cons
   p.b_cols = cols;
   p.sb_step = p.kind == kTensor && sB_count > 1;
   p.c = C;
-  p.zero_tail = zero_tail != 0;
+  p.zero_tail = zero_tail == 2 ? 2 : zero_tail != 0;
   return grouped(p, A, fa, ra, sA, B, fb, rb, sB, capacity, K, cols ? N : n_experts * N, cols ? n_experts * K : K, capacity, out,
                  stream);
 }

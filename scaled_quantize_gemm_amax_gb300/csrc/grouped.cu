@@ -62,7 +62,8 @@ __device__ __forceinline__ void list_tiles(const GroupedParams& p, int tile_rows
     __syncwarp();
     for (int e = lane; e <= p.n_experts; e += 32) first[e] = 0;
     if (lane == 0) {
-      offs[p.n_experts] = static_cast<int>(p.capacity);   // no rows behind the last segment either
+      offs[0] = 0;   // no rows in front of the first segment and behind the last either
+      offs[p.n_experts] = static_cast<int>(p.capacity);
       if (blockIdx.x == 0) atomicOr(p.err, kErrBadState);
     }
   }
@@ -113,12 +114,17 @@ __device__ __forceinline__ Tile tile_of(const GroupedParams& p, const int* offs,
   return w;
 }
 
-// Rows behind the last segment set to 0, by the 32 * kEpi epilogue threads of every CTA.
-__device__ __forceinline__ void zero_tail(const GroupedParams& p, int from, int thread) {
-  const int64_t row_bytes = static_cast<int64_t>(p.N) * (p.out_fp32 ? 4 : 2), total = p.capacity * row_bytes;
+// Rows [from, to) of C set to 0, by the 32 * kEpi epilogue threads of every CTA.
+__device__ __forceinline__ void zero_rows(const GroupedParams& p, int64_t from, int64_t to, int thread) {
+  const int64_t row_bytes = static_cast<int64_t>(p.N) * (p.out_fp32 ? 4 : 2), end = to * row_bytes;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (32 * kEpi) * 16;
-  for (int64_t at = from * row_bytes + (static_cast<int64_t>(blockIdx.x) * (32 * kEpi) + thread) * 16; at < total; at += step)
-    FP8Q_GUARD(at, 16, total, p.err) { stg128(static_cast<uint8_t*>(p.c) + at, 0u, 0u, 0u, 0u); }
+  for (int64_t at = from * row_bytes + (static_cast<int64_t>(blockIdx.x) * (32 * kEpi) + thread) * 16; at < end; at += step)
+    FP8Q_GUARD(at, 16, p.capacity * row_bytes, p.err) { stg128(static_cast<uint8_t*>(p.c) + at, 0u, 0u, 0u, 0u); }
+}
+// The rows outside the segments, as p.zero_tail asks.
+__device__ __forceinline__ void zero_outside(const GroupedParams& p, const int* offs, int thread) {
+  if (p.zero_tail > 0) zero_rows(p, offs[p.n_experts], p.capacity, thread);
+  if (p.zero_tail > 1) zero_rows(p, 0, offs[0], thread);
 }
 
 __host__ __device__ constexpr uint32_t table_bytes(int n_experts) { return 8u * static_cast<uint32_t>(n_experts + 1); }   // offs, first
@@ -439,7 +445,7 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
         }
       }
     }
-    if (p.zero_tail) zero_tail(p, offs[p.n_experts], static_cast<int>(threadIdx.x) - 64);
+    zero_outside(p, offs, static_cast<int>(threadIdx.x) - 64);
     if (lane == 0) bulk_wait_all<0>();   // this warp's stores have finished
   }
 
@@ -742,7 +748,7 @@ __global__ void __launch_bounds__(grouped_threads<KIND>(), 1)
         ++acc_it;
       }
     }
-    if (p.zero_tail) zero_tail(p, offs[p.n_experts], static_cast<int>(threadIdx.x) - 64);
+    zero_outside(p, offs, static_cast<int>(threadIdx.x) - 64);
     if (lane == 0) bulk_wait_all<0>();   // this warp's stores have finished
   }
 

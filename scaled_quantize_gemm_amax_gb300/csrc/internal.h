@@ -416,7 +416,7 @@ struct GroupedParams {
   const float* sb;       // kTensor: float[1] or (sb_step 1) one an expert
   int sb_step;
   void* c;
-  int zero_tail;         // rows: rows behind the last segment are set to 0
+  int zero_tail;         // rows: 1: rows behind the last segment are set to 0, 2: those in front of the first too
   int loads;             // whether there is anything to multiply (the tensor maps of A and B are valid)
   uint32_t* err;
 };

@@ -616,7 +616,7 @@ PyObject* grouped_gemm(PyObject* const* v) {
     refuse(PyExc_ValueError, "b: " + std::to_string(experts) + " experts' matrices of depth " + std::to_string(depth) +
                                  (cols ? " side by side" : " one below the other") + " are needed, not " + shape_of(*b.t));
   on_gpu({v[0], v[3], v[4], v[7], v[8]});
-  const bool zero_tail = truth(v[11]);
+  const int32_t zero_tail = truth(v[11]) ? 2 : 0;   // the allocation's rows outside the segments, in front and behind
   Place on;
   const cudaStream_t stream = stream_of(v[12], *a.t, on);
   at::Tensor c;

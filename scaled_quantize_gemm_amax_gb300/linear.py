@@ -218,7 +218,7 @@ def fp8_grouped_linear(xs, weight, offsets, recipe=None, states=None):
     """Every expert's rows of xs [capacity, K] (bf16 or float32) times its weight of [experts, N, K] (float32), through
     three grouped FP8 products; offsets [experts + 1] as ``moe_route`` with align 128 gives them.
 
-    Rows behind the last segment give 0; those of xs, and of the output's gradient, must be finite (per-tensor scaling takes
+    Rows outside the segments give 0; those of xs, and of the output's gradient, must be finite (per-tensor scaling takes
     its amax over them; ``moe_dispatch`` and the gradient of ``moe_combine`` set them to 0)."""
     recipe = recipe if recipe is not None else get_fp8_recipe()
     if xs.dim() != 2 or weight.dim() != 3 or xs.shape[1] != weight.shape[2]:
