@@ -123,8 +123,9 @@ __device__ __forceinline__ void zero_rows(const GroupedParams& p, int64_t from, 
 }
 // The rows outside the segments, as p.zero_tail asks.
 __device__ __forceinline__ void zero_outside(const GroupedParams& p, const int* offs, int thread) {
-  if (p.zero_tail > 0) zero_rows(p, offs[p.n_experts], p.capacity, thread);
-  if (p.zero_tail > 1) zero_rows(p, 0, offs[0], thread);
+  const int lo = offs[0], hi = offs[p.n_experts];
+  if (p.zero_tail > 0 && hi < p.capacity) zero_rows(p, hi, p.capacity, thread);
+  if (p.zero_tail > 1 && lo > 0) zero_rows(p, 0, lo, thread);
 }
 
 __host__ __device__ constexpr uint32_t table_bytes(int n_experts) { return 8u * static_cast<uint32_t>(n_experts + 1); }   // offs, first
