@@ -663,6 +663,17 @@ fp8_status fp8_debug_index_check(int64_t index, int64_t extent, cudaStream_t str
 fp8_status fp8_debug_gemm_plan(fp8_recipe ra, fp8_recipe rb, fp8_out_dtype out, int64_t M, int64_t N, int64_t K,
                                int32_t fused, int32_t num_sms, int32_t resident_pairs, int64_t* plan);
 
+/*
+ * fp8_debug_grouped_plan -- how fp8_grouped_gemm (M 0) or fp8_grouped_wgrad (its M) would divide a
+ * product of N columns with these recipes and output type on a device with `num_sms` SMs: host logic
+ * only, no device call.  Writes plan[0..2] = {columns of a CTA's tile of 128 rows, 0 for CTA pairs on
+ * tiles of 256 x 256; stages of the ring of B's blocks; accumulators in TMEM}.  Errors as the argument
+ * checks of those calls; `plan` (3 int64, host memory) is the caller's.  Exists to test the dispatch
+ * rule without a GPU.
+ */
+fp8_status fp8_debug_grouped_plan(fp8_recipe ra, fp8_recipe rb, fp8_out_dtype out, int32_t n_experts, int64_t capacity, int64_t M,
+                                  int64_t N, int32_t num_sms, int64_t* plan);
+
 /* Human-readable name of a status code (static storage). */
 const char* fp8_status_string(fp8_status status);
 

@@ -14,7 +14,7 @@ Entry points with the C names take tensors (or None for NULL) and raise
 ``amax_history_update``, ``fp8_quantize``, ``fp8_cast_transpose``, ``fp8_cast_transpose_f32``,
 ``fp8_cast_transpose_multi``,
 ``fp8_dequantize``, ``fp8_allreduce_sum``, ``fp8_scaled_gemm``, ``fp8_scaled_gemm_amax``,
-``fp8_get_device_status``, ``fp8_debug_wait_timeout``, ``fp8_debug_gemm_plan``,
+``fp8_get_device_status``, ``fp8_debug_wait_timeout``, ``fp8_debug_gemm_plan``, ``fp8_debug_grouped_plan``,
 ``fp8_debug_index_check``; and the row operators between the linear layers,
 ``fp8_layer_norm``, ``fp8_layer_norm_backward``, ``fp8_gated_act``,
 ``fp8_gated_act_backward``, ``fp8_moe_route``, ``fp8_moe_dispatch``, ``fp8_moe_combine``,
@@ -43,7 +43,7 @@ __all__ = [
     "fp8_cast_transpose_f32",
     "fp8_cast_transpose_multi", "CastJob",
     "fp8_dequantize", "fp8_allreduce_sum", "fp8_allreduce_sum_noalloc", "fp8_scaled_gemm", "fp8_scaled_gemm_amax", "fp8_get_device_status",
-    "fp8_debug_wait_timeout", "fp8_debug_gemm_plan", "fp8_debug_index_check", "fp8_status_string",
+    "fp8_debug_wait_timeout", "fp8_debug_gemm_plan", "fp8_debug_grouped_plan", "fp8_debug_index_check", "fp8_status_string",
     "scale_shape", "cast_transpose", "cast_transpose_multi", "dequantize", "allreduce_sum", "scaled_gemm", "scaled_gemm_amax",
     "DelayedScaling",
     "Activation", "MoeRoute",
@@ -170,6 +170,7 @@ _SIGNATURES = {
     "fp8_grad_norm_workspace": [_I32, _P],
     "fp8_get_device_status": [_P],
     "fp8_debug_wait_timeout": [_P],
+    "fp8_debug_grouped_plan": [_E, _E, _E, _I32, _I64, _I64, _I64, _I32, _P],
     "fp8_debug_gemm_plan": [_E, _E, _E, _I64, _I64, _I64, _I32, _I32, _I32, _P],
     "fp8_debug_index_check": [_I64, _I64, _P],
     "fp8_status_string": [_E],
@@ -714,6 +715,14 @@ def fp8_debug_gemm_plan(ra, rb, out, m: int, n: int, k: int, fused: bool = False
                                                                       num_sms, resident_pairs, plan))
     keys = ("pair", "variant", "block_n", "tiles", "streamk", "split", "tail0", "launched")
     return dict(zip(keys, (int(v) for v in plan)))
+
+
+def fp8_debug_grouped_plan(ra, rb, out, experts: int, capacity: int, n: int, m: int = 0, num_sms: int = 152) -> dict:
+    """The division fp8_grouped_gemm, or with m fp8_grouped_wgrad, would choose (host logic only, no device call)."""
+    plan = (ctypes.c_int64 * 3)()
+    _check("fp8_debug_grouped_plan",
+           load_library().fp8_debug_grouped_plan(int(ra), int(rb), int(out), experts, capacity, m, n, num_sms, plan))
+    return dict(zip(("width", "stages", "accumulators"), (int(v) for v in plan)))
 
 
 # ------------------------------------------------------------------ allocation helpers

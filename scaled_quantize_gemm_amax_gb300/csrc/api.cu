@@ -1117,7 +1117,8 @@ fp8_status grouped(GroupedParams& p, const uint8_t* A, fp8_format fa, fp8_recipe
   p.sb = static_cast<const float*>(sB);
   p.loads = loads;
   p.err = d->err;
-  const int width = grouped_width(p, d->num_sms);
+  const GroupedPlan g = grouped_plan(p, d->num_sms);
+  const int width = g.width;
   GroupedMaps m;
   std::memset(&m, 0, sizeof(m));
   if (loads) {
@@ -1138,7 +1139,7 @@ fp8_status grouped(GroupedParams& p, const uint8_t* A, fp8_format fa, fp8_recipe
                       ? make_map(&m.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.c, p.N, c_rows, 64, 32)
                       : make_map(&m.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.c, p.N, c_rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (!ok) return FP8_ERR_CUDA;
-  return cuda_status(launch_grouped(p, m, width, d->num_sms, stream));
+  return cuda_status(launch_grouped(p, m, g, d->num_sms, stream));
 }
 
 // The kind of a pairing, among those that the grouped products take.
@@ -1198,6 +1199,26 @@ fp8_status fp8_grouped_wgrad(const uint8_t* A, fp8_format fa, fp8_recipe ra, con
   p.N = static_cast<int>(N);
   p.c = C;
   return grouped(p, A, fa, ra, sA, B, fb, rb, sB, M, capacity, N, capacity, n_experts * M, out, stream);
+}
+
+fp8_status fp8_debug_grouped_plan(fp8_recipe ra, fp8_recipe rb, fp8_out_dtype out, int32_t n_experts, int64_t capacity, int64_t M,
+                                  int64_t N, int32_t num_sms, int64_t* plan) {
+  GroupedParams p{};
+  if (plan == nullptr || capacity < 0 || M < 0 || N < 0 || n_experts < 1 || num_sms < 2) return FP8_ERR_INVALID_ARG;
+  if (fp8_status st = grouped_kind(FP8_E4M3, ra, FP8_E4M3, rb, out, &p.kind)) return st;
+  if (capacity % 128 || M % 128 || N % 128 || n_experts > kMaxExperts || capacity > kMaxDim || M > kMaxDim || N > kMaxDim)
+    return FP8_ERR_SHAPE;
+  p.depth = M > 0;
+  p.n_experts = n_experts;
+  p.capacity = capacity;
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.out_fp32 = out == FP8_OUT_FP32;
+  const GroupedPlan g = grouped_plan(p, num_sms);
+  plan[0] = g.width;
+  plan[1] = g.stages;
+  plan[2] = g.accumulators;
+  return FP8_OK;
 }
 
 }  // extern "C"

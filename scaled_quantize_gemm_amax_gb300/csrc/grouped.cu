@@ -818,8 +818,6 @@ int64_t most_tiles(const GroupedParams& p, int tile_rows, int tile_cols) {
   return (blocks + used * (per - 1)) / per * tn;
 }
 
-}  // namespace
-
 // The tile width of a call: 0 for CTA pairs, else that of one CTA's 128-row tiles: what takes the fewest cycles a
 // 128-deep block, rounds of tiles times a tile's.  A pair's tile is bound by its four MMAs (~175 each); a tile of
 // one CTA by what it fetches, A's 128 rows and its width of B's at 48 bytes a cycle, and where TMEM holds one
@@ -856,12 +854,29 @@ int grouped_width(const GroupedParams& p, int num_sms) {
   return best;
 }
 
-cudaError_t launch_grouped(const GroupedParams& p, const GroupedMaps& m, int width, int num_sms, cudaStream_t s) {
+}  // namespace
+
+GroupedPlan grouped_plan(const GroupedParams& p, int num_sms) {
+  GroupedPlan g{};
   const bool mx = p.kind == kMx;
+  g.width = grouped_width(p, num_sms);
+  if (g.width == 0) {
+    g.stages = !mx && p.n_experts <= kSixStageExperts ? 6 : 5;
+    g.accumulators = mx ? PairLayout<kMx, 5>::ACC : PairLayout<kTensor, 5>::ACC;
+  } else {
+    g.stages = FewLayout(g.width, mx, p.out_fp32 != 0, p.n_experts).sb;
+    g.accumulators = FewLayout::accumulators(mx, g.width);
+  }
+  return g;
+}
+
+cudaError_t launch_grouped(const GroupedParams& p, const GroupedMaps& m, const GroupedPlan& g, int num_sms, cudaStream_t s) {
+  const bool mx = p.kind == kMx;
+  const int width = g.width;
   if (width == 0) {
     const int64_t tiles = most_tiles(p, 2 * kRows, kPairCols);
     if (mx) return run_pairs<kMx, 5>(p, m, tiles, num_sms, s);
-    return p.n_experts <= kSixStageExperts ? run_pairs<kTensor, 6>(p, m, tiles, num_sms, s) : run_pairs<kTensor, 5>(p, m, tiles, num_sms, s);
+    return g.stages == 6 ? run_pairs<kTensor, 6>(p, m, tiles, num_sms, s) : run_pairs<kTensor, 5>(p, m, tiles, num_sms, s);
   }
   const int64_t tiles = most_tiles(p, kRows, width);
   return mx ? run_few<kMx>(p, m, width, tiles, num_sms, s) : run_few<kTensor>(p, m, width, tiles, num_sms, s);

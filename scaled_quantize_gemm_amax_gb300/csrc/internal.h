@@ -423,10 +423,15 @@ struct GroupedParams {
 struct GroupedMaps {
   CUtensorMap a, b, sfa, sfb, c;
 };
-// Columns of a CTA's tile, 0 for CTA pairs.  Boxes have 128 rows of A; 128 of B for pairs, else the width; of C 32 rows of
+// How a call is divided.  Boxes have 128 rows of A; 128 of B for pairs, else the width; of C 32 rows of
 // 128 bytes, or of 64 with bf16 and no pairs, swizzled as wide.  Pairs with per-tensor scales have A by boxes of 64 rows in sfa.
-int grouped_width(const GroupedParams& p, int num_sms);
-cudaError_t launch_grouped(const GroupedParams& p, const GroupedMaps& m, int width, int num_sms, cudaStream_t s);
+struct GroupedPlan {
+  int width;             // columns of a CTA's tile of 128 rows, 0 for CTA pairs and tiles of 256 x 256
+  int stages;            // of the ring (without pairs of B's)
+  int accumulators;      // in TMEM
+};
+GroupedPlan grouped_plan(const GroupedParams& p, int num_sms);
+cudaError_t launch_grouped(const GroupedParams& p, const GroupedMaps& m, const GroupedPlan& g, int num_sms, cudaStream_t s);
 
 // Bounded-wait self test: one CTA waits on an mbarrier nothing arrives on.
 cudaError_t launch_wait_selftest(uint32_t* err, cudaStream_t s);
