@@ -87,3 +87,15 @@ def test_an_input_changed_before_the_backward_pass_is_noticed(shape):
         x += 1
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.sum().backward()
+
+
+@pytest.mark.parametrize("used", [(True, True), (True, False), (False, True)])
+@pytest.mark.parametrize("way", ["leaf", "product", "sum of a leaf"])
+@pytest.mark.parametrize("shape", [(6, 8), (2, 3, 8)])
+def test_one_tensor_as_both_inputs(shape, way, used):
+    x, = leaves(shape)
+    grads = [g for g, u in zip((torch.randn(shape, dtype=torch.float64), torch.randn(shape, dtype=torch.float64)), used) if u]
+    a = WAYS[way]((x,))
+    torch.autograd.backward([t for t, u in zip(B.rms_norm(a, None, a), used) if u], grads)
+    want, = torch.autograd.grad([t for t, u in zip(reference(x, None, x), used) if u], x, grads)
+    assert torch.allclose(x.grad, want)
