@@ -556,7 +556,9 @@ fp8_status fp8_rms_norm_workspace(int64_t rows, int64_t cols, int64_t* bytes);
  *   capacity    rows that A (and C, or B) have; a multiple of 128
  * Operands are FP8, row-major and dense, with the recipes (ra, rb) = (FP8_TENSOR, FP8_TENSOR) or
  * two of FP8_MX_1x32_TILED and FP8_MX_1x32_FLOOR_TILED, scales as fp8_cast_transpose writes them
- * (other pairings FP8_ERR_UNSUPPORTED).  Accumulation is binary32; C is rounded once.  M, N, K and
+ * (other pairings FP8_ERR_UNSUPPORTED).  Accumulation is the tensor core's, as fp8_scaled_gemm's: binary32
+ * whose additions truncate (a sum over a depth of 2000 is off by about 3e-7, three times a rounded one);
+ * C is rounded once.  M, N, K and
  * capacity are multiples of 128, and they, n_experts times M, N or K and the number of 128 x 32
  * tiles that the outputs could have below 2^31 (FP8_ERR_SHAPE).  Matrices and tiled scales are 16-byte aligned.
  */

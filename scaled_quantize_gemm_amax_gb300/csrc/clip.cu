@@ -11,7 +11,8 @@
 //
 // Bound by HBM: the gradients once in for the norm, once in and once out for the clipping: 810 million bf16 734 us (three
 // passes of 1.6 GB take 718 at a copy's rate), 39.5 million 36 us (the second read from L2: two passes take 23, four to five us
-// of launches and first loads in each).
+// of launches and first loads in each).  Outputs that lie at another place of their 16 bytes than their gradients are written element
+// by element, bound by those accesses: 134 million bf16 475 us instead of 126, half as many binary32 283.
 #include <cfloat>
 
 #include "internal.h"

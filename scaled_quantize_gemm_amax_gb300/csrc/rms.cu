@@ -22,8 +22,8 @@ namespace {
 template <typename T, bool VECTOR, int V>
 constexpr int kBlockWarps = V == 8 ? 32 : (V == 32 && !VECTOR && sizeof(T) == 4 ? 16 : 24);
 // Bytes of a block's rows and of its stages (rms_plan).  With a residual, bf16 and 1x128 codes, 65536x4096: 64 KB 275 us,
-// 96 KB 300, two stages of 96 KB 319; 8192x4096 39.7, 39.8 and 43.5.  Unaligned rows are bound by their instructions and take
-// the warps that fit: 8192x4099 65 us with 96 KB, 73 with 64.
+// 96 KB 300, two stages of 96 KB 319; 8192x4096 39.7, 39.8 and 43.5.  Unaligned rows take 2.2 times the instructions, whose waits
+// (issue slots 39 % busy, shared memory 44 %) more warps hide, as many as fit: 8192x4099 65 us with 96 KB, 73 with 64.
 template <bool VECTOR>
 constexpr int kMost = (VECTOR ? 64 : 96) * 1024;
 constexpr int kInFlight = 64 * 1024;
@@ -324,7 +324,7 @@ cudaError_t run_rms(const RmsParams& p, int num_sms, cudaStream_t s) {
 
 // Values a lane: 8 for rows of up to 256 columns; 32 halve what a row costs besides its values; 16 where that would leave
 // lanes empty (up to 512 columns) or where a row's latency counts and there are warps to spare, and for unaligned rows,
-// bound by their instructions, while a row's ends cost more than its middle: binary32 (4096x4099 with a residual 45 us, 73 with
+// which wait for their own instructions, while a row's ends cost more than its middle: binary32 (4096x4099 with a residual 45 us, 73 with
 // 32 values; 2048x9001 50 and 77) and bf16 up to 3584 columns (16384x1003 42 and 52, 8192x3001 50 and 51; 8192x4099 74 and 65).
 template <typename T, bool VECTOR>
 cudaError_t run_rms(const RmsParams& p, int num_sms, cudaStream_t s) {
