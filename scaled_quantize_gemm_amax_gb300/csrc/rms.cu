@@ -324,8 +324,8 @@ cudaError_t run_rms(const RmsParams& p, int num_sms, cudaStream_t s) {
 
 // Values a lane: 8 for rows of up to 256 columns; 32 halve what a row costs besides its values; 16 where that would leave
 // lanes empty (up to 512 columns) or where a row's latency counts and there are warps to spare, and for unaligned rows,
-// which wait for their own instructions, while a row's ends cost more than its middle: binary32 (4096x4099 with a residual 45 us, 73 with
-// 32 values; 2048x9001 50 and 77) and bf16 up to 3584 columns (16384x1003 42 and 52, 8192x3001 50 and 51; 8192x4099 74 and 65).
+// which wait for their own instructions, while a row's ends cost more than its middle: binary32 (4096x4099 with a residual 45
+// us, 73 with 32 values; 2048x9001 50 and 77) and bf16 up to 3584 columns (16384x1003 42 and 52, 8192x3001 50 and 51; 8192x4099 74 and 65).
 template <typename T, bool VECTOR>
 cudaError_t run_rms(const RmsParams& p, int num_sms, cudaStream_t s) {
   constexpr int64_t kMost16 = kBlockWarps<T, VECTOR, 16> * 512, kMostUnaligned = sizeof(T) == 4 ? kMost16 : 7 * 512;

@@ -10,8 +10,8 @@
 // sum a block, added up by a second, small launch.  Few rows take one launch of another kind (k_rms_backward_few).
 // bf16 with dh: 8192x4096 44 to 46 us (6.0 TB/s, 0.89 of what a copy reaches), 65536x4096 307 (1.03), 4096x8192 46; without
 // dh 2048x12288 32 (0.69), 8192x12288 95 (0.94): what does not grow with the rows is the weights' way to every SM (1.8
-// us) and the column sums (4.4 us, the second launch included).  binary32 8192x4096 81 to 92 (0.97 to 0.86, boxes differ); 2048x16384, whose dh
-// does not fit beside dy and h and is read late, 123 (0.65).  Unaligned bf16 8192x4099 91 (0.44), binary32 4096x4099 67 (0.59).
+// us) and the column sums (4.4 us, the second launch included).  binary32 8192x4096 81 to 92 (0.97 to 0.86, boxes differ);
+// 2048x16384, whose dh does not fit beside dy and h and is read late, 123 (0.65).  Unaligned bf16 8192x4099 91 (0.44), binary32 4096x4099 67 (0.59).
 // Rows of more than kMostCols columns are read three times, once for dw: bf16 2048x16512 90 (0.44).
 #include "rms.cuh"
 
@@ -29,9 +29,11 @@ constexpr int kInFlight = 104 * 1024;
 
 // Few rows (no more than SMs; half as many if unaligned binary32), of any width: one launch for both results, which need only the
 // rstd of the forward pass.  Block r < rows takes row r, in two passes; the blocks behind them sum dw over all rows, kFewCols columns
-// each, warp w the rows w, w + kFewWarps, ...  Without the latter, dx of rows that registers cannot hold.  bf16 with dh, us, and by partial sums and a second launch: 1x4096 2.1 and 3.9,
-// 16x12288 3.8 and 7.1, 64x4096 2.2 and 4.9, 152x8192 4.8 and 7.9; binary32 152x12288 9.8 and 10.8.  Beyond as many rows as SMs a second round of blocks soon costs more than the
-// second launch: of narrow rows 256x1024 are a little faster in one launch (4.0 and 4.6), 512x1024 are not (7.6 and 4.8); unaligned binary32 64x5849 5.6 and 7.9, 128x5849 11.4 and 8.9.
+// each, warp w the rows w, w + kFewWarps, ...  Without the latter, dx of rows that registers cannot hold.  bf16 with dh, us, and by
+// partial sums and a second launch: 1x4096 2.1 and 3.9, 16x12288 3.8 and 7.1, 64x4096 2.2 and 4.9, 152x8192 4.8 and 7.9; binary32
+// 152x12288 9.8 and 10.8; unaligned binary32 64x5849 5.6 and 7.9, 128x5849 11.4 and 8.9.  Beyond as many rows as SMs a second round
+// of blocks soon costs more than the second launch: of narrow rows 256x1024 are a little faster in one launch (4.0 and 4.6),
+// 512x1024 are not (7.6 and 4.8).
 constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32, kFewLane = 4, kFewCols = 32 * kFewLane;
 __device__ __forceinline__ void load4(const float* m, float* v) {
   const float4 u = __ldg(reinterpret_cast<const float4*>(m));
