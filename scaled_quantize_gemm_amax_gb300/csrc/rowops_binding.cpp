@@ -6,6 +6,7 @@
 // are handed over by bind(), so that this module and the ctypes binding use the same loaded
 // library.  Arguments are positional (the Python helpers give them names and defaults).
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -683,8 +684,9 @@ const at::Tensor& dense(PyObject* o, const char* what) {
 }
 
 // The memory of a call's tensors: what one of them writes must not be part of another, whose turn may come first
-// or last.  Tensors of different storages are apart, and those of one storage are seen to be apart on the way when
-// they come in ascending order, as views into a buffer do; only others are sorted.
+// or last.  Tensors of different storages are apart if torch's allocator made both (one taken over from elsewhere, as by DLPack, may
+// lie in another's memory), and those of one storage are seen to be apart on the way when they come in ascending
+// order, as views into a buffer do; only others are sorted.
 class Spans {
  public:
   explicit Spans(size_t n) {
@@ -698,7 +700,8 @@ class Spans {
     const auto lo = reinterpret_cast<uintptr_t>(t.const_data_ptr());
     const uintptr_t hi = lo + static_cast<uintptr_t>(t.numel() * t.element_size());
     all_.push_back({lo, hi, written});
-    const void* storage = t.unsafeGetTensorImpl()->unsafe_storage().unsafeGetStorageImpl();
+    const c10::StorageImpl* const storage = t.unsafeGetTensorImpl()->unsafe_storage().unsafeGetStorageImpl();
+    if (storage->data_ptr().get_deleter() != own_) sorted_ = false;
     size_t i = (reinterpret_cast<uintptr_t>(storage) >> 4) * 0x9E3779B97F4A7C15ull >> 20;
     while (true) {
       End& e = ends_[i++ & (ends_.size() - 1)];
@@ -729,6 +732,7 @@ class Spans {
     const void* storage = nullptr;
     uintptr_t hi = 0;
   };
+  const c10::DeleterFnPtr own_ = c10::cuda::CUDACachingAllocator::get()->raw_deleter();
   std::vector<Span> all_;
   std::vector<End> ends_;   // by storage, open addressing
   bool sorted_ = true;

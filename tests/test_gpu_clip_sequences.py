@@ -91,3 +91,22 @@ def test_generators():
         assert torch.equal(fq.clip_grad_norm(make(grads), 0.5), norm)
         for a, b, c in zip(outs, grads, want):
             assert torch.equal(a, c) and torch.equal(b, c)
+
+
+def test_refuses_memory_shared_by_another_storage():
+    """A tensor taken over by DLPack has a storage of its own in the other's memory."""
+    b = torch.randn(1000, generator=gen(9), device="cuda")
+    other = torch.from_dlpack(b)
+    assert other.untyped_storage().data_ptr() == b.untyped_storage().data_ptr() and other.data_ptr() == b.data_ptr()
+    was = b.clone()
+    for grads, out in (([b, other], None), ([other, b], None), ([b[:600], torch.from_dlpack(b[500:])], None),
+                       ([torch.from_dlpack(b[500:]), b[:600]], None), ([b[:500]], [other[250:750]]), ([other[:500]], [b[250:750]])):
+        with pytest.raises(ValueError, match="share memory"):
+            fq.clip_grad_norm(grads, 0.1, out=out)
+        assert torch.equal(b, was)
+    norm, want = expected([was[:500], was[500:]], 0.1)
+    assert torch.equal(fq.clip_grad_norm([b[:500], torch.from_dlpack(b[500:])], 0.1), norm)    # apart
+    assert torch.equal(b, torch.cat(want))
+    b.copy_(was)
+    assert torch.equal(fq.clip_grad_norm([b[:500], b[500:]], 0.1, out=[other[:500], other[500:]]), norm)   # each in itself
+    assert torch.equal(b, torch.cat(want))
