@@ -497,7 +497,7 @@ PyObject* rms_norm(PyObject* const* a) {
   {
     Unlocked unlocked;
     // the codes and their multipliers in one allocation; with little data (a few tokens) all outputs are.  The statistics, which
-    // a backward pass holds long after the codes were used, are apart from much of them.
+    // a backward pass holds long after the codes were used, are apart from much of them: with h, which it holds too, or alone.
     int64_t shape[3] = {1, 1, 1}, dims = 1, scales = 0;
     if (copy) {
       if (is_tiled(recipe)) {
@@ -521,14 +521,21 @@ PyObject* rms_norm(PyObject* const* a) {
       return part(whole, at - data, x.t->scalar_type(), {x.rows, x.cols}, {x.cols, 1});
     };
     y = matrix(keep_y);
-    h = matrix(res.t != nullptr);
+    if (!together && stats && res.t != nullptr) {
+      const at::Tensor kept = make({data + rest}, at::kByte, *x.t);
+      h = part(kept, 0, x.t->scalar_type(), {x.rows, x.cols}, {x.cols, 1});
+      rstd = part(kept, data, at::kFloat, {x.rows}, {1});
+    } else {
+      h = matrix(res.t != nullptr);
+    }
     if (copy) {
       const int64_t strides[3] = {dims == 1 ? 1 : shape[1] * shape[2], dims == 2 ? 1 : shape[2], 1};
       q = part(whole, at, at::kByte, {x.rows, x.cols}, {ldq, 1});
       s = part(whole, at + codes, is_mx(recipe) ? at::kByte : at::kFloat, {shape, static_cast<size_t>(dims)},
                {strides, static_cast<size_t>(dims)});
     }
-    if (stats) rstd = together ? part(whole, at + codes + scales, at::kFloat, {x.rows}, {1}) : make({x.rows}, at::kFloat, *x.t);
+    if (stats && !rstd.defined())
+      rstd = together ? part(whole, at + codes + scales, at::kFloat, {x.rows}, {1}) : make({x.rows}, at::kFloat, *x.t);
     st = p_fp8_rms_norm(x.p(), x.rows, x.cols, x.ld, dt, res.p(), res.ld, w, wdt, static_cast<float>(eps), ptr<void>(h), x.cols,
                         ptr<void>(y), x.cols, ptr<float>(rstd), recipe, fmt, scale, amax, ptr<uint8_t>(q), ldq, ptr<void>(s),
                         stream);

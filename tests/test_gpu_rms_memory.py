@@ -27,7 +27,7 @@ def test_statistics_do_not_hold_the_codes(residual, keep_y, recipe):
     before = torch.cuda.memory_allocated()
     y, h, rstd, q, s = fq.rms_norm(x, None, res, recipe=recipe, scale=scale if recipe == R.TENSOR else None, keep_y=keep_y)
     held = rstd.untyped_storage().nbytes()
-    assert held <= 4 * rows + 16
+    assert held <= (2 * rows * cols if residual else 0) + 4 * rows + 16     # h stays as long as they do
     del y, q, s
     # h, and rstd rounded up to the allocator's 512 bytes
     kept = torch.cuda.memory_allocated() - before
