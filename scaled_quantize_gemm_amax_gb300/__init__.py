@@ -926,7 +926,8 @@ def grouped_gemm(a, fa, ra, sa, b, fb, rb, sb, offsets, out=OutDtype.BF16, stack
                  stream=None):
     """Allocate C [capacity, N] and run fp8_grouped_gemm: every expert's rows of a times its matrix of b.
 
-    Rows in front of the first segment and behind the last are 0, or with zero_tail=False whatever the allocation held."""
+    Rows in front of the first segment and behind the last are 0, or with zero_tail=False whatever the allocation held.
+    Offsets that the product does not take (fp8_get_device_status reports them) leave all of C so."""
     return (_ext or _rowops()).grouped_gemm(a, fa, ra, sa, b, fb, rb, sb, offsets, out, stacked, zero_tail, stream)
 
 

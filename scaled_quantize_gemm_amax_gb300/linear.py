@@ -219,7 +219,8 @@ def fp8_grouped_linear(xs, weight, offsets, recipe=None, states=None):
     three grouped FP8 products; offsets [experts + 1] as ``moe_route`` with align 128 gives them.
 
     Rows outside the segments give 0; those of xs, and of the output's gradient, must be finite (per-tensor scaling takes
-    its amax over them; ``moe_dispatch`` and the gradient of ``moe_combine`` set them to 0)."""
+    its amax over them; ``moe_dispatch`` and the gradient of ``moe_combine`` set them to 0).  Offsets that are not ascending
+    multiples of 128 within the capacity leave the outputs unwritten, which ``fp8_get_device_status`` reports."""
     recipe = recipe if recipe is not None else get_fp8_recipe()
     if xs.dim() != 2 or weight.dim() != 3 or xs.shape[1] != weight.shape[2]:
         raise ValueError(f"fp8_grouped_linear: [capacity, K] rows and [experts, N, K] weights are needed, not {tuple(xs.shape)} and "
