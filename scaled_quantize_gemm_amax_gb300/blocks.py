@@ -84,8 +84,11 @@ class _RMSNormFn(torch.autograd.Function):
     def forward(ctx, x, weight, residual, eps):
         ctx.set_materialize_grads(False)
         w = weight.detach() if weight is not None else None
-        y, h, rstd, _, _ = _rms_norm(_flat(x), w, _flat(residual) if residual is not None else None, eps)
-        ctx.save_for_backward(w, x if residual is None else h, rstd)
+        rows = _flat(x)
+        y, h, rstd, _, _ = _rms_norm(rows, w, _flat(residual) if residual is not None else None, eps)
+        if residual is None:   # x itself, whose changes autograd notices, or the copy that was made of it
+            h = x if rows.data_ptr() == x.data_ptr() else rows
+        ctx.save_for_backward(w, h, rstd)
         ctx.has_residual, ctx.shape = residual is not None, x.shape
         return (y, h) if residual is not None else y
 

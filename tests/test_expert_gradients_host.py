@@ -99,3 +99,21 @@ def test_one_tensor_as_both_inputs(shape, way, used):
     torch.autograd.backward([t for t, u in zip(B.rms_norm(a, None, a), used) if u], grads)
     want, = torch.autograd.grad([t for t, u in zip(reference(x, None, x), used) if u], x, grads)
     assert torch.allclose(x.grad, want)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+def test_inputs_that_are_copied_are_copied_once(residual, monkeypatch):
+    """A transposed input is made contiguous for the forward pass; the backward pass takes that copy."""
+    x, = leaves((8, 6))
+    seen = []
+    forward, backward = B._rms_norm, B._rms_norm_backward
+    monkeypatch.setattr(B, "_rms_norm", lambda x, *a: seen.append(x.data_ptr()) or forward(x, *a))
+    monkeypatch.setattr(B, "_rms_norm_backward", lambda dy, h, *a, **k: seen.append(h.data_ptr()) or backward(dy, h, *a, **k))
+    res = torch.randn(6, 8, dtype=torch.float64) if residual else None
+    y = B.rms_norm(x.t(), None, res)
+    y = y[0] if residual else y
+    dy = torch.randn(6, 8, dtype=torch.float64)
+    got, = torch.autograd.grad(y, x, dy)
+    want, = torch.autograd.grad(reference(x.t(), None, res)[0], x, dy)
+    assert torch.allclose(got, want)
+    assert seen[0] != x.data_ptr() and (residual or seen[1] == seen[0])
